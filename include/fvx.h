@@ -388,6 +388,89 @@ fvx_status fvx_hits_view(fvx_hits h, const int64_t** offsets, const int32_t** vo
                          int64_t* n_hits, int64_t* n_rays);
 fvx_status fvx_hits_destroy(fvx_hits h);
 
+/* ---------------------------------------------------------------------------
+ * Layer norm over voxel features, activation checkpoints in 8 bits, and cross
+ * attention to an encoder's states: what a network around the sparse
+ * convolution trains on between two convolutions.
+ *
+ * Types: FVX_F32 (fp32 tensors) or FVX_BF16 (bf16 tensors in and out);
+ * statistics, sums and softmax are fp32 in both.  Weights, biases and their
+ * gradients are fp32.  All calls are asynchronous and do not synchronise; any
+ * alignment of whole elements and any row pitch (in elements) is accepted,
+ * 16-byte aligned rows are faster.
+ *
+ * Layer norm, per row r of x [n, c] (c in 1..65536, row pitch ldx >= c):
+ *   mean = sum x / c;  rstd = 1 / sqrt(sum (x - mean)^2 / c + eps)
+ *   y = (x - mean) * rstd * w + b      (w, b: device [c], NULL = ones / zeros)
+ * mean, rstd: device [n], written; the backward pass reads them.
+ * group 32, 64 or 128: x's checkpoint is written by the same pass to codes and
+ * steps (below); group 0: none, and both are ignored.
+ * Errors: FVX_ERR_INVALID_ARG. */
+fvx_status fvx_layer_norm(fvx_dtype dt, const void* x, int64_t ldx, int64_t n, int64_t c, const float* w,
+                          const float* b, float eps, void* y, int64_t ldy, float* mean, float* rstd, int32_t group,
+                          int8_t* codes, float* steps, fvx_stream stream);
+
+/* With xh = (x - mean) * rstd and g = dy * w:
+ *   dx = rstd * (g - sum(g) / c - xh * sum(g * xh) / c)
+ *   dw = sum over rows of dy * xh;  db = sum over rows of dy   (fp32 [c])
+ * x is read from the tensor (group 0) or, with x NULL, from its checkpoint.
+ * dw, db may be NULL.  The order of every sum is fixed: the same call gives
+ * the same bits.  dx may be dy's own memory (row pitch lddx = lddy). */
+fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, const void* x, int64_t ldx,
+                                   int32_t group, const int8_t* codes, const float* steps, int64_t n, int64_t c,
+                                   const float* w, const float* mean, const float* rstd, void* dx, int64_t lddx,
+                                   float* dw, float* db, fvx_stream stream);
+
+/* Activation checkpoint of x [n, c]: codes int8 [n, c] and steps fp32
+ * [n, ceil(c / group)], both dense.  A group is `group` (32, 64 or 128)
+ * consecutive channels of a row (the last may be shorter); with
+ * top = max |x| of the group, step = top / 127 and
+ * code = round-half-even(x * (127 / top)), in fp32.  The value held is
+ * code * step: within step / 2 of x, up to fp32 rounding.  A group with top
+ * below 2^-100 holds zeros; one with an infinity or a NaN holds NaN. */
+fvx_status fvx_checkpoint_pack(fvx_dtype dt, const void* x, int64_t ldx, int64_t n, int64_t c, int32_t group,
+                               int8_t* codes, float* steps, fvx_stream stream);
+
+/* The values a checkpoint holds, written to out [n, c] (pitch ldo); with mean
+ * and rstd, their layer norm (v - mean) * rstd * w + b instead: the input of
+ * whatever followed the norm, for its backward pass. */
+fvx_status fvx_checkpoint_restore(fvx_dtype dt, int32_t group, const int8_t* codes, const float* steps, int64_t n,
+                                  int64_t c, const float* mean, const float* rstd, const float* w, const float* b,
+                                  void* out, int64_t ldo, fvx_stream stream);
+
+/* Cross attention of a ragged batch: query row i of batch element b attends to
+ * the kept keys j of the same element.
+ *   s_ij = scale * q_i . k_j;  lse_i = log sum_j exp(s_ij);  out_i = sum_j exp(s_ij - lse_i) v_j
+ * q [nq, heads, d], k and v [nk, kv_heads, d]: device, the last dimension
+ * dense, token and head strides in elements (not negative).  heads is a
+ * multiple of kv_heads; query head h reads key head h / (heads / kv_heads).
+ * 1 <= d <= 128.
+ * q_offsets, kv_offsets: HOST int64 [B + 1], CSR over tokens, read during the
+ * call; fvx_grid_batch_offsets gives a grid's.  Lengths may be 0.
+ * key_mask: device, one byte per key, nonzero = kept; NULL keeps all.  A masked
+ * key takes part in nothing, whatever its row holds.
+ * out: device [nq, heads, d], dense, 16-byte aligned.  lse: device fp32 [nq, heads], dense.  A
+ * row without kept keys gets out = 0 and lse = -infinity.
+ * Errors: FVX_ERR_INVALID_ARG; FVX_ERR_RANGE past 2^30 rows (tokens * heads). */
+fvx_status fvx_cross_attention(fvx_dtype dt, const void* q, int64_t q_token, int64_t q_head, const void* k,
+                               int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                               const int64_t* q_offsets, const int64_t* kv_offsets, int32_t B, int32_t heads,
+                               int32_t kv_heads, int32_t d, const uint8_t* key_mask, float scale, void* out,
+                               float* lse, fvx_stream stream);
+
+/* Gradients of out with respect to q, k and v, given dout (strides as q's) and
+ * the forward call's out and lse.  dq [nq, heads, d], dk and dv [nk, kv_heads,
+ * d]: dense, 16-byte aligned, fully overwritten; gradients of a key head sum over the query
+ * heads that read it, those of a masked key are zero.  The order of every sum
+ * is fixed: the same call gives the same bits. */
+fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t do_token, int64_t do_head,
+                                        const void* q, int64_t q_token, int64_t q_head, const void* k,
+                                        int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                                        int64_t v_head, const void* out, const float* lse, const int64_t* q_offsets,
+                                        const int64_t* kv_offsets, int32_t B, int32_t heads, int32_t kv_heads,
+                                        int32_t d, const uint8_t* key_mask, float scale, void* dq, void* dk, void* dv,
+                                        fvx_stream stream);
+
 fvx_status fvx_grid_destroy(fvx_grid g);
 fvx_status fvx_kmap_destroy(fvx_kmap m);
 

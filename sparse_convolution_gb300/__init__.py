@@ -52,6 +52,7 @@ def load():
         raise FvxError("FVX_NOT_BUILT", f"{LIB_PATH} is missing; build the CUDA library first")
     lib = ctypes.CDLL(LIB_PATH)
     P, I64, I32, U64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_uint64
+    F32 = ctypes.c_float
     PP = ctypes.POINTER(ctypes.c_void_p)
     sigs = {
         "fvx_set_allocator": ([P, P, P], I32),
@@ -74,6 +75,13 @@ def load():
         "fvx_voxels_along_rays": ([P, P, P, P, I64, ctypes.c_float, ctypes.c_float, P, PP], I32),
         "fvx_hits_view": ([P, PP, PP, PP, P, P], I32),
         "fvx_hits_destroy": ([P], I32),
+        "fvx_layer_norm": ([I32, P, I64, I64, I64, P, P, F32, P, I64, P, P, I32, P, P, P], I32),
+        "fvx_layer_norm_backward": ([I32, P, I64, P, I64, I32, P, P, I64, I64, P, P, P, P, I64, P, P, P], I32),
+        "fvx_checkpoint_pack": ([I32, P, I64, I64, I64, I32, P, P, P], I32),
+        "fvx_checkpoint_restore": ([I32, I32, P, P, I64, I64, P, P, P, P, P, I64, P], I32),
+        "fvx_cross_attention": ([I32] + 3 * [P, I64, I64] + [P, P, I32, I32, I32, I32, P, F32, P, P, P], I32),
+        "fvx_cross_attention_backward": ([I32] + 4 * [P, I64, I64] + [P, P, P, P, I32, I32, I32, I32, P, F32, P, P, P,
+                                                                     P], I32),
         "fvx_grid_destroy": ([P], I32),
         "fvx_kmap_destroy": ([P], I32),
         "fvx_status_string": ([I32], ctypes.c_char_p),
@@ -388,6 +396,312 @@ def sparse_conv_wgrad(gin: Grid, gout: Grid, kmap: KernelMap, feats, dout, out=N
     _check(load().fvx_sparse_conv_wgrad(gin._h, gout._h, kmap._h, dt, _ptr(feats), cin, _ptr(dout), cout, _ptr(out),
                                         _stream(stream)))
     return out
+
+
+# ---------------------------------------------------------------- layer norm, checkpoints, cross attention
+def _refuse(message):
+    raise FvxError("FVX_ERR_INVALID_ARG", message)
+
+
+def _dtype_code(t, who):
+    import torch
+
+    if t.dtype == torch.bfloat16:
+        return FVX_BF16
+    if t.dtype != torch.float32:
+        _refuse(f"{who}: tensors must be float32 or bfloat16, got {t.dtype}")
+    return FVX_F32
+
+
+def _on_device(who, *tensors):
+    """Every tensor on the current CUDA device (the library launches there)."""
+    import torch
+
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.device.index != dev):
+            _refuse(f"{who}: every tensor must be on the current CUDA device {dev}, got {t.device}")
+
+
+class _On:
+    """Makes `stream` (default: the current one) current, so that what a call
+    allocates belongs to the stream its kernels run on."""
+
+    def __init__(self, stream):
+        import torch
+
+        self._guard = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+        import torch
+
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        if self._guard is not None:
+            self._guard.__exit__(*e)
+
+
+def _rows(t, who, name):
+    """t as rows of dense channels: (tensor, pitch); a copy only where the channels are strided."""
+    if t.dim() != 2:
+        _refuse(f"{who}: {name} must be [rows, channels], got {tuple(t.shape)}")
+    n, c = t.shape
+    if c < 1:
+        _refuse(f"{who}: {name} has no channels")
+    if (c > 1 and t.stride(1) != 1) or (n > 1 and t.stride(0) < c):
+        t = t.contiguous()
+    return t, (t.stride(0) if n > 1 else c)
+
+
+def _channel_vector(t, c, who, name):
+    import torch
+
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != c:
+        _refuse(f"{who}: {name} must be float32 [{c}], got {t.dtype} {tuple(t.shape)}")
+    return t if t.stride(0) == 1 or c == 1 else t.contiguous()
+
+
+def _row_vector(t, n, who, name):
+    import torch
+
+    if t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != n:
+        _refuse(f"{who}: {name} must be float32 [{n}], got {t.dtype} {tuple(t.shape)}")
+    return t if t.is_contiguous() else t.contiguous()
+
+
+def _at(t):
+    return t.data_ptr() if t is not None else None
+
+
+class Checkpoint8:
+    """Activations [rows, channels] held in 8 bits: ``codes`` int8 and one fp32
+    ``steps`` value per group of 32, 64 or 128 channels of a row; the value held
+    is code * step, within half a step of the activation.
+
+    Made by ``Checkpoint8.pack`` or by ``layer_norm(checkpoint_group=...)`` and
+    read by ``restore``, by ``layer_norm`` (the norm's output computed again) and
+    by ``layer_norm_backward``."""
+
+    def __init__(self, codes, steps, group, dtype):
+        self.codes, self.steps, self.group, self.dtype = codes, steps, group, dtype
+
+    @staticmethod
+    def _empty(x, group, who):
+        import torch
+
+        if group not in (32, 64, 128):
+            _refuse(f"{who}: the checkpoint's group must be 32, 64 or 128, got {group}")
+        n, c = x.shape
+        return Checkpoint8(torch.empty((n, c), dtype=torch.int8, device=x.device),
+                           torch.empty((n, -(-c // group)), dtype=torch.float32, device=x.device), group, x.dtype)
+
+    @classmethod
+    def pack(cls, x, group=64, stream=None) -> "Checkpoint8":
+        """x: float32 or bfloat16 [rows, channels]."""
+        who = "Checkpoint8.pack"
+        dt = _dtype_code(x, who)
+        _on_device(who, x)
+        with _On(stream) as s:
+            x, ld = _rows(x, who, "x")
+            ck = cls._empty(x, group, who)
+            _check(load().fvx_checkpoint_pack(dt, x.data_ptr(), ld, x.shape[0], x.shape[1], group,
+                                              ck.codes.data_ptr(), ck.steps.data_ptr(), s))
+        return ck
+
+    @property
+    def shape(self):
+        return self.codes.shape
+
+    @property
+    def nbytes(self):
+        return self.codes.numel() + 4 * self.steps.numel()
+
+    def _restore(self, who, mean, rstd, weight, bias, dtype, out, stream):
+        import torch
+
+        n, c = self.codes.shape
+        if not self.codes.is_contiguous() or not self.steps.is_contiguous():
+            _refuse(f"{who}: codes and steps must be contiguous")
+        with _On(stream) as s:
+            if out is None:
+                out = torch.empty((n, c), dtype=dtype or self.dtype, device=self.codes.device)
+            dt = _dtype_code(out, who)
+            if tuple(out.shape) != (n, c) or (c > 1 and out.stride(1) != 1) or (n > 1 and out.stride(0) < c):
+                _refuse(f"{who}: out must be [{n}, {c}] with dense channels, got {tuple(out.shape)}")
+            _on_device(who, self.codes, self.steps, mean, rstd, weight, bias, out)
+            _check(load().fvx_checkpoint_restore(dt, self.group, self.codes.data_ptr(), self.steps.data_ptr(), n, c,
+                                                 _at(mean), _at(rstd), _at(weight), _at(bias), out.data_ptr(),
+                                                 out.stride(0) if n > 1 else c, s))
+        return out
+
+    def restore(self, dtype=None, out=None, stream=None):
+        """The values held, in the activations' type or ``dtype``."""
+        return self._restore("Checkpoint8.restore", None, None, None, None, dtype, out, stream)
+
+    def layer_norm(self, mean, rstd, weight=None, bias=None, dtype=None, out=None, stream=None):
+        """Layer norm of the values held, with the forward pass's statistics:
+        the input of what followed the norm, for its backward pass."""
+        who = "Checkpoint8.layer_norm"
+        n, c = self.codes.shape
+        with _On(stream):
+            mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
+            weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
+        return self._restore(who, mean, rstd, weight, bias, dtype, out, stream)
+
+
+def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint_group=None, stream=None):
+    """Layer norm of each row of x [rows, channels] (float32 or bfloat16);
+    weight and bias float32 [channels] or None.  Returns (y, mean, rstd), the
+    statistics float32 [rows]; with checkpoint_group (32, 64 or 128) also x's
+    Checkpoint8, written by the same pass."""
+    import torch
+
+    who = "layer_norm"
+    dt = _dtype_code(x, who)
+    _on_device(who, x, weight, bias)
+    with _On(stream) as s:
+        x, ld = _rows(x, who, "x")
+        n, c = x.shape
+        weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
+        y = torch.empty((n, c), dtype=x.dtype, device=x.device)
+        mean = torch.empty((n,), dtype=torch.float32, device=x.device)
+        rstd = torch.empty((n,), dtype=torch.float32, device=x.device)
+        ck = Checkpoint8._empty(x, checkpoint_group, who) if checkpoint_group else None
+        _check(load().fvx_layer_norm(dt, x.data_ptr(), ld, n, c, _at(weight), _at(bias), float(eps), y.data_ptr(), c,
+                                     mean.data_ptr(), rstd.data_ptr(), checkpoint_group or 0,
+                                     ck.codes.data_ptr() if ck else None, ck.steps.data_ptr() if ck else None, s))
+    return (y, mean, rstd, ck) if ck else (y, mean, rstd)
+
+
+def layer_norm_backward(dy, x, mean, rstd, weight=None, stream=None):
+    """Gradients of layer_norm: (dx, dweight, dbias), dx in dy's type, the
+    others float32 [channels].  x: the tensor given to layer_norm, or its
+    Checkpoint8 (then x is read from its 8-bit codes)."""
+    import torch
+
+    who = "layer_norm_backward"
+    dt = _dtype_code(dy, who)
+    ck = x if isinstance(x, Checkpoint8) else None
+    if tuple(x.shape) != tuple(dy.shape):
+        _refuse(f"{who}: x is {tuple(x.shape)}, dy {tuple(dy.shape)}")
+    if x.dtype != dy.dtype:
+        _refuse(f"{who}: x is {x.dtype}, dy {dy.dtype}")
+    _on_device(who, dy, mean, rstd, weight, *((ck.codes, ck.steps) if ck else (x,)))
+    with _On(stream) as s:
+        dy, lddy = _rows(dy, who, "dy")
+        n, c = dy.shape
+        if ck:
+            if not ck.codes.is_contiguous() or not ck.steps.is_contiguous():
+                _refuse(f"{who}: the checkpoint's codes and steps must be contiguous")
+            source = (None, c, ck.group, ck.codes.data_ptr(), ck.steps.data_ptr())
+        else:
+            x, ldx = _rows(x, who, "x")
+            source = (x.data_ptr(), ldx, 0, None, None)
+        mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
+        weight = _channel_vector(weight, c, who, "weight")
+        dx = torch.empty((n, c), dtype=dy.dtype, device=dy.device)
+        sums = torch.empty((2, c), dtype=torch.float32, device=dy.device)
+        dw, db = sums[0], sums[1]
+        _check(load().fvx_layer_norm_backward(dt, dy.data_ptr(), lddy, *source, n, c, _at(weight), mean.data_ptr(),
+                                              rstd.data_ptr(), dx.data_ptr(), c, dw.data_ptr(), db.data_ptr(), s))
+    return dx, dw, db
+
+
+def _heads(t, who, name):
+    """t [tokens, heads, d] with a dense last dimension: a copy where it is
+    not, and where a stride is no multiple of 16 bytes in bf16 (the tensor
+    cores' copies need that)."""
+    if t.dim() != 3:
+        _refuse(f"{who}: {name} must be [tokens, heads, size], got {tuple(t.shape)}")
+    st = t.stride()
+    if (t.shape[2] > 1 and st[2] != 1) or (not t.is_contiguous() and t.dtype.itemsize == 2 and
+                                           ((st[0] | st[1] | (t.data_ptr() >> 1)) & 7 or not st[0] or not st[1])):
+        t = t.contiguous()
+    return t
+
+
+def _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask):
+    import torch
+
+    q, k, v = _heads(q, who, "q"), _heads(k, who, "k"), _heads(v, who, "v")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        _refuse(f"{who}: q, k and v must have one type, got {q.dtype}, {k.dtype}, {v.dtype}")
+    nq, heads, d = q.shape
+    nk, kv_heads, dk = k.shape
+    if v.shape != k.shape or dk != d:
+        _refuse(f"{who}: q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not belong together")
+    B = len(q_offsets) - 1
+    if B < 1 or len(kv_offsets) != B + 1:
+        _refuse(f"{who}: q_offsets and kv_offsets must both have B + 1 values, B at least 1")
+    if q_offsets[B] != nq or kv_offsets[B] != nk:
+        _refuse(f"{who}: the offsets end at {int(q_offsets[B])} and {int(kv_offsets[B])}, the tensors at {nq} and {nk}")
+    if key_mask is not None:
+        if key_mask.dtype not in (torch.bool, torch.uint8) or tuple(key_mask.shape) != (nk,):
+            _refuse(f"{who}: key_mask must be bool [{nk}], got {key_mask.dtype} {tuple(key_mask.shape)}")
+        key_mask = key_mask.contiguous()
+    offs = ctypes.c_int64 * (B + 1)
+    return q, k, v, key_mask, offs(*map(int, q_offsets)), offs(*map(int, kv_offsets)), B
+
+
+def cross_attention(q, k, v, q_offsets, kv_offsets, key_mask=None, scale=None, stream=None):
+    """Attention from the query rows of each batch element to that element's
+    keys.  q [nq, heads, size], k and v [nk, kv_heads, size], all float32 or
+    all bfloat16, heads a multiple of kv_heads, size at most 128; q_offsets and
+    kv_offsets: CSR [B + 1] over tokens (host sequences; Grid.batch_offsets()
+    gives a grid's); key_mask: bool [nk], True = kept; scale: default
+    1 / sqrt(size).  Returns (out [nq, heads, size], lse float32 [nq, heads]);
+    a row without kept keys gets zeros and -inf."""
+    import torch
+
+    who = "cross_attention"
+    dt = _dtype_code(q, who)
+    _on_device(who, q, k, v, key_mask)
+    with _On(stream) as s:
+        q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
+        nq, heads, d = q.shape
+        out = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
+        lse = torch.empty((nq, heads), dtype=torch.float32, device=q.device)
+        _check(load().fvx_cross_attention(dt, *_strided(q), *_strided(k), *_strided(v), qo, ko, B, heads, k.shape[1],
+                                          d, _at(key_mask), d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                          lse.data_ptr(), s))
+    return out, lse
+
+
+def cross_attention_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, key_mask=None, scale=None, stream=None):
+    """Gradients (dq, dk, dv) of cross_attention, in the tensors' type, from
+    dout and what cross_attention returned; a key head's gradients sum over the
+    query heads that read it."""
+    import torch
+
+    who = "cross_attention_backward"
+    dt = _dtype_code(q, who)
+    _on_device(who, dout, q, k, v, out, lse, key_mask)
+    with _On(stream) as s:
+        q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
+        nq, heads, d = q.shape
+        for name, t in (("dout", dout), ("out", out)):
+            if t.dtype != q.dtype or t.shape != q.shape:
+                _refuse(f"{who}: {name} must be {q.dtype} {tuple(q.shape)}, got {t.dtype} {tuple(t.shape)}")
+        if lse.dtype != torch.float32 or tuple(lse.shape) != (nq, heads):
+            _refuse(f"{who}: lse must be float32 [{nq}, {heads}], got {lse.dtype} {tuple(lse.shape)}")
+        dout, out, lse = _heads(dout, who, "dout"), out.contiguous(), lse.contiguous()
+        dq = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
+        dk = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
+        dv = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
+        _check(load().fvx_cross_attention_backward(
+            dt, *_strided(dout), *_strided(q), *_strided(k), *_strided(v), out.data_ptr(), lse.data_ptr(), qo, ko, B,
+            heads, k.shape[1], d, _at(key_mask), d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(),
+            dv.data_ptr(), s))
+    return dq, dk, dv
+
+
+def _strided(t):
+    return t.data_ptr(), t.stride(0), t.stride(1)
 
 
 def device_status(stream=None):

@@ -1,0 +1,784 @@
+// Cross attention from the voxels of each batch element to that element's
+// encoder states, forward and backward: the C entry points, the fp32 kernels
+// on the CUDA cores, and the reductions that the tensor-core kernels
+// (attn_tc.cu) share.
+//
+// For query row i and the kept keys j of its batch element:
+//   s_ij = scale q_i . k_j;  lse_i = log sum_j exp s_ij;  p_ij = exp(s_ij - lse_i);  out_i = sum_j p_ij v_j
+// and backward, with delta_i = dout_i . out_i:
+//   dv_j = sum_i p_ij dout_i;  ds_ij = p_ij (dout_i . v_j - delta_i) scale;
+//   dq_i = sum_j ds_ij k_j;    dk_j = sum_i ds_ij q_i
+// A row without kept keys has out = 0, lse = -inf and no gradient.  A masked
+// key takes part in nothing: whatever its row holds (infinities, NaN) is read
+// as zeros, and its gradients are zero.
+//
+// `shared` query heads read one key head.  They are rows of one tile (row =
+// token * shared + head within the group), so that keys and values are fetched
+// once for all of them and their gradients sum inside the tile's products.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <vector>
+
+#include "attn.cuh"
+
+namespace fvx {
+namespace {
+
+constexpr int kMaxD = 128;
+constexpr int kTile = 64;    // rows and keys of a tile
+constexpr int kPitch = 68;   // 64 + 4: float4 reads stay aligned, columns spread over the banks
+constexpr int kFmaThreads = 256;
+
+template <typename T>
+__device__ __forceinline__ float as_f32(T v);
+template <>
+__device__ __forceinline__ float as_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float as_f32<__nv_bfloat16>(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <typename T>
+__device__ __forceinline__ T from_f32(float v);
+template <>
+__device__ __forceinline__ float from_f32<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
+
+struct FmaArgs {
+  AttnItems items;
+  HeadsView q, k, v, dout;
+  const uint8_t* mask;
+  const float* delta;
+  const float* lse_in;
+  void* out;         // forward: out (one split); dq
+  float* lse;
+  float *part, *top, *total;  // several splits: [split][nq * heads][d], [split][nq * heads]
+  float *dk_part, *dv_part;   // [split][nk * kv_heads][d]
+  int64_t nq, nk;
+  int heads, kv_heads, shared, d, splits;
+  float scale;
+};
+
+// rows [r0, r0 + 64) of an item's (token, shared head) rows into dst[d][row], zeros past the end
+template <typename T, int DP>
+__device__ __forceinline__ void load_rows(float* dst, const HeadsView& t, int token0, int r0, int rows, int shared,
+                                          int head0, int d) {
+  for (int e = threadIdx.x; e < kTile * DP; e += kFmaThreads) {
+    const int r = e / DP, c = e - r * DP;
+    float v = 0.0f;
+    if (r0 + r < rows && c < d) {
+      const int tok = (r0 + r) / shared, g = (r0 + r) - tok * shared;
+      v = as_f32<T>(reinterpret_cast<const T*>(t.p)[(int64_t)(token0 + tok) * t.token +
+                                                    (int64_t)(head0 + g) * t.head + c]);
+    }
+    dst[c * kPitch + r] = v;
+  }
+}
+// keys [j0, j0 + 64) of head h; a key that is masked or past the end reads as zeros
+template <typename T, int DP>
+__device__ __forceinline__ void load_keys(float* dst, const HeadsView& t, const uint8_t* mask, int key0, int j0,
+                                          int keys, int h, int d) {
+  for (int e = threadIdx.x; e < kTile * DP; e += kFmaThreads) {
+    const int j = e / DP, c = e - j * DP;
+    float v = 0.0f;
+    if (j0 + j < keys && c < d && (!mask || mask[key0 + j0 + j]))
+      v = as_f32<T>(reinterpret_cast<const T*>(t.p)[(int64_t)(key0 + j0 + j) * t.token + (int64_t)h * t.head + c]);
+    dst[c * kPitch + j] = v;
+  }
+}
+
+// acc[i][j] = sum_d a[d][4 ty + i] b[d][4 tx + j]
+template <int DP>
+__device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty, int tx, int d, float (&acc)[4][4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+#pragma unroll 4
+  for (int c = 0; c < d; ++c) {
+    const float4 u = *reinterpret_cast<const float4*>(a + c * kPitch + 4 * ty);
+    const float4 w = *reinterpret_cast<const float4*>(b + c * kPitch + 4 * tx);
+    const float x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+  }
+}
+
+// acc[i][n] += sum_t p[t][4 ty + i] x[tx + 16 n][t]
+template <int DP>
+__device__ __forceinline__ void tile_accumulate(const float* p, const float* x, int ty, int tx,
+                                                float (&acc)[4][DP / 16]) {
+#pragma unroll 2
+  for (int t = 0; t < kTile; ++t) {
+    const float4 u = *reinterpret_cast<const float4*>(p + t * kPitch + 4 * ty);
+    const float a[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n) {
+      const float w = x[(tx + 16 * n) * kPitch + t];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[i][n] = fmaf(a[i], w, acc[i][n]);
+    }
+  }
+}
+
+// true when key j0 + j of the item takes part
+__device__ __forceinline__ bool kept(const FmaArgs& a, int key0, int j, int keys) {
+  return j < keys && (!a.mask || a.mask[key0 + j]);
+}
+
+// reductions over the 16 threads that share a row
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+struct FmaUnit {
+  int b, tile, h, split, q0, rows, key0, keys;
+};
+// Units of an item: tile fastest (neighbours read the same keys), then key
+// head, then split.
+__device__ __forceinline__ FmaUnit fma_unit(const FmaArgs& a, int u, bool by_keys) {
+  FmaUnit w;
+  w.b = a.items.item_of(u);
+  w.q0 = a.items.q0(w.b);
+  w.rows = (a.items.q0(w.b + 1) - w.q0) * a.shared;
+  w.key0 = a.items.k0(w.b);
+  w.keys = a.items.k0(w.b + 1) - w.key0;
+  const int tiles = ((by_keys ? w.keys : w.rows) + kTile - 1) / kTile;
+  int i = u - a.items.u0(w.b);
+  w.tile = i % tiles;
+  i /= tiles;
+  w.h = i % a.kv_heads;
+  w.split = i / a.kv_heads;
+  return w;
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFmaThreads) k_attn_fma(const __grid_constant__ FmaArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float *qs = sm, *ks = qs + DP * kPitch, *vs = ks + DP * kPitch, *ps = vs + DP * kPitch;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const FmaUnit w = fma_unit(a, blockIdx.x, false);
+  const int r0 = w.tile * kTile;
+  load_rows<T, DP>(qs, a.q, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
+  float acc[4][DP / 16], top[4], total[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    top[i] = -INFINITY;
+    total[i] = 0.0f;
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n) acc[i][n] = 0.0f;
+  }
+  const int kt = (w.keys + kTile - 1) / kTile;
+  const int t0 = (int)((int64_t)kt * w.split / a.splits), t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
+  for (int t = t0; t < t1; ++t) {
+    const int j0 = t * kTile;
+    __syncthreads();
+    load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
+    load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
+    __syncthreads();
+    float s[4][4];
+    tile_dot<DP>(qs, ks, ty, tx, a.d, s);
+    bool keep[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + 4 * tx + j, w.keys);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float m = -INFINITY;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = keep[j] ? s[i][j] * a.scale : -INFINITY;
+        m = fmaxf(m, s[i][j]);
+      }
+      m = fmaxf(max16(m), top[i]);
+      const float base = m == -INFINITY ? 0.0f : m;  // nothing kept so far: every exp below is 0
+      const float fade = expf(top[i] - base);
+      float add = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        s[i][j] = expf(s[i][j] - base);
+        add += s[i][j];
+        ps[(4 * tx + j) * kPitch + 4 * ty + i] = s[i][j];
+      }
+      top[i] = m;
+      total[i] = total[i] * fade + sum16(add);
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n) acc[i][n] *= fade;
+    }
+    __syncthreads();
+    tile_accumulate<DP>(ps, vs, ty, tx, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;
+    if (r >= w.rows) continue;
+    const int tok = r / a.shared, g = r - tok * a.shared;
+    const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+    if (a.splits == 1) {
+      const float inv = total[i] > 0.0f ? 1.0f / total[i] : 0.0f;
+      if (tx == 0) a.lse[row] = top[i] + logf(total[i]);
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n)
+        if (tx + 16 * n < a.d) reinterpret_cast<T*>(a.out)[row * a.d + tx + 16 * n] = from_f32<T>(acc[i][n] * inv);
+    } else {
+      const int64_t at = (int64_t)w.split * a.nq * a.heads + row;
+      if (tx == 0) {
+        a.top[at] = top[i];
+        a.total[at] = total[i];
+      }
+#pragma unroll
+      for (int n = 0; n < DP / 16; ++n)
+        if (tx + 16 * n < a.d) a.part[at * a.d + tx + 16 * n] = acc[i][n];
+    }
+  }
+}
+
+// p and ds of one tile: s and dp in, both overwritten
+__device__ __forceinline__ void tile_gradient(const FmaArgs& a, float (&s)[4][4], float (&dp)[4][4],
+                                              const bool (&keep)[4], const float (&lse)[4], const float (&delta)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = keep[j] && lse[i] != -INFINITY ? expf(s[i][j] * a.scale - lse[i]) : 0.0f;
+      s[i][j] = p;
+      dp[i][j] = p * (dp[i][j] - delta[i]) * a.scale;
+    }
+}
+__device__ __forceinline__ void row_constants(const FmaArgs& a, const FmaUnit& w, int r, float* lse, float* delta) {
+  *lse = -INFINITY;
+  *delta = 0.0f;
+  if (r < w.rows) {
+    const int tok = r / a.shared, g = r - tok * a.shared;
+    const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+    *lse = __ldg(a.lse_in + row);
+    *delta = __ldg(a.delta + row);
+  }
+}
+
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFmaThreads) k_attn_fma_dq(const __grid_constant__ FmaArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float *qs = sm, *os = qs + DP * kPitch, *ks = os + DP * kPitch, *vs = ks + DP * kPitch, *ps = vs + DP * kPitch;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const FmaUnit w = fma_unit(a, blockIdx.x, false);
+  const int r0 = w.tile * kTile;
+  load_rows<T, DP>(qs, a.q, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
+  load_rows<T, DP>(os, a.dout, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
+  float acc[4][DP / 16], lse[4], delta[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    row_constants(a, w, r0 + 4 * ty + i, &lse[i], &delta[i]);
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n) acc[i][n] = 0.0f;
+  }
+  const int kt = (w.keys + kTile - 1) / kTile;
+  const int t0 = (int)((int64_t)kt * w.split / a.splits), t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
+  for (int t = t0; t < t1; ++t) {
+    const int j0 = t * kTile;
+    __syncthreads();
+    load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
+    load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
+    __syncthreads();
+    float s[4][4], dp[4][4];
+    bool keep[4];
+    tile_dot<DP>(qs, ks, ty, tx, a.d, s);
+    tile_dot<DP>(os, vs, ty, tx, a.d, dp);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + 4 * tx + j, w.keys);
+    tile_gradient(a, s, dp, keep, lse, delta);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) ps[(4 * tx + j) * kPitch + 4 * ty + i] = dp[i][j];
+    __syncthreads();
+    tile_accumulate<DP>(ps, ks, ty, tx, acc);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = r0 + 4 * ty + i;
+    if (r >= w.rows) continue;
+    const int tok = r / a.shared, g = r - tok * a.shared;
+    const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n) {
+      if (tx + 16 * n >= a.d) continue;
+      if (a.splits == 1) reinterpret_cast<T*>(a.out)[row * a.d + tx + 16 * n] = from_f32<T>(acc[i][n]);
+      else a.part[((int64_t)w.split * a.nq * a.heads + row) * a.d + tx + 16 * n] = acc[i][n];
+    }
+  }
+}
+
+// dk and dv of one tile of keys over a range of row tiles.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFmaThreads) k_attn_fma_dkv(const __grid_constant__ FmaArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  float *qs = sm, *os = qs + DP * kPitch, *ks = os + DP * kPitch, *vs = ks + DP * kPitch, *ps = vs + DP * kPitch,
+        *ds = ps + kTile * kPitch;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const FmaUnit w = fma_unit(a, blockIdx.x, true);
+  const int j0 = w.tile * kTile;
+  load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
+  load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
+  float dk[4][DP / 16], dv[4][DP / 16];
+  bool keep[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    keep[i] = kept(a, w.key0, j0 + 4 * tx + i, w.keys);
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n) dk[i][n] = dv[i][n] = 0.0f;
+  }
+  const int rt = (w.rows + kTile - 1) / kTile;
+  const int t0 = (int)((int64_t)rt * w.split / a.splits), t1 = (int)((int64_t)rt * (w.split + 1) / a.splits);
+  for (int t = t0; t < t1; ++t) {
+    const int r0 = t * kTile;
+    __syncthreads();
+    load_rows<T, DP>(qs, a.q, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
+    load_rows<T, DP>(os, a.dout, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
+    __syncthreads();
+    float s[4][4], dp[4][4], lse[4], delta[4];
+    tile_dot<DP>(qs, ks, ty, tx, a.d, s);
+    tile_dot<DP>(os, vs, ty, tx, a.d, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row_constants(a, w, r0 + 4 * ty + i, &lse[i], &delta[i]);
+    tile_gradient(a, s, dp, keep, lse, delta);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      *reinterpret_cast<float4*>(ps + (4 * ty + i) * kPitch + 4 * tx) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
+      *reinterpret_cast<float4*>(ds + (4 * ty + i) * kPitch + 4 * tx) =
+          make_float4(dp[i][0], dp[i][1], dp[i][2], dp[i][3]);
+    }
+    __syncthreads();
+    tile_accumulate<DP>(ps, os, ty, tx, dv);
+    tile_accumulate<DP>(ds, qs, ty, tx, dk);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = j0 + 4 * ty + i;
+    if (j >= w.keys) continue;
+    const int64_t at = ((int64_t)w.split * a.nk + w.key0 + j) * a.kv_heads + w.h;
+#pragma unroll
+    for (int n = 0; n < DP / 16; ++n)
+      if (tx + 16 * n < a.d) {
+        a.dk_part[at * a.d + tx + 16 * n] = dk[i][n];
+        a.dv_part[at * a.d + tx + 16 * n] = dv[i][n];
+      }
+  }
+}
+
+// ---------------------------------------------------------------- reductions
+// One warp per row: the partial results over ranges of keys, each relative to
+// its own maximum, brought to the common one and divided by the common sum.
+template <typename T>
+__global__ void __launch_bounds__(kFmaThreads) k_attn_join(const float* __restrict__ part,
+                                                           const float* __restrict__ top,
+                                                           const float* __restrict__ total, int splits, int64_t rows,
+                                                           int d, T* __restrict__ out, float* __restrict__ lse) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (kFmaThreads / 32) + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  float m = -INFINITY;
+  for (int s = lane; s < splits; s += 32) m = fmaxf(m, __ldg(top + s * rows + row));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float base = m == -INFINITY ? 0.0f : m;
+  float l = 0.0f;
+  float acc[kMaxD / 32] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int s = 0; s < splits; ++s) {
+    const float f = expf(__ldg(top + s * rows + row) - base), t = __ldg(total + s * rows + row);
+    if (t == 0.0f) continue;  // no kept key in this range; a NaN goes on
+    l = fmaf(f, t, l);
+#pragma unroll
+    for (int i = 0; i < kMaxD / 32; ++i)
+      if (lane + 32 * i < d) acc[i] = fmaf(f, __ldg(part + (s * rows + row) * d + lane + 32 * i), acc[i]);
+  }
+  const float inv = l > 0.0f ? 1.0f / l : 0.0f;
+  if (lane == 0) lse[row] = m + logf(l);
+#pragma unroll
+  for (int i = 0; i < kMaxD / 32; ++i)
+    if (lane + 32 * i < d) out[row * d + lane + 32 * i] = from_f32<T>(acc[i] * inv);
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kFmaThreads) k_attn_sum(const float* __restrict__ part, int splits, int64_t n,
+                                                          T* __restrict__ dst) {
+  for (int64_t i = (int64_t)blockIdx.x * kFmaThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kFmaThreads) {
+    float s = 0.0f;
+    for (int k = 0; k < splits; ++k) s += __ldg(part + k * n + i);
+    dst[i] = from_f32<T>(s);
+  }
+}
+
+// delta of each row: one warp per row, dout and out dense along d
+template <typename T>
+__global__ void __launch_bounds__(kFmaThreads) k_attn_delta(HeadsView dout, const T* __restrict__ out, int64_t rows,
+                                                            int heads, int d, float* __restrict__ delta) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = (int64_t)blockIdx.x * (kFmaThreads / 32) + (threadIdx.x >> 5);
+  if (row >= rows) return;
+  const int64_t tok = row / heads;
+  const int h = (int)(row - tok * heads);
+  const T* p = reinterpret_cast<const T*>(dout.p) + tok * dout.token + h * dout.head;
+  float s = 0.0f;
+  for (int c = lane; c < d; c += 32) s = fmaf(as_f32<T>(p[c]), as_f32<T>(out[row * d + c]), s);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) delta[row] = s;
+}
+
+// Offsets of more items than the arguments hold, written a piece at a time.
+struct Piece {
+  int32_t v[960];
+};
+__global__ void k_attn_offsets(const __grid_constant__ Piece p, int n, int32_t* dst) {
+  for (int i = threadIdx.x; i < n; i += blockDim.x) dst[i] = p.v[i];
+}
+
+// ---------------------------------------------------------------- host
+fvx_status bad(const char* who, const char* what) {
+  set_error("%s: %s", who, what);
+  return FVX_ERR_INVALID_ARG;
+}
+
+size_t elem_size(fvx_dtype dt) { return dt == FVX_F32 ? 4 : 2; }
+
+fvx_status check_offsets(const char* who, const char* name, const int64_t* o, int32_t B, int64_t* total) {
+  if (!o) {
+    set_error("%s: NULL %s", who, name);
+    return FVX_ERR_INVALID_ARG;
+  }
+  if (o[0] != 0) {
+    set_error("%s: %s must start at 0", who, name);
+    return FVX_ERR_INVALID_ARG;
+  }
+  for (int b = 0; b < B; ++b)
+    if (o[b + 1] < o[b]) {
+      set_error("%s: %s must be monotone", who, name);
+      return FVX_ERR_INVALID_ARG;
+    }
+  *total = o[B];
+  return FVX_OK;
+}
+
+fvx_status check_heads(const char* who, const char* name, fvx_dtype dt, const HeadsView& t, int64_t n) {
+  if ((n > 0 && !t.p) || reinterpret_cast<uintptr_t>(t.p) % elem_size(dt)) {
+    set_error("%s: %s is NULL or not aligned to its elements", who, name);
+    return FVX_ERR_INVALID_ARG;
+  }
+  if (t.token < 0 || t.head < 0) {
+    set_error("%s: %s has a negative stride", who, name);
+    return FVX_ERR_INVALID_ARG;
+  }
+  return FVX_OK;
+}
+
+fvx_status check_call(const char* who, AttnCall& c, int32_t B, int32_t heads, int32_t kv_heads, int32_t d) {
+  if (c.dt != FVX_F32 && c.dt != FVX_BF16) return bad(who, "dtype must be FVX_F32 or FVX_BF16");
+  if (B < 1) return bad(who, "B must be at least 1");
+  if (heads < 1 || kv_heads < 1 || heads % kv_heads) return bad(who, "heads must be a positive multiple of kv_heads");
+  if (d < 1 || d > kMaxD) return bad(who, "the head size must be in 1..128");
+  if (!(fabsf(c.scale) <= 3.0e38f)) return bad(who, "scale must be finite");
+  FVX_TRY(check_offsets(who, "q_offsets", c.q_offsets, B, &c.nq));
+  FVX_TRY(check_offsets(who, "kv_offsets", c.kv_offsets, B, &c.nk));
+  c.items = B;
+  c.heads = heads;
+  c.kv_heads = kv_heads;
+  c.shared = heads / kv_heads;
+  c.d = d;
+  // rows and work units are counted in 32 bits
+  if (c.nq > ((int64_t)1 << 30) / heads || c.nk > ((int64_t)1 << 30) / kv_heads) {
+    set_error("%s: more than 2^30 rows (tokens times heads)", who);
+    return FVX_ERR_RANGE;
+  }
+  // the stride of a dimension of one element says nothing
+  auto dense = [&](HeadsView& t, int64_t tokens, int h) {
+    if (h == 1) t.head = d;
+    if (tokens <= 1) t.token = (int64_t)h * d;
+  };
+  dense(c.q, c.nq, heads);
+  dense(c.dout, c.nq, heads);
+  dense(c.k, c.nk, kv_heads);
+  dense(c.v, c.nk, kv_heads);
+  FVX_TRY(check_heads(who, "q", c.dt, c.q, c.nq));
+  FVX_TRY(check_heads(who, "k", c.dt, c.k, c.nk));
+  FVX_TRY(check_heads(who, "v", c.dt, c.v, c.nk));
+  if (c.nq > 0 && (!c.out || !c.lse)) return bad(who, "NULL out or lse");
+  if (reinterpret_cast<uintptr_t>(c.out) % 16) return bad(who, "out is not aligned to 16 bytes");
+  if (reinterpret_cast<uintptr_t>(c.lse) % 4) return bad(who, "lse is not aligned to 4 bytes");
+  return FVX_OK;
+}
+
+// Prefix of the items' units; `splits` gives each tile that many.
+std::vector<int32_t> unit_prefix(const AttnCall& c, bool by_keys, int splits, int64_t* units) {
+  std::vector<int32_t> p((size_t)c.items + 1);
+  int64_t n = 0;
+  for (int b = 0; b < c.items; ++b) {
+    p[b] = (int32_t)n;
+    const int64_t len = by_keys ? c.kv_offsets[b + 1] - c.kv_offsets[b] : (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared;
+    n += (len + kTile - 1) / kTile * c.kv_heads * splits;
+  }
+  p[c.items] = (int32_t)n;
+  *units = n;
+  return p;
+}
+
+// Splits of the inner loop: enough units for two blocks per multiprocessor,
+// no more than the longest inner loop has tiles, and at most 32.
+int pick_splits(const AttnCall& c, bool by_keys, int sms) {
+  int64_t units = 0, longest = 1;
+  unit_prefix(c, by_keys, 1, &units);
+  for (int b = 0; b < c.items; ++b) {
+    const int64_t len = by_keys ? (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared : c.kv_offsets[b + 1] - c.kv_offsets[b];
+    longest = std::max(longest, (len + kTile - 1) / kTile);
+  }
+  const int64_t want = units > 0 ? (2 * sms + units - 1) / units : 1;
+  return (int)std::max<int64_t>(1, std::min<int64_t>({want, longest, 32}));
+}
+
+FmaArgs fma_args(const AttnCall& c) {
+  FmaArgs a = {};
+  a.q = c.q;
+  a.k = c.k;
+  a.v = c.v;
+  a.dout = c.dout;
+  a.mask = c.mask;
+  a.nq = c.nq;
+  a.nk = c.nk;
+  a.heads = c.heads;
+  a.kv_heads = c.kv_heads;
+  a.shared = c.shared;
+  a.d = c.d;
+  a.scale = c.scale;
+  return a;
+}
+
+template <typename K>
+fvx_status fma_launch(const char* name, K kernel, int64_t units, size_t smem, cudaStream_t s, const FmaArgs& a) {
+  FVX_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  LaunchScope ls(name, s);
+  kernel<<<(unsigned)units, kFmaThreads, smem, s>>>(a);
+  return check_launch(name);
+}
+constexpr size_t fma_smem(int dp, int operands, int tiles) {
+  return (size_t)(dp * operands + kTile * tiles) * kPitch * 4;
+}
+
+template <typename T, int DP>
+fvx_status fma_forward(const AttnCall& c, cudaStream_t s, Scratch& scr, int sms) {
+  FmaArgs a = fma_args(c);
+  a.splits = pick_splits(c, false, sms);
+  int64_t units = 0;
+  const std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &units);
+  FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+  a.out = c.out;
+  a.lse = c.lse;
+  const int64_t rows = c.nq * c.heads;
+  if (a.splits > 1) {
+    a.part = scr.get<float>((size_t)a.splits * rows * c.d);
+    a.top = scr.get<float>((size_t)a.splits * rows);
+    a.total = scr.get<float>((size_t)a.splits * rows);
+    if (!a.part || !a.top || !a.total) return FVX_ERR_ALLOC;
+  }
+  FVX_TRY(fma_launch("attn_fma", k_attn_fma<T, DP>, units, fma_smem(DP, 3, 1), s, a));
+  return a.splits > 1 ? attn_join(c, a.part, a.top, a.total, a.splits, s) : FVX_OK;
+}
+
+template <typename T, int DP>
+fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, Scratch& scr, int sms) {
+  FmaArgs a = fma_args(c);
+  a.delta = delta;
+  a.lse_in = c.lse;
+  int64_t units = 0;
+  {
+    a.splits = pick_splits(c, false, sms);
+    const std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &units);
+    FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+    a.out = c.dq;
+    const int64_t values = c.nq * c.heads * c.d;
+    if (a.splits > 1 && !(a.part = scr.get<float>((size_t)a.splits * values))) return FVX_ERR_ALLOC;
+    if (units > 0) {
+      FVX_TRY(fma_launch("attn_fma_dq", k_attn_fma_dq<T, DP>, units, fma_smem(DP, 4, 1), s, a));
+      if (a.splits > 1) FVX_TRY(attn_sum(c.dt, a.part, a.splits, values, c.dq, s));
+    }
+  }
+  a.splits = pick_splits(c, true, sms);
+  const std::vector<int32_t> prefix = unit_prefix(c, true, a.splits, &units);
+  if (units == 0) return FVX_OK;
+  FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+  const int64_t values = c.nk * c.kv_heads * c.d;
+  a.dk_part = scr.get<float>((size_t)a.splits * values);
+  a.dv_part = scr.get<float>((size_t)a.splits * values);
+  if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
+  FVX_TRY(fma_launch("attn_fma_dkv", k_attn_fma_dkv<T, DP>, units, fma_smem(DP, 4, 2), s, a));
+  FVX_TRY(attn_sum(c.dt, a.dk_part, a.splits, values, c.dk, s));
+  return attn_sum(c.dt, a.dv_part, a.splits, values, c.dv, s);
+}
+
+template <typename F>
+fvx_status by_type(fvx_dtype dt, int d, F&& f) {
+  if (dt == FVX_F32) return d <= 64 ? f.template operator()<float, 64>() : f.template operator()<float, 128>();
+  return d <= 64 ? f.template operator()<__nv_bfloat16, 64>() : f.template operator()<__nv_bfloat16, 128>();
+}
+
+}  // namespace
+
+fvx_status attn_items(const AttnCall& c, const int32_t* unit_prefix, cudaStream_t s, Scratch& scr, AttnItems* out) {
+  const int n = c.items + 1;
+  out->items = c.items;
+  out->ptr = nullptr;
+  auto value = [&](int i) {
+    return i < n ? (int32_t)c.q_offsets[i] : i < 2 * n ? (int32_t)c.kv_offsets[i - n] : unit_prefix[i - 2 * n];
+  };
+  if (c.items <= kInlineItems) {
+    for (int i = 0; i < 3 * n; ++i) out->in[i] = value(i);
+    return FVX_OK;
+  }
+  int32_t* dev = scr.get<int32_t>((size_t)3 * n);
+  if (!dev) return FVX_ERR_ALLOC;
+  constexpr int kPiece = (int)(sizeof(Piece) / 4);
+  for (int i = 0; i < 3 * n; i += kPiece) {
+    Piece p;
+    const int m = std::min(kPiece, 3 * n - i);
+    for (int j = 0; j < m; ++j) p.v[j] = value(i + j);
+    LaunchScope ls("attn_offsets", s);
+    k_attn_offsets<<<1, kFmaThreads, 0, s>>>(p, m, dev + i);
+    FVX_TRY(check_launch("attn_offsets"));
+  }
+  out->ptr = dev;
+  return FVX_OK;
+}
+
+fvx_status attn_join(const AttnCall& c, const float* part, const float* top, const float* total, int splits,
+                     cudaStream_t s) {
+  const int64_t rows = c.nq * c.heads;
+  const unsigned grid = (unsigned)((rows + kFmaThreads / 32 - 1) / (kFmaThreads / 32));
+  LaunchScope ls("attn_join", s);
+  if (c.dt == FVX_F32)
+    k_attn_join<float><<<grid, kFmaThreads, 0, s>>>(part, top, total, splits, rows, c.d, (float*)c.out, c.lse);
+  else
+    k_attn_join<__nv_bfloat16>
+        <<<grid, kFmaThreads, 0, s>>>(part, top, total, splits, rows, c.d, (__nv_bfloat16*)c.out, c.lse);
+  return check_launch("attn_join");
+}
+
+fvx_status attn_sum(fvx_dtype dt, const float* part, int splits, int64_t n, void* dst, cudaStream_t s) {
+  if (n == 0) return FVX_OK;
+  const unsigned grid = (unsigned)std::min<int64_t>((n + kFmaThreads - 1) / kFmaThreads, 152 * 16);
+  LaunchScope ls("attn_sum", s);
+  if (dt == FVX_F32) k_attn_sum<float><<<grid, kFmaThreads, 0, s>>>(part, splits, n, (float*)dst);
+  else k_attn_sum<__nv_bfloat16><<<grid, kFmaThreads, 0, s>>>(part, splits, n, (__nv_bfloat16*)dst);
+  return check_launch("attn_sum");
+}
+
+}  // namespace fvx
+
+using namespace fvx;
+
+extern "C" {
+
+fvx_status fvx_cross_attention(fvx_dtype dt, const void* q, int64_t q_token, int64_t q_head, const void* k,
+                               int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
+                               const int64_t* q_offsets, const int64_t* kv_offsets, int32_t B, int32_t heads,
+                               int32_t kv_heads, int32_t d, const uint8_t* key_mask, float scale, void* out,
+                               float* lse, fvx_stream stream) {
+  const char* who = "fvx_cross_attention";
+  EntryScope entry(who);
+  try {
+    AttnCall c = {};
+    c.dt = dt;
+    c.q = HeadsView{q, q_token, q_head};
+    c.k = HeadsView{k, k_token, k_head};
+    c.v = HeadsView{v, v_token, v_head};
+    c.q_offsets = q_offsets;
+    c.kv_offsets = kv_offsets;
+    c.mask = key_mask;
+    c.scale = scale;
+    c.out = out;
+    c.lse = lse;
+    FVX_TRY(check_call(who, c, B, heads, kv_heads, d));
+    if (c.nq == 0) return FVX_OK;
+    cudaStream_t s = (cudaStream_t)stream;
+    int sms = 0;
+    FVX_TRY(device_sm_count(&sms));
+    Scratch scr(s);
+    return by_type(dt, d, [&]<typename T, int DP>() { return fma_forward<T, DP>(c, s, scr, sms); });
+  } catch (const std::exception& e) {
+    set_error("%s: %s", who, e.what());
+    return FVX_ERR_ALLOC;
+  }
+}
+
+fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t do_token, int64_t do_head,
+                                        const void* q, int64_t q_token, int64_t q_head, const void* k,
+                                        int64_t k_token, int64_t k_head, const void* v, int64_t v_token,
+                                        int64_t v_head, const void* out, const float* lse, const int64_t* q_offsets,
+                                        const int64_t* kv_offsets, int32_t B, int32_t heads, int32_t kv_heads,
+                                        int32_t d, const uint8_t* key_mask, float scale, void* dq, void* dk, void* dv,
+                                        fvx_stream stream) {
+  const char* who = "fvx_cross_attention_backward";
+  EntryScope entry(who);
+  try {
+    AttnCall c = {};
+    c.dt = dt;
+    c.q = HeadsView{q, q_token, q_head};
+    c.k = HeadsView{k, k_token, k_head};
+    c.v = HeadsView{v, v_token, v_head};
+    c.dout = HeadsView{dout, do_token, do_head};
+    c.q_offsets = q_offsets;
+    c.kv_offsets = kv_offsets;
+    c.mask = key_mask;
+    c.scale = scale;
+    c.out = const_cast<void*>(out);
+    c.lse = const_cast<float*>(lse);
+    c.dq = dq;
+    c.dk = dk;
+    c.dv = dv;
+    FVX_TRY(check_call(who, c, B, heads, kv_heads, d));
+    FVX_TRY(check_heads(who, "dout", dt, c.dout, c.nq));
+    if ((c.nq > 0 && !dq) || (c.nk > 0 && (!dk || !dv))) return bad(who, "NULL dq, dk or dv");
+    if (reinterpret_cast<uintptr_t>(dq) % 16 || reinterpret_cast<uintptr_t>(dk) % 16 ||
+        reinterpret_cast<uintptr_t>(dv) % 16)
+      return bad(who, "dq, dk or dv is not aligned to 16 bytes");
+    cudaStream_t s = (cudaStream_t)stream;
+    const size_t kv_bytes = (size_t)c.nk * kv_heads * d * elem_size(dt);
+    if (c.nq == 0) {
+      if (c.nk > 0) {
+        FVX_CUDA(cudaMemsetAsync(dk, 0, kv_bytes, s));
+        FVX_CUDA(cudaMemsetAsync(dv, 0, kv_bytes, s));
+      }
+      return FVX_OK;
+    }
+    int sms = 0;
+    FVX_TRY(device_sm_count(&sms));
+    Scratch scr(s);
+    const int64_t rows = c.nq * heads;
+    float* delta = scr.get<float>((size_t)rows);
+    if (!delta) return FVX_ERR_ALLOC;
+    {
+      const unsigned grid = (unsigned)((rows + kFmaThreads / 32 - 1) / (kFmaThreads / 32));
+      LaunchScope ls("attn_delta", s);
+      if (dt == FVX_F32)
+        k_attn_delta<float><<<grid, kFmaThreads, 0, s>>>(c.dout, (const float*)out, rows, heads, d, delta);
+      else
+        k_attn_delta<__nv_bfloat16>
+            <<<grid, kFmaThreads, 0, s>>>(c.dout, (const __nv_bfloat16*)out, rows, heads, d, delta);
+      FVX_TRY(check_launch("attn_delta"));
+    }
+    return by_type(dt, d, [&]<typename T, int DP>() { return fma_backward<T, DP>(c, delta, s, scr, sms); });
+  } catch (const std::exception& e) {
+    set_error("%s: %s", who, e.what());
+    return FVX_ERR_ALLOC;
+  }
+}
+
+}  // extern "C"

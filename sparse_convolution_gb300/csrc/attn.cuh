@@ -1,0 +1,69 @@
+// Shared by the cross-attention kernels (attn.cu: fp32 arithmetic on the CUDA
+// cores, reductions and the C entry points; attn_tc.cu: bf16 on the tensor cores).
+#pragma once
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fvx_internal.cuh"
+
+namespace fvx {
+
+constexpr int kInlineItems = 64;  // batch elements whose offsets travel in the kernel's arguments
+
+// Offsets of a ragged batch and the prefix of its work units: three arrays of
+// items + 1 values, held in the arguments or (more items) in device memory.
+struct AttnItems {
+  const int32_t* ptr;
+  int32_t items;
+  int32_t in[3 * (kInlineItems + 1)];
+#ifdef __CUDACC__
+  __device__ __forceinline__ int at(int i) const { return ptr ? __ldg(ptr + i) : in[i]; }
+  __device__ __forceinline__ int q0(int b) const { return at(b); }
+  __device__ __forceinline__ int k0(int b) const { return at(items + 1 + b); }
+  __device__ __forceinline__ int u0(int b) const { return at(2 * (items + 1) + b); }
+  // the item that work unit u belongs to
+  __device__ __forceinline__ int item_of(int u) const {
+    int lo = 0, hi = items;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (u0(mid) <= u) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+#endif
+};
+
+struct HeadsView {  // [tokens, heads, d] with the last dimension dense; strides in elements
+  const void* p;
+  int64_t token, head;
+};
+
+struct AttnCall {
+  fvx_dtype dt;
+  HeadsView q, k, v, dout;
+  const int64_t* q_offsets;  // host
+  const int64_t* kv_offsets;
+  int items, heads, kv_heads, shared, d;  // shared: query heads per key head
+  int64_t nq, nk;
+  const uint8_t* mask;
+  float scale;
+  void* out;  // [nq, heads, d]; the backward pass reads it
+  float* lse; // [nq, heads]
+  void *dq, *dk, *dv;
+};
+
+// The bf16 tensor-core kernels (attn_tc.cu) take a call when this says so.
+bool attn_tc_serves(const AttnCall& c, bool backward);
+fvx_status attn_tc_forward(const AttnCall& c, cudaStream_t s, Scratch& scr);
+fvx_status attn_tc_backward(const AttnCall& c, const float* delta, cudaStream_t s, Scratch& scr);
+
+// attn.cu helpers that both use
+fvx_status attn_items(const AttnCall& c, const int32_t* unit_prefix, cudaStream_t s, Scratch& scr, AttnItems* out);
+// out = softmax-weighted join of `splits` partial results over ranges of keys
+fvx_status attn_join(const AttnCall& c, const float* part, const float* top, const float* total, int splits,
+                     cudaStream_t s);
+// dst[i] = sum over splits of part[split][i], n values
+fvx_status attn_sum(fvx_dtype dt, const float* part, int splits, int64_t n, void* dst, cudaStream_t s);
+
+}  // namespace fvx
