@@ -1,0 +1,621 @@
+// Cross attention in bf16 on the tcgen05 tensor cores (the formulas are in attn.cu).
+//
+// Forward.  One persistent block per multiprocessor; a work unit is a pair of
+// 128-row query tiles of one key head of one batch element, and a range of its
+// 128-key tiles.  A query tile's rows are (token, shared head) pairs, so all
+// query heads of a key head meet its keys in one product.  Warp roles:
+//   warps 0-3, 4-7  softmax of the pair's first / second tile, one row per
+//                   thread: scores out of tensor memory, running maximum and
+//                   sum in registers, probabilities back to tensor memory as
+//                   bf16 (the A operand of the second product), the row's
+//                   result at the end
+//   warp 8          TMA loads: queries, and a ring of key and value tiles
+//   warp 9          issues the products S = Q K^T and O += P V
+// While one tile is in its softmax, the other's products run.
+//
+// The accumulated O is relative to the running maximum m_ref of its row.  It
+// is brought to a new maximum only when that exceeds m_ref by more than 2^8
+// (in the exponent's base 2): until then p <= 2^8, far inside bf16's and
+// fp32's range, and the final division by the sum removes the factor exactly.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <mutex>
+#include <vector>
+
+#include "attn.cuh"
+#include "tc.cuh"
+
+namespace fvx {
+namespace {
+
+using namespace tc;
+
+constexpr int kM = 128;             // rows of a query tile, keys of a key tile
+constexpr int kAtom = kM * 128;     // bytes of 128 rows of 64 bf16
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kLazy = 8.0f;       // growth of the maximum (in powers of 2) that O may lag behind
+
+constexpr int kFwdThreads = 320;
+
+template <int DP>
+struct Fwd {
+  static constexpr int kAtoms = DP / 64;
+  static constexpr int kTileBytes = kAtoms * kAtom;
+  // 64-wide heads leave tensor memory for probabilities of their own (the next
+  // scores are computed while the probabilities are still read) and shared
+  // memory for a second set of queries; 128-wide ones put the probabilities
+  // over the scores.
+  static constexpr bool kOwnP = DP == 64;
+  static constexpr int kQBufs = DP == 64 ? 2 : 1;
+  static constexpr int kRing = DP == 64 ? 8 : 5;
+  static constexpr int kS = 0, kO = 256, kP = kOwnP ? 384 : 0, kPStep = kOwnP ? 64 : 128;
+  static constexpr size_t kSmem = (size_t)(2 * kQBufs + kRing) * kTileBytes + 1024 + 512;
+};
+
+struct alignas(128) FwdArgs {
+  CUtensorMap tq, tk, tv;
+  AttnItems items;
+  const uint8_t* mask;
+  __nv_bfloat16* out;
+  float* lse;
+  float *part, *top, *total;
+  uint32_t* status;
+  int64_t all_rows;  // nq * heads
+  int units, splits, heads, kv_heads, shared, d;
+  int tile_rows;     // rows of a query tile in use: shared * floor(128 / shared)
+  float c;           // scale * log2(e)
+};
+
+struct FwdUnit {
+  int q0, rows, key0, keys, r0, h, split, t0, t1;
+};
+__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
+  FwdUnit w;
+  const int b = a.items.item_of(u);
+  w.q0 = a.items.q0(b);
+  w.rows = (a.items.q0(b + 1) - w.q0) * a.shared;
+  w.key0 = a.items.k0(b);
+  w.keys = a.items.k0(b + 1) - w.key0;
+  const int pairs = (w.rows + 2 * a.tile_rows - 1) / (2 * a.tile_rows);
+  int i = u - a.items.u0(b);
+  w.r0 = (i % pairs) * 2 * a.tile_rows;
+  i /= pairs;
+  w.h = i % a.kv_heads;
+  w.split = i / a.kv_heads;
+  const int kt = (w.keys + kM - 1) / kM;
+  w.t0 = (int)((int64_t)kt * w.split / a.splits);
+  w.t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
+  return w;
+}
+
+// Kept keys of tile t of a unit, four words of 32; warp-uniform.
+struct Kept {
+  uint32_t w[4];
+  __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu; }
+};
+__device__ __forceinline__ void mask_bytes(const uint8_t* mask, int key0, int keys, int t, int lane, uint8_t (&b)[4]) {
+  if (!mask) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int j = t * kM + 32 * i + lane;
+    b[i] = j < keys ? __ldg(mask + key0 + j) : 0;
+  }
+}
+__device__ __forceinline__ Kept kept_keys(const uint8_t* mask, int keys, int t, const uint8_t (&b)[4]) {
+  Kept k;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int left = keys - t * kM - 32 * i;
+    k.w[i] = left >= 32 ? 0xffffffffu : left <= 0 ? 0u : (1u << left) - 1u;
+    if (mask) k.w[i] &= __ballot_sync(0xffffffffu, b[i] != 0);
+  }
+  return k;
+}
+// Zeros in the rows of a key or value tile that take no part: a probability of
+// 0 times an infinity or a NaN would not be 0.  One warp; the products read
+// shared memory through the async proxy, hence the fence.
+template <int ATOMS>
+__device__ __forceinline__ void zero_dropped(unsigned char* tile, const Kept& k, int lane) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t drop = ~k.w[i];
+    while (drop) {
+      const int r = 32 * i + __ffs(drop) - 1;
+      drop &= drop - 1;
+#pragma unroll
+      for (int at = 0; at < ATOMS; ++at) reinterpret_cast<uint32_t*>(tile + at * kAtom + r * 128)[lane] = 0u;
+    }
+  }
+  fence_proxy_async();
+  __syncwarp();
+}
+
+struct FwdHead {
+  uint64_t kv_full[8], kv_empty[8], q_full[2][2], q_empty[2][2];
+  uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], o_free[2];
+  uint32_t tmem;
+};
+
+template <int DP>
+__global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_constant__ FwdArgs a) {
+  using C = Fwd<DP>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned char* const ring = sm + (size_t)2 * C::kQBufs * C::kTileBytes;
+  FwdHead& h = *reinterpret_cast<FwdHead*>(ring + (size_t)C::kRing * C::kTileBytes);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* const status = a.status;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kRing; ++i) {
+      mbar_init(smem_u32(&h.kv_full[i]), 1);
+      mbar_init(smem_u32(&h.kv_empty[i]), 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&h.q_full[s][b]), 1);
+        mbar_init(smem_u32(&h.q_empty[s][b]), 1);
+      }
+      mbar_init(smem_u32(&h.s_full[s]), 1);
+      mbar_init(smem_u32(&h.s_free[s]), 4);
+      mbar_init(smem_u32(&h.p_ready[s]), 4);
+      mbar_init(smem_u32(&h.pv_done[s]), 1);
+      mbar_init(smem_u32(&h.o_free[s]), 4);
+    }
+    mbar_init_fence();
+  }
+  if (warp == 9) tmem_alloc(smem_u32(&h.tmem), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = h.tmem;
+
+  if (warp < 8) {
+    // ---------------------------------------------------------------- softmax
+    const int slot = warp >> 2;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + C::kS + slot * 128, to = tmem + lanes + C::kO + slot * DP,
+                   tp = tmem + lanes + C::kP + slot * C::kPStep;
+    const uint32_t s_full = smem_u32(&h.s_full[slot]), s_free = smem_u32(&h.s_free[slot]),
+                   p_ready = smem_u32(&h.p_ready[slot]), pv_done = smem_u32(&h.pv_done[slot]),
+                   o_free = smem_u32(&h.o_free[slot]);
+    const int row = (warp & 3) * 32 + lane;
+    uint32_t step = 0;
+    for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+      const FwdUnit w = fwd_unit(a, u);
+      const int r0 = w.r0 + slot * a.tile_rows;
+      if (r0 >= w.rows) continue;  // the pair's second tile has no rows
+      const int n = w.t1 - w.t0;
+      float m_ref = -INFINITY, total = 0.0f;
+      uint8_t mb[4];
+      if (n > 0) mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
+      for (int j = 0; j < n; ++j, ++step) {
+        const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
+        if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
+        mbar_wait(s_full, step & 1u, status);
+        __syncwarp();
+        fence_after();
+        uint32_t r[128];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, r + 32 * i);
+        tmem_ld_wait(r);
+        if constexpr (C::kOwnP) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(s_free);
+        }
+        float mx = -INFINITY, c = a.c;
+        if (!kept.all() || !(c > 0.0f)) {
+          // a score that takes no part is -infinity after scaling
+#pragma unroll
+          for (int i = 0; i < 128; ++i)
+            r[i] = (kept.w[i >> 5] >> (i & 31)) & 1u ? __float_as_uint(__uint_as_float(r[i]) * c) : 0xff800000u;
+          c = 1.0f;
+        }
+        {
+          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+          for (int i = 0; i < 128; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              m4[k] = fmaxf(m4[k], fmaxf(__uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1])));
+          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+        }
+        bool waited = false;
+        if (j == 0) {
+          m_ref = mx;
+        } else if (__any_sync(0xffffffffu, mx > m_ref + kLazy)) {
+          mbar_wait(pv_done, (step - 1) & 1u, status);
+          __syncwarp();
+          fence_after();
+          waited = true;
+          const float m_new = fmaxf(mx, m_ref);
+          const float f = m_ref == -INFINITY ? 0.0f : exp2_fast(m_ref - m_new);
+          total *= f;
+          m_ref = m_new;
+#pragma unroll 1
+          for (int cc = 0; cc < DP; cc += 32) {
+            uint32_t o[32];
+            tmem_ld32(to + cc, o);
+            tmem_ld_wait(o);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st32(to + cc, o);
+          }
+        }
+        // the previous product has read the previous probabilities
+        if (C::kOwnP && j > 0 && !waited) {
+          mbar_wait(pv_done, (step - 1) & 1u, status);
+          __syncwarp();
+          fence_after();
+        }
+        const float base = m_ref == -INFINITY ? 0.0f : m_ref;
+        float add0 = 0.0f, add1 = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float x = exp2_fast(fmaf(__uint_as_float(r[32 * i + 2 * k]), c, -base));
+            const float y = exp2_fast(fmaf(__uint_as_float(r[32 * i + 2 * k + 1]), c, -base));
+            add0 += x;
+            add1 += y;
+            p[k] = pack_bf16(x, y);
+          }
+          tmem_st16(tp + 16 * i, p);
+        }
+        total += add0 + add1;
+        tmem_st_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_ready);
+      }
+      // ---- the rows' results
+      const int r = r0 + row;
+      const bool live = row < a.tile_rows && r < w.rows;
+      const int tok = live ? r / a.shared : 0, g = r - tok * a.shared;
+      const int64_t at = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+      const int64_t pat = (int64_t)w.split * a.all_rows + at;
+      const float inv = total > 0.0f ? 1.0f / total : 0.0f;
+      if (live) {
+        if (a.splits == 1) {
+          a.lse[at] = (m_ref + log2f(total)) * kLn2;
+        } else {
+          a.top[pat] = m_ref * kLn2;
+          a.total[pat] = total;
+        }
+      }
+      if (n == 0) {
+        // no keys: zeros (a range without keys joins with total 0, its sums are not read)
+        if (live && a.splits == 1)
+          for (int cc = 0; cc < a.d; cc += 8) *reinterpret_cast<uint4*>(a.out + at * a.d + cc) = make_uint4(0, 0, 0, 0);
+        __syncwarp();
+        continue;
+      }
+      mbar_wait(pv_done, (step - 1) & 1u, status);
+      __syncwarp();
+      fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < DP; cc += 32) {
+        uint32_t o[32];
+        tmem_ld32(to + cc, o);
+        tmem_ld_wait(o);
+        if (live && a.splits == 1) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 8) {
+            if (cc + k >= a.d) break;
+            uint4 v;
+            uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              pv[i] = pack_bf16(__uint_as_float(o[k + 2 * i]) * inv, __uint_as_float(o[k + 2 * i + 1]) * inv);
+            *reinterpret_cast<uint4*>(a.out + at * a.d + cc + k) = v;
+          }
+        } else if (live) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            if (cc + k >= a.d) break;
+            *reinterpret_cast<uint4*>(a.part + pat * a.d + cc + k) = make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+          }
+        }
+        __syncwarp();  // the tensor-memory loads need the whole warp
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(o_free);
+    }
+  } else if (warp == 8) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      tma_prefetch_map(&a.tq);
+      tma_prefetch_map(&a.tk);
+      tma_prefetch_map(&a.tv);
+      uint32_t e = 0, nq[2] = {0, 0};
+      auto load_kv = [&](const CUtensorMap* map, const FwdUnit& w, int t) {
+        const uint32_t i = e % C::kRing, round = e / C::kRing;
+        if (round > 0) mbar_wait(smem_u32(&h.kv_empty[i]), (round - 1) & 1u, status);
+        const uint32_t bar = smem_u32(&h.kv_full[i]);
+        mbar_expect_tx(bar, C::kTileBytes);
+#pragma unroll
+        for (int at = 0; at < C::kAtoms; ++at)
+          tma_tile3d(smem_u32(ring) + i * C::kTileBytes + at * kAtom, map, 64 * at, w.h, w.key0 + t * kM, bar);
+        ++e;
+      };
+      FwdUnit prev = {};
+      int prev_t = -1;
+      for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+        const FwdUnit w = fwd_unit(a, u);
+        if (w.t0 == w.t1) continue;
+        for (int s = 0; s < 2; ++s) {
+          const int r0 = w.r0 + s * a.tile_rows;
+          if (r0 >= w.rows) continue;
+          const uint32_t i = nq[s] % C::kQBufs, round = nq[s] / C::kQBufs;
+          ++nq[s];
+          if (round > 0) mbar_wait(smem_u32(&h.q_empty[s][i]), (round - 1) & 1u, status);
+          const uint32_t bar = smem_u32(&h.q_full[s][i]);
+          mbar_expect_tx(bar, (uint32_t)(C::kAtoms * a.tile_rows * 128));
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at)
+            tma_tile3d(smem_u32(sm) + (s * C::kQBufs + i) * C::kTileBytes + at * kAtom, &a.tq, 64 * at,
+                       w.h * a.shared, w.q0 + r0 / a.shared, bar);
+        }
+        for (int t = w.t0; t < w.t1; ++t) {
+          load_kv(&a.tk, w, t);
+          if (prev_t >= 0) load_kv(&a.tv, prev, prev_t);
+          prev = w;
+          prev_t = t;
+        }
+      }
+      if (prev_t >= 0) load_kv(&a.tv, prev, prev_t);
+      // after a give-up, let the copies in flight land before the block exits
+      for (uint32_t k = 0; k < C::kRing && k < e; ++k) {
+        const uint32_t x = e - 1 - k;
+        mbar_drain(smem_u32(&h.kv_full[x % C::kRing]), (x / C::kRing) & 1u);
+      }
+      for (int s = 0; s < 2; ++s)
+        for (uint32_t k = 0; k < C::kQBufs && k < nq[s]; ++k) {
+          const uint32_t x = nq[s] - 1 - k;
+          mbar_drain(smem_u32(&h.q_full[s][x % C::kQBufs]), (x / C::kQBufs) & 1u);
+        }
+    }
+    __syncwarp();
+  } else {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t kIdS = idesc(kM, kM), kIdO = idesc(kM, DP) | kMnB;
+    const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
+    uint32_t e = 0, nq[2] = {0, 0}, qk[2] = {0, 0}, pv[2] = {0, 0}, opened[2] = {0, 0};
+    // the step whose second product is still to come
+    bool pend[2] = {false, false}, first = false;
+    Kept pend_kept = {};
+    auto do_qk = [&](int s, uint32_t qi, uint32_t ki) {
+      if (C::kOwnP && qk[s] > 0) mbar_wait(smem_u32(&h.s_free[s]), (qk[s] - 1) & 1u, status);
+      fence_after();
+      if (lane == 0) {
+        const uint64_t qd = desc_k(sq + (s * C::kQBufs + qi) * C::kTileBytes), kd = desc_k(sr + ki * C::kTileBytes);
+#pragma unroll
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = (uint32_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
+          mma_ss(tmem + C::kS + s * 128, qd + off, kd + off, kIdS, k > 0);
+        }
+        commit(smem_u32(&h.s_full[s]));
+      }
+      ++qk[s];
+    };
+    auto do_pv = [&](int s, uint32_t vi) {
+      mbar_wait(smem_u32(&h.p_ready[s]), pv[s] & 1u, status);
+      if (first) {
+        if (opened[s] > 0) mbar_wait(smem_u32(&h.o_free[s]), (opened[s] - 1) & 1u, status);
+        ++opened[s];
+      }
+      fence_after();
+      if (lane == 0) {
+        const uint64_t vd = desc_mn(sr + vi * C::kTileBytes, kAtom);
+#pragma unroll
+        for (int k = 0; k < kM / 16; ++k)
+          mma_ts(tmem + C::kO + s * DP, tmem + C::kP + s * C::kPStep + 8 * k, vd + (uint32_t)(k * 128), kIdO,
+                 !(first && k == 0));
+        commit(smem_u32(&h.pv_done[s]));
+      }
+      ++pv[s];
+    };
+    auto take_v = [&]() -> uint32_t {
+      const uint32_t i = e % C::kRing;
+      mbar_wait(smem_u32(&h.kv_full[i]), (e / C::kRing) & 1u, status);
+      ++e;
+      if (!pend_kept.all()) zero_dropped<C::kAtoms>(ring + (size_t)i * C::kTileBytes, pend_kept, lane);
+      return i;
+    };
+    for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+      const FwdUnit w = fwd_unit(a, u);
+      const int n = w.t1 - w.t0;
+      if (n == 0) continue;
+      const bool two = w.r0 + a.tile_rows < w.rows;
+      uint32_t qi[2];
+      for (int s = 0; s < 2; ++s) qi[s] = nq[s] % C::kQBufs;
+      uint8_t mb[4];
+      mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
+      for (int j = 0; j < n; ++j) {
+        const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
+        if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
+        const uint32_t ki = e % C::kRing;
+        mbar_wait(smem_u32(&h.kv_full[ki]), (e / C::kRing) & 1u, status);
+        ++e;
+        const bool any = pend[0] || pend[1];
+        const uint32_t vi = any ? take_v() : 0u;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          const bool active = s == 0 || two;
+          if (!C::kOwnP && pend[s]) do_pv(s, vi);
+          if (active) {
+            if (j == 0) mbar_wait(smem_u32(&h.q_full[s][qi[s]]), (nq[s] / C::kQBufs) & 1u, status);
+            do_qk(s, qi[s], ki);
+            if (j == n - 1 && lane == 0) commit(smem_u32(&h.q_empty[s][qi[s]]));
+          }
+          if (C::kOwnP && pend[s]) do_pv(s, vi);
+          pend[s] = active;
+        }
+        if (lane == 0) {
+          if (any) commit(smem_u32(&h.kv_empty[vi]));
+          commit(smem_u32(&h.kv_empty[ki]));
+        }
+        __syncwarp();
+        pend_kept = kept;
+        first = j == 0;
+      }
+      ++nq[0];
+      if (two) ++nq[1];
+    }
+    if (pend[0] || pend[1]) {
+      const uint32_t vi = take_v();
+      for (int s = 0; s < 2; ++s)
+        if (pend[s]) do_pv(s, vi);
+    }
+    // every product has completed before tensor memory is freed
+    for (int s = 0; s < 2; ++s)
+      if (pv[s] > 0) mbar_drain(smem_u32(&h.pv_done[s]), (pv[s] - 1) & 1u);
+    __syncwarp();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == 9) {
+    fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- host
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+// cuTensorMapEncodeTiled from the driver through the runtime; null when it has none.
+EncodeTiledFn encode_tiled() {
+  static EncodeTiledFn fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = (EncodeTiledFn)p;
+    (void)cudaGetLastError();
+  });
+  return fn;
+}
+
+// [tokens][heads][d] read in boxes of 64 values of `box_heads` heads of
+// `box_tokens` tokens; columns past d and tokens past the end read as zeros.
+fvx_status encode_heads(CUtensorMap* tm, const HeadsView& t, int64_t tokens, int heads, int d, int box_heads,
+                        int box_tokens) {
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) {
+    set_error("%s: the driver has no cuTensorMapEncodeTiled", t_entry);
+    return FVX_ERR_CUDA;
+  }
+  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)heads, (cuuint64_t)tokens};
+  const cuuint64_t strides[2] = {(cuuint64_t)t.head * 2, (cuuint64_t)t.token * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tokens};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r =
+      fn(tm, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(t.p), dims, strides, box, estr,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) {
+    set_error("%s: tensor map encoding failed (driver error %d)", t_entry, (int)r);
+    return FVX_ERR_CUDA;
+  }
+  return FVX_OK;
+}
+
+bool tma_ready(const HeadsView& t) {
+  return (reinterpret_cast<uintptr_t>(t.p) % 16) == 0 && t.token % 8 == 0 && t.head % 8 == 0 && t.token > 0 &&
+         t.head > 0 && t.token < ((int64_t)1 << 38) && t.head < ((int64_t)1 << 38);
+}
+
+int tile_rows(const AttnCall& c) { return c.shared * (kM / c.shared); }
+
+// Units of the forward pass: pairs of query tiles per key head and split.
+int64_t fwd_units(const AttnCall& c, int splits, std::vector<int32_t>* prefix) {
+  int64_t n = 0;
+  for (int b = 0; b < c.items; ++b) {
+    if (prefix) (*prefix)[b] = (int32_t)n;
+    const int64_t rows = (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared;
+    n += (rows + 2 * tile_rows(c) - 1) / (2 * tile_rows(c)) * c.kv_heads * splits;
+  }
+  if (prefix) (*prefix)[c.items] = (int32_t)n;
+  return n;
+}
+
+template <int DP>
+fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
+  using C = Fwd<DP>;
+  int sms = 0;
+  FVX_TRY(device_sm_count(&sms));
+  FwdArgs a;
+  int64_t longest = 1;
+  for (int b = 0; b < c.items; ++b)
+    longest = std::max(longest, (c.kv_offsets[b + 1] - c.kv_offsets[b] + kM - 1) / kM);
+  const int64_t tiles = fwd_units(c, 1, nullptr);
+  // Split the keys only where there are fewer units than multiprocessors.
+  a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / std::max<int64_t>(tiles, 1), longest, 64}));
+  std::vector<int32_t> prefix((size_t)c.items + 1);
+  a.units = (int)fwd_units(c, a.splits, &prefix);
+  FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+  FVX_TRY(encode_heads(&a.tq, c.q, c.nq, c.heads, c.d, c.shared, kM / c.shared));
+  // without any key the maps are never read: the queries' stands in
+  a.tk = a.tv = a.tq;
+  if (c.nk > 0) {
+    FVX_TRY(encode_heads(&a.tk, c.k, c.nk, c.kv_heads, c.d, 1, kM));
+    FVX_TRY(encode_heads(&a.tv, c.v, c.nk, c.kv_heads, c.d, 1, kM));
+  }
+  a.mask = c.mask;
+  a.out = (__nv_bfloat16*)c.out;
+  a.lse = c.lse;
+  a.part = a.top = a.total = nullptr;
+  a.all_rows = c.nq * c.heads;
+  if (a.splits > 1) {
+    a.part = scr.get<float>((size_t)a.splits * a.all_rows * c.d);
+    a.top = scr.get<float>((size_t)a.splits * a.all_rows);
+    a.total = scr.get<float>((size_t)a.splits * a.all_rows);
+    if (!a.part || !a.top || !a.total) return FVX_ERR_ALLOC;
+  }
+  a.status = device_status_word();
+  if (!a.status) {
+    set_error("%s: could not set up the device status word", t_entry);
+    return FVX_ERR_CUDA;
+  }
+  a.heads = c.heads;
+  a.kv_heads = c.kv_heads;
+  a.shared = c.shared;
+  a.d = c.d;
+  a.tile_rows = tile_rows(c);
+  a.c = c.scale * kLog2e;
+  FVX_CUDA(cudaFuncSetAttribute(k_attn_tc_fwd<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+  {
+    LaunchScope ls("attn_tc_fwd", s);
+    k_attn_tc_fwd<DP><<<std::min(a.units, sms), kFwdThreads, C::kSmem, s>>>(a);
+    FVX_TRY(check_launch("attn_tc_fwd"));
+  }
+  return a.splits > 1 ? attn_join(c, a.part, a.top, a.total, a.splits, s) : FVX_OK;
+}
+
+}  // namespace
+
+// The tensor cores take bf16 heads of a multiple of 8 values whose rows TMA
+// can read (16-byte aligned bases and strides); anything else runs in fp32
+// arithmetic on the CUDA cores.
+bool attn_tc_serves(const AttnCall& c, bool backward) {
+  if (c.dt != FVX_BF16 || c.d % 8 || c.shared > kM || backward) return false;
+  return tma_ready(c.q) && (c.nk == 0 || (tma_ready(c.k) && tma_ready(c.v)));
+}
+
+fvx_status attn_tc_forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
+  return c.d <= 64 ? forward<64>(c, s, scr) : forward<128>(c, s, scr);
+}
+
+}  // namespace fvx
