@@ -331,10 +331,12 @@ __global__ void __launch_bounds__(kFmaThreads) k_attn_fma_dkv(const __grid_const
   load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
   load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
   float dk[4][DP / 16], dv[4][DP / 16];
-  bool keep[4];
+  bool keep[4], keep_out[4];  // of the scores' columns, of the rows written
+
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     keep[i] = kept(a, w.key0, j0 + 4 * tx + i, w.keys);
+    keep_out[i] = kept(a, w.key0, j0 + 4 * ty + i, w.keys);
 #pragma unroll
     for (int n = 0; n < DP / 16; ++n) dk[i][n] = dv[i][n] = 0.0f;
   }
@@ -370,8 +372,8 @@ __global__ void __launch_bounds__(kFmaThreads) k_attn_fma_dkv(const __grid_const
 #pragma unroll
     for (int n = 0; n < DP / 16; ++n)
       if (tx + 16 * n < a.d) {
-        a.dk_part[at * a.d + tx + 16 * n] = dk[i][n];
-        a.dv_part[at * a.d + tx + 16 * n] = dv[i][n];
+        a.dk_part[at * a.d + tx + 16 * n] = keep_out[i] ? dk[i][n] : 0.0f;
+        a.dv_part[at * a.d + tx + 16 * n] = keep_out[i] ? dv[i][n] : 0.0f;
       }
   }
 }
@@ -579,7 +581,7 @@ fvx_status fma_forward(const AttnCall& c, cudaStream_t s, Scratch& scr, int sms)
   a.splits = pick_splits(c, false, sms);
   int64_t units = 0;
   const std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &units);
-  FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+  FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
   a.out = c.out;
   a.lse = c.lse;
   const int64_t rows = c.nq * c.heads;
@@ -602,7 +604,7 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
   {
     a.splits = pick_splits(c, false, sms);
     const std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &units);
-    FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+    FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
     a.out = c.dq;
     const int64_t values = c.nq * c.heads * c.d;
     if (a.splits > 1 && !(a.part = scr.get<float>((size_t)a.splits * values))) return FVX_ERR_ALLOC;
@@ -614,7 +616,7 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
   a.splits = pick_splits(c, true, sms);
   const std::vector<int32_t> prefix = unit_prefix(c, true, a.splits, &units);
   if (units == 0) return FVX_OK;
-  FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+  FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
   const int64_t values = c.nk * c.kv_heads * c.d;
   a.dk_part = scr.get<float>((size_t)a.splits * values);
   a.dv_part = scr.get<float>((size_t)a.splits * values);
@@ -632,23 +634,24 @@ fvx_status by_type(fvx_dtype dt, int d, F&& f) {
 
 }  // namespace
 
-fvx_status attn_items(const AttnCall& c, const int32_t* unit_prefix, cudaStream_t s, Scratch& scr, AttnItems* out) {
+fvx_status attn_items(const AttnCall& c, const int32_t* more, int arrays, cudaStream_t s, Scratch& scr,
+                      AttnItems* out) {
   const int n = c.items + 1;
   out->items = c.items;
   out->ptr = nullptr;
   auto value = [&](int i) {
-    return i < n ? (int32_t)c.q_offsets[i] : i < 2 * n ? (int32_t)c.kv_offsets[i - n] : unit_prefix[i - 2 * n];
+    return i < n ? (int32_t)c.q_offsets[i] : i < 2 * n ? (int32_t)c.kv_offsets[i - n] : more[i - 2 * n];
   };
   if (c.items <= kInlineItems) {
-    for (int i = 0; i < 3 * n; ++i) out->in[i] = value(i);
+    for (int i = 0; i < arrays * n; ++i) out->in[i] = value(i);
     return FVX_OK;
   }
-  int32_t* dev = scr.get<int32_t>((size_t)3 * n);
+  int32_t* dev = scr.get<int32_t>((size_t)arrays * n);
   if (!dev) return FVX_ERR_ALLOC;
   constexpr int kPiece = (int)(sizeof(Piece) / 4);
-  for (int i = 0; i < 3 * n; i += kPiece) {
+  for (int i = 0; i < arrays * n; i += kPiece) {
     Piece p;
-    const int m = std::min(kPiece, 3 * n - i);
+    const int m = std::min(kPiece, arrays * n - i);
     for (int j = 0; j < m; ++j) p.v[j] = value(i + j);
     LaunchScope ls("attn_offsets", s);
     k_attn_offsets<<<1, kFmaThreads, 0, s>>>(p, m, dev + i);
@@ -762,6 +765,7 @@ fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t 
     int sms = 0;
     FVX_TRY(device_sm_count(&sms));
     Scratch scr(s);
+    if (attn_tc_serves(c, true)) return attn_tc_backward(c, s, scr);
     const int64_t rows = c.nq * heads;
     float* delta = scr.get<float>((size_t)rows);
     if (!delta) return FVX_ERR_ALLOC;

@@ -10,27 +10,41 @@ namespace fvx {
 
 constexpr int kInlineItems = 64;  // batch elements whose offsets travel in the kernel's arguments
 
-// Offsets of a ragged batch and the prefix of its work units: three arrays of
-// items + 1 values, held in the arguments or (more items) in device memory.
+// Arrays of items + 1 values that describe a ragged batch to a kernel, held in
+// its arguments or (more items) in device memory.  Which arrays follow the
+// offsets depends on the kernel.
+enum AttnArray {
+  kItemQ = 0,      // first query token
+  kItemK = 1,      // first key token
+  kItemUnit = 2,   // first work unit
+  kItemTile = 3,   // backward: first row tile
+  kItemRows = 4,   // backward: ranges that the item's row tiles are cut into
+  kItemKeys = 5,   // backward: ranges that its key tiles are cut into
+  kItemArrays = 6
+};
 struct AttnItems {
   const int32_t* ptr;
   int32_t items;
-  int32_t in[3 * (kInlineItems + 1)];
+  int32_t in[kItemArrays * (kInlineItems + 1)];
 #ifdef __CUDACC__
-  __device__ __forceinline__ int at(int i) const { return ptr ? __ldg(ptr + i) : in[i]; }
-  __device__ __forceinline__ int q0(int b) const { return at(b); }
-  __device__ __forceinline__ int k0(int b) const { return at(items + 1 + b); }
-  __device__ __forceinline__ int u0(int b) const { return at(2 * (items + 1) + b); }
-  // the item that work unit u belongs to
-  __device__ __forceinline__ int item_of(int u) const {
+  __device__ __forceinline__ int at(int array, int b) const {
+    const int i = array * (items + 1) + b;
+    return ptr ? __ldg(ptr + i) : in[i];
+  }
+  __device__ __forceinline__ int q0(int b) const { return at(kItemQ, b); }
+  __device__ __forceinline__ int k0(int b) const { return at(kItemK, b); }
+  __device__ __forceinline__ int u0(int b) const { return at(kItemUnit, b); }
+  // the item whose range of the (rising) array holds value v
+  __device__ __forceinline__ int find(int array, int v) const {
     int lo = 0, hi = items;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (u0(mid) <= u) lo = mid;
+      if (at(array, mid) <= v) lo = mid;
       else hi = mid;
     }
     return lo;
   }
+  __device__ __forceinline__ int item_of(int u) const { return find(kItemUnit, u); }
 #endif
 };
 
@@ -56,10 +70,12 @@ struct AttnCall {
 // The bf16 tensor-core kernels (attn_tc.cu) take a call when this says so.
 bool attn_tc_serves(const AttnCall& c, bool backward);
 fvx_status attn_tc_forward(const AttnCall& c, cudaStream_t s, Scratch& scr);
-fvx_status attn_tc_backward(const AttnCall& c, const float* delta, cudaStream_t s, Scratch& scr);
+fvx_status attn_tc_backward(const AttnCall& c, cudaStream_t s, Scratch& scr);
 
 // attn.cu helpers that both use
-fvx_status attn_items(const AttnCall& c, const int32_t* unit_prefix, cudaStream_t s, Scratch& scr, AttnItems* out);
+// more: the arrays after the offsets, `arrays - 2` times items + 1 values
+fvx_status attn_items(const AttnCall& c, const int32_t* more, int arrays, cudaStream_t s, Scratch& scr,
+                      AttnItems* out);
 // out = softmax-weighted join of `splits` partial results over ranges of keys
 fvx_status attn_join(const AttnCall& c, const float* part, const float* top, const float* total, int splits,
                      cudaStream_t s);

@@ -489,6 +489,638 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
   }
 }
 
+// ================================================================ backward
+// Scores are computed transposed, keys in the lanes and query rows in the
+// columns: then P^T and dS^T are A operands straight from tensor memory for
+//   dV += P^T dO   and   dK += dS^T Q
+// and only dQ = dS K needs dS through shared memory.  A work unit is a range of
+// key tiles and a range of row tiles of one key head: for each key tile (K and
+// V resident, dK and dV accumulating in tensor memory) it walks its row tiles.
+// dQ of a row tile collects over the key tiles in fp32 in a workspace that only
+// this unit touches, one thread per value, so the order of every sum is fixed;
+// units that share keys (or rows) write partial sums that are added in order.
+// Warp roles:
+//   warps 0-3, 4-7  P and dS of the columns 0-63 / 64-127 of the tile; at the
+//                   end of a key tile dV / dK out of tensor memory
+//   warps 8-11      dQ out of tensor memory
+//   warp 12         TMA loads
+//   warp 13         issues the five products
+constexpr int kBwdThreads = 512;  // warps 14, 15 only give their registers away
+constexpr int kBwdLoad = 12, kBwdMma = 13;
+
+template <int DP>
+struct Bwd {
+  static constexpr int kAtoms = DP / 64;
+  static constexpr int kTileBytes = kAtoms * kAtom;
+  static constexpr bool kWide = DP == 128;
+  static constexpr int kKvBufs = kWide ? 1 : 2;
+  static constexpr int kStages = kWide ? 2 : 3;
+  // tensor memory: P over the scores.  64-wide heads: dS and dQ in columns of
+  // their own; 128-wide: dS over dP, and dQ over both once dK has read dS.
+  static constexpr int kS = 0, kDp = 128, kDv = 256, kDk = kWide ? 384 : 320, kDq = kWide ? 128 : 384,
+                       kDs = kWide ? 128 : 448, kDsHalf = kWide ? 64 : 32;
+  static constexpr size_t kKv = 0, kQ = (size_t)2 * kKvBufs * kTileBytes,
+                          kSmDs = kQ + (size_t)2 * kStages * kTileBytes, kStats = kSmDs + 2 * kAtom,
+                          kHead = kStats + (size_t)kStages * 1024, kSmem = kHead + 512;
+};
+
+struct alignas(128) BwdArgs {
+  CUtensorMap tq, tdo, tk, tv;
+  AttnItems items;
+  const uint8_t* mask;
+  const float* stats;  // [row tile][key head][-lse2 of 128 rows, delta of 128 rows]
+  float* dq_sum;       // [key range][row tile][key head][DP / 4][128][4]
+  float *dk_part, *dv_part;  // [row range][nk][kv_heads][d]
+  __nv_bfloat16 *dq, *dk, *dv;
+  uint32_t* status;
+  int64_t nk;
+  int units, tiles, heads, kv_heads, shared, d, tile_rows;
+  float c, scale;
+};
+
+struct BwdUnit {
+  int q0, rows, key0, keys, h, tile0, i0, i1, t0, t1, r_range, k_range, r_ranges, key_tiles;
+};
+__device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
+  BwdUnit w;
+  const int b = a.items.item_of(u);
+  w.q0 = a.items.q0(b);
+  w.rows = (a.items.q0(b + 1) - w.q0) * a.shared;
+  w.key0 = a.items.k0(b);
+  w.keys = a.items.k0(b + 1) - w.key0;
+  w.tile0 = a.items.at(kItemTile, b);
+  const int tiles = a.items.at(kItemTile, b + 1) - w.tile0;
+  w.key_tiles = (w.keys + kM - 1) / kM;
+  w.r_ranges = a.items.at(kItemRows, b);
+  const int k_ranges = a.items.at(kItemKeys, b);
+  int i = u - a.items.u0(b);
+  w.r_range = i % w.r_ranges;
+  i /= w.r_ranges;
+  w.k_range = i % k_ranges;
+  w.h = i / k_ranges;
+  w.i0 = (int)((int64_t)tiles * w.r_range / w.r_ranges);
+  w.i1 = (int)((int64_t)tiles * (w.r_range + 1) / w.r_ranges);
+  w.t0 = (int)((int64_t)w.key_tiles * w.k_range / k_ranges);
+  w.t1 = (int)((int64_t)w.key_tiles * (w.k_range + 1) / k_ranges);
+  return w;
+}
+
+struct BwdHead {
+  uint64_t kv_full[2], kv_empty[2], q_full[3], q_empty[3];
+  uint64_t s_full, dp_full, p_ready, ds_ready, dq_full, dq_free, acc_full, acc_free;
+  uint32_t tmem;
+};
+
+// The block's steps in order: units, their key tiles, their row tiles.  Every
+// unit has at least one of each.
+struct BwdCursor {
+  BwdUnit w;
+  int u, t, i;
+  uint32_t step, tile;  // counted over the block's life
+  bool valid;
+  __device__ __forceinline__ void start(const BwdArgs& a) {
+    u = blockIdx.x;
+    step = tile = 0;
+    valid = u < a.units;
+    if (valid) {
+      w = bwd_unit(a, u);
+      t = w.t0;
+      i = w.i0;
+    }
+  }
+  __device__ __forceinline__ void next(const BwdArgs& a) {
+    ++step;
+    if (++i < w.i1) return;
+    i = w.i0;
+    ++tile;
+    if (++t < w.t1) return;
+    u += gridDim.x;
+    valid = u < a.units;
+    if (valid) {
+      w = bwd_unit(a, u);
+      t = w.t0;
+      i = w.i0;
+    }
+  }
+  __device__ __forceinline__ bool first() const { return i == w.i0; }
+  __device__ __forceinline__ bool last() const { return i + 1 == w.i1; }
+};
+
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_constant__ BwdArgs a) {
+  using C = Bwd<DP>;
+  extern __shared__ __align__(1024) unsigned char sm[];
+  BwdHead& h = *reinterpret_cast<BwdHead*>(sm + C::kHead);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t* const status = a.status;
+  const uint32_t sb = smem_u32(sm);
+  // The tiles fill shared memory to within a few hundred bytes, so its base
+  // must sit on the swizzle's 1024-byte period by itself.
+  if (sb & 1023u) {
+    if (threadIdx.x == 0) report_device_error(status, DEV_CHECK);
+    return;
+  }
+  // rows that no copy writes (128 is not a multiple of every group of heads) read as zeros
+  for (int e = threadIdx.x; e < (int)(2 * C::kStages * C::kTileBytes / 16); e += kBwdThreads)
+    reinterpret_cast<uint4*>(sm + C::kQ)[e] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&h.kv_full[i]), 1);
+      mbar_init(smem_u32(&h.kv_empty[i]), 1);
+    }
+    for (int i = 0; i < 3; ++i) {
+      mbar_init(smem_u32(&h.q_full[i]), 1);
+      mbar_init(smem_u32(&h.q_empty[i]), 1);
+    }
+    mbar_init(smem_u32(&h.s_full), 1);
+    mbar_init(smem_u32(&h.dp_full), 1);
+    mbar_init(smem_u32(&h.p_ready), 8);
+    mbar_init(smem_u32(&h.ds_ready), 8);
+    mbar_init(smem_u32(&h.dq_full), 1);
+    mbar_init(smem_u32(&h.dq_free), 4);
+    mbar_init(smem_u32(&h.acc_full), 1);
+    mbar_init(smem_u32(&h.acc_free), 8);
+    mbar_init_fence();
+  }
+  if (warp == kBwdMma) tmem_alloc(smem_u32(&h.tmem), 512);
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = h.tmem;
+  const uint32_t q_tile = (uint32_t)C::kTileBytes;
+
+  // Registers: 512 threads at 128 are launched; 2 x 128 at 176, 128 at 88 and
+  // 128 at 72 are 65,536 in all.
+  if (warp < 8) {
+    setmaxnreg_inc<176>();
+    // ---------------------------------------------------------------- P and dS
+    const int half = warp >> 2;
+    const int key = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + C::kS + half * 64, tdp = tmem + lanes + C::kDp + half * 64,
+                   tds = tmem + lanes + C::kDs + half * C::kDsHalf;
+    unsigned char* const ds_row = sm + C::kSmDs + half * kAtom + key * 128;
+    BwdCursor cur;
+    cur.start(a);
+    bool kept = false;
+    while (cur.valid) {
+      const BwdUnit& w = cur.w;
+      if (cur.first()) {
+        const int j = cur.t * kM + key;
+        kept = j < w.keys && (!a.mask || __ldg(a.mask + w.key0 + j) != 0);
+      }
+      const uint32_t par = cur.step & 1u;
+      const uint32_t stage = cur.step % C::kStages;
+      const float* st = reinterpret_cast<const float*>(sm + C::kStats + stage * 1024) + half * 64;
+      // the row constants come with the stage's copies
+      mbar_wait(smem_u32(&h.q_full[stage]), (cur.step / C::kStages) & 1u, status);
+      mbar_wait(smem_u32(&h.s_full), par, status);
+      __syncwarp();
+      fence_after();
+      float p[64];
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t r[32];
+        tmem_ld32(ts + 32 * cc, r);
+        tmem_ld_wait(r);
+        uint32_t o[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 nl = *reinterpret_cast<const float4*>(st + 32 * cc + k);
+          const float l[4] = {nl.x, nl.y, nl.z, nl.w};
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const float e = exp2_fast(fmaf(__uint_as_float(r[k + x]), a.c, l[x]));
+            p[32 * cc + k + x] = kept ? e : 0.0f;
+          }
+          o[k / 2] = pack_bf16(p[32 * cc + k], p[32 * cc + k + 1]);
+          o[k / 2 + 1] = pack_bf16(p[32 * cc + k + 2], p[32 * cc + k + 3]);
+        }
+        tmem_st16(ts + 16 * cc, o);
+      }
+      tmem_st_wait();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&h.p_ready));
+
+      mbar_wait(smem_u32(&h.dp_full), par, status);
+      // dQ of the step before has read dS from shared memory
+      if (cur.step > 0) mbar_wait(smem_u32(&h.dq_full), (cur.step - 1) & 1u, status);
+      __syncwarp();
+      fence_after();
+#pragma unroll
+      for (int cc = 0; cc < 2; ++cc) {
+        uint32_t r[32];
+        tmem_ld32(tdp + 32 * cc, r);
+        tmem_ld_wait(r);
+        uint32_t o[16];
+#pragma unroll
+        for (int k = 0; k < 32; k += 4) {
+          const float4 dl = *reinterpret_cast<const float4*>(st + 128 + 32 * cc + k);
+          const float l[4] = {dl.x, dl.y, dl.z, dl.w};
+          float d[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            d[x] = p[32 * cc + k + x] * (__uint_as_float(r[k + x]) - l[x]);
+            if (!kept) d[x] = 0.0f;  // the row of a dropped value vector may hold anything
+          }
+          o[k / 2] = pack_bf16(d[0], d[1]);
+          o[k / 2 + 1] = pack_bf16(d[2], d[3]);
+        }
+        tmem_st16(tds + 16 * cc, o);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(ds_row + (((4 * cc + k) ^ (key & 7)) << 4)) =
+              make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+      tmem_st_wait();
+      fence_proxy_async();
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&h.ds_ready));
+
+      if (cur.last()) {
+        // dV (first half) and dK (second) of the key tile
+        mbar_wait(smem_u32(&h.acc_full), cur.tile & 1u, status);
+        __syncwarp();
+        fence_after();
+        const uint32_t tacc = tmem + lanes + (half ? C::kDk : C::kDv);
+        const float f = half ? a.scale : 1.0f;
+        const int j = cur.t * kM + key;
+        const int64_t row = (int64_t)(w.key0 + j) * a.kv_heads + w.h;
+        const bool live = j < w.keys;
+#pragma unroll 1
+        for (int cc = 0; cc < DP; cc += 32) {
+          uint32_t r[32];
+          tmem_ld32(tacc + cc, r);
+          tmem_ld_wait(r);
+#pragma unroll
+          for (int k = 0; k < 32; ++k) r[k] = kept ? __float_as_uint(__uint_as_float(r[k]) * f) : 0u;
+          if (live && w.r_ranges == 1) {
+            __nv_bfloat16* out = (half ? a.dk : a.dv) + row * a.d + cc;
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              if (cc + k >= a.d) break;
+              uint4 v;
+              uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                pv[x] = pack_bf16(__uint_as_float(r[k + 2 * x]), __uint_as_float(r[k + 2 * x + 1]));
+              *reinterpret_cast<uint4*>(out + k) = v;
+            }
+          } else if (live) {
+            float* out = (half ? a.dk_part : a.dv_part) + ((int64_t)w.r_range * a.nk * a.kv_heads + row) * a.d + cc;
+#pragma unroll
+            for (int k = 0; k < 32; k += 4) {
+              if (cc + k >= a.d) break;
+              *reinterpret_cast<uint4*>(out + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
+            }
+          }
+          __syncwarp();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&h.acc_free));
+      }
+      cur.next(a);
+    }
+  } else if (warp < 12) {
+    setmaxnreg_dec<88>();
+    // ---------------------------------------------------------------- dQ
+    const int row = (warp & 3) * 32 + lane;
+    const uint32_t tdq = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kDq;
+    BwdCursor cur;
+    cur.start(a);
+    while (cur.valid) {
+      const BwdUnit& w = cur.w;
+      const int r = cur.i * a.tile_rows + row;
+      const bool live = row < a.tile_rows && r < w.rows;
+      const int tok = live ? r / a.shared : 0, g = r - tok * a.shared;
+      const bool only = w.key_tiles == 1;  // nothing to collect
+      __nv_bfloat16* out = a.dq + ((int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g) * a.d;
+      float* sum = a.dq_sum + (((int64_t)w.k_range * a.tiles + w.tile0 + cur.i) * a.kv_heads + w.h) * (kM * DP) + row * 4;
+      mbar_wait(smem_u32(&h.dq_full), cur.step & 1u, status);
+      __syncwarp();
+      fence_after();
+#pragma unroll 1
+      for (int cc = 0; cc < DP; cc += 32) {
+        uint32_t v[32];
+        tmem_ld32(tdq + cc, v);
+        tmem_ld_wait(v);
+        if (only) {
+          if (live) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 8) {
+              if (cc + k >= a.d) break;
+              uint4 o;
+              uint32_t* po = reinterpret_cast<uint32_t*>(&o);
+#pragma unroll
+              for (int x = 0; x < 4; ++x)
+                po[x] = pack_bf16(__uint_as_float(v[k + 2 * x]) * a.scale, __uint_as_float(v[k + 2 * x + 1]) * a.scale);
+              *reinterpret_cast<uint4*>(out + cc + k) = o;
+            }
+          }
+          __syncwarp();
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4) {
+            float* at = sum + (cc + k) / 4 * (kM * 4);
+            if (cur.t == w.t0)
+              *reinterpret_cast<uint4*>(at) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
+            else
+              asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(__uint_as_float(v[k])),
+                           "f"(__uint_as_float(v[k + 1])), "f"(__uint_as_float(v[k + 2])),
+                           "f"(__uint_as_float(v[k + 3]))
+                           : "memory");
+          }
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&h.dq_free));
+      cur.next(a);
+    }
+  } else {
+    setmaxnreg_dec<72>();
+    if (warp == kBwdLoad) {
+      // -------------------------------------------------------------- loads
+      if (lane == 0) {
+        tma_prefetch_map(&a.tq);
+        tma_prefetch_map(&a.tdo);
+        tma_prefetch_map(&a.tk);
+        tma_prefetch_map(&a.tv);
+        BwdCursor cur;
+        cur.start(a);
+        while (cur.valid) {
+          const BwdUnit& w = cur.w;
+          if (cur.first()) {
+            const uint32_t b = cur.tile % C::kKvBufs, round = cur.tile / C::kKvBufs;
+            if (round > 0) mbar_wait(smem_u32(&h.kv_empty[b]), (round - 1) & 1u, status);
+            const uint32_t bar = smem_u32(&h.kv_full[b]), dst = sb + (uint32_t)C::kKv + 2 * b * q_tile;
+            mbar_expect_tx(bar, 2 * q_tile);
+#pragma unroll
+            for (int at = 0; at < C::kAtoms; ++at) {
+              tma_tile3d(dst + at * kAtom, &a.tk, 64 * at, w.h, w.key0 + cur.t * kM, bar);
+              tma_tile3d(dst + q_tile + at * kAtom, &a.tv, 64 * at, w.h, w.key0 + cur.t * kM, bar);
+            }
+          }
+          const uint32_t s = cur.step % C::kStages, round = cur.step / C::kStages;
+          if (round > 0) mbar_wait(smem_u32(&h.q_empty[s]), (round - 1) & 1u, status);
+          const uint32_t bar = smem_u32(&h.q_full[s]), dst = sb + (uint32_t)C::kQ + 2 * s * q_tile;
+          mbar_expect_tx(bar, (uint32_t)(2 * C::kAtoms * a.tile_rows * 128 + 1024));
+          const int tok = w.q0 + cur.i * (a.tile_rows / a.shared);
+#pragma unroll
+          for (int at = 0; at < C::kAtoms; ++at) {
+            tma_tile3d(dst + at * kAtom, &a.tq, 64 * at, w.h * a.shared, tok, bar);
+            tma_tile3d(dst + q_tile + at * kAtom, &a.tdo, 64 * at, w.h * a.shared, tok, bar);
+          }
+          bulk_load(sb + (uint32_t)C::kStats + s * 1024, a.stats + ((int64_t)(w.tile0 + cur.i) * a.kv_heads + w.h) * 256,
+                    1024, bar);
+          cur.next(a);
+        }
+        // after a give-up, let the copies in flight land before the block exits
+        for (uint32_t k = 0; k < C::kStages && k < cur.step; ++k) {
+          const uint32_t x = cur.step - 1 - k;
+          mbar_drain(smem_u32(&h.q_full[x % C::kStages]), (x / C::kStages) & 1u);
+        }
+        for (uint32_t k = 0; k < C::kKvBufs && k < cur.tile; ++k) {
+          const uint32_t x = cur.tile - 1 - k;
+          mbar_drain(smem_u32(&h.kv_full[x % C::kKvBufs]), (x / C::kKvBufs) & 1u);
+        }
+      }
+      __syncwarp();
+    } else if (warp == kBwdMma) {
+      // -------------------------------------------------------------- products
+      constexpr uint32_t kIdS = idesc(kM, kM), kIdKv = idesc(kM, DP) | kMnB, kIdQ = idesc(kM, DP) | kMnA | kMnB;
+      const uint32_t s_full = smem_u32(&h.s_full), dp_full = smem_u32(&h.dp_full);
+      auto k_at = [&](const BwdCursor& x) { return sb + (uint32_t)C::kKv + 2 * (x.tile % C::kKvBufs) * q_tile; };
+      auto q_at = [&](const BwdCursor& x) { return sb + (uint32_t)C::kQ + 2 * (x.step % C::kStages) * q_tile; };
+      // 128 x 128 scores: K-major operands, 16 values of the head per product
+      auto scores = [&](uint32_t d, uint32_t ka, uint32_t qa, uint32_t bar) {
+        if (lane == 0) {
+          const uint64_t kd = desc_k(ka), qd = desc_k(qa);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
+            mma_ss(tmem + d, kd + off, qd + off, kIdS, k > 0);
+          }
+          commit(bar);
+        }
+        __syncwarp();
+      };
+      auto issue_s = [&](const BwdCursor& x) {
+        if (x.first()) {
+          const uint32_t b = x.tile % C::kKvBufs;
+          uint8_t mb[4];
+          mask_bytes(a.mask, x.w.key0, x.w.keys, x.t, lane, mb);
+          const Kept kept = kept_keys(a.mask, x.w.keys, x.t, mb);
+          mbar_wait(smem_u32(&h.kv_full[b]), (x.tile / C::kKvBufs) & 1u, status);
+          __syncwarp();
+          if (!kept.all()) zero_dropped<C::kAtoms>(sm + C::kKv + 2 * b * C::kTileBytes, kept, lane);
+        }
+        const uint32_t s = x.step % C::kStages;
+        mbar_wait(smem_u32(&h.q_full[s]), (x.step / C::kStages) & 1u, status);
+        __syncwarp();
+        const int left = x.w.rows - x.i * a.tile_rows;
+        if (left < a.tile_rows) {
+          // rows of the next sample, or past the end
+          Kept live;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            live.w[i] = left >= 32 * (i + 1) ? 0xffffffffu : left <= 32 * i ? 0u : (1u << (left - 32 * i)) - 1u;
+          zero_dropped<C::kAtoms>(sm + C::kQ + 2 * s * C::kTileBytes, live, lane);
+          zero_dropped<C::kAtoms>(sm + C::kQ + (2 * s + 1) * C::kTileBytes, live, lane);
+        }
+        fence_after();
+        scores(C::kS, k_at(x), q_at(x), s_full);
+      };
+      auto issue_dp = [&](const BwdCursor& x) { scores(C::kDp, k_at(x) + q_tile, q_at(x) + q_tile, dp_full); };
+
+      BwdCursor cur, nx;
+      cur.start(a);
+      if (cur.valid) {
+        issue_s(cur);
+        issue_dp(cur);
+      }
+      nx = cur;
+      while (cur.valid) {
+        nx.next(a);
+        const uint32_t par = cur.step & 1u;
+        const bool defer = C::kKvBufs == 1 && nx.valid && nx.first();  // its keys replace this tile's
+        // ---- dV += P^T dO
+        mbar_wait(smem_u32(&h.p_ready), par, status);
+        if (cur.first() && cur.tile > 0) mbar_wait(smem_u32(&h.acc_free), (cur.tile - 1) & 1u, status);
+        __syncwarp();
+        fence_after();
+        if (lane == 0) {
+          const uint64_t od = desc_mn(q_at(cur) + q_tile, kAtom);
+#pragma unroll
+          for (int k = 0; k < kM / 16; ++k)
+            mma_ts(tmem + C::kDv, tmem + C::kS + (k >> 2) * 64 + (k & 3) * 8, od + (uint32_t)(k * 128), kIdKv,
+                   !(cur.first() && k == 0));
+        }
+        __syncwarp();
+        if (nx.valid && !defer) issue_s(nx);
+        mbar_wait(smem_u32(&h.ds_ready), par, status);
+        if (!C::kWide && cur.step > 0) mbar_wait(smem_u32(&h.dq_free), (cur.step - 1) & 1u, status);
+        __syncwarp();
+        fence_after();
+        if (!C::kWide && nx.valid) issue_dp(nx);
+        if (lane == 0) {
+          // ---- dK += dS^T Q
+          const uint64_t qd = desc_mn(q_at(cur), kAtom);
+#pragma unroll
+          for (int k = 0; k < kM / 16; ++k)
+            mma_ts(tmem + C::kDk, tmem + C::kDs + (k >> 2) * C::kDsHalf + (k & 3) * 8, qd + (uint32_t)(k * 128), kIdKv,
+                   !(cur.first() && k == 0));
+          commit(smem_u32(&h.q_empty[cur.step % C::kStages]));
+          if (cur.last()) commit(smem_u32(&h.acc_full));
+          // ---- dQ = dS K
+          const uint64_t sd = desc_mn(sb + (uint32_t)C::kSmDs, kAtom), kd = desc_mn(k_at(cur), kAtom);
+#pragma unroll
+          for (int k = 0; k < kM / 16; ++k)
+            mma_ss(tmem + C::kDq, sd + (uint32_t)(k * 128), kd + (uint32_t)(k * 128), kIdQ, k > 0);
+          commit(smem_u32(&h.dq_full));
+          if (cur.last()) commit(smem_u32(&h.kv_empty[cur.tile % C::kKvBufs]));
+        }
+        __syncwarp();
+        if (nx.valid && defer) issue_s(nx);
+        if (C::kWide && nx.valid) {
+          mbar_wait(smem_u32(&h.dq_free), par, status);
+          __syncwarp();
+          fence_after();
+          issue_dp(nx);
+        }
+        cur = nx;
+      }
+      // every product has completed before tensor memory is freed
+      if (cur.step > 0) mbar_drain(smem_u32(&h.dq_full), (cur.step - 1) & 1u);
+      __syncwarp();
+    }
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == kBwdMma) {
+    fence_after();
+    tmem_free(tmem, 512);
+  }
+}
+
+// -lse in powers of 2 and delta = dout . out of every row tile's rows, one warp
+// per row; the places of rows that do not exist hold -infinity (a probability
+// of 0) and 0.
+__global__ void __launch_bounds__(256) k_attn_stats(const __grid_constant__ AttnItems items, HeadsView dout,
+                                                    const __nv_bfloat16* __restrict__ out,
+                                                    const float* __restrict__ lse, int heads, int kv_heads, int shared,
+                                                    int tile_rows, int d, float* __restrict__ stats) {
+  const int lane = threadIdx.x & 31;
+  const int tile = blockIdx.x / kv_heads, kh = blockIdx.x - tile * kv_heads;
+  const int b = items.find(kItemTile, tile);
+  const int q0 = items.q0(b), rows = (items.q0(b + 1) - q0) * shared;
+  float* st = stats + (int64_t)blockIdx.x * 256;
+  for (int row = threadIdx.x >> 5; row < kM; row += 8) {
+    const int r = (tile - items.at(kItemTile, b)) * tile_rows + row;
+    float s = 0.0f, nl = -INFINITY;
+    if (row < tile_rows && r < rows) {
+      const int64_t tok = q0 + r / shared;
+      const int hd = kh * shared + r % shared;
+      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(dout.p) + tok * dout.token + hd * dout.head;
+      const __nv_bfloat16* o = out + (tok * heads + hd) * d;
+      for (int c = lane; c < d; c += 32) s = fmaf(__bfloat162float(p[c]), __bfloat162float(o[c]), s);
+#pragma unroll
+      for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+      nl = -__ldg(lse + tok * heads + hd) * kLog2e;
+    }
+    if (lane == 0) {
+      st[row] = nl;
+      st[kM + row] = s;
+    }
+  }
+}
+
+// dQ out of its workspace: the key ranges' sums added in order, scaled and
+// rounded; one block per row tile and key head.  Items of one key tile were
+// written by the main kernel; items without keys get zeros.
+template <int DP>
+__global__ void __launch_bounds__(256) k_attn_dq_out(const __grid_constant__ BwdArgs a) {
+  const int tile = blockIdx.x / a.kv_heads, kh = blockIdx.x - tile * a.kv_heads;
+  const int b = a.items.find(kItemTile, tile);
+  const int q0 = a.items.q0(b), rows = (a.items.q0(b + 1) - q0) * a.shared;
+  const int keys = a.items.k0(b + 1) - a.items.k0(b);
+  if (keys > 0 && keys <= kM) return;
+  const int ranges = keys > 0 ? a.items.at(kItemKeys, b) : 0;
+  const int64_t slab = (int64_t)a.tiles * a.kv_heads * (kM * DP);
+  const float* src = a.dq_sum + (int64_t)blockIdx.x * (kM * DP);
+  const int row = threadIdx.x & 127;
+  const int r = (tile - a.items.at(kItemTile, b)) * a.tile_rows + row;
+  if (row >= a.tile_rows || r >= rows) return;
+  const int tok = r / a.shared, g = r - tok * a.shared;
+  __nv_bfloat16* out = a.dq + ((int64_t)(q0 + tok) * a.heads + kh * a.shared + g) * a.d;
+  for (int cc = (threadIdx.x >> 7) * 8; cc < a.d; cc += 16) {
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < ranges; ++k) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4) * (kM * 4) + row * 4));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4 + 1) * (kM * 4) + row * 4));
+      s[0] += x.x;
+      s[1] += x.y;
+      s[2] += x.z;
+      s[3] += x.w;
+      s[4] += y.x;
+      s[5] += y.y;
+      s[6] += y.z;
+      s[7] += y.w;
+    }
+    uint4 v;
+    uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x] * a.scale, s[2 * x + 1] * a.scale);
+    *reinterpret_cast<uint4*>(out + cc) = v;
+  }
+}
+
+// dK and dV of the items whose rows were cut into ranges: the ranges' parts
+// added in order.  Items without rows get zeros.  One thread per 8 values.
+__global__ void __launch_bounds__(256) k_attn_dkv_out(const __grid_constant__ BwdArgs a) {
+  const int per = a.d / 8;
+  const int64_t n = a.nk * a.kv_heads * per, all = a.nk * a.kv_heads * a.d;
+  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < 2 * n; e += (int64_t)gridDim.x * 256) {
+    const bool second = e >= n;
+    const int64_t i = second ? e - n : e;
+    const int b = a.items.find(kItemK, (int)(i / per / a.kv_heads));
+    const int ranges = a.items.at(kItemRows, b);
+    if (ranges == 1) continue;
+    const float* src = (second ? a.dv_part : a.dk_part) + i * 8;
+    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+    for (int k = 0; k < ranges; ++k) {
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src + k * all));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(src + k * all + 4));
+      s[0] += x.x;
+      s[1] += x.y;
+      s[2] += x.z;
+      s[3] += x.w;
+      s[4] += y.x;
+      s[5] += y.y;
+      s[6] += y.z;
+      s[7] += y.w;
+    }
+    uint4 v;
+    uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+    for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x], s[2 * x + 1]);
+    *reinterpret_cast<uint4*>((second ? a.dv : a.dk) + i * 8) = v;
+  }
+}
+
 // ---------------------------------------------------------------- host
 typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
@@ -565,7 +1197,7 @@ fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   a.splits = (int)std::max<int64_t>(1, std::min<int64_t>({sms / std::max<int64_t>(tiles, 1), longest, 64}));
   std::vector<int32_t> prefix((size_t)c.items + 1);
   a.units = (int)fwd_units(c, a.splits, &prefix);
-  FVX_TRY(attn_items(c, prefix.data(), s, scr, &a.items));
+  FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
   FVX_TRY(encode_heads(&a.tq, c.q, c.nq, c.heads, c.d, c.shared, kM / c.shared));
   // without any key the maps are never read: the queries' stands in
   a.tk = a.tv = a.tq;
@@ -604,18 +1236,148 @@ fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   return a.splits > 1 ? attn_join(c, a.part, a.top, a.total, a.splits, s) : FVX_OK;
 }
 
+// Cuts the backward pass into units.  An item's work is (row tiles) x (key
+// tiles); it is cut along its longer side first, so that what the cut costs
+// (partial sums of the other side's gradients) stays small, into ranges of
+// about `target` tile pairs.
+struct BwdPlan {
+  std::vector<int32_t> more;  // units, tiles, row ranges, key ranges: items + 1 values each
+  int units = 0, tiles = 0, most_rows = 1, most_keys = 1;
+  bool dq_sums = false, dq_zeros = false, dkv_parts = false;
+};
+BwdPlan bwd_plan(const AttnCall& c, int sms) {
+  const int n = c.items + 1;
+  BwdPlan p;
+  p.more.assign((size_t)4 * n, 0);
+  int32_t *units = p.more.data(), *tiles = units + n, *rr = tiles + n, *kr = rr + n;
+  auto row_tiles = [&](int b) {
+    return ((c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared + tile_rows(c) - 1) / tile_rows(c);
+  };
+  auto key_tiles = [&](int b) { return (c.kv_offsets[b + 1] - c.kv_offsets[b] + kM - 1) / kM; };
+  int64_t work = 0;
+  for (int b = 0; b < c.items; ++b) work += row_tiles(b) * key_tiles(b) * c.kv_heads;
+  const int64_t target = std::max<int64_t>(1, (work + sms - 1) / sms);
+  int64_t u = 0, t = 0;
+  for (int b = 0; b < c.items; ++b) {
+    const int64_t T = row_tiles(b), K = key_tiles(b);
+    units[b] = (int32_t)u;
+    tiles[b] = (int32_t)t;
+    t += T;
+    if (T == 0 || K == 0) {
+      p.dq_zeros |= T > 0;
+      p.dkv_parts |= K > 0;
+      continue;
+    }
+    const int64_t want = std::max<int64_t>(1, (T * K + target / 2) / target);
+    int64_t r, k;
+    if (T >= K) {
+      r = std::min(want, T);
+      k = std::min(K, (want + r - 1) / r);
+    } else {
+      k = std::min(want, K);
+      r = std::min(T, (want + k - 1) / k);
+    }
+    rr[b] = (int32_t)r;
+    kr[b] = (int32_t)k;
+    u += r * k * c.kv_heads;
+    p.most_rows = std::max(p.most_rows, (int)r);
+    p.most_keys = std::max(p.most_keys, (int)k);
+    p.dq_sums |= K > 1;
+    p.dkv_parts |= r > 1;
+  }
+  units[c.items] = p.units = (int)u;
+  tiles[c.items] = p.tiles = (int)t;
+  return p;
+}
+
+template <int DP>
+fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
+  using C = Bwd<DP>;
+  int sms = 0;
+  FVX_TRY(device_sm_count(&sms));
+  const BwdPlan p = bwd_plan(c, sms);
+  BwdArgs a;
+  FVX_TRY(attn_items(c, p.more.data(), kItemArrays, s, scr, &a.items));
+  FVX_TRY(encode_heads(&a.tq, c.q, c.nq, c.heads, c.d, c.shared, kM / c.shared));
+  FVX_TRY(encode_heads(&a.tdo, c.dout, c.nq, c.heads, c.d, c.shared, kM / c.shared));
+  a.tk = a.tv = a.tq;
+  if (c.nk > 0) {
+    FVX_TRY(encode_heads(&a.tk, c.k, c.nk, c.kv_heads, c.d, 1, kM));
+    FVX_TRY(encode_heads(&a.tv, c.v, c.nk, c.kv_heads, c.d, 1, kM));
+  }
+  a.mask = c.mask;
+  a.dq = (__nv_bfloat16*)c.dq;
+  a.dk = (__nv_bfloat16*)c.dk;
+  a.dv = (__nv_bfloat16*)c.dv;
+  a.nk = c.nk;
+  a.units = p.units;
+  a.tiles = p.tiles;
+  a.heads = c.heads;
+  a.kv_heads = c.kv_heads;
+  a.shared = c.shared;
+  a.d = c.d;
+  a.tile_rows = tile_rows(c);
+  a.c = c.scale * kLog2e;
+  a.scale = c.scale;
+  a.dq_sum = a.dk_part = a.dv_part = nullptr;
+  a.status = device_status_word();
+  if (!a.status) {
+    set_error("%s: could not set up the device status word", t_entry);
+    return FVX_ERR_CUDA;
+  }
+  const size_t row_blocks = (size_t)p.tiles * c.kv_heads;
+  if (p.units > 0) {
+    float* stats = scr.get<float>(row_blocks * 256);
+    if (!stats) return FVX_ERR_ALLOC;
+    a.stats = stats;
+    if (p.dq_sums && !(a.dq_sum = scr.get<float>(row_blocks * kM * DP * p.most_keys))) return FVX_ERR_ALLOC;
+    if (p.most_rows > 1) {
+      const size_t values = (size_t)c.nk * c.kv_heads * c.d;
+      a.dk_part = scr.get<float>(values * p.most_rows);
+      a.dv_part = scr.get<float>(values * p.most_rows);
+      if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
+    }
+    {
+      LaunchScope ls("attn_stats", s);
+      k_attn_stats<<<(unsigned)row_blocks, 256, 0, s>>>(a.items, c.dout, (const __nv_bfloat16*)c.out, c.lse, c.heads,
+                                                        c.kv_heads, c.shared, a.tile_rows, c.d, stats);
+      FVX_TRY(check_launch("attn_stats"));
+    }
+    FVX_CUDA(cudaFuncSetAttribute(k_attn_tc_bwd<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+    LaunchScope ls("attn_tc_bwd", s);
+    k_attn_tc_bwd<DP><<<std::min(a.units, sms), kBwdThreads, C::kSmem, s>>>(a);
+    FVX_TRY(check_launch("attn_tc_bwd"));
+  }
+  if (p.dq_sums || p.dq_zeros) {
+    LaunchScope ls("attn_dq_out", s);
+    k_attn_dq_out<DP><<<(unsigned)row_blocks, 256, 0, s>>>(a);
+    FVX_TRY(check_launch("attn_dq_out"));
+  }
+  if (p.dkv_parts) {
+    const int64_t n = 2 * c.nk * c.kv_heads * (c.d / 8);
+    LaunchScope ls("attn_dkv_out", s);
+    k_attn_dkv_out<<<(unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8), 256, 0, s>>>(a);
+    FVX_TRY(check_launch("attn_dkv_out"));
+  }
+  return FVX_OK;
+}
+
 }  // namespace
 
 // The tensor cores take bf16 heads of a multiple of 8 values whose rows TMA
 // can read (16-byte aligned bases and strides); anything else runs in fp32
 // arithmetic on the CUDA cores.
 bool attn_tc_serves(const AttnCall& c, bool backward) {
-  if (c.dt != FVX_BF16 || c.d % 8 || c.shared > kM || backward) return false;
-  return tma_ready(c.q) && (c.nk == 0 || (tma_ready(c.k) && tma_ready(c.v)));
+  if (c.dt != FVX_BF16 || c.d % 8 || c.shared > kM) return false;
+  return tma_ready(c.q) && (c.nk == 0 || (tma_ready(c.k) && tma_ready(c.v))) && (!backward || tma_ready(c.dout));
 }
 
 fvx_status attn_tc_forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   return c.d <= 64 ? forward<64>(c, s, scr) : forward<128>(c, s, scr);
+}
+
+fvx_status attn_tc_backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
+  return c.d <= 64 ? backward<64>(c, s, scr) : backward<128>(c, s, scr);
 }
 
 }  // namespace fvx

@@ -41,10 +41,10 @@ __device__ __forceinline__ uint32_t mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok;
 }
-// The rest of a wait that the first poll did not end, out of line.  Gives up
+// The rest of a wait that the first poll did not end.  Gives up
 // after kWaitNs, or soon after any block has reported a failure, recording
 // DEV_TIMEOUT; the caller goes on (its results are void, the status says so).
-__device__ __noinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t* status) {
+__device__ __forceinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t* status) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 1;; ++it) {
     if (mbar_try(bar, parity)) return;
@@ -73,6 +73,12 @@ __device__ __forceinline__ void tma_tile3d(uint32_t dst, const void* tmap, int c
       "[%5];" ::"r"(dst),
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
       : "memory");
+}
+// Untiled copy: 16-byte aligned addresses, a multiple of 16 bytes.
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void tma_prefetch_map(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(tmap) : "memory");
