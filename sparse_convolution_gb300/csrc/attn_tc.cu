@@ -9,7 +9,8 @@
 //                   sum in registers, probabilities back to tensor memory as
 //                   bf16 (the A operand of the second product), the row's
 //                   result at the end
-//   warp 8          TMA loads: queries, and a ring of key and value tiles
+//   warp 8          finds the block's units and publishes them in shared memory;
+//                   TMA loads: queries, and a ring of key and value tiles
 //   warp 9          issues the products S = Q K^T and O += P V
 // While one tile is in its softmax, the other's products run.
 //
@@ -41,7 +42,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;       // growth of the maximum (in powers of 2) that O may lag behind
 
-constexpr int kFwdThreads = 320;
+constexpr int kFwdThreads = 384;  // warps 10, 11 only give their registers away
+constexpr int kFwdLoad = 8, kFwdMma = 9;
 
 template <int DP>
 struct Fwd {
@@ -69,11 +71,12 @@ struct alignas(128) FwdArgs {
   int64_t all_rows;  // nq * heads
   int units, splits, heads, kv_heads, shared, d;
   int tile_rows;     // rows of a query tile in use: shared * floor(128 / shared)
+  int wide_out;      // rows of out start at multiples of 32 bytes
   float c;           // scale * log2(e)
 };
 
 struct FwdUnit {
-  int q0, rows, key0, keys, r0, h, split, t0, t1;
+  int q0, rows, key0, keys, r0, h, split, t0, t1, valid;
 };
 __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
   FwdUnit w;
@@ -91,6 +94,7 @@ __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
   const int kt = (w.keys + kM - 1) / kM;
   w.t0 = (int)((int64_t)kt * w.split / a.splits);
   w.t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
+  w.valid = 1;
   return w;
 }
 
@@ -139,8 +143,20 @@ __device__ __forceinline__ void zero_dropped(unsigned char* tile, const Kept& k,
 struct FwdHead {
   uint64_t kv_full[8], kv_empty[8], q_full[2][2], q_empty[2][2];
   uint64_t s_full[2], s_free[2], p_ready[2], pv_done[2], o_free[2];
+  uint64_t info_full[2], info_free[2];
   uint32_t tmem;
+  FwdUnit info[2];
 };
+static_assert(sizeof(FwdHead) <= 512, "the shared-memory layout holds 512 bytes for it");
+
+// The k-th unit of the block, as the loading warp published it; the whole warp.
+__device__ __forceinline__ FwdUnit fwd_take(FwdHead& h, uint32_t k, int lane, uint32_t* status) {
+  mbar_wait(smem_u32(&h.info_full[k & 1u]), (k >> 1) & 1u, status);
+  FwdUnit w = *const_cast<const FwdUnit*>(&h.info[k & 1u]);
+  __syncwarp();
+  if (lane == 0) mbar_arrive(smem_u32(&h.info_free[k & 1u]));
+  return w;
+}
 
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_constant__ FwdArgs a) {
@@ -167,16 +183,20 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       mbar_init(smem_u32(&h.p_ready[s]), 4);
       mbar_init(smem_u32(&h.pv_done[s]), 1);
       mbar_init(smem_u32(&h.o_free[s]), 4);
+      mbar_init(smem_u32(&h.info_full[s]), 1);
+      mbar_init(smem_u32(&h.info_free[s]), 9);
     }
     mbar_init_fence();
   }
-  if (warp == 9) tmem_alloc(smem_u32(&h.tmem), 512);
+  if (warp == kFwdMma) tmem_alloc(smem_u32(&h.tmem), 512);
   fence_before();
   __syncthreads();
   fence_after();
   const uint32_t tmem = h.tmem;
 
+  // Registers: 384 threads at 168 are launched, 64,512; 256 at 208 and 128 at 80 are 63,488.
   if (warp < 8) {
+    setmaxnreg_inc<208>();
     // ---------------------------------------------------------------- softmax
     const int slot = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -187,8 +207,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
                    o_free = smem_u32(&h.o_free[slot]);
     const int row = (warp & 3) * 32 + lane;
     uint32_t step = 0;
-    for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-      const FwdUnit w = fwd_unit(a, u);
+    for (uint32_t uk = 0;; ++uk) {
+      const FwdUnit w = fwd_take(h, uk, lane, status);
+      if (!w.valid) break;
       const int r0 = w.r0 + slot * a.tile_rows;
       if (r0 >= w.rows) continue;  // the pair's second tile has no rows
       const int n = w.t1 - w.t0;
@@ -210,22 +231,29 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);
         }
-        float mx = -INFINITY, c = a.c;
-        if (!kept.all() || !(c > 0.0f)) {
-          // a score that takes no part is -infinity after scaling
+        float c = a.c;
+        if (!(c > 0.0f)) {
+          // the sign, or the zero, of the scale goes into the scores: below, c > 0
+          const float f = c < 0.0f ? -1.0f : 0.0f;
+          c = c < 0.0f ? -c : 1.0f;
+#pragma unroll
+          for (int i = 0; i < 128; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+        }
+        if (!kept.all()) {
 #pragma unroll
           for (int i = 0; i < 128; ++i)
-            r[i] = (kept.w[i >> 5] >> (i & 31)) & 1u ? __float_as_uint(__uint_as_float(r[i]) * c) : 0xff800000u;
-          c = 1.0f;
+            if (!((kept.w[i >> 5] >> (i & 31)) & 1u)) r[i] = 0xff800000u;  // -infinity
         }
+        float mx;
         {
-          float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          float m4[4];
 #pragma unroll
-          for (int i = 0; i < 128; i += 8)
+          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 4]));
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              m4[k] = fmaxf(m4[k], fmaxf(__uint_as_float(r[i + 2 * k]), __uint_as_float(r[i + 2 * k + 1])));
-          mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c;
+          for (int i = 8; i < 128; i += 8)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], __uint_as_float(r[i + k]), __uint_as_float(r[i + k + 4]));
+          mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c;
         }
         bool waited = false;
         if (j == 0) {
@@ -256,21 +284,33 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           fence_after();
         }
         const float base = m_ref == -INFINITY ? 0.0f : m_ref;
-        float add0 = 0.0f, add1 = 0.0f;
+        const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
+        uint64_t add0 = pair(total, 0.0f), add1 = pair(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           uint32_t p[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float x = exp2_fast(fmaf(__uint_as_float(r[32 * i + 2 * k]), c, -base));
-            const float y = exp2_fast(fmaf(__uint_as_float(r[32 * i + 2 * k + 1]), c, -base));
-            add0 += x;
-            add1 += y;
+          for (int k = 0; k < 16; k += 2) {
+            float x, y, z, t;
+            unpair(fma2(pair(__uint_as_float(r[32 * i + 2 * k]), __uint_as_float(r[32 * i + 2 * k + 1])), c2, b2), x, y);
+            unpair(fma2(pair(__uint_as_float(r[32 * i + 2 * k + 2]), __uint_as_float(r[32 * i + 2 * k + 3])), c2, b2), z,
+                   t);
+            x = exp2_fast(x);
+            y = exp2_fast(y);
+            z = exp2_fast(z);
+            t = exp2_fast(t);
+            add0 = add2(add0, pair(x, y));
+            add1 = add2(add1, pair(z, t));
             p[k] = pack_bf16(x, y);
+            p[k + 1] = pack_bf16(z, t);
           }
           tmem_st16(tp + 16 * i, p);
         }
-        total += add0 + add1;
+        {
+          float x, y;
+          unpair(add2(add0, add1), x, y);
+          total = x + y;
+        }
         tmem_st_wait();
         fence_before();
         __syncwarp();
@@ -279,7 +319,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       // ---- the rows' results
       const int r = r0 + row;
       const bool live = row < a.tile_rows && r < w.rows;
-      const int tok = live ? r / a.shared : 0, g = r - tok * a.shared;
+      const int tok = a.shared == 1 ? r : r / a.shared, g = r - tok * a.shared;
       const int64_t at = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
       const int64_t pat = (int64_t)w.split * a.all_rows + at;
       const float inv = total > 0.0f ? 1.0f / total : 0.0f;
@@ -306,16 +346,26 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
         uint32_t o[32];
         tmem_ld32(to + cc, o);
         tmem_ld_wait(o);
+        if (cc + 32 >= DP) {
+          // read: the next unit's product may overwrite it
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(o_free);
+        }
         if (live && a.splits == 1) {
+          __nv_bfloat16* out = a.out + at * a.d + cc;
 #pragma unroll
-          for (int k = 0; k < 32; k += 8) {
-            if (cc + k >= a.d) break;
-            uint4 v;
-            uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+          for (int k = 0; k < 32; k += 16) {
+            uint32_t v[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              pv[i] = pack_bf16(__uint_as_float(o[k + 2 * i]) * inv, __uint_as_float(o[k + 2 * i + 1]) * inv);
-            *reinterpret_cast<uint4*>(a.out + at * a.d + cc + k) = v;
+            for (int i = 0; i < 8; ++i)
+              v[i] = pack_bf16(__uint_as_float(o[k + 2 * i]) * inv, __uint_as_float(o[k + 2 * i + 1]) * inv);
+            if (a.wide_out) {
+              if (cc + k < a.d) store32(out + k, v);
+            } else {
+              if (cc + k < a.d) *reinterpret_cast<uint4*>(out + k) = make_uint4(v[0], v[1], v[2], v[3]);
+              if (cc + k + 8 < a.d) *reinterpret_cast<uint4*>(out + k + 8) = make_uint4(v[4], v[5], v[6], v[7]);
+            }
           }
         } else if (live) {
 #pragma unroll
@@ -326,164 +376,204 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
         }
         __syncwarp();  // the tensor-memory loads need the whole warp
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(o_free);
     }
-  } else if (warp == 8) {
-    // ---------------------------------------------------------------- loads
-    if (lane == 0) {
-      tma_prefetch_map(&a.tq);
-      tma_prefetch_map(&a.tk);
-      tma_prefetch_map(&a.tv);
-      uint32_t e = 0, nq[2] = {0, 0};
-      auto load_kv = [&](const CUtensorMap* map, const FwdUnit& w, int t) {
-        const uint32_t i = e % C::kRing, round = e / C::kRing;
-        if (round > 0) mbar_wait(smem_u32(&h.kv_empty[i]), (round - 1) & 1u, status);
-        const uint32_t bar = smem_u32(&h.kv_full[i]);
-        mbar_expect_tx(bar, C::kTileBytes);
-#pragma unroll
-        for (int at = 0; at < C::kAtoms; ++at)
-          tma_tile3d(smem_u32(ring) + i * C::kTileBytes + at * kAtom, map, 64 * at, w.h, w.key0 + t * kM, bar);
-        ++e;
-      };
-      FwdUnit prev = {};
-      int prev_t = -1;
-      for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-        const FwdUnit w = fwd_unit(a, u);
-        if (w.t0 == w.t1) continue;
-        for (int s = 0; s < 2; ++s) {
-          const int r0 = w.r0 + s * a.tile_rows;
-          if (r0 >= w.rows) continue;
-          const uint32_t i = nq[s] % C::kQBufs, round = nq[s] / C::kQBufs;
-          ++nq[s];
-          if (round > 0) mbar_wait(smem_u32(&h.q_empty[s][i]), (round - 1) & 1u, status);
-          const uint32_t bar = smem_u32(&h.q_full[s][i]);
-          mbar_expect_tx(bar, (uint32_t)(C::kAtoms * a.tile_rows * 128));
+  } else {
+    setmaxnreg_dec<80>();
+    if (warp == kFwdLoad) {
+      // -------------------------------------------------------------- units and loads
+      if (lane == 0) {
+        tma_prefetch_map(&a.tq);
+        tma_prefetch_map(&a.tk);
+        tma_prefetch_map(&a.tv);
+        uint32_t e = 0, nq[2] = {0, 0}, uk = 0;
+        auto publish = [&](const FwdUnit& w) {
+          const uint32_t i = uk & 1u;
+          if (uk >= 2) mbar_wait(smem_u32(&h.info_free[i]), ((uk >> 1) - 1) & 1u, status);
+          h.info[i] = w;
+          mbar_arrive(smem_u32(&h.info_full[i]));
+          ++uk;
+        };
+        auto load_kv = [&](const CUtensorMap* map, const FwdUnit& w, int t) {
+          const uint32_t i = e % C::kRing, round = e / C::kRing;
+          if (round > 0) mbar_wait(smem_u32(&h.kv_empty[i]), (round - 1) & 1u, status);
+          const uint32_t bar = smem_u32(&h.kv_full[i]);
+          mbar_expect_tx(bar, C::kTileBytes);
 #pragma unroll
           for (int at = 0; at < C::kAtoms; ++at)
-            tma_tile3d(smem_u32(sm) + (s * C::kQBufs + i) * C::kTileBytes + at * kAtom, &a.tq, 64 * at,
-                       w.h * a.shared, w.q0 + r0 / a.shared, bar);
-        }
-        for (int t = w.t0; t < w.t1; ++t) {
-          load_kv(&a.tk, w, t);
-          if (prev_t >= 0) load_kv(&a.tv, prev, prev_t);
-          prev = w;
-          prev_t = t;
-        }
-      }
-      if (prev_t >= 0) load_kv(&a.tv, prev, prev_t);
-      // after a give-up, let the copies in flight land before the block exits
-      for (uint32_t k = 0; k < C::kRing && k < e; ++k) {
-        const uint32_t x = e - 1 - k;
-        mbar_drain(smem_u32(&h.kv_full[x % C::kRing]), (x / C::kRing) & 1u);
-      }
-      for (int s = 0; s < 2; ++s)
-        for (uint32_t k = 0; k < C::kQBufs && k < nq[s]; ++k) {
-          const uint32_t x = nq[s] - 1 - k;
-          mbar_drain(smem_u32(&h.q_full[s][x % C::kQBufs]), (x / C::kQBufs) & 1u);
-        }
-    }
-    __syncwarp();
-  } else {
-    // ---------------------------------------------------------------- products
-    constexpr uint32_t kIdS = idesc(kM, kM), kIdO = idesc(kM, DP) | kMnB;
-    const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
-    uint32_t e = 0, nq[2] = {0, 0}, qk[2] = {0, 0}, pv[2] = {0, 0}, opened[2] = {0, 0};
-    // the step whose second product is still to come
-    bool pend[2] = {false, false}, first = false;
-    Kept pend_kept = {};
-    auto do_qk = [&](int s, uint32_t qi, uint32_t ki) {
-      if (C::kOwnP && qk[s] > 0) mbar_wait(smem_u32(&h.s_free[s]), (qk[s] - 1) & 1u, status);
-      fence_after();
-      if (lane == 0) {
-        const uint64_t qd = desc_k(sq + (s * C::kQBufs + qi) * C::kTileBytes), kd = desc_k(sr + ki * C::kTileBytes);
+            tma_tile3d(smem_u32(ring) + i * C::kTileBytes + at * kAtom, map, 64 * at, w.h, w.key0 + t * kM, bar);
+          ++e;
+        };
+        for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
+          const FwdUnit w = fwd_unit(a, u);
+          publish(w);
+          if (w.t0 == w.t1) continue;
+          for (int s = 0; s < 2; ++s) {
+            const int r0 = w.r0 + s * a.tile_rows;
+            if (r0 >= w.rows) continue;
+            const uint32_t i = nq[s] % C::kQBufs, round = nq[s] / C::kQBufs;
+            ++nq[s];
+            if (round > 0) mbar_wait(smem_u32(&h.q_empty[s][i]), (round - 1) & 1u, status);
+            const uint32_t bar = smem_u32(&h.q_full[s][i]);
+            mbar_expect_tx(bar, (uint32_t)(C::kAtoms * a.tile_rows * 128));
 #pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          const uint32_t off = (uint32_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
-          mma_ss(tmem + C::kS + s * 128, qd + off, kd + off, kIdS, k > 0);
-        }
-        commit(smem_u32(&h.s_full[s]));
-      }
-      ++qk[s];
-    };
-    auto do_pv = [&](int s, uint32_t vi) {
-      mbar_wait(smem_u32(&h.p_ready[s]), pv[s] & 1u, status);
-      if (first) {
-        if (opened[s] > 0) mbar_wait(smem_u32(&h.o_free[s]), (opened[s] - 1) & 1u, status);
-        ++opened[s];
-      }
-      fence_after();
-      if (lane == 0) {
-        const uint64_t vd = desc_mn(sr + vi * C::kTileBytes, kAtom);
-#pragma unroll
-        for (int k = 0; k < kM / 16; ++k)
-          mma_ts(tmem + C::kO + s * DP, tmem + C::kP + s * C::kPStep + 8 * k, vd + (uint32_t)(k * 128), kIdO,
-                 !(first && k == 0));
-        commit(smem_u32(&h.pv_done[s]));
-      }
-      ++pv[s];
-    };
-    auto take_v = [&]() -> uint32_t {
-      const uint32_t i = e % C::kRing;
-      mbar_wait(smem_u32(&h.kv_full[i]), (e / C::kRing) & 1u, status);
-      ++e;
-      if (!pend_kept.all()) zero_dropped<C::kAtoms>(ring + (size_t)i * C::kTileBytes, pend_kept, lane);
-      return i;
-    };
-    for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-      const FwdUnit w = fwd_unit(a, u);
-      const int n = w.t1 - w.t0;
-      if (n == 0) continue;
-      const bool two = w.r0 + a.tile_rows < w.rows;
-      uint32_t qi[2];
-      for (int s = 0; s < 2; ++s) qi[s] = nq[s] % C::kQBufs;
-      uint8_t mb[4];
-      mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
-      for (int j = 0; j < n; ++j) {
-        const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
-        if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
-        const uint32_t ki = e % C::kRing;
-        mbar_wait(smem_u32(&h.kv_full[ki]), (e / C::kRing) & 1u, status);
-        ++e;
-        const bool any = pend[0] || pend[1];
-        const uint32_t vi = any ? take_v() : 0u;
-#pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          const bool active = s == 0 || two;
-          if (!C::kOwnP && pend[s]) do_pv(s, vi);
-          if (active) {
-            if (j == 0) mbar_wait(smem_u32(&h.q_full[s][qi[s]]), (nq[s] / C::kQBufs) & 1u, status);
-            do_qk(s, qi[s], ki);
-            if (j == n - 1 && lane == 0) commit(smem_u32(&h.q_empty[s][qi[s]]));
+            for (int at = 0; at < C::kAtoms; ++at)
+              tma_tile3d(smem_u32(sm) + (s * C::kQBufs + i) * C::kTileBytes + at * kAtom, &a.tq, 64 * at,
+                         w.h * a.shared, w.q0 + r0 / a.shared, bar);
           }
-          if (C::kOwnP && pend[s]) do_pv(s, vi);
-          pend[s] = active;
+          // in the order of their use: K0, K1, V0, K2, V1, ..., V(n-1)
+          load_kv(&a.tk, w, w.t0);
+          for (int t = w.t0; t < w.t1; ++t) {
+            if (t + 1 < w.t1) load_kv(&a.tk, w, t + 1);
+            load_kv(&a.tv, w, t);
+          }
         }
-        if (lane == 0) {
-          if (any) commit(smem_u32(&h.kv_empty[vi]));
-          commit(smem_u32(&h.kv_empty[ki]));
+        FwdUnit end = {};
+        publish(end);
+        // after a give-up, let the copies in flight land before the block exits
+        for (uint32_t k = 0; k < C::kRing && k < e; ++k) {
+          const uint32_t x = e - 1 - k;
+          mbar_drain(smem_u32(&h.kv_full[x % C::kRing]), (x / C::kRing) & 1u);
+        }
+        for (int s = 0; s < 2; ++s)
+          for (uint32_t k = 0; k < C::kQBufs && k < nq[s]; ++k) {
+            const uint32_t x = nq[s] - 1 - k;
+            mbar_drain(smem_u32(&h.q_full[s][x % C::kQBufs]), (x / C::kQBufs) & 1u);
+          }
+      }
+      __syncwarp();
+    } else if (warp == kFwdMma) {
+      // -------------------------------------------------------------- products
+      constexpr uint32_t kIdS = idesc(kM, kM), kIdO = idesc(kM, DP) | kMnB;
+      const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
+      uint32_t e = 0, nq[2] = {0, 0}, qk[2] = {0, 0}, pv[2] = {0, 0}, opened[2] = {0, 0};
+      // the step whose second product is still to come
+      bool pend[2] = {false, false}, first = false;
+      Kept pend_kept = {};
+      auto full = [&](uint32_t x) { return smem_u32(&h.kv_full[x % C::kRing]); };
+      auto do_qk = [&](int s, uint32_t qi, uint32_t ki) {
+        if (C::kOwnP && qk[s] > 0) mbar_wait(smem_u32(&h.s_free[s]), (qk[s] - 1) & 1u, status);
+        __syncwarp();
+        fence_after();
+        if (elect()) {
+          const uint64_t qd = desc_k(sq + (s * C::kQBufs + qi) * C::kTileBytes), kd = desc_k(sr + ki * C::kTileBytes);
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const uint32_t off = (uint32_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
+            mma_ss(tmem + C::kS + s * 128, qd + off, kd + off, kIdS, k > 0);
+          }
+          commit(smem_u32(&h.s_full[s]));
+        }
+        ++qk[s];
+      };
+      auto do_pv = [&](int s, uint32_t vi) {
+        mbar_wait(smem_u32(&h.p_ready[s]), pv[s] & 1u, status);
+        if (first) {
+          if (opened[s] > 0) mbar_wait(smem_u32(&h.o_free[s]), (opened[s] - 1) & 1u, status);
+          ++opened[s];
         }
         __syncwarp();
-        pend_kept = kept;
-        first = j == 0;
+        fence_after();
+        if (elect()) {
+          const uint64_t vd = desc_mn(sr + vi * C::kTileBytes, kAtom);
+#pragma unroll
+          for (int k = 0; k < kM / 16; ++k)
+            mma_ts(tmem + C::kO + s * DP, tmem + C::kP + s * C::kPStep + 8 * k, vd + (uint32_t)(k * 128), kIdO,
+                   !(first && k == 0));
+          commit(smem_u32(&h.pv_done[s]));
+        }
+        ++pv[s];
+      };
+      // the value tile at ring position x, its dropped keys' rows zeroed
+      auto take_v = [&](uint32_t x) -> uint32_t {
+        mbar_wait(full(x), (x / C::kRing) & 1u, status);
+        __syncwarp();
+        const uint32_t i = x % C::kRing;
+        if (!pend_kept.all()) zero_dropped<C::kAtoms>(ring + (size_t)i * C::kTileBytes, pend_kept, lane);
+        return i;
+      };
+      auto flush = [&]() {
+        if (!pend[0]) return;
+        const uint32_t vi = take_v(e);
+        ++e;
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          if (pend[s]) do_pv(s, vi);
+          pend[s] = false;
+        }
+        if (elect()) commit(smem_u32(&h.kv_empty[vi]));
+        __syncwarp();
+      };
+      for (uint32_t uk = 0;; ++uk) {
+        const FwdUnit w = fwd_take(h, uk, lane, status);
+        if (!w.valid) break;
+        const int n = w.t1 - w.t0;
+        if (n == 0) {
+          // The softmax warps of the unit before wait for its last product,
+          // and units are published at most two ahead of them.
+          flush();
+          continue;
+        }
+        const bool two = w.r0 + a.tile_rows < w.rows;
+        uint32_t qi[2];
+        for (int s = 0; s < 2; ++s) qi[s] = nq[s] % C::kQBufs;
+        uint8_t mb[4];
+        mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
+        for (int j = 0; j < n; ++j) {
+          const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
+          if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
+          const bool any = pend[0];  // slot 0 is in every unit
+          // ring order: V of the unit before, K0 | K of this step, V of the one before
+          const uint32_t kx = j == 0 && any ? e + 1 : e, vx = j == 0 ? e : e + 1;
+          e += any ? 2 : 1;
+          // With probabilities of their own the scores go first, so that they
+          // are ready when the softmax comes back; at a unit's start only if
+          // its operands are there, for the unit before waits for its last product.
+          bool qk_first = C::kOwnP;
+          if (C::kOwnP && j == 0 && any)
+            qk_first = __all_sync(0xffffffffu, mbar_try(smem_u32(&h.q_full[0][qi[0]]), (nq[0] / C::kQBufs) & 1u) &&
+                                                   mbar_try(full(kx), (kx / C::kRing) & 1u));
+          const uint32_t ki = kx % C::kRing;
+          uint32_t vi = 0;
+          if (any && !qk_first) vi = take_v(vx);
+          bool k_here = false;
+#pragma unroll
+          for (int s = 0; s < 2; ++s) {
+            const bool active = s == 0 || two;
+            if (!qk_first && pend[s]) do_pv(s, vi);
+            if (active) {
+              if (!k_here) mbar_wait(full(kx), (kx / C::kRing) & 1u, status);
+              k_here = true;
+              if (j == 0) mbar_wait(smem_u32(&h.q_full[s][qi[s]]), (nq[s] / C::kQBufs) & 1u, status);
+              do_qk(s, qi[s], ki);
+              if (j == n - 1 && elect()) commit(smem_u32(&h.q_empty[s][qi[s]]));
+            }
+            if (qk_first && pend[s]) {
+              if (s == 0) vi = take_v(vx);
+              do_pv(s, vi);
+            }
+            pend[s] = active;
+          }
+          if (elect()) {
+            if (any) commit(smem_u32(&h.kv_empty[vi]));
+            commit(smem_u32(&h.kv_empty[ki]));
+          }
+          __syncwarp();
+          pend_kept = kept;
+          first = j == 0;
+        }
+        ++nq[0];
+        if (two) ++nq[1];
       }
-      ++nq[0];
-      if (two) ++nq[1];
-    }
-    if (pend[0] || pend[1]) {
-      const uint32_t vi = take_v();
+      flush();
+      // every product has completed before tensor memory is freed
       for (int s = 0; s < 2; ++s)
-        if (pend[s]) do_pv(s, vi);
+        if (pv[s] > 0) mbar_drain(smem_u32(&h.pv_done[s]), (pv[s] - 1) & 1u);
+      __syncwarp();
     }
-    // every product has completed before tensor memory is freed
-    for (int s = 0; s < 2; ++s)
-      if (pv[s] > 0) mbar_drain(smem_u32(&h.pv_done[s]), (pv[s] - 1) & 1u);
-    __syncwarp();
   }
   fence_before();
   __syncthreads();
-  if (warp == 9) {
+  if (warp == kFwdMma) {
     fence_after();
     tmem_free(tmem, 512);
   }
@@ -605,15 +695,6 @@ struct BwdCursor {
   __device__ __forceinline__ bool first() const { return i == w.i0; }
   __device__ __forceinline__ bool last() const { return i + 1 == w.i1; }
 };
-
-template <int N>
-__device__ __forceinline__ void setmaxnreg_inc() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void setmaxnreg_dec() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
 
 template <int DP>
 __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_constant__ BwdArgs a) {
@@ -907,7 +988,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       auto q_at = [&](const BwdCursor& x) { return sb + (uint32_t)C::kQ + 2 * (x.step % C::kStages) * q_tile; };
       // 128 x 128 scores: K-major operands, 16 values of the head per product
       auto scores = [&](uint32_t d, uint32_t ka, uint32_t qa, uint32_t bar) {
-        if (lane == 0) {
+        if (elect()) {
           const uint64_t kd = desc_k(ka), qd = desc_k(qa);
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
@@ -962,7 +1043,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
         if (cur.first() && cur.tile > 0) mbar_wait(smem_u32(&h.acc_free), (cur.tile - 1) & 1u, status);
         __syncwarp();
         fence_after();
-        if (lane == 0) {
+        if (elect()) {
           const uint64_t od = desc_mn(q_at(cur) + q_tile, kAtom);
 #pragma unroll
           for (int k = 0; k < kM / 16; ++k)
@@ -976,7 +1057,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
         __syncwarp();
         fence_after();
         if (!C::kWide && nx.valid) issue_dp(nx);
-        if (lane == 0) {
+        if (elect()) {
           // ---- dK += dS^T Q
           const uint64_t qd = desc_mn(q_at(cur), kAtom);
 #pragma unroll
@@ -1226,6 +1307,7 @@ fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   a.shared = c.shared;
   a.d = c.d;
   a.tile_rows = tile_rows(c);
+  a.wide_out = c.d % 16 == 0 && reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
   a.c = c.scale * kLog2e;
   FVX_CUDA(cudaFuncSetAttribute(k_attn_tc_fwd<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
   {

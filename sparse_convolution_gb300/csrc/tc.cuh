@@ -41,16 +41,21 @@ __device__ __forceinline__ uint32_t mbar_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok;
 }
-// The rest of a wait that the first poll did not end.  Gives up
-// after kWaitNs, or soon after any block has reported a failure, recording
+// The rest of a wait that the first poll did not end.  Gives up after about
+// kWaitNs, or soon after any block has reported a failure, recording
 // DEV_TIMEOUT; the caller goes on (its results are void, the status says so).
+// The clock is a slow read: it is first taken after 1024 polls, which a wait
+// inside a running pipeline never reaches.
 __device__ __forceinline__ void mbar_wait_slow(uint32_t bar, uint32_t parity, uint32_t* status) {
-  const unsigned long long t0 = globaltimer();
+  unsigned long long t0 = 0;
   for (uint32_t it = 1;; ++it) {
     if (mbar_try(bar, parity)) return;
-    if ((it & 1023u) == 0u && (globaltimer() - t0 > kWaitNs || *(volatile uint32_t*)status != 0u)) {
-      report_device_error(status, DEV_TIMEOUT);
-      return;
+    if ((it & 1023u) == 0u) {
+      if (t0 == 0) t0 = globaltimer();
+      if (globaltimer() - t0 > kWaitNs || *(volatile uint32_t*)status != 0u) {
+        report_device_error(status, DEV_TIMEOUT);
+        return;
+      }
     }
   }
 }
@@ -62,6 +67,15 @@ __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = globaltimer();
   for (uint32_t it = 0; !mbar_try(bar, parity); ++it)
     if ((it & 1023u) == 1023u && globaltimer() - t0 > kWaitNs) return;
+}
+
+// One lane of a converged warp.  The tensor-core instructions take their
+// operands from uniform registers; behind this predicate the compiler knows
+// that one thread runs and moves them there directly.
+__device__ __forceinline__ bool elect() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
@@ -166,6 +180,49 @@ __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Two fp32 operations at once (each half rounded like the single operation).
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+// 32 bytes to a 32-byte aligned global address
+__device__ __forceinline__ void store32(void* p, const uint32_t (&v)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+               "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 // 2^x by the special-function unit: relative error about 2^-22, 2^-inf = 0
 __device__ __forceinline__ float exp2_fast(float x) {
