@@ -57,7 +57,7 @@ struct Fwd {
   static constexpr int kQBufs = DP == 64 ? 2 : 1;
   static constexpr int kRing = DP == 64 ? 8 : 5;
   static constexpr int kS = 0, kO = 256, kP = kOwnP ? 384 : 0, kPStep = kOwnP ? 64 : 128;
-  static constexpr size_t kSmem = (size_t)(2 * kQBufs + kRing) * kTileBytes + 1024 + 512;
+  static constexpr size_t kHead = (size_t)(2 * kQBufs + kRing) * kTileBytes, kSmem = kHead + 512 + 800;
 };
 
 struct alignas(128) FwdArgs {
@@ -78,22 +78,30 @@ struct alignas(128) FwdArgs {
 struct FwdUnit {
   int q0, rows, key0, keys, r0, h, split, t0, t1, valid;
 };
-__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
+// items: the offsets and unit prefix in shared memory (or where the items are
+// many, in global memory); b: the item of the unit before, units only rise.
+__device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, const int32_t* items, int u, int& b) {
+  const int n = a.items.items + 1;
+  while (items[2 * n + b + 1] <= u) ++b;
   FwdUnit w;
-  const int b = a.items.item_of(u);
-  w.q0 = a.items.q0(b);
-  w.rows = (a.items.q0(b + 1) - w.q0) * a.shared;
-  w.key0 = a.items.k0(b);
-  w.keys = a.items.k0(b + 1) - w.key0;
+  w.q0 = items[b];
+  w.rows = (items[b + 1] - w.q0) * a.shared;
+  w.key0 = items[n + b];
+  w.keys = items[n + b + 1] - w.key0;
   const int pairs = (w.rows + 2 * a.tile_rows - 1) / (2 * a.tile_rows);
-  int i = u - a.items.u0(b);
-  w.r0 = (i % pairs) * 2 * a.tile_rows;
-  i /= pairs;
-  w.h = i % a.kv_heads;
-  w.split = i / a.kv_heads;
+  int i = u - items[2 * n + b];
+  w.h = i / pairs;
+  w.r0 = (i - w.h * pairs) * 2 * a.tile_rows;
   const int kt = (w.keys + kM - 1) / kM;
-  w.t0 = (int)((int64_t)kt * w.split / a.splits);
-  w.t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
+  w.split = 0;
+  w.t0 = 0;
+  w.t1 = kt;
+  if (a.splits > 1) {
+    w.split = w.h / a.kv_heads;
+    w.h -= w.split * a.kv_heads;
+    w.t0 = (int)((int64_t)kt * w.split / a.splits);
+    w.t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
+  }
   w.valid = 1;
   return w;
 }
@@ -102,7 +110,13 @@ __device__ __forceinline__ FwdUnit fwd_unit(const FwdArgs& a, int u) {
 struct Kept {
   uint32_t w[4];
   __device__ __forceinline__ bool all() const { return (w[0] & w[1] & w[2] & w[3]) == 0xffffffffu; }
+  // words up to the last that keeps a key, at least one: the rest is not computed
+  __device__ __forceinline__ int used() const { return w[3] ? 4 : w[2] ? 3 : w[1] ? 2 : 1; }
 };
+// Whether tile t may drop keys at all; the common tile takes no mask arithmetic.
+__device__ __forceinline__ bool may_drop(const uint8_t* mask, int keys, int t) {
+  return mask != nullptr || keys - t * kM < kM;
+}
 __device__ __forceinline__ void mask_bytes(const uint8_t* mask, int key0, int keys, int t, int lane, uint8_t (&b)[4]) {
   if (!mask) return;
 #pragma unroll
@@ -125,10 +139,10 @@ __device__ __forceinline__ Kept kept_keys(const uint8_t* mask, int keys, int t, 
 // 0 times an infinity or a NaN would not be 0.  One warp; the products read
 // shared memory through the async proxy, hence the fence.
 template <int ATOMS>
-__device__ __forceinline__ void zero_dropped(unsigned char* tile, const Kept& k, int lane) {
+__device__ __forceinline__ void zero_dropped(unsigned char* tile, const Kept& k, int words, int lane) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t drop = ~k.w[i];
+    uint32_t drop = i < words ? ~k.w[i] : 0u;
     while (drop) {
       const int r = 32 * i + __ffs(drop) - 1;
       drop &= drop - 1;
@@ -147,7 +161,8 @@ struct FwdHead {
   uint32_t tmem;
   FwdUnit info[2];
 };
-static_assert(sizeof(FwdHead) <= 512, "the shared-memory layout holds 512 bytes for it");
+constexpr int kFwdItems = 512;  // behind the head: the items' offsets
+static_assert(sizeof(FwdHead) <= kFwdItems, "the shared-memory layout holds 512 bytes for it");
 
 // The k-th unit of the block, as the loading warp published it; the whole warp.
 __device__ __forceinline__ FwdUnit fwd_take(FwdHead& h, uint32_t k, int lane, uint32_t* status) {
@@ -161,12 +176,20 @@ __device__ __forceinline__ FwdUnit fwd_take(FwdHead& h, uint32_t k, int lane, ui
 template <int DP>
 __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_constant__ FwdArgs a) {
   using C = Fwd<DP>;
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  unsigned char* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  extern __shared__ __align__(1024) unsigned char sm[];
   unsigned char* const ring = sm + (size_t)2 * C::kQBufs * C::kTileBytes;
-  FwdHead& h = *reinterpret_cast<FwdHead*>(ring + (size_t)C::kRing * C::kTileBytes);
+  FwdHead& h = *reinterpret_cast<FwdHead*>(sm + C::kHead);
+  int32_t* const items = reinterpret_cast<int32_t*>(sm + C::kHead + kFwdItems);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* const status = a.status;
+  // The tiles fill shared memory to within a few hundred bytes, so its base
+  // must sit on the swizzle's 1024-byte period by itself.
+  if (smem_u32(sm) & 1023u) {
+    if (threadIdx.x == 0) report_device_error(status, DEV_CHECK);
+    return;
+  }
+  if (!a.items.ptr)
+    for (int i = threadIdx.x; i < 3 * (a.items.items + 1); i += kFwdThreads) items[i] = a.items.in[i];
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kRing; ++i) {
@@ -194,9 +217,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
   fence_after();
   const uint32_t tmem = h.tmem;
 
-  // Registers: 384 threads at 168 are launched, 64,512; 256 at 208 and 128 at 80 are 63,488.
+  // Registers: 384 threads at 168 are launched, 64,512: 256 at 200 and 128 at 104.
   if (warp < 8) {
-    setmaxnreg_inc<208>();
+    setmaxnreg_inc<200>();
     // ---------------------------------------------------------------- softmax
     const int slot = warp >> 2;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -206,6 +229,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
                    p_ready = smem_u32(&h.p_ready[slot]), pv_done = smem_u32(&h.pv_done[slot]),
                    o_free = smem_u32(&h.o_free[slot]);
     const int row = (warp & 3) * 32 + lane;
+    // A scale that is not positive: its sign, or zero, goes into the scores, so that c > 0.
+    const bool negate = !(a.c > 0.0f);
+    const float sign = a.c < 0.0f ? -1.0f : 0.0f, c = a.c > 0.0f ? a.c : a.c < 0.0f ? -a.c : 1.0f;
     uint32_t step = 0;
     for (uint32_t uk = 0;; ++uk) {
       const FwdUnit w = fwd_take(h, uk, lane, status);
@@ -217,8 +243,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       uint8_t mb[4];
       if (n > 0) mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
       for (int j = 0; j < n; ++j, ++step) {
-        const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
-        if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
         mbar_wait(s_full, step & 1u, status);
         __syncwarp();
         fence_after();
@@ -231,29 +255,31 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           __syncwarp();
           if (lane == 0) mbar_arrive(s_free);
         }
-        float c = a.c;
-        if (!(c > 0.0f)) {
-          // the sign, or the zero, of the scale goes into the scores: below, c > 0
-          const float f = c < 0.0f ? -1.0f : 0.0f;
-          c = c < 0.0f ? -c : 1.0f;
+        int used = 4;
+        if (negate) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+          for (int i = 0; i < 128; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * sign);
         }
-        if (!kept.all()) {
+        if (may_drop(a.mask, w.keys, w.t0 + j)) {
+          const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
+          if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
+          used = kept.used();
+          if (!kept.all()) {
 #pragma unroll
-          for (int i = 0; i < 128; ++i)
-            if (!((kept.w[i >> 5] >> (i & 31)) & 1u)) r[i] = 0xff800000u;  // -infinity
+            for (int i = 0; i < 128; ++i)
+              if (!((kept.w[i >> 5] >> (i & 31)) & 1u)) r[i] = 0xff800000u;  // -infinity
+          }
         }
         float mx;
         {
-          float m4[4];
+          float m8[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) m4[k] = fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 4]));
+          for (int k = 0; k < 8; ++k) m8[k] = fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 8]));
 #pragma unroll
-          for (int i = 8; i < 128; i += 8)
+          for (int i = 16; i < 128; i += 16)
 #pragma unroll
-            for (int k = 0; k < 4; ++k) m4[k] = max3(m4[k], __uint_as_float(r[i + k]), __uint_as_float(r[i + k + 4]));
-          mx = max3(m4[0], m4[1], fmaxf(m4[2], m4[3])) * c;
+            for (int k = 0; k < 8; ++k) m8[k] = max3(m8[k], __uint_as_float(r[i + k]), __uint_as_float(r[i + k + 8]));
+          mx = fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3(m8[5], m8[6], m8[7])) * c;
         }
         bool waited = false;
         if (j == 0) {
@@ -288,6 +314,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
         uint64_t add0 = pair(total, 0.0f), add1 = pair(0.0f, 0.0f);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
+          if (i >= used) break;
           uint32_t p[16];
 #pragma unroll
           for (int k = 0; k < 16; k += 2) {
@@ -378,7 +405,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       }
     }
   } else {
-    setmaxnreg_dec<80>();
+    setmaxnreg_dec<104>();
     if (warp == kFwdLoad) {
       // -------------------------------------------------------------- units and loads
       if (lane == 0) {
@@ -403,8 +430,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
             tma_tile3d(smem_u32(ring) + i * C::kTileBytes + at * kAtom, map, 64 * at, w.h, w.key0 + t * kM, bar);
           ++e;
         };
+        const int32_t* const at_items = a.items.ptr ? a.items.ptr : items;
+        int b = 0;
         for (int u = blockIdx.x; u < a.units; u += gridDim.x) {
-          const FwdUnit w = fwd_unit(a, u);
+          const FwdUnit w = fwd_unit(a, at_items, u, b);
           publish(w);
           if (w.t0 == w.t1) continue;
           for (int s = 0; s < 2; ++s) {
@@ -445,12 +474,23 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       // -------------------------------------------------------------- products
       constexpr uint32_t kIdS = idesc(kM, kM), kIdO = idesc(kM, DP) | kMnB;
       const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
-      uint32_t e = 0, nq[2] = {0, 0}, qk[2] = {0, 0}, pv[2] = {0, 0}, opened[2] = {0, 0};
+      // Everything in this loop is in the way of the tensor cores, so it keeps
+      // running indices and phases and touches masks only where keys may drop.
+      struct Ring {
+        uint32_t i, phase;
+        __device__ __forceinline__ void next() {
+          if (++i == (uint32_t)C::kRing) {
+            i = 0;
+            phase ^= 1u;
+          }
+        }
+      } at = {0, 0};
+      uint32_t nq[2] = {0, 0}, qk[2] = {0, 0}, pv[2] = {0, 0}, opened[2] = {0, 0};
       // the step whose second product is still to come
-      bool pend[2] = {false, false}, first = false;
+      bool pend[2] = {false, false}, first = false, pend_drop = false;
       Kept pend_kept = {};
-      auto full = [&](uint32_t x) { return smem_u32(&h.kv_full[x % C::kRing]); };
-      auto do_qk = [&](int s, uint32_t qi, uint32_t ki) {
+      auto wait_full = [&](const Ring& x) { mbar_wait(smem_u32(&h.kv_full[x.i]), x.phase, status); };
+      auto do_qk = [&](int s, uint32_t qi, uint32_t ki, uint32_t id) {
         if (C::kOwnP && qk[s] > 0) mbar_wait(smem_u32(&h.s_free[s]), (qk[s] - 1) & 1u, status);
         __syncwarp();
         fence_after();
@@ -459,7 +499,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
 #pragma unroll
           for (int k = 0; k < DP / 16; ++k) {
             const uint32_t off = (uint32_t)((k >> 2) * (kAtom >> 4) + (k & 3) * 2);
-            mma_ss(tmem + C::kS + s * 128, qd + off, kd + off, kIdS, k > 0);
+            mma_ss(tmem + C::kS + s * 128, qd + off, kd + off, id, k > 0);
           }
           commit(smem_u32(&h.s_full[s]));
         }
@@ -475,33 +515,41 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
         fence_after();
         if (elect()) {
           const uint64_t vd = desc_mn(sr + vi * C::kTileBytes, kAtom);
+          const uint32_t td = tmem + C::kO + s * DP, tp = tmem + C::kP + s * C::kPStep;
+          mma_ts(td, tp, vd, kIdO, !first);
+          if (!pend_drop) {
 #pragma unroll
-          for (int k = 0; k < kM / 16; ++k)
-            mma_ts(tmem + C::kO + s * DP, tmem + C::kP + s * C::kPStep + 8 * k, vd + (uint32_t)(k * 128), kIdO,
-                   !(first && k == 0));
+            for (int k = 1; k < kM / 16; ++k) mma_ts(td, tp + 8 * k, vd + (uint32_t)(k * 128), kIdO, 1u);
+          } else {
+            const int steps = 2 * pend_kept.used();
+#pragma unroll 1
+            for (int k = 1; k < steps; ++k) mma_ts(td, tp + 8 * k, vd + (uint32_t)(k * 128), kIdO, 1u);
+          }
           commit(smem_u32(&h.pv_done[s]));
         }
         ++pv[s];
       };
-      // the value tile at ring position x, its dropped keys' rows zeroed
-      auto take_v = [&](uint32_t x) -> uint32_t {
-        mbar_wait(full(x), (x / C::kRing) & 1u, status);
-        __syncwarp();
-        const uint32_t i = x % C::kRing;
-        if (!pend_kept.all()) zero_dropped<C::kAtoms>(ring + (size_t)i * C::kTileBytes, pend_kept, lane);
-        return i;
+      // the value tile at a ring position, its dropped keys' rows zeroed
+      auto take_v = [&](const Ring& x) {
+        wait_full(x);
+        if (pend_drop && !pend_kept.all()) {
+          __syncwarp();
+          zero_dropped<C::kAtoms>(ring + (size_t)x.i * C::kTileBytes, pend_kept, pend_kept.used(), lane);
+        }
+      };
+      auto release = [&](uint32_t i) {
+        if (elect()) commit(smem_u32(&h.kv_empty[i]));
       };
       auto flush = [&]() {
         if (!pend[0]) return;
-        const uint32_t vi = take_v(e);
-        ++e;
+        take_v(at);
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-          if (pend[s]) do_pv(s, vi);
+          if (pend[s]) do_pv(s, at.i);
           pend[s] = false;
         }
-        if (elect()) commit(smem_u32(&h.kv_empty[vi]));
-        __syncwarp();
+        release(at.i);
+        at.next();
       };
       for (uint32_t uk = 0;; ++uk) {
         const FwdUnit w = fwd_take(h, uk, lane, status);
@@ -514,51 +562,80 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           continue;
         }
         const bool two = w.r0 + a.tile_rows < w.rows;
-        uint32_t qi[2];
-        for (int s = 0; s < 2; ++s) qi[s] = nq[s] % C::kQBufs;
+        uint32_t qi[2], qp[2];
+#pragma unroll
+        for (int s = 0; s < 2; ++s) {
+          qi[s] = nq[s] % C::kQBufs;
+          qp[s] = (nq[s] / C::kQBufs) & 1u;
+        }
         uint8_t mb[4];
         mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
         for (int j = 0; j < n; ++j) {
-          const Kept kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
-          if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
-          const bool any = pend[0];  // slot 0 is in every unit
-          // ring order: V of the unit before, K0 | K of this step, V of the one before
-          const uint32_t kx = j == 0 && any ? e + 1 : e, vx = j == 0 ? e : e + 1;
-          e += any ? 2 : 1;
-          // With probabilities of their own the scores go first, so that they
-          // are ready when the softmax comes back; at a unit's start only if
-          // its operands are there, for the unit before waits for its last product.
-          bool qk_first = C::kOwnP;
-          if (C::kOwnP && j == 0 && any)
-            qk_first = __all_sync(0xffffffffu, mbar_try(smem_u32(&h.q_full[0][qi[0]]), (nq[0] / C::kQBufs) & 1u) &&
-                                                   mbar_try(full(kx), (kx / C::kRing) & 1u));
-          const uint32_t ki = kx % C::kRing;
-          uint32_t vi = 0;
-          if (any && !qk_first) vi = take_v(vx);
-          bool k_here = false;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const bool active = s == 0 || two;
-            if (!qk_first && pend[s]) do_pv(s, vi);
-            if (active) {
-              if (!k_here) mbar_wait(full(kx), (kx / C::kRing) & 1u, status);
-              k_here = true;
-              if (j == 0) mbar_wait(smem_u32(&h.q_full[s][qi[s]]), (nq[s] / C::kQBufs) & 1u, status);
-              do_qk(s, qi[s], ki);
-              if (j == n - 1 && elect()) commit(smem_u32(&h.q_empty[s][qi[s]]));
-            }
-            if (qk_first && pend[s]) {
-              if (s == 0) vi = take_v(vx);
-              do_pv(s, vi);
-            }
-            pend[s] = active;
+          Kept kept;
+          const bool drop = may_drop(a.mask, w.keys, w.t0 + j);
+          uint32_t id = idesc(kM, kM);
+          if (drop) {
+            kept = kept_keys(a.mask, w.keys, w.t0 + j, mb);
+            if (j + 1 < n) mask_bytes(a.mask, w.key0, w.keys, w.t0 + j + 1, lane, mb);
+            id = idesc(kM, 32 * kept.used());
           }
-          if (elect()) {
-            if (any) commit(smem_u32(&h.kv_empty[vi]));
-            commit(smem_u32(&h.kv_empty[ki]));
+          if (j == 0) {
+            // Ring order: V of the unit before, then this unit's K.  With
+            // probabilities of their own the scores can go first, if their
+            // operands are there; the unit before waits for its last product.
+            Ring kx = at;
+            if (pend[0]) kx.next();
+            const bool ahead =
+                C::kOwnP && pend[0] &&
+                __all_sync(0xffffffffu, mbar_try(smem_u32(&h.q_full[0][qi[0]]), qp[0]) &&
+                                            (!two || mbar_try(smem_u32(&h.q_full[1][qi[1]]), qp[1])) &&
+                                            mbar_try(smem_u32(&h.kv_full[kx.i]), kx.phase));
+            if (!ahead) {
+              flush();
+              wait_full(kx);
+            }
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+              if (s == 0 || two) {
+                mbar_wait(smem_u32(&h.q_full[s][qi[s]]), qp[s], status);
+                do_qk(s, qi[s], kx.i, id);
+              }
+            if (ahead) flush();
+            release(kx.i);
+            at = kx;
+            at.next();
+          } else {
+            // ring order: K of this step, V of the one before
+            const uint32_t ki = at.i;
+            wait_full(at);
+            at.next();
+            const uint32_t vi = at.i;
+            if (C::kOwnP) do_qk(0, qi[0], ki, id);
+            take_v(at);
+            at.next();
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+              if (s == 1 && !two) break;
+              if (C::kOwnP) {
+                if (s == 1) do_qk(1, qi[1], ki, id);
+                do_pv(s, vi);
+              } else {
+                do_pv(s, vi);
+                do_qk(s, qi[s], ki, id);
+              }
+            }
+            release(vi);
+            release(ki);
+          }
+          if (j == n - 1 && elect()) {
+            commit(smem_u32(&h.q_empty[0][qi[0]]));
+            if (two) commit(smem_u32(&h.q_empty[1][qi[1]]));
           }
           __syncwarp();
-          pend_kept = kept;
+          pend[0] = true;
+          pend[1] = two;
+          pend_drop = drop;
+          if (drop) pend_kept = kept;
           first = j == 0;
         }
         ++nq[0];
@@ -1007,7 +1084,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
           const Kept kept = kept_keys(a.mask, x.w.keys, x.t, mb);
           mbar_wait(smem_u32(&h.kv_full[b]), (x.tile / C::kKvBufs) & 1u, status);
           __syncwarp();
-          if (!kept.all()) zero_dropped<C::kAtoms>(sm + C::kKv + 2 * b * C::kTileBytes, kept, lane);
+          if (!kept.all()) zero_dropped<C::kAtoms>(sm + C::kKv + 2 * b * C::kTileBytes, kept, 4, lane);
         }
         const uint32_t s = x.step % C::kStages;
         mbar_wait(smem_u32(&h.q_full[s]), (x.step / C::kStages) & 1u, status);
@@ -1019,8 +1096,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             live.w[i] = left >= 32 * (i + 1) ? 0xffffffffu : left <= 32 * i ? 0u : (1u << (left - 32 * i)) - 1u;
-          zero_dropped<C::kAtoms>(sm + C::kQ + 2 * s * C::kTileBytes, live, lane);
-          zero_dropped<C::kAtoms>(sm + C::kQ + (2 * s + 1) * C::kTileBytes, live, lane);
+          zero_dropped<C::kAtoms>(sm + C::kQ + 2 * s * C::kTileBytes, live, 4, lane);
+          zero_dropped<C::kAtoms>(sm + C::kQ + (2 * s + 1) * C::kTileBytes, live, 4, lane);
         }
         fence_after();
         scores(C::kS, k_at(x), q_at(x), s_full);
