@@ -11,8 +11,14 @@
 //                   result at the end
 //   warp 8          finds the block's units and publishes them in shared memory;
 //                   TMA loads: queries, and a ring of key and value tiles
-//   warp 9          issues the products S = Q K^T and O += P V
-// While one tile is in its softmax, the other's products run.
+//   warps 9, 10     issue the products S = Q K^T and O += P V
+// While one tile is in its softmax, the other's products run.  For 64-wide
+// heads each tile has a warp that issues its products (with one warp for both,
+// each waited for the other's softmax: 16,384 rows x 1200 keys x 8 heads took
+// 133 us, not 115).  For 128-wide heads, where the products are the longer
+// part, one warp issues both tiles' in turn: two warps drew the tiles into
+// step, and the tensor cores idled while both were in their softmax (65,536
+// rows x 2048 keys x 8 heads: 498 us, not 391).
 //
 // The accumulated O is relative to the running maximum m_ref of its row.  It
 // is brought to a new maximum only when that exceeds m_ref by more than 2^8
@@ -42,7 +48,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kLazy = 8.0f;       // growth of the maximum (in powers of 2) that O may lag behind
 
-constexpr int kFwdThreads = 384;  // warps 10, 11 only give their registers away
+constexpr int kFwdThreads = 384;  // warp 11 only gives its registers away
 constexpr int kFwdLoad = 8, kFwdMma = 9;
 
 template <int DP>
@@ -54,6 +60,7 @@ struct Fwd {
   // memory for a second set of queries; 128-wide ones put the probabilities
   // over the scores.
   static constexpr bool kOwnP = DP == 64;
+  static constexpr int kPerWarp = kOwnP ? 1 : 2;  // tiles whose products one warp issues
   static constexpr int kQBufs = DP == 64 ? 2 : 1;
   static constexpr int kRing = DP == 64 ? 8 : 5;
   static constexpr int kS = 0, kO = 256, kP = kOwnP ? 384 : 0, kPStep = kOwnP ? 64 : 128;
@@ -194,7 +201,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
   if (threadIdx.x == 0) {
     for (int i = 0; i < C::kRing; ++i) {
       mbar_init(smem_u32(&h.kv_full[i]), 1);
-      mbar_init(smem_u32(&h.kv_empty[i]), 1);
+      mbar_init(smem_u32(&h.kv_empty[i]), 2 / C::kPerWarp);
     }
     for (int s = 0; s < 2; ++s) {
       for (int b = 0; b < 2; ++b) {
@@ -207,7 +214,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       mbar_init(smem_u32(&h.pv_done[s]), 1);
       mbar_init(smem_u32(&h.o_free[s]), 4);
       mbar_init(smem_u32(&h.info_full[s]), 1);
-      mbar_init(smem_u32(&h.info_free[s]), 9);
+      mbar_init(smem_u32(&h.info_free[s]), 8 + 2 / C::kPerWarp);
     }
     mbar_init_fence();
   }
@@ -270,8 +277,57 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
               if (!((kept.w[i >> 5] >> (i & 31)) & 1u)) r[i] = 0xff800000u;  // -infinity
           }
         }
+        // Probabilities relative to `base`: their sum, and as bf16 into tensor
+        // memory; m8, if given, collects the scores' maximum in the same pass.
+        auto top_of = [&](float* m8) {
+          return fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3(m8[5], m8[6], m8[7])) * c;
+        };
+        uint64_t add0, add1;
+        auto powers = [&](float base, float* m8) {
+          const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
+          add0 = add1 = pair(0.0f, 0.0f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            if (i >= used) break;
+            uint32_t p[16];
+#pragma unroll
+            for (int k = 0; k < 16; k += 2) {
+              const float s0 = __uint_as_float(r[32 * i + 2 * k]), s1 = __uint_as_float(r[32 * i + 2 * k + 1]);
+              const float s2 = __uint_as_float(r[32 * i + 2 * k + 2]), s3 = __uint_as_float(r[32 * i + 2 * k + 3]);
+              if (m8) {
+                m8[k % 8] = max3(m8[k % 8], s0, s1);
+                m8[k % 8 + 1] = max3(m8[k % 8 + 1], s2, s3);
+              }
+              float x, y, z, t;
+              unpair(fma2(pair(s0, s1), c2, b2), x, y);
+              unpair(fma2(pair(s2, s3), c2, b2), z, t);
+              x = exp2_fast(x);
+              y = exp2_fast(y);
+              z = exp2_fast(z);
+              t = exp2_fast(t);
+              add0 = add2(add0, pair(x, y));
+              add1 = add2(add1, pair(z, t));
+              p[k] = pack_bf16(x, y);
+              p[k + 1] = pack_bf16(z, t);
+            }
+            tmem_st16(tp + 16 * i, p);
+          }
+        };
+        bool done = false;
         float mx;
-        {
+        if (C::kOwnP && j > 0) {
+          // the previous product has read the previous probabilities
+          mbar_wait(pv_done, (step - 1) & 1u, status);
+          __syncwarp();
+          fence_after();
+          // Most tiles bring no new maximum worth a rescale: the powers are
+          // taken relative to the old one while the new one is still being
+          // found, and taken again in the few tiles where it matters.
+          float m8[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
+          powers(m_ref == -INFINITY ? 0.0f : m_ref, m8);
+          mx = top_of(m8);
+          done = !__any_sync(0xffffffffu, mx > m_ref + kLazy);
+        } else {
           float m8[8];
 #pragma unroll
           for (int k = 0; k < 8; ++k) m8[k] = fmaxf(__uint_as_float(r[k]), __uint_as_float(r[k + 8]));
@@ -279,64 +335,35 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           for (int i = 16; i < 128; i += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = max3(m8[k], __uint_as_float(r[i + k]), __uint_as_float(r[i + k + 8]));
-          mx = fmaxf(max3(max3(m8[0], m8[1], m8[2]), m8[3], m8[4]), max3(m8[5], m8[6], m8[7])) * c;
+          mx = top_of(m8);
         }
-        bool waited = false;
         if (j == 0) {
           m_ref = mx;
-        } else if (__any_sync(0xffffffffu, mx > m_ref + kLazy)) {
-          mbar_wait(pv_done, (step - 1) & 1u, status);
-          __syncwarp();
-          fence_after();
-          waited = true;
+        } else if (!done && __any_sync(0xffffffffu, mx > m_ref + kLazy)) {
+          if (!C::kOwnP) {
+            mbar_wait(pv_done, (step - 1) & 1u, status);
+            __syncwarp();
+            fence_after();
+          }
           const float m_new = fmaxf(mx, m_ref);
           const float f = m_ref == -INFINITY ? 0.0f : exp2_fast(m_ref - m_new);
           total *= f;
           m_ref = m_new;
 #pragma unroll 1
-          for (int cc = 0; cc < DP; cc += 32) {
-            uint32_t o[32];
-            tmem_ld32(to + cc, o);
+          for (int cc = 0; cc < DP; cc += 16) {
+            uint32_t o[16];
+            tmem_ld16(to + cc, o);
             tmem_ld_wait(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-            tmem_st32(to + cc, o);
+            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+            tmem_st16(to + cc, o);
           }
         }
-        // the previous product has read the previous probabilities
-        if (C::kOwnP && j > 0 && !waited) {
-          mbar_wait(pv_done, (step - 1) & 1u, status);
-          __syncwarp();
-          fence_after();
-        }
-        const float base = m_ref == -INFINITY ? 0.0f : m_ref;
-        const uint64_t c2 = pair(c, c), b2 = pair(-base, -base);
-        uint64_t add0 = pair(total, 0.0f), add1 = pair(0.0f, 0.0f);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          if (i >= used) break;
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 16; k += 2) {
-            float x, y, z, t;
-            unpair(fma2(pair(__uint_as_float(r[32 * i + 2 * k]), __uint_as_float(r[32 * i + 2 * k + 1])), c2, b2), x, y);
-            unpair(fma2(pair(__uint_as_float(r[32 * i + 2 * k + 2]), __uint_as_float(r[32 * i + 2 * k + 3])), c2, b2), z,
-                   t);
-            x = exp2_fast(x);
-            y = exp2_fast(y);
-            z = exp2_fast(z);
-            t = exp2_fast(t);
-            add0 = add2(add0, pair(x, y));
-            add1 = add2(add1, pair(z, t));
-            p[k] = pack_bf16(x, y);
-            p[k + 1] = pack_bf16(z, t);
-          }
-          tmem_st16(tp + 16 * i, p);
-        }
+        if (!done) powers(m_ref == -INFINITY ? 0.0f : m_ref, nullptr);
         {
           float x, y;
           unpair(add2(add0, add1), x, y);
-          total = x + y;
+          total += x + y;
         }
         tmem_st_wait();
         fence_before();
@@ -470,7 +497,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           }
       }
       __syncwarp();
-    } else if (warp == kFwdMma) {
+    } else if (warp >= kFwdMma && warp < kFwdMma + 2 / C::kPerWarp) {
       // -------------------------------------------------------------- products
       constexpr uint32_t kIdS = idesc(kM, kM), kIdO = idesc(kM, DP) | kMnB;
       const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
@@ -485,13 +512,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           }
         }
       } at = {0, 0};
-      uint32_t nq[2] = {0, 0}, qk[2] = {0, 0}, pv[2] = {0, 0}, opened[2] = {0, 0};
+      constexpr int kN = C::kPerWarp;
+      const int slot0 = kN == 1 ? warp - kFwdMma : 0;
+      uint32_t nq[kN] = {}, qk[kN] = {}, pv[kN] = {}, opened[kN] = {};
       // the step whose second product is still to come
-      bool pend[2] = {false, false}, first = false, pend_drop = false;
+      bool pend = false, first = false, pend_drop = false, pend_mine[kN] = {};
       Kept pend_kept = {};
-      auto wait_full = [&](const Ring& x) { mbar_wait(smem_u32(&h.kv_full[x.i]), x.phase, status); };
-      auto do_qk = [&](int s, uint32_t qi, uint32_t ki, uint32_t id) {
-        if (C::kOwnP && qk[s] > 0) mbar_wait(smem_u32(&h.s_free[s]), (qk[s] - 1) & 1u, status);
+      auto wait_full = [&](const Ring& x) {
+        mbar_wait(smem_u32(&h.kv_full[x.i]), x.phase, status);
+        __syncwarp();
+      };
+      // this warp's products have read a ring position, or never will
+      auto release = [&](uint32_t i, bool used) {
+        if (elect()) {
+          if (used) commit(smem_u32(&h.kv_empty[i]));
+          else mbar_arrive(smem_u32(&h.kv_empty[i]));
+        }
+        __syncwarp();
+      };
+      auto do_qk = [&](int i, uint32_t qi, uint32_t ki, uint32_t id) {
+        const int s = slot0 + i;
+        if (C::kOwnP && qk[i] > 0) mbar_wait(smem_u32(&h.s_free[s]), (qk[i] - 1) & 1u, status);
         __syncwarp();
         fence_after();
         if (elect()) {
@@ -503,53 +544,49 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           }
           commit(smem_u32(&h.s_full[s]));
         }
-        ++qk[s];
+        ++qk[i];
       };
-      auto do_pv = [&](int s, uint32_t vi) {
-        mbar_wait(smem_u32(&h.p_ready[s]), pv[s] & 1u, status);
+      auto do_pv = [&](int i, uint32_t vi) {
+        const int s = slot0 + i;
+        mbar_wait(smem_u32(&h.p_ready[s]), pv[i] & 1u, status);
         if (first) {
-          if (opened[s] > 0) mbar_wait(smem_u32(&h.o_free[s]), (opened[s] - 1) & 1u, status);
-          ++opened[s];
+          if (opened[i] > 0) mbar_wait(smem_u32(&h.o_free[s]), (opened[i] - 1) & 1u, status);
+          ++opened[i];
         }
         __syncwarp();
         fence_after();
         if (elect()) {
           const uint64_t vd = desc_mn(sr + vi * C::kTileBytes, kAtom);
-          const uint32_t td = tmem + C::kO + s * DP, tp = tmem + C::kP + s * C::kPStep;
-          mma_ts(td, tp, vd, kIdO, !first);
+          const uint32_t to = tmem + C::kO + s * DP, tp = tmem + C::kP + s * C::kPStep;
+          mma_ts(to, tp, vd, kIdO, !first);
           if (!pend_drop) {
 #pragma unroll
-            for (int k = 1; k < kM / 16; ++k) mma_ts(td, tp + 8 * k, vd + (uint32_t)(k * 128), kIdO, 1u);
+            for (int k = 1; k < kM / 16; ++k) mma_ts(to, tp + 8 * k, vd + (uint32_t)(k * 128), kIdO, 1u);
           } else {
             const int steps = 2 * pend_kept.used();
 #pragma unroll 1
-            for (int k = 1; k < steps; ++k) mma_ts(td, tp + 8 * k, vd + (uint32_t)(k * 128), kIdO, 1u);
+            for (int k = 1; k < steps; ++k) mma_ts(to, tp + 8 * k, vd + (uint32_t)(k * 128), kIdO, 1u);
           }
           commit(smem_u32(&h.pv_done[s]));
         }
-        ++pv[s];
+        ++pv[i];
       };
-      // the value tile at a ring position, its dropped keys' rows zeroed
+      // The value tile of the pending products, dropped keys' rows zeroed (by
+      // both warps where there are two: they write the same).
       auto take_v = [&](const Ring& x) {
         wait_full(x);
-        if (pend_drop && !pend_kept.all()) {
-          __syncwarp();
+        if (pend_drop && !pend_kept.all() && pend_mine[0])
           zero_dropped<C::kAtoms>(ring + (size_t)x.i * C::kTileBytes, pend_kept, pend_kept.used(), lane);
-        }
-      };
-      auto release = [&](uint32_t i) {
-        if (elect()) commit(smem_u32(&h.kv_empty[i]));
       };
       auto flush = [&]() {
-        if (!pend[0]) return;
+        if (!pend) return;
         take_v(at);
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          if (pend[s]) do_pv(s, at.i);
-          pend[s] = false;
-        }
-        release(at.i);
+        for (int i = 0; i < kN; ++i)
+          if (pend_mine[i]) do_pv(i, at.i);
+        release(at.i, pend_mine[0]);
         at.next();
+        pend = false;
       };
       for (uint32_t uk = 0;; ++uk) {
         const FwdUnit w = fwd_take(h, uk, lane, status);
@@ -561,12 +598,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           flush();
           continue;
         }
-        const bool two = w.r0 + a.tile_rows < w.rows;
-        uint32_t qi[2], qp[2];
+        bool mine[kN];
+        uint32_t qi[kN], qp[kN];
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-          qi[s] = nq[s] % C::kQBufs;
-          qp[s] = (nq[s] / C::kQBufs) & 1u;
+        for (int i = 0; i < kN; ++i) {
+          mine[i] = w.r0 + (slot0 + i) * a.tile_rows < w.rows;
+          qi[i] = nq[i] % C::kQBufs;
+          qp[i] = (nq[i] / C::kQBufs) & 1u;
         }
         uint8_t mb[4];
         mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
@@ -584,67 +622,64 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
             // probabilities of their own the scores can go first, if their
             // operands are there; the unit before waits for its last product.
             Ring kx = at;
-            if (pend[0]) kx.next();
-            const bool ahead =
-                C::kOwnP && pend[0] &&
-                __all_sync(0xffffffffu, mbar_try(smem_u32(&h.q_full[0][qi[0]]), qp[0]) &&
-                                            (!two || mbar_try(smem_u32(&h.q_full[1][qi[1]]), qp[1])) &&
-                                            mbar_try(smem_u32(&h.kv_full[kx.i]), kx.phase));
+            if (pend) kx.next();
+            const bool ahead = C::kOwnP && pend &&
+                               __all_sync(0xffffffffu, (!mine[0] || mbar_try(smem_u32(&h.q_full[slot0][qi[0]]), qp[0])) &&
+                                                           mbar_try(smem_u32(&h.kv_full[kx.i]), kx.phase));
             if (!ahead) {
               flush();
               wait_full(kx);
             }
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-              if (s == 0 || two) {
-                mbar_wait(smem_u32(&h.q_full[s][qi[s]]), qp[s], status);
-                do_qk(s, qi[s], kx.i, id);
+            for (int i = 0; i < kN; ++i)
+              if (mine[i]) {
+                mbar_wait(smem_u32(&h.q_full[slot0 + i][qi[i]]), qp[i], status);
+                do_qk(i, qi[i], kx.i, id);
               }
+            release(kx.i, mine[0]);
             if (ahead) flush();
-            release(kx.i);
             at = kx;
-            at.next();
           } else {
             // ring order: K of this step, V of the one before
             const uint32_t ki = at.i;
             wait_full(at);
             at.next();
-            const uint32_t vi = at.i;
-            if (C::kOwnP) do_qk(0, qi[0], ki, id);
-            take_v(at);
-            at.next();
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              if (s == 1 && !two) break;
-              if (C::kOwnP) {
-                if (s == 1) do_qk(1, qi[1], ki, id);
-                do_pv(s, vi);
-              } else {
-                do_pv(s, vi);
-                do_qk(s, qi[s], ki, id);
-              }
+            if (C::kOwnP) {
+              if (mine[0]) do_qk(0, qi[0], ki, id);
+              release(ki, mine[0]);
             }
-            release(vi);
-            release(ki);
+            take_v(at);
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (mine[i]) {
+                do_pv(i, at.i);
+                if (!C::kOwnP) do_qk(i, qi[i], ki, id);
+              }
+            release(at.i, mine[0]);
+            if (!C::kOwnP) release(ki, true);
           }
-          if (j == n - 1 && elect()) {
-            commit(smem_u32(&h.q_empty[0][qi[0]]));
-            if (two) commit(smem_u32(&h.q_empty[1][qi[1]]));
+          at.next();
+          if (j == n - 1) {
+#pragma unroll
+            for (int i = 0; i < kN; ++i)
+              if (mine[i] && elect()) commit(smem_u32(&h.q_empty[slot0 + i][qi[i]]));
+            __syncwarp();
           }
-          __syncwarp();
-          pend[0] = true;
-          pend[1] = two;
+          pend = true;
+#pragma unroll
+          for (int i = 0; i < kN; ++i) pend_mine[i] = mine[i];
           pend_drop = drop;
           if (drop) pend_kept = kept;
           first = j == 0;
         }
-        ++nq[0];
-        if (two) ++nq[1];
+#pragma unroll
+        for (int i = 0; i < kN; ++i) nq[i] += mine[i];
       }
       flush();
       // every product has completed before tensor memory is freed
-      for (int s = 0; s < 2; ++s)
-        if (pv[s] > 0) mbar_drain(smem_u32(&h.pv_done[s]), (pv[s] - 1) & 1u);
+#pragma unroll
+      for (int i = 0; i < kN; ++i)
+        if (pv[i] > 0) mbar_drain(smem_u32(&h.pv_done[slot0 + i]), (pv[i] - 1) & 1u);
       __syncwarp();
     }
   }
