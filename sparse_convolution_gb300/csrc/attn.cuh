@@ -20,7 +20,8 @@ enum AttnArray {
   kItemTile = 3,   // backward: first row tile
   kItemRows = 4,   // backward: ranges that the item's row tiles are cut into
   kItemKeys = 5,   // backward: ranges that its key tiles are cut into
-  kItemArrays = 6
+  kItemKeyTile = 6,  // backward: first key tile
+  kItemArrays = 7
 };
 struct AttnItems {
   const int32_t* ptr;

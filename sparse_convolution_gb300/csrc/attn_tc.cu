@@ -702,13 +702,16 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
 // this unit touches, one thread per value, so the order of every sum is fixed;
 // units that share keys (or rows) write partial sums that are added in order.
 // Warp roles:
-//   warps 0-3, 4-7  P and dS of the columns 0-63 / 64-127 of the tile; at the
-//                   end of a key tile dV / dK out of tensor memory
-//   warps 8-11      dQ out of tensor memory
-//   warp 12         TMA loads
-//   warp 13         issues the five products
-constexpr int kBwdThreads = 512;  // warps 14, 15 only give their registers away
-constexpr int kBwdLoad = 12, kBwdMma = 13;
+//   warps 0-15      P and dS, 32 of the tile's columns each (four warps per
+//                   scheduler hide the latencies of a step's phases; with two,
+//                   64 columns each, a step took more than twice the
+//                   products' time); at the end of a key tile dV and dK out of
+//                   tensor memory
+//   warps 16-19     dQ out of tensor memory
+//   warp 20         TMA loads
+//   warp 21         issues the five products
+constexpr int kBwdThreads = 768;  // warps 22, 23 only give their registers away
+constexpr int kBwdLoad = 20, kBwdMma = 21;
 
 template <int DP>
 struct Bwd {
@@ -720,7 +723,7 @@ struct Bwd {
   // tensor memory: P over the scores.  64-wide heads: dS and dQ in columns of
   // their own; 128-wide: dS over dP, and dQ over both once dK has read dS.
   static constexpr int kS = 0, kDp = 128, kDv = 256, kDk = kWide ? 384 : 320, kDq = kWide ? 128 : 384,
-                       kDs = kWide ? 128 : 448, kDsHalf = kWide ? 64 : 32;
+                       kDs = kWide ? 128 : 448, kDsStep = kWide ? 32 : 16;  // per 32 rows
   static constexpr size_t kKv = 0, kQ = (size_t)2 * kKvBufs * kTileBytes,
                           kSmDs = kQ + (size_t)2 * kStages * kTileBytes, kStats = kSmDs + 2 * kAtom,
                           kHead = kStats + (size_t)kStages * 1024, kSmem = kHead + 512;
@@ -730,18 +733,17 @@ struct alignas(128) BwdArgs {
   CUtensorMap tq, tdo, tk, tv;
   AttnItems items;
   const uint8_t* mask;
-  const float* stats;  // [row tile][key head][-lse2 of 128 rows, delta of 128 rows]
+  const float* stats;  // [row tile][key head][-lse2 of 128 rows, -delta of 128 rows]
   float* dq_sum;       // [key range][row tile][key head][DP / 4][128][4]
-  float *dk_part, *dv_part;  // [row range][nk][kv_heads][d]
+  float *dk_part, *dv_part;  // [row range][key tile][key head][DP / 4][128][4]
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* status;
-  int64_t nk;
-  int units, tiles, heads, kv_heads, shared, d, tile_rows;
+  int units, tiles, key_tiles, heads, kv_heads, shared, d, tile_rows;
   float c, scale;
 };
 
 struct BwdUnit {
-  int q0, rows, key0, keys, h, tile0, i0, i1, t0, t1, r_range, k_range, r_ranges, key_tiles;
+  int q0, rows, key0, keys, h, tile0, key_tile0, i0, i1, t0, t1, r_range, k_range, r_ranges, key_tiles;
 };
 __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   BwdUnit w;
@@ -752,6 +754,7 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   w.keys = a.items.k0(b + 1) - w.key0;
   w.tile0 = a.items.at(kItemTile, b);
   const int tiles = a.items.at(kItemTile, b + 1) - w.tile0;
+  w.key_tile0 = a.items.at(kItemKeyTile, b);
   w.key_tiles = (w.keys + kM - 1) / kM;
   w.r_ranges = a.items.at(kItemRows, b);
   const int k_ranges = a.items.at(kItemKeys, b);
@@ -837,12 +840,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
     }
     mbar_init(smem_u32(&h.s_full), 1);
     mbar_init(smem_u32(&h.dp_full), 1);
-    mbar_init(smem_u32(&h.p_ready), 8);
-    mbar_init(smem_u32(&h.ds_ready), 8);
+    mbar_init(smem_u32(&h.p_ready), 16);
+    mbar_init(smem_u32(&h.ds_ready), 16);
     mbar_init(smem_u32(&h.dq_full), 1);
     mbar_init(smem_u32(&h.dq_free), 4);
     mbar_init(smem_u32(&h.acc_full), 1);
-    mbar_init(smem_u32(&h.acc_free), 8);
+    mbar_init(smem_u32(&h.acc_free), 16);
     mbar_init_fence();
   }
   if (warp == kBwdMma) tmem_alloc(smem_u32(&h.tmem), 512);
@@ -852,132 +855,140 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
   const uint32_t tmem = h.tmem;
   const uint32_t q_tile = (uint32_t)C::kTileBytes;
 
-  // Registers: 512 threads at 128 are launched; 2 x 128 at 176, 128 at 88 and
-  // 128 at 72 are 65,536 in all.
-  if (warp < 8) {
-    setmaxnreg_inc<176>();
+  // Registers: 768 threads at 80 are launched, 61,440: 512 at 88 and 256 at 64.
+  if (warp < 16) {
+    setmaxnreg_inc<88>();
     // ---------------------------------------------------------------- P and dS
-    const int half = warp >> 2;
+    const int quarter = warp >> 2;
     const int key = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + C::kS + half * 64, tdp = tmem + lanes + C::kDp + half * 64,
-                   tds = tmem + lanes + C::kDs + half * C::kDsHalf;
-    unsigned char* const ds_row = sm + C::kSmDs + half * kAtom + key * 128;
+    const uint32_t ts = tmem + lanes + C::kS + quarter * 32, tdp = tmem + lanes + C::kDp + quarter * 32,
+                   tds = tmem + lanes + C::kDs + quarter * C::kDsStep;
+    unsigned char* const ds_row = sm + C::kSmDs + (quarter >> 1) * kAtom + key * 128;
+    const int chunk0 = (quarter & 1) * 4;
+    const uint32_t s_full = smem_u32(&h.s_full), dp_full = smem_u32(&h.dp_full), p_ready = smem_u32(&h.p_ready),
+                   ds_ready = smem_u32(&h.ds_ready), dq_full = smem_u32(&h.dq_full);
+    const uint64_t c2 = pair(a.c, a.c);
     BwdCursor cur;
     cur.start(a);
-    bool kept = false;
+    bool kept = false, whole = false;
+    uint32_t stage = 0, stage_phase = 0;
     while (cur.valid) {
       const BwdUnit& w = cur.w;
       if (cur.first()) {
         const int j = cur.t * kM + key;
         kept = j < w.keys && (!a.mask || __ldg(a.mask + w.key0 + j) != 0);
+        whole = __all_sync(0xffffffffu, kept);
       }
       const uint32_t par = cur.step & 1u;
-      const uint32_t stage = cur.step % C::kStages;
-      const float* st = reinterpret_cast<const float*>(sm + C::kStats + stage * 1024) + half * 64;
+      const float* st = reinterpret_cast<const float*>(sm + C::kStats + stage * 1024) + quarter * 32;
       // the row constants come with the stage's copies
-      mbar_wait(smem_u32(&h.q_full[stage]), (cur.step / C::kStages) & 1u, status);
-      mbar_wait(smem_u32(&h.s_full), par, status);
+      mbar_wait(smem_u32(&h.q_full[stage]), stage_phase, status);
+      if (++stage == (uint32_t)C::kStages) {
+        stage = 0;
+        stage_phase ^= 1u;
+      }
+      mbar_wait(s_full, par, status);
       __syncwarp();
       fence_after();
-      float p[64];
+      float p[32];
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        uint32_t r[32];
-        tmem_ld32(ts + 32 * cc, r);
+        uint32_t r[16], o[8];
+        tmem_ld16(ts + 16 * cc, r);
         tmem_ld_wait(r);
-        uint32_t o[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float4 nl = *reinterpret_cast<const float4*>(st + 32 * cc + k);
-          const float l[4] = {nl.x, nl.y, nl.z, nl.w};
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const float e = exp2_fast(fmaf(__uint_as_float(r[k + x]), a.c, l[x]));
-            p[32 * cc + k + x] = kept ? e : 0.0f;
-          }
-          o[k / 2] = pack_bf16(p[32 * cc + k], p[32 * cc + k + 1]);
-          o[k / 2 + 1] = pack_bf16(p[32 * cc + k + 2], p[32 * cc + k + 3]);
+        for (int k = 0; k < 16; k += 4) {
+          const float4 nl = *reinterpret_cast<const float4*>(st + 16 * cc + k);
+          float x, y, z, t;
+          unpair(fma2(pair(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), c2, pair(nl.x, nl.y)), x, y);
+          unpair(fma2(pair(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), c2, pair(nl.z, nl.w)), z, t);
+          p[16 * cc + k] = exp2_fast(x);
+          p[16 * cc + k + 1] = exp2_fast(y);
+          p[16 * cc + k + 2] = exp2_fast(z);
+          p[16 * cc + k + 3] = exp2_fast(t);
         }
-        tmem_st16(ts + 16 * cc, o);
+        if (!whole) {
+          // the scores of a dropped key, whose row reads as zeros, are 0, not -infinity
+#pragma unroll
+          for (int k = 0; k < 16; ++k) p[16 * cc + k] = kept ? p[16 * cc + k] : 0.0f;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) o[k] = pack_bf16(p[16 * cc + 2 * k], p[16 * cc + 2 * k + 1]);
+        tmem_st8(ts + 8 * cc, o);
       }
       tmem_st_wait();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&h.p_ready));
+      if (lane == 0) mbar_arrive(p_ready);
 
-      mbar_wait(smem_u32(&h.dp_full), par, status);
+      mbar_wait(dp_full, par, status);
       // dQ of the step before has read dS from shared memory
-      if (cur.step > 0) mbar_wait(smem_u32(&h.dq_full), (cur.step - 1) & 1u, status);
+      if (cur.step > 0) mbar_wait(dq_full, par ^ 1u, status);
       __syncwarp();
       fence_after();
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
-        uint32_t r[32];
-        tmem_ld32(tdp + 32 * cc, r);
+        uint32_t r[16], o[8];
+        tmem_ld16(tdp + 16 * cc, r);
         tmem_ld_wait(r);
-        uint32_t o[16];
 #pragma unroll
-        for (int k = 0; k < 32; k += 4) {
-          const float4 dl = *reinterpret_cast<const float4*>(st + 128 + 32 * cc + k);
-          const float l[4] = {dl.x, dl.y, dl.z, dl.w};
-          float d[4];
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            d[x] = p[32 * cc + k + x] * (__uint_as_float(r[k + x]) - l[x]);
-            if (!kept) d[x] = 0.0f;  // the row of a dropped value vector may hold anything
-          }
-          o[k / 2] = pack_bf16(d[0], d[1]);
-          o[k / 2 + 1] = pack_bf16(d[2], d[3]);
+        for (int k = 0; k < 16; k += 4) {
+          const float4 nd = *reinterpret_cast<const float4*>(st + 128 + 16 * cc + k);  // -delta
+          float x, y, z, t;
+          unpair(mul2(add2(pair(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), pair(nd.x, nd.y)),
+                      pair(p[16 * cc + k], p[16 * cc + k + 1])),
+                 x, y);
+          unpair(mul2(add2(pair(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), pair(nd.z, nd.w)),
+                      pair(p[16 * cc + k + 2], p[16 * cc + k + 3])),
+                 z, t);
+          o[k / 2] = pack_bf16(x, y);
+          o[k / 2 + 1] = pack_bf16(z, t);
         }
-        tmem_st16(tds + 16 * cc, o);
+        tmem_st8(tds + 8 * cc, o);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(ds_row + (((4 * cc + k) ^ (key & 7)) << 4)) =
+        for (int k = 0; k < 2; ++k)
+          *reinterpret_cast<uint4*>(ds_row + (((chunk0 + 2 * cc + k) ^ (key & 7)) << 4)) =
               make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
       tmem_st_wait();
       fence_proxy_async();
       fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&h.ds_ready));
+      if (lane == 0) mbar_arrive(ds_ready);
 
       if (cur.last()) {
-        // dV (first half) and dK (second) of the key tile
+        // dV (quarters 0, 1) and dK (2, 3) of the key tile, half of the columns each
+        const bool is_k = quarter >= 2;
+        const int col0 = (quarter & 1) * (DP / 2);
+        const float f = is_k ? a.scale : 1.0f;
+        const int j = cur.t * kM + key;
+        const int64_t row = (int64_t)(w.key0 + j) * a.kv_heads + w.h;
+        const bool live = j < w.keys, direct = w.r_ranges == 1;
+        __nv_bfloat16* const out = (is_k ? a.dk : a.dv) + row * a.d;
+        float* const part = (is_k ? a.dk_part : a.dv_part) +
+                            (((int64_t)w.r_range * a.key_tiles + w.key_tile0 + cur.t) * a.kv_heads + w.h) * (kM * DP) +
+                            key * 4;
         mbar_wait(smem_u32(&h.acc_full), cur.tile & 1u, status);
         __syncwarp();
         fence_after();
-        const uint32_t tacc = tmem + lanes + (half ? C::kDk : C::kDv);
-        const float f = half ? a.scale : 1.0f;
-        const int j = cur.t * kM + key;
-        const int64_t row = (int64_t)(w.key0 + j) * a.kv_heads + w.h;
-        const bool live = j < w.keys;
 #pragma unroll 1
-        for (int cc = 0; cc < DP; cc += 32) {
-          uint32_t r[32];
-          tmem_ld32(tacc + cc, r);
+        for (int cc = col0; cc < col0 + DP / 2; cc += 16) {
+          uint32_t r[16];
+          tmem_ld16(tmem + lanes + (is_k ? C::kDk : C::kDv) + cc, r);
           tmem_ld_wait(r);
 #pragma unroll
-          for (int k = 0; k < 32; ++k) r[k] = kept ? __float_as_uint(__uint_as_float(r[k]) * f) : 0u;
-          if (live && w.r_ranges == 1) {
-            __nv_bfloat16* out = (half ? a.dk : a.dv) + row * a.d + cc;
+          for (int k = 0; k < 16; ++k) r[k] = kept ? __float_as_uint(__uint_as_float(r[k]) * f) : 0u;
+          if (!direct) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
-              if (cc + k >= a.d) break;
-              uint4 v;
-              uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-              for (int x = 0; x < 4; ++x)
-                pv[x] = pack_bf16(__uint_as_float(r[k + 2 * x]), __uint_as_float(r[k + 2 * x + 1]));
-              *reinterpret_cast<uint4*>(out + k) = v;
-            }
+            for (int k = 0; k < 16; k += 4)
+              *reinterpret_cast<uint4*>(part + (cc + k) / 4 * (kM * 4)) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
           } else if (live) {
-            float* out = (half ? a.dk_part : a.dv_part) + ((int64_t)w.r_range * a.nk * a.kv_heads + row) * a.d + cc;
+            uint32_t v[8];
 #pragma unroll
-            for (int k = 0; k < 32; k += 4) {
-              if (cc + k >= a.d) break;
-              *reinterpret_cast<uint4*>(out + k) = make_uint4(r[k], r[k + 1], r[k + 2], r[k + 3]);
-            }
+            for (int k = 0; k < 8; ++k) v[k] = pack_bf16(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+            if (cc < a.d) *reinterpret_cast<uint4*>(out + cc) = make_uint4(v[0], v[1], v[2], v[3]);
+            if (cc + 8 < a.d) *reinterpret_cast<uint4*>(out + cc + 8) = make_uint4(v[4], v[5], v[6], v[7]);
           }
           __syncwarp();
         }
@@ -987,8 +998,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       }
       cur.next(a);
     }
-  } else if (warp < 12) {
-    setmaxnreg_dec<88>();
+  } else if (warp < 20) {
+    setmaxnreg_dec<64>();
     // ---------------------------------------------------------------- dQ
     const int row = (warp & 3) * 32 + lane;
     const uint32_t tdq = tmem + ((uint32_t)((warp & 3) * 32) << 16) + C::kDq;
@@ -1006,14 +1017,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       __syncwarp();
       fence_after();
 #pragma unroll 1
-      for (int cc = 0; cc < DP; cc += 32) {
-        uint32_t v[32];
-        tmem_ld32(tdq + cc, v);
+      for (int cc = 0; cc < DP; cc += 16) {
+        uint32_t v[16];
+        tmem_ld16(tdq + cc, v);
         tmem_ld_wait(v);
         if (only) {
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 8) {
+            for (int k = 0; k < 16; k += 8) {
               if (cc + k >= a.d) break;
               uint4 o;
               uint32_t* po = reinterpret_cast<uint32_t*>(&o);
@@ -1026,7 +1037,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
           __syncwarp();
         } else {
 #pragma unroll
-          for (int k = 0; k < 32; k += 4) {
+          for (int k = 0; k < 16; k += 4) {
             float* at = sum + (cc + k) / 4 * (kM * 4);
             if (cur.t == w.t0)
               *reinterpret_cast<uint4*>(at) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
@@ -1044,7 +1055,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       cur.next(a);
     }
   } else {
-    setmaxnreg_dec<72>();
+    setmaxnreg_dec<64>();
     if (warp == kBwdLoad) {
       // -------------------------------------------------------------- loads
       if (lane == 0) {
@@ -1114,12 +1125,18 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       auto issue_s = [&](const BwdCursor& x) {
         if (x.first()) {
           const uint32_t b = x.tile % C::kKvBufs;
-          uint8_t mb[4];
-          mask_bytes(a.mask, x.w.key0, x.w.keys, x.t, lane, mb);
-          const Kept kept = kept_keys(a.mask, x.w.keys, x.t, mb);
           mbar_wait(smem_u32(&h.kv_full[b]), (x.tile / C::kKvBufs) & 1u, status);
           __syncwarp();
-          if (!kept.all()) zero_dropped<C::kAtoms>(sm + C::kKv + 2 * b * C::kTileBytes, kept, 4, lane);
+          if (may_drop(a.mask, x.w.keys, x.t)) {
+            uint8_t mb[4];
+            mask_bytes(a.mask, x.w.key0, x.w.keys, x.t, lane, mb);
+            const Kept kept = kept_keys(a.mask, x.w.keys, x.t, mb);
+            if (!kept.all()) {
+              // keys meet dS in dQ; values meet dO in dP, which P = 0 must not turn into a NaN
+              zero_dropped<C::kAtoms>(sm + C::kKv + 2 * b * C::kTileBytes, kept, 4, lane);
+              zero_dropped<C::kAtoms>(sm + C::kKv + (2 * b + 1) * C::kTileBytes, kept, 4, lane);
+            }
+          }
         }
         const uint32_t s = x.step % C::kStages;
         mbar_wait(smem_u32(&h.q_full[s]), (x.step / C::kStages) & 1u, status);
@@ -1159,7 +1176,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
           const uint64_t od = desc_mn(q_at(cur) + q_tile, kAtom);
 #pragma unroll
           for (int k = 0; k < kM / 16; ++k)
-            mma_ts(tmem + C::kDv, tmem + C::kS + (k >> 2) * 64 + (k & 3) * 8, od + (uint32_t)(k * 128), kIdKv,
+            mma_ts(tmem + C::kDv, tmem + C::kS + (k >> 1) * 32 + (k & 1) * 8, od + (uint32_t)(k * 128), kIdKv,
                    !(cur.first() && k == 0));
         }
         __syncwarp();
@@ -1174,7 +1191,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
           const uint64_t qd = desc_mn(q_at(cur), kAtom);
 #pragma unroll
           for (int k = 0; k < kM / 16; ++k)
-            mma_ts(tmem + C::kDk, tmem + C::kDs + (k >> 2) * C::kDsHalf + (k & 3) * 8, qd + (uint32_t)(k * 128), kIdKv,
+            mma_ts(tmem + C::kDk, tmem + C::kDs + (k >> 1) * C::kDsStep + (k & 1) * 8, qd + (uint32_t)(k * 128), kIdKv,
                    !(cur.first() && k == 0));
           commit(smem_u32(&h.q_empty[cur.step % C::kStages]));
           if (cur.last()) commit(smem_u32(&h.acc_full));
@@ -1209,34 +1226,47 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
   }
 }
 
-// -lse in powers of 2 and delta = dout . out of every row tile's rows, one warp
-// per row; the places of rows that do not exist hold -infinity (a probability
-// of 0) and 0.
+// -lse in powers of 2 and -delta = -(dout . out) of every row tile's rows, 8
+// (16 for 128-wide heads) lanes per row; the places of rows that do not exist
+// hold -infinity (a probability of 0) and 0.
+template <int DP>
 __global__ void __launch_bounds__(256) k_attn_stats(const __grid_constant__ AttnItems items, HeadsView dout,
                                                     const __nv_bfloat16* __restrict__ out,
                                                     const float* __restrict__ lse, int heads, int kv_heads, int shared,
                                                     int tile_rows, int d, float* __restrict__ stats) {
-  const int lane = threadIdx.x & 31;
+  constexpr int kLanes = DP / 8, kRows = 256 / kLanes;  // rows of a block's turn
+  const int part = threadIdx.x % kLanes;
   const int tile = blockIdx.x / kv_heads, kh = blockIdx.x - tile * kv_heads;
   const int b = items.find(kItemTile, tile);
-  const int q0 = items.q0(b), rows = (items.q0(b + 1) - q0) * shared;
+  const int q0 = items.q0(b), rows = (items.q0(b + 1) - q0) * shared, tile0 = items.at(kItemTile, b);
   float* st = stats + (int64_t)blockIdx.x * 256;
-  for (int row = threadIdx.x >> 5; row < kM; row += 8) {
-    const int r = (tile - items.at(kItemTile, b)) * tile_rows + row;
-    float s = 0.0f, nl = -INFINITY;
-    if (row < tile_rows && r < rows) {
-      const int64_t tok = q0 + r / shared;
-      const int hd = kh * shared + r % shared;
-      const __nv_bfloat16* p = reinterpret_cast<const __nv_bfloat16*>(dout.p) + tok * dout.token + hd * dout.head;
-      const __nv_bfloat16* o = out + (tok * heads + hd) * d;
-      for (int c = lane; c < d; c += 32) s = fmaf(__bfloat162float(p[c]), __bfloat162float(o[c]), s);
 #pragma unroll
-      for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-      nl = -__ldg(lse + tok * heads + hd) * kLog2e;
+  for (int row = threadIdx.x / kLanes; row < kM; row += kRows) {
+    const int r = (tile - tile0) * tile_rows + row;
+    const bool live = row < tile_rows && r < rows;
+    float s = 0.0f, nl = -INFINITY;
+    if (live) {
+      const int t = shared == 1 ? r : r / shared;
+      const int64_t tok = q0 + t;
+      const int hd = kh * shared + r - t * shared;
+      if (part * 8 < d) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(dout.p) +
+                                                             tok * dout.token + hd * dout.head + part * 8));
+        const uint4 y = __ldg(reinterpret_cast<const uint4*>(out + (tok * heads + hd) * d + part * 8));
+        const uint32_t u[4] = {x.x, x.y, x.z, x.w}, v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          s = fmaf(__uint_as_float(u[k] << 16), __uint_as_float(v[k] << 16), s);
+          s = fmaf(__uint_as_float(u[k] & 0xffff0000u), __uint_as_float(v[k] & 0xffff0000u), s);
+        }
+      }
+      if (part == 0) nl = -__ldg(lse + tok * heads + hd) * kLog2e;
     }
-    if (lane == 0) {
+#pragma unroll
+    for (int k = kLanes / 2; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
+    if (part == 0) {
       st[row] = nl;
-      st[kM + row] = s;
+      st[kM + row] = -s;
     }
   }
 }
@@ -1282,21 +1312,26 @@ __global__ void __launch_bounds__(256) k_attn_dq_out(const __grid_constant__ Bwd
 }
 
 // dK and dV of the items whose rows were cut into ranges: the ranges' parts
-// added in order.  Items without rows get zeros.  One thread per 8 values.
+// added in order, one block per key tile and key head.  Items without rows get
+// zeros.
+template <int DP>
 __global__ void __launch_bounds__(256) k_attn_dkv_out(const __grid_constant__ BwdArgs a) {
-  const int per = a.d / 8;
-  const int64_t n = a.nk * a.kv_heads * per, all = a.nk * a.kv_heads * a.d;
-  for (int64_t e = (int64_t)blockIdx.x * 256 + threadIdx.x; e < 2 * n; e += (int64_t)gridDim.x * 256) {
-    const bool second = e >= n;
-    const int64_t i = second ? e - n : e;
-    const int b = a.items.find(kItemK, (int)(i / per / a.kv_heads));
-    const int ranges = a.items.at(kItemRows, b);
-    if (ranges == 1) continue;
-    const float* src = (second ? a.dv_part : a.dk_part) + i * 8;
+  const int tile = blockIdx.x / a.kv_heads, kh = blockIdx.x - tile * a.kv_heads;
+  const int b = a.items.find(kItemKeyTile, tile);
+  const int ranges = a.items.at(kItemRows, b);
+  if (ranges == 1) return;
+  const int key0 = a.items.k0(b), keys = a.items.k0(b + 1) - key0;
+  const int row = threadIdx.x & 127, j = (tile - a.items.at(kItemKeyTile, b)) * kM + row;
+  if (j >= keys) return;
+  const bool second = threadIdx.x >= 128;
+  const int64_t slab = (int64_t)a.key_tiles * a.kv_heads * (kM * DP);
+  const float* src = (second ? a.dv_part : a.dk_part) + (int64_t)blockIdx.x * (kM * DP) + row * 4;
+  __nv_bfloat16* out = (second ? a.dv : a.dk) + ((int64_t)(key0 + j) * a.kv_heads + kh) * a.d;
+  for (int cc = blockIdx.y * 8; cc < a.d; cc += 8 * gridDim.y) {
     float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
     for (int k = 0; k < ranges; ++k) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(src + k * all));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(src + k * all + 4));
+      const float4 x = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4) * (kM * 4)));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4 + 1) * (kM * 4)));
       s[0] += x.x;
       s[1] += x.y;
       s[2] += x.z;
@@ -1310,7 +1345,7 @@ __global__ void __launch_bounds__(256) k_attn_dkv_out(const __grid_constant__ Bw
     uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
 #pragma unroll
     for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x], s[2 * x + 1]);
-    *reinterpret_cast<uint4*>((second ? a.dv : a.dk) + i * 8) = v;
+    *reinterpret_cast<uint4*>(out + cc) = v;
   }
 }
 
@@ -1430,57 +1465,85 @@ fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   return a.splits > 1 ? attn_join(c, a.part, a.top, a.total, a.splits, s) : FVX_OK;
 }
 
-// Cuts the backward pass into units.  An item's work is (row tiles) x (key
-// tiles); it is cut along its longer side first, so that what the cut costs
-// (partial sums of the other side's gradients) stays small, into ranges of
-// about `target` tile pairs.
+// Cuts the backward pass into units of ranges of row tiles and key tiles of an
+// item and key head.  A cut of the rows costs partial sums of dK and dV for
+// every key tile, one of the keys a partial sum of dQ for every row tile, and a
+// unit pays for each of its key tiles (loads, results), so the cut that gives
+// an item its share of units is the one with the least of
+//   steps of the longest unit + its key tiles + the partial sums' traffic,
+// in cycles: a step's products and softmax about 1500, a key tile 3000 (with
+// partial sums 5000), 25 bytes a cycle and multiprocessor for the sums.
 struct BwdPlan {
-  std::vector<int32_t> more;  // units, tiles, row ranges, key ranges: items + 1 values each
-  int units = 0, tiles = 0, most_rows = 1, most_keys = 1;
+  std::vector<int32_t> more;  // units, row tiles, row ranges, key ranges, key tiles: items + 1 values each
+  int units = 0, tiles = 0, key_tiles = 0, most_rows = 1, most_keys = 1;
   bool dq_sums = false, dq_zeros = false, dkv_parts = false;
 };
 BwdPlan bwd_plan(const AttnCall& c, int sms) {
   const int n = c.items + 1;
   BwdPlan p;
-  p.more.assign((size_t)4 * n, 0);
-  int32_t *units = p.more.data(), *tiles = units + n, *rr = tiles + n, *kr = rr + n;
+  p.more.assign((size_t)5 * n, 0);
+  int32_t *units = p.more.data(), *tiles = units + n, *rr = tiles + n, *kr = rr + n, *key_tiles = kr + n;
   auto row_tiles = [&](int b) {
     return ((c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared + tile_rows(c) - 1) / tile_rows(c);
   };
-  auto key_tiles = [&](int b) { return (c.kv_offsets[b + 1] - c.kv_offsets[b] + kM - 1) / kM; };
-  int64_t work = 0;
-  for (int b = 0; b < c.items; ++b) work += row_tiles(b) * key_tiles(b) * c.kv_heads;
-  const int64_t target = std::max<int64_t>(1, (work + sms - 1) / sms);
-  int64_t u = 0, t = 0;
+  auto tiles_of_keys = [&](int b) { return (c.kv_offsets[b + 1] - c.kv_offsets[b] + kM - 1) / kM; };
+  int64_t work = 0, single = 0;
   for (int b = 0; b < c.items; ++b) {
-    const int64_t T = row_tiles(b), K = key_tiles(b);
+    const int64_t w = row_tiles(b) * tiles_of_keys(b);
+    work += w * c.kv_heads;
+    single += w > 0 ? c.kv_heads : 0;
+  }
+  auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  const double sum_cost = 128.0 * 4 * (c.d <= 64 ? 64 : 128) * c.kv_heads / (sms * 25.0);
+  // Units of 1 / sms of the work each, or a little more, so that they fit in
+  // one wave; with more items than that, one unit per item and key head.
+  for (double room : {1.0, 1.06, 1.15, 1.3, 1.6, 2.0}) {
+    const double target = std::max(1.0, room * (double)work / sms);
+    int64_t u = 0;
+    for (int b = 0; b < c.items; ++b) {
+      const int64_t T = row_tiles(b), K = tiles_of_keys(b);
+      rr[b] = kr[b] = 0;
+      if (T == 0 || K == 0) continue;
+      int64_t want = single >= sms ? 1 : std::max<int64_t>(1, (int64_t)((double)(T * K) / target + 0.999));
+      want = std::min(want, T * K);
+      double best = 1e300;
+      for (int64_t r = 1; r <= std::min(T, want); ++r) {
+        if (r > 24 && r < std::min(T, want)) continue;  // a long tail of small differences
+        const int64_t k = std::min(K, ceil_div(want, r));
+        const double cost = (double)(ceil_div(T, r) * ceil_div(K, k)) * 1500.0 + (double)ceil_div(K, k) * (r > 1 ? 5000.0 : 3000.0) +
+                            sum_cost * ((r > 1 ? 4.0 * r * K : 0.0) + (double)(k * T));
+        if (cost < best) {
+          best = cost;
+          rr[b] = (int32_t)r;
+          kr[b] = (int32_t)k;
+        }
+      }
+      u += (int64_t)rr[b] * kr[b] * c.kv_heads;
+    }
+    if (u <= sms || single >= sms) break;
+  }
+  int64_t u = 0, t = 0, kt = 0;
+  for (int b = 0; b < c.items; ++b) {
+    const int64_t T = row_tiles(b), K = tiles_of_keys(b);
     units[b] = (int32_t)u;
     tiles[b] = (int32_t)t;
+    key_tiles[b] = (int32_t)kt;
     t += T;
+    kt += K;
     if (T == 0 || K == 0) {
       p.dq_zeros |= T > 0;
       p.dkv_parts |= K > 0;
       continue;
     }
-    const int64_t want = std::max<int64_t>(1, (T * K + target / 2) / target);
-    int64_t r, k;
-    if (T >= K) {
-      r = std::min(want, T);
-      k = std::min(K, (want + r - 1) / r);
-    } else {
-      k = std::min(want, K);
-      r = std::min(T, (want + k - 1) / k);
-    }
-    rr[b] = (int32_t)r;
-    kr[b] = (int32_t)k;
-    u += r * k * c.kv_heads;
-    p.most_rows = std::max(p.most_rows, (int)r);
-    p.most_keys = std::max(p.most_keys, (int)k);
+    u += (int64_t)rr[b] * kr[b] * c.kv_heads;
+    p.most_rows = std::max(p.most_rows, rr[b]);
+    p.most_keys = std::max(p.most_keys, kr[b]);
     p.dq_sums |= K > 1;
-    p.dkv_parts |= r > 1;
+    p.dkv_parts |= rr[b] > 1;
   }
   units[c.items] = p.units = (int)u;
   tiles[c.items] = p.tiles = (int)t;
+  key_tiles[c.items] = p.key_tiles = (int)kt;
   return p;
 }
 
@@ -1503,9 +1566,9 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   a.dq = (__nv_bfloat16*)c.dq;
   a.dk = (__nv_bfloat16*)c.dk;
   a.dv = (__nv_bfloat16*)c.dv;
-  a.nk = c.nk;
   a.units = p.units;
   a.tiles = p.tiles;
+  a.key_tiles = p.key_tiles;
   a.heads = c.heads;
   a.kv_heads = c.kv_heads;
   a.shared = c.shared;
@@ -1526,14 +1589,14 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
     a.stats = stats;
     if (p.dq_sums && !(a.dq_sum = scr.get<float>(row_blocks * kM * DP * p.most_keys))) return FVX_ERR_ALLOC;
     if (p.most_rows > 1) {
-      const size_t values = (size_t)c.nk * c.kv_heads * c.d;
+      const size_t values = (size_t)p.key_tiles * c.kv_heads * kM * DP;
       a.dk_part = scr.get<float>(values * p.most_rows);
       a.dv_part = scr.get<float>(values * p.most_rows);
       if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
     }
     {
       LaunchScope ls("attn_stats", s);
-      k_attn_stats<<<(unsigned)row_blocks, 256, 0, s>>>(a.items, c.dout, (const __nv_bfloat16*)c.out, c.lse, c.heads,
+      k_attn_stats<DP><<<(unsigned)row_blocks, 256, 0, s>>>(a.items, c.dout, (const __nv_bfloat16*)c.out, c.lse, c.heads,
                                                         c.kv_heads, c.shared, a.tile_rows, c.d, stats);
       FVX_TRY(check_launch("attn_stats"));
     }
@@ -1548,9 +1611,8 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
     FVX_TRY(check_launch("attn_dq_out"));
   }
   if (p.dkv_parts) {
-    const int64_t n = 2 * c.nk * c.kv_heads * (c.d / 8);
     LaunchScope ls("attn_dkv_out", s);
-    k_attn_dkv_out<<<(unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8), 256, 0, s>>>(a);
+    k_attn_dkv_out<DP><<<dim3((unsigned)(p.key_tiles * c.kv_heads), DP / 32), 256, 0, s>>>(a);
     FVX_TRY(check_launch("attn_dkv_out"));
   }
   return FVX_OK;
