@@ -1017,14 +1017,21 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       __syncwarp();
       fence_after();
 #pragma unroll 1
-      for (int cc = 0; cc < DP; cc += 16) {
-        uint32_t v[16];
-        tmem_ld16(tdq + cc, v);
+      for (int cc = 0; cc < DP; cc += 32) {
+        uint32_t v[32];
+        tmem_ld32(tdq + cc, v);
         tmem_ld_wait(v);
+        if (cc + 32 >= DP) {
+          // read: what is written below keeps nobody waiting
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&h.dq_free));
+        }
+        float* const at = sum + cc / 4 * (kM * 4);
         if (only) {
           if (live) {
 #pragma unroll
-            for (int k = 0; k < 16; k += 8) {
+            for (int k = 0; k < 32; k += 8) {
               if (cc + k >= a.d) break;
               uint4 o;
               uint32_t* po = reinterpret_cast<uint32_t*>(&o);
@@ -1035,80 +1042,98 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
             }
           }
           __syncwarp();
+        } else if (cur.t == w.t0) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 4)
+            *reinterpret_cast<uint4*>(at + k / 4 * (kM * 4)) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
         } else {
 #pragma unroll
-          for (int k = 0; k < 16; k += 4) {
-            float* at = sum + (cc + k) / 4 * (kM * 4);
-            if (cur.t == w.t0)
-              *reinterpret_cast<uint4*>(at) = make_uint4(v[k], v[k + 1], v[k + 2], v[k + 3]);
-            else
-              asm volatile("red.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(at), "f"(__uint_as_float(v[k])),
-                           "f"(__uint_as_float(v[k + 1])), "f"(__uint_as_float(v[k + 2])),
-                           "f"(__uint_as_float(v[k + 3]))
-                           : "memory");
-          }
+          for (int k = 0; k < 32; k += 4) red4(at + k / 4 * (kM * 4), v + k);
         }
       }
-      fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&h.dq_free));
       cur.next(a);
     }
   } else {
     setmaxnreg_dec<64>();
     if (warp == kBwdLoad) {
       // -------------------------------------------------------------- loads
+      // Lane l issues copy l of a step: Q and dO (an atom each), the row constants.
       if (lane == 0) {
         tma_prefetch_map(&a.tq);
         tma_prefetch_map(&a.tdo);
         tma_prefetch_map(&a.tk);
         tma_prefetch_map(&a.tv);
-        BwdCursor cur;
-        cur.start(a);
-        while (cur.valid) {
-          const BwdUnit& w = cur.w;
-          if (cur.first()) {
-            const uint32_t b = cur.tile % C::kKvBufs, round = cur.tile / C::kKvBufs;
-            if (round > 0) mbar_wait(smem_u32(&h.kv_empty[b]), (round - 1) & 1u, status);
-            const uint32_t bar = smem_u32(&h.kv_full[b]), dst = sb + (uint32_t)C::kKv + 2 * b * q_tile;
-            mbar_expect_tx(bar, 2 * q_tile);
-#pragma unroll
-            for (int at = 0; at < C::kAtoms; ++at) {
-              tma_tile3d(dst + at * kAtom, &a.tk, 64 * at, w.h, w.key0 + cur.t * kM, bar);
-              tma_tile3d(dst + q_tile + at * kAtom, &a.tv, 64 * at, w.h, w.key0 + cur.t * kM, bar);
-            }
+      }
+      BwdCursor cur;
+      cur.start(a);
+      uint32_t s = 0, s_phase = 1, b = 0, b_phase = 1;  // the first round waits for nobody
+      const uint32_t bytes = (uint32_t)(2 * C::kAtoms * a.tile_rows * 128 + 1024);
+      const int tile_tokens = a.tile_rows / a.shared;
+      const int atom = lane % C::kAtoms, second = lane / C::kAtoms;
+      while (cur.valid) {
+        if (cur.first()) {
+          const uint32_t bar = smem_u32(&h.kv_full[b]);
+          if (cur.tile >= (uint32_t)C::kKvBufs) mbar_wait(smem_u32(&h.kv_empty[b]), b_phase, status);
+          __syncwarp();
+          if (lane == 0) mbar_expect_tx(bar, 2 * q_tile);
+          __syncwarp();
+          if (lane < 2 * C::kAtoms)
+            tma_tile3d(sb + (uint32_t)C::kKv + (2 * b + second) * q_tile + atom * kAtom, second ? &a.tv : &a.tk, 64 * atom,
+                       cur.w.h, cur.w.key0 + cur.t * kM, bar);
+          if (++b == (uint32_t)C::kKvBufs) {
+            b = 0;
+            b_phase ^= 1u;
           }
-          const uint32_t s = cur.step % C::kStages, round = cur.step / C::kStages;
-          if (round > 0) mbar_wait(smem_u32(&h.q_empty[s]), (round - 1) & 1u, status);
-          const uint32_t bar = smem_u32(&h.q_full[s]), dst = sb + (uint32_t)C::kQ + 2 * s * q_tile;
-          mbar_expect_tx(bar, (uint32_t)(2 * C::kAtoms * a.tile_rows * 128 + 1024));
-          const int tok = w.q0 + cur.i * (a.tile_rows / a.shared);
-#pragma unroll
-          for (int at = 0; at < C::kAtoms; ++at) {
-            tma_tile3d(dst + at * kAtom, &a.tq, 64 * at, w.h * a.shared, tok, bar);
-            tma_tile3d(dst + q_tile + at * kAtom, &a.tdo, 64 * at, w.h * a.shared, tok, bar);
-          }
-          bulk_load(sb + (uint32_t)C::kStats + s * 1024, a.stats + ((int64_t)(w.tile0 + cur.i) * a.kv_heads + w.h) * 256,
-                    1024, bar);
-          cur.next(a);
         }
-        // after a give-up, let the copies in flight land before the block exits
-        for (uint32_t k = 0; k < C::kStages && k < cur.step; ++k) {
-          const uint32_t x = cur.step - 1 - k;
-          mbar_drain(smem_u32(&h.q_full[x % C::kStages]), (x / C::kStages) & 1u);
+        const uint32_t bar = smem_u32(&h.q_full[s]);
+        if (cur.step >= (uint32_t)C::kStages) mbar_wait(smem_u32(&h.q_empty[s]), s_phase, status);
+        __syncwarp();
+        if (lane == 0) mbar_expect_tx(bar, bytes);
+        __syncwarp();
+        if (lane < 2 * C::kAtoms)
+          tma_tile3d(sb + (uint32_t)C::kQ + (2 * s + second) * q_tile + atom * kAtom, second ? &a.tdo : &a.tq, 64 * atom,
+                     cur.w.h * a.shared, cur.w.q0 + cur.i * tile_tokens, bar);
+        else if (lane == 2 * C::kAtoms)
+          bulk_load(sb + (uint32_t)C::kStats + s * 1024,
+                    a.stats + ((int64_t)(cur.w.tile0 + cur.i) * a.kv_heads + cur.w.h) * 256, 1024, bar);
+        if (++s == (uint32_t)C::kStages) {
+          s = 0;
+          s_phase ^= 1u;
         }
-        for (uint32_t k = 0; k < C::kKvBufs && k < cur.tile; ++k) {
-          const uint32_t x = cur.tile - 1 - k;
-          mbar_drain(smem_u32(&h.kv_full[x % C::kKvBufs]), (x / C::kKvBufs) & 1u);
-        }
+        cur.next(a);
+      }
+      // after a give-up, let the copies in flight land before the block exits
+      for (uint32_t k = 0; k < C::kStages && k < cur.step; ++k) {
+        const uint32_t x = cur.step - 1 - k;
+        mbar_drain(smem_u32(&h.q_full[x % C::kStages]), (x / C::kStages) & 1u);
+      }
+      for (uint32_t k = 0; k < C::kKvBufs && k < cur.tile; ++k) {
+        const uint32_t x = cur.tile - 1 - k;
+        mbar_drain(smem_u32(&h.kv_full[x % C::kKvBufs]), (x / C::kKvBufs) & 1u);
       }
       __syncwarp();
     } else if (warp == kBwdMma) {
       // -------------------------------------------------------------- products
       constexpr uint32_t kIdS = idesc(kM, kM), kIdKv = idesc(kM, DP) | kMnB, kIdQ = idesc(kM, DP) | kMnA | kMnB;
       const uint32_t s_full = smem_u32(&h.s_full), dp_full = smem_u32(&h.dp_full);
-      auto k_at = [&](const BwdCursor& x) { return sb + (uint32_t)C::kKv + 2 * (x.tile % C::kKvBufs) * q_tile; };
-      auto q_at = [&](const BwdCursor& x) { return sb + (uint32_t)C::kQ + 2 * (x.step % C::kStages) * q_tile; };
+      // Where a step's operands are: running indices, as every instruction here
+      // is in the way of the tensor cores.
+      struct Place {
+        uint32_t q, q_phase, kv, kv_phase;
+      };
+      auto after = [](Place x, bool next_tile) {
+        if (++x.q == (uint32_t)C::kStages) {
+          x.q = 0;
+          x.q_phase ^= 1u;
+        }
+        if (next_tile && ++x.kv == (uint32_t)C::kKvBufs) {
+          x.kv = 0;
+          x.kv_phase ^= 1u;
+        }
+        return x;
+      };
+      auto k_at = [&](const Place& x) { return sb + (uint32_t)C::kKv + 2 * x.kv * q_tile; };
+      auto q_at = [&](const Place& x) { return sb + (uint32_t)C::kQ + 2 * x.q * q_tile; };
       // 128 x 128 scores: K-major operands, 16 values of the head per product
       auto scores = [&](uint32_t d, uint32_t ka, uint32_t qa, uint32_t bar) {
         if (elect()) {
@@ -1122,10 +1147,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
         }
         __syncwarp();
       };
-      auto issue_s = [&](const BwdCursor& x) {
+      // waits for a step's operands and zeros what takes no part
+      auto ready = [&](const BwdCursor& x, const Place& at) {
         if (x.first()) {
-          const uint32_t b = x.tile % C::kKvBufs;
-          mbar_wait(smem_u32(&h.kv_full[b]), (x.tile / C::kKvBufs) & 1u, status);
+          mbar_wait(smem_u32(&h.kv_full[at.kv]), at.kv_phase, status);
           __syncwarp();
           if (may_drop(a.mask, x.w.keys, x.t)) {
             uint8_t mb[4];
@@ -1133,13 +1158,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
             const Kept kept = kept_keys(a.mask, x.w.keys, x.t, mb);
             if (!kept.all()) {
               // keys meet dS in dQ; values meet dO in dP, which P = 0 must not turn into a NaN
-              zero_dropped<C::kAtoms>(sm + C::kKv + 2 * b * C::kTileBytes, kept, 4, lane);
-              zero_dropped<C::kAtoms>(sm + C::kKv + (2 * b + 1) * C::kTileBytes, kept, 4, lane);
+              zero_dropped<C::kAtoms>(sm + C::kKv + 2 * at.kv * C::kTileBytes, kept, 4, lane);
+              zero_dropped<C::kAtoms>(sm + C::kKv + (2 * at.kv + 1) * C::kTileBytes, kept, 4, lane);
             }
           }
         }
-        const uint32_t s = x.step % C::kStages;
-        mbar_wait(smem_u32(&h.q_full[s]), (x.step / C::kStages) & 1u, status);
+        mbar_wait(smem_u32(&h.q_full[at.q]), at.q_phase, status);
         __syncwarp();
         const int left = x.w.rows - x.i * a.tile_rows;
         if (left < a.tile_rows) {
@@ -1148,73 +1172,93 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
 #pragma unroll
           for (int i = 0; i < 4; ++i)
             live.w[i] = left >= 32 * (i + 1) ? 0xffffffffu : left <= 32 * i ? 0u : (1u << (left - 32 * i)) - 1u;
-          zero_dropped<C::kAtoms>(sm + C::kQ + 2 * s * C::kTileBytes, live, 4, lane);
-          zero_dropped<C::kAtoms>(sm + C::kQ + (2 * s + 1) * C::kTileBytes, live, 4, lane);
+          zero_dropped<C::kAtoms>(sm + C::kQ + 2 * at.q * C::kTileBytes, live, 4, lane);
+          zero_dropped<C::kAtoms>(sm + C::kQ + (2 * at.q + 1) * C::kTileBytes, live, 4, lane);
         }
-        fence_after();
-        scores(C::kS, k_at(x), q_at(x), s_full);
       };
-      auto issue_dp = [&](const BwdCursor& x) { scores(C::kDp, k_at(x) + q_tile, q_at(x) + q_tile, dp_full); };
+      auto issue_s = [&](const Place& at) { scores(C::kS, k_at(at), q_at(at), s_full); };
+      auto issue_dp = [&](const Place& at) { scores(C::kDp, k_at(at) + q_tile, q_at(at) + q_tile, dp_full); };
 
-      BwdCursor cur, nx;
-      cur.start(a);
-      if (cur.valid) {
-        issue_s(cur);
-        issue_dp(cur);
+      BwdCursor nx;  // the step after the current one
+      nx.start(a);
+      bool valid = nx.valid;
+      Place here = {0, 0, 0, 0}, there = here;
+      if (valid) {
+        ready(nx, here);
+        fence_after();
+        issue_s(here);
+        issue_dp(here);
       }
-      nx = cur;
-      while (cur.valid) {
+      uint32_t par = 0, tile = 0;
+      bool begun = false;
+      while (valid) {
+        const bool fresh = nx.first(), last = nx.last();
         nx.next(a);
-        const uint32_t par = cur.step & 1u;
-        const bool defer = C::kKvBufs == 1 && nx.valid && nx.first();  // its keys replace this tile's
-        // ---- dV += P^T dO
+        there = after(here, last);
+        const bool more = nx.valid, defer = C::kKvBufs == 1 && last;  // its keys replace this tile's
+        // the next step's operands while this one's probabilities are made
+        if (more && !defer) ready(nx, there);
+        // ---- dV += P^T dO, and the next scores over the probabilities
         mbar_wait(smem_u32(&h.p_ready), par, status);
-        if (cur.first() && cur.tile > 0) mbar_wait(smem_u32(&h.acc_free), (cur.tile - 1) & 1u, status);
+        if (fresh && tile > 0) mbar_wait(smem_u32(&h.acc_free), (tile - 1) & 1u, status);
         __syncwarp();
         fence_after();
         if (elect()) {
-          const uint64_t od = desc_mn(q_at(cur) + q_tile, kAtom);
+          const uint64_t od = desc_mn(q_at(here) + q_tile, kAtom);
 #pragma unroll
           for (int k = 0; k < kM / 16; ++k)
             mma_ts(tmem + C::kDv, tmem + C::kS + (k >> 1) * 32 + (k & 1) * 8, od + (uint32_t)(k * 128), kIdKv,
-                   !(cur.first() && k == 0));
+                   !(fresh && k == 0));
         }
         __syncwarp();
-        if (nx.valid && !defer) issue_s(nx);
+        if (more && !defer) issue_s(there);
         mbar_wait(smem_u32(&h.ds_ready), par, status);
-        if (!C::kWide && cur.step > 0) mbar_wait(smem_u32(&h.dq_free), (cur.step - 1) & 1u, status);
         __syncwarp();
         fence_after();
-        if (!C::kWide && nx.valid) issue_dp(nx);
+        if (!C::kWide && more) issue_dp(there);
+        // ---- dK += dS^T Q
         if (elect()) {
-          // ---- dK += dS^T Q
-          const uint64_t qd = desc_mn(q_at(cur), kAtom);
+          const uint64_t qd = desc_mn(q_at(here), kAtom);
 #pragma unroll
           for (int k = 0; k < kM / 16; ++k)
             mma_ts(tmem + C::kDk, tmem + C::kDs + (k >> 1) * C::kDsStep + (k & 1) * 8, qd + (uint32_t)(k * 128), kIdKv,
-                   !(cur.first() && k == 0));
-          commit(smem_u32(&h.q_empty[cur.step % C::kStages]));
-          if (cur.last()) commit(smem_u32(&h.acc_full));
-          // ---- dQ = dS K
-          const uint64_t sd = desc_mn(sb + (uint32_t)C::kSmDs, kAtom), kd = desc_mn(k_at(cur), kAtom);
+                   !(fresh && k == 0));
+          commit(smem_u32(&h.q_empty[here.q]));
+          if (last) commit(smem_u32(&h.acc_full));
+        }
+        __syncwarp();
+        // ---- dQ = dS K
+        if (!C::kWide && begun) mbar_wait(smem_u32(&h.dq_free), par ^ 1u, status);
+        __syncwarp();
+        fence_after();
+        if (elect()) {
+          const uint64_t sd = desc_mn(sb + (uint32_t)C::kSmDs, kAtom), kd = desc_mn(k_at(here), kAtom);
 #pragma unroll
           for (int k = 0; k < kM / 16; ++k)
             mma_ss(tmem + C::kDq, sd + (uint32_t)(k * 128), kd + (uint32_t)(k * 128), kIdQ, k > 0);
           commit(smem_u32(&h.dq_full));
-          if (cur.last()) commit(smem_u32(&h.kv_empty[cur.tile % C::kKvBufs]));
+          if (last) commit(smem_u32(&h.kv_empty[here.kv]));
         }
         __syncwarp();
-        if (nx.valid && defer) issue_s(nx);
-        if (C::kWide && nx.valid) {
+        if (more && defer) {
+          ready(nx, there);
+          fence_after();
+          issue_s(there);
+        }
+        if (C::kWide && more) {
           mbar_wait(smem_u32(&h.dq_free), par, status);
           __syncwarp();
           fence_after();
-          issue_dp(nx);
+          issue_dp(there);
         }
-        cur = nx;
+        here = there;
+        par ^= 1u;
+        tile += last;
+        begun = true;
+        valid = more;
       }
       // every product has completed before tensor memory is freed
-      if (cur.step > 0) mbar_drain(smem_u32(&h.dq_full), (cur.step - 1) & 1u);
+      if (begun) mbar_drain(smem_u32(&h.dq_full), par ^ 1u);
       __syncwarp();
     }
   }
