@@ -414,34 +414,24 @@ def _dtype_code(t, who):
 
 
 def _on_device(who, *tensors):
-    """Every tensor on the current CUDA device (the library launches there)."""
+    """Every tensor on the current CUDA device (the library launches there);
+    returns the current stream's handle."""
     import torch
 
     dev = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.device.index != dev):
+        if t is not None and t.get_device() != dev:
             _refuse(f"{who}: every tensor must be on the current CUDA device {dev}, got {t.device}")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-class _On:
-    """Makes `stream` (default: the current one) current, so that what a call
-    allocates belongs to the stream its kernels run on."""
+def _on_stream(stream, call, *args, **kw):
+    """call(*args, **kw) with `stream` current, so that what it allocates
+    belongs to the stream its kernels run on."""
+    import torch
 
-    def __init__(self, stream):
-        import torch
-
-        self._guard = torch.cuda.stream(stream) if stream is not None else None
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *e):
-        if self._guard is not None:
-            self._guard.__exit__(*e)
+    with torch.cuda.stream(stream):
+        return call(*args, **kw)
 
 
 def _rows(t, who, name):
@@ -503,14 +493,15 @@ class Checkpoint8:
     @classmethod
     def pack(cls, x, group=64, stream=None) -> "Checkpoint8":
         """x: float32 or bfloat16 [rows, channels]."""
+        if stream is not None:
+            return _on_stream(stream, cls.pack, x, group)
         who = "Checkpoint8.pack"
         dt = _dtype_code(x, who)
-        _on_device(who, x)
-        with _On(stream) as s:
-            x, ld = _rows(x, who, "x")
-            ck = cls._empty(x, group, who)
-            _check(load().fvx_checkpoint_pack(dt, x.data_ptr(), ld, x.shape[0], x.shape[1], group,
-                                              ck.codes.data_ptr(), ck.steps.data_ptr(), s))
+        s = _on_device(who, x)
+        x, ld = _rows(x, who, "x")
+        ck = cls._empty(x, group, who)
+        n, c = ck.codes.shape
+        _check(load().fvx_checkpoint_pack(dt, x.data_ptr(), ld, n, c, group, ck.codes.data_ptr(), ck.steps.data_ptr(), s))
         return ck
 
     @property
@@ -521,37 +512,42 @@ class Checkpoint8:
     def nbytes(self):
         return self.codes.numel() + 4 * self.steps.numel()
 
-    def _restore(self, who, mean, rstd, weight, bias, dtype, out, stream):
+    def _restore(self, who, mean, rstd, weight, bias, dtype, out):
         import torch
 
-        n, c = self.codes.shape
-        if not self.codes.is_contiguous() or not self.steps.is_contiguous():
+        codes, steps = self.codes, self.steps
+        n, c = codes.shape
+        if not codes.is_contiguous() or not steps.is_contiguous():
             _refuse(f"{who}: codes and steps must be contiguous")
-        with _On(stream) as s:
-            if out is None:
-                out = torch.empty((n, c), dtype=dtype or self.dtype, device=self.codes.device)
-            dt = _dtype_code(out, who)
+        if out is None:
+            out = torch.empty((n, c), dtype=dtype or self.dtype, device=codes.device)
+            ld = c
+        else:
             if tuple(out.shape) != (n, c) or (c > 1 and out.stride(1) != 1) or (n > 1 and out.stride(0) < c):
                 _refuse(f"{who}: out must be [{n}, {c}] with dense channels, got {tuple(out.shape)}")
-            _on_device(who, self.codes, self.steps, mean, rstd, weight, bias, out)
-            _check(load().fvx_checkpoint_restore(dt, self.group, self.codes.data_ptr(), self.steps.data_ptr(), n, c,
-                                                 _at(mean), _at(rstd), _at(weight), _at(bias), out.data_ptr(),
-                                                 out.stride(0) if n > 1 else c, s))
+            ld = out.stride(0) if n > 1 else c
+        dt = _dtype_code(out, who)
+        s = _on_device(who, codes, steps, mean, rstd, weight, bias, out)
+        _check(load().fvx_checkpoint_restore(dt, self.group, codes.data_ptr(), steps.data_ptr(), n, c, _at(mean),
+                                             _at(rstd), _at(weight), _at(bias), out.data_ptr(), ld, s))
         return out
 
     def restore(self, dtype=None, out=None, stream=None):
         """The values held, in the activations' type or ``dtype``."""
-        return self._restore("Checkpoint8.restore", None, None, None, None, dtype, out, stream)
+        if stream is not None:
+            return _on_stream(stream, self.restore, dtype, out)
+        return self._restore("Checkpoint8.restore", None, None, None, None, dtype, out)
 
     def layer_norm(self, mean, rstd, weight=None, bias=None, dtype=None, out=None, stream=None):
         """Layer norm of the values held, with the forward pass's statistics:
         the input of what followed the norm, for its backward pass."""
+        if stream is not None:
+            return _on_stream(stream, self.layer_norm, mean, rstd, weight, bias, dtype, out)
         who = "Checkpoint8.layer_norm"
         n, c = self.codes.shape
-        with _On(stream):
-            mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
-            weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
-        return self._restore(who, mean, rstd, weight, bias, dtype, out, stream)
+        mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
+        weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
+        return self._restore(who, mean, rstd, weight, bias, dtype, out)
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint_group=None, stream=None):
@@ -561,21 +557,27 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint_group=None, strea
     Checkpoint8, written by the same pass."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, layer_norm, x, weight, bias, eps, checkpoint_group)
     who = "layer_norm"
     dt = _dtype_code(x, who)
-    _on_device(who, x, weight, bias)
-    with _On(stream) as s:
-        x, ld = _rows(x, who, "x")
-        n, c = x.shape
-        weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
-        y = torch.empty((n, c), dtype=x.dtype, device=x.device)
-        mean = torch.empty((n,), dtype=torch.float32, device=x.device)
-        rstd = torch.empty((n,), dtype=torch.float32, device=x.device)
-        ck = Checkpoint8._empty(x, checkpoint_group, who) if checkpoint_group else None
-        _check(load().fvx_layer_norm(dt, x.data_ptr(), ld, n, c, _at(weight), _at(bias), float(eps), y.data_ptr(), c,
-                                     mean.data_ptr(), rstd.data_ptr(), checkpoint_group or 0,
-                                     ck.codes.data_ptr() if ck else None, ck.steps.data_ptr() if ck else None, s))
-    return (y, mean, rstd, ck) if ck else (y, mean, rstd)
+    s = _on_device(who, x, weight, bias)
+    x, ld = _rows(x, who, "x")
+    n, c = x.shape
+    weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
+    dev = x.device
+    y = torch.empty((n, c), dtype=x.dtype, device=dev)
+    mean = torch.empty((n,), dtype=torch.float32, device=dev)
+    rstd = torch.empty((n,), dtype=torch.float32, device=dev)
+    if not checkpoint_group:
+        _check(load().fvx_layer_norm(dt, x.data_ptr(), ld, n, c, _at(weight), _at(bias), eps, y.data_ptr(), c,
+                                     mean.data_ptr(), rstd.data_ptr(), 0, None, None, s))
+        return y, mean, rstd
+    ck = Checkpoint8._empty(x, checkpoint_group, who)
+    _check(load().fvx_layer_norm(dt, x.data_ptr(), ld, n, c, _at(weight), _at(bias), eps, y.data_ptr(), c,
+                                 mean.data_ptr(), rstd.data_ptr(), checkpoint_group, ck.codes.data_ptr(),
+                                 ck.steps.data_ptr(), s))
+    return y, mean, rstd, ck
 
 
 def layer_norm_backward(dy, x, mean, rstd, weight=None, stream=None):
@@ -584,45 +586,57 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, stream=None):
     Checkpoint8 (then x is read from its 8-bit codes)."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, layer_norm_backward, dy, x, mean, rstd, weight)
     who = "layer_norm_backward"
     dt = _dtype_code(dy, who)
     ck = x if isinstance(x, Checkpoint8) else None
-    if tuple(x.shape) != tuple(dy.shape):
+    if x.shape != dy.shape:
         _refuse(f"{who}: x is {tuple(x.shape)}, dy {tuple(dy.shape)}")
     if x.dtype != dy.dtype:
         _refuse(f"{who}: x is {x.dtype}, dy {dy.dtype}")
-    _on_device(who, dy, mean, rstd, weight, *((ck.codes, ck.steps) if ck else (x,)))
-    with _On(stream) as s:
-        dy, lddy = _rows(dy, who, "dy")
-        n, c = dy.shape
-        if ck:
-            if not ck.codes.is_contiguous() or not ck.steps.is_contiguous():
-                _refuse(f"{who}: the checkpoint's codes and steps must be contiguous")
-            source = (None, c, ck.group, ck.codes.data_ptr(), ck.steps.data_ptr())
-        else:
-            x, ldx = _rows(x, who, "x")
-            source = (x.data_ptr(), ldx, 0, None, None)
-        mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
-        weight = _channel_vector(weight, c, who, "weight")
-        dx = torch.empty((n, c), dtype=dy.dtype, device=dy.device)
-        sums = torch.empty((2, c), dtype=torch.float32, device=dy.device)
-        dw, db = sums[0], sums[1]
-        _check(load().fvx_layer_norm_backward(dt, dy.data_ptr(), lddy, *source, n, c, _at(weight), mean.data_ptr(),
-                                              rstd.data_ptr(), dx.data_ptr(), c, dw.data_ptr(), db.data_ptr(), s))
+    dy, lddy = _rows(dy, who, "dy")
+    n, c = dy.shape
+    if ck:
+        s = _on_device(who, dy, mean, rstd, weight, ck.codes, ck.steps)
+        if not ck.codes.is_contiguous() or not ck.steps.is_contiguous():
+            _refuse(f"{who}: the checkpoint's codes and steps must be contiguous")
+        source = (None, c, ck.group, ck.codes.data_ptr(), ck.steps.data_ptr())
+    else:
+        s = _on_device(who, dy, mean, rstd, weight, x)
+        x, ldx = _rows(x, who, "x")
+        source = (x.data_ptr(), ldx, 0, None, None)
+    mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
+    weight = _channel_vector(weight, c, who, "weight")
+    dev = dy.device
+    dx = torch.empty((n, c), dtype=dy.dtype, device=dev)
+    dw = torch.empty((c,), dtype=torch.float32, device=dev)
+    db = torch.empty((c,), dtype=torch.float32, device=dev)
+    _check(load().fvx_layer_norm_backward(dt, dy.data_ptr(), lddy, *source, n, c, _at(weight), mean.data_ptr(),
+                                          rstd.data_ptr(), dx.data_ptr(), c, dw.data_ptr(), db.data_ptr(), s))
     return dx, dw, db
 
 
 def _heads(t, who, name):
     """t [tokens, heads, d] with a dense last dimension: a copy where it is
-    not, and where a stride is no multiple of 16 bytes in bf16 (the tensor
-    cores' copies need that)."""
+    not, and where a bf16 tensor's base or a stride is no multiple of 16 bytes
+    (the tensor cores' copies need that)."""
     if t.dim() != 3:
         _refuse(f"{who}: {name} must be [tokens, heads, size], got {tuple(t.shape)}")
+    if t.is_contiguous():
+        return t if t.dtype.itemsize == 4 or not t.data_ptr() & 15 else t.clone()
     st = t.stride()
-    if (t.shape[2] > 1 and st[2] != 1) or (not t.is_contiguous() and t.dtype.itemsize == 2 and
+    if (t.shape[2] > 1 and st[2] != 1) or (t.dtype.itemsize == 2 and
                                            ((st[0] | st[1] | (t.data_ptr() >> 1)) & 7 or not st[0] or not st[1])):
         t = t.contiguous()
     return t
+
+
+def _host_offsets(o):
+    try:
+        return (ctypes.c_int64 * len(o))(*o)
+    except TypeError:  # a tensor's or an array's elements
+        return (ctypes.c_int64 * len(o))(*map(int, o))
 
 
 def _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask):
@@ -644,8 +658,7 @@ def _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask):
         if key_mask.dtype not in (torch.bool, torch.uint8) or tuple(key_mask.shape) != (nk,):
             _refuse(f"{who}: key_mask must be bool [{nk}], got {key_mask.dtype} {tuple(key_mask.shape)}")
         key_mask = key_mask.contiguous()
-    offs = ctypes.c_int64 * (B + 1)
-    return q, k, v, key_mask, offs(*map(int, q_offsets)), offs(*map(int, kv_offsets)), B
+    return q, k, v, key_mask, _host_offsets(q_offsets), _host_offsets(kv_offsets), B
 
 
 def cross_attention(q, k, v, q_offsets, kv_offsets, key_mask=None, scale=None, stream=None):
@@ -658,17 +671,18 @@ def cross_attention(q, k, v, q_offsets, kv_offsets, key_mask=None, scale=None, s
     a row without kept keys gets zeros and -inf."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, cross_attention, q, k, v, q_offsets, kv_offsets, key_mask, scale)
     who = "cross_attention"
     dt = _dtype_code(q, who)
-    _on_device(who, q, k, v, key_mask)
-    with _On(stream) as s:
-        q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
-        nq, heads, d = q.shape
-        out = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
-        lse = torch.empty((nq, heads), dtype=torch.float32, device=q.device)
-        _check(load().fvx_cross_attention(dt, *_strided(q), *_strided(k), *_strided(v), qo, ko, B, heads, k.shape[1],
-                                          d, _at(key_mask), d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                          lse.data_ptr(), s))
+    s = _on_device(who, q, k, v, key_mask)
+    q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
+    nq, heads, d = q.shape
+    out = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
+    lse = torch.empty((nq, heads), dtype=torch.float32, device=q.device)
+    _check(load().fvx_cross_attention(dt, *_strided(q), *_strided(k), *_strided(v), qo, ko, B, heads, k.shape[1], d,
+                                      _at(key_mask), d ** -0.5 if scale is None else scale, out.data_ptr(),
+                                      lse.data_ptr(), s))
     return out, lse
 
 
@@ -678,30 +692,33 @@ def cross_attention_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, key
     query heads that read it."""
     import torch
 
+    if stream is not None:
+        return _on_stream(stream, cross_attention_backward, dout, q, k, v, out, lse, q_offsets, kv_offsets, key_mask,
+                          scale)
     who = "cross_attention_backward"
     dt = _dtype_code(q, who)
-    _on_device(who, dout, q, k, v, out, lse, key_mask)
-    with _On(stream) as s:
-        q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
-        nq, heads, d = q.shape
-        for name, t in (("dout", dout), ("out", out)):
-            if t.dtype != q.dtype or t.shape != q.shape:
-                _refuse(f"{who}: {name} must be {q.dtype} {tuple(q.shape)}, got {t.dtype} {tuple(t.shape)}")
-        if lse.dtype != torch.float32 or tuple(lse.shape) != (nq, heads):
-            _refuse(f"{who}: lse must be float32 [{nq}, {heads}], got {lse.dtype} {tuple(lse.shape)}")
-        dout, out, lse = _heads(dout, who, "dout"), out.contiguous(), lse.contiguous()
-        dq = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
-        dk = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
-        dv = torch.empty(tuple(k.shape), dtype=q.dtype, device=q.device)
-        _check(load().fvx_cross_attention_backward(
-            dt, *_strided(dout), *_strided(q), *_strided(k), *_strided(v), out.data_ptr(), lse.data_ptr(), qo, ko, B,
-            heads, k.shape[1], d, _at(key_mask), d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(),
-            dv.data_ptr(), s))
+    s = _on_device(who, dout, q, k, v, out, lse, key_mask)
+    q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
+    nq, heads, d = q.shape
+    for name, t in (("dout", dout), ("out", out)):
+        if t.dtype != q.dtype or t.shape != q.shape:
+            _refuse(f"{who}: {name} must be {q.dtype} {tuple(q.shape)}, got {t.dtype} {tuple(t.shape)}")
+    if lse.dtype != torch.float32 or tuple(lse.shape) != (nq, heads):
+        _refuse(f"{who}: lse must be float32 [{nq}, {heads}], got {lse.dtype} {tuple(lse.shape)}")
+    dout, out, lse = _heads(dout, who, "dout"), out.contiguous(), lse.contiguous()
+    dq = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
+    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    _check(load().fvx_cross_attention_backward(
+        dt, *_strided(dout), *_strided(q), *_strided(k), *_strided(v), out.data_ptr(), lse.data_ptr(), qo, ko, B, heads,
+        k.shape[1], d, _at(key_mask), d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(),
+        dv.data_ptr(), s))
     return dq, dk, dv
 
 
 def _strided(t):
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    st = t.stride()
+    return t.data_ptr(), st[0], st[1]
 
 
 def device_status(stream=None):

@@ -15,321 +15,18 @@
 // memory bounds it.  So each row is read once, stays in registers between its
 // two reductions, and the checkpoint is written by the pass that reads x.
 // Statistics, products and sums are fp32 whatever the storage type.
-#include <cuda_bf16.h>
-#include <cuda_runtime.h>
-#include <stdint.h>
-
-#include <algorithm>
-
-#include "fvx_internal.cuh"
+#include "norm.cuh"
 
 namespace fvx {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kRegCols = 1024;      // widest row held in a warp's registers
-constexpr int64_t kMaxCols = 65536;
-constexpr float kTiny = 7.888609052210118e-31f;  // 2^-100
-
-template <typename T>
-struct Elem;
-template <>
-struct Elem<float> {
-  static __device__ __forceinline__ float get(float v) { return v; }
-  static __device__ __forceinline__ float put(float v) { return v; }
-};
-template <>
-struct Elem<__nv_bfloat16> {
-  static __device__ __forceinline__ float get(__nv_bfloat16 v) { return __bfloat162float(v); }
-  static __device__ __forceinline__ __nv_bfloat16 put(float v) { return __float2bfloat16_rn(v); }
-};
-
-template <typename T, int VEC>
-struct alignas(sizeof(T) * VEC) Pack {
-  T v[VEC];
-};
-
-template <typename T, int VEC>
-__device__ __forceinline__ void load_vec(const T* p, float (&f)[VEC]) {
-  const Pack<T, VEC> u = *reinterpret_cast<const Pack<T, VEC>*>(p);
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) f[j] = Elem<T>::get(u.v[j]);
-}
-template <typename T, int VEC>
-__device__ __forceinline__ void store_vec(T* p, const float (&f)[VEC]) {
-  Pack<T, VEC> u;
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) u.v[j] = Elem<T>::put(f[j]);
-  *reinterpret_cast<Pack<T, VEC>*>(p) = u;
-}
-
-// Sum over the `width` lanes (a power of two) that share a row.
-__device__ __forceinline__ float lanes_sum(float v, int width) {
-  for (int o = width >> 1; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
-}
-
-// Magnitudes are compared as integers: the same order as the floats', with
-// infinity above every number and NaN above infinity.
-__device__ __forceinline__ uint32_t mag_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
-
-struct CodeScale {
-  float inv, step;
-};
-__device__ __forceinline__ CodeScale code_scale(uint32_t top_bits) {
-  const float top = __uint_as_float(top_bits);
-  CodeScale s;
-  if (top_bits >= 0x7f800000u) {
-    s.inv = 0.0f;
-    s.step = __uint_as_float(0x7fc00000u);
-  } else if (top < kTiny) {
-    s.inv = 0.0f;
-    s.step = 0.0f;
-  } else {
-    s.inv = __fdiv_rn(127.0f, top);
-    s.step = __fdiv_rn(top, 127.0f);
-  }
-  return s;
-}
-__device__ __forceinline__ int8_t code_of(float x, float inv) {
-  // inv is 0 for a group of zeros or of NaN; x * 0 may be NaN there and converts to 0
-  return (int8_t)__float2int_rn(__fmul_rn(x, inv));
-}
-
-struct RowArgs {
-  const void* x;       // [n, c], row pitch ldx
-  const int8_t* codes; // or 8-bit codes [n, c]
-  const float* steps;  // [n, groups]
-  const void* dy;
-  const float* w;  // [c] or null
-  const float* b;
-  const float* mean_in;
-  const float* rstd_in;
-  void* y;  // forward output or dx
-  int8_t* codes_out;
-  float* steps_out;
-  float* mean;
-  float* rstd;
-  float* part;  // backward: [gridDim.x][2][c] partial sums of dw, db (null: not wanted)
-  int64_t n, ldx, lddy, ldy;
-  int c, groups, group_shift;
-  int lanes;  // lanes that share a row (power of two)
-  float eps;
-};
-
-// Group maxima for the codes.  Lane l of a row holds vectors l, l + 32, ...
-// (or one vector when the row has at most 32).  A group is 2^group_shift
-// values: a run of lanes of one vector index, or (narrow vectors) all lanes of
-// 2 or 4 consecutive indices.
-template <int VEC, int ITER>
-__device__ __forceinline__ void group_tops(uint32_t (&top)[ITER], int group_shift, int lanes) {
-  const int per = (1 << group_shift) / VEC;  // vectors of a group
-  const int width = min(per, lanes);
-#pragma unroll
-  for (int i = 0; i < ITER; ++i)
-    for (int o = width >> 1; o > 0; o >>= 1) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-  if constexpr (ITER >= 2) {
-    if (per >= 64) {
-#pragma unroll
-      for (int i = 0; i < ITER; i += 2) top[i] = top[i + 1] = max(top[i], top[i + 1]);
-    }
-  }
-  if constexpr (ITER >= 4) {
-    if (per >= 128) {
-#pragma unroll
-      for (int i = 0; i < ITER; i += 4) top[i] = top[i + 1] = top[i + 2] = top[i + 3] = max(top[i], top[i + 2]);
-    }
-  }
-}
-
-// Rows of up to 1024 values: `lanes` lanes per row, ITER vectors per lane.
-// CODES: the checkpoint is written too.
-template <typename T, int VEC, int ITER, bool CODES>
-__global__ void __launch_bounds__(kThreads) k_norm_rows(const __grid_constant__ RowArgs a) {
-  const int lane = threadIdx.x & (a.lanes - 1);
+template <typename T, int VEC, int ITER, int OP>
+__global__ void __launch_bounds__(kThreads) k_rows(const __grid_constant__ RowArgs a) {
+  extern __shared__ float sh[];  // backward: [kThreads / lanes][c]
+  Rows<T, VEC, ITER, OP, 0> rows(a);
   const int per_block = kThreads / a.lanes;
-  const int sub = threadIdx.x / a.lanes;
-  const int nv = a.c / VEC;
-  const float inv_c = 1.0f / (float)a.c;
-  float w[ITER][VEC], b[ITER][VEC];
-#pragma unroll
-  for (int i = 0; i < ITER; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int at = (i * 32 + lane) * VEC + j;
-      w[i][j] = a.w && at < a.c ? __ldg(a.w + at) : 1.0f;
-      b[i][j] = a.b && at < a.c ? __ldg(a.b + at) : 0.0f;
-    }
-  // every lane of a warp takes the same number of turns (the shuffles need them all)
-  const int64_t turns = (a.n + (int64_t)gridDim.x * per_block - 1) / ((int64_t)gridDim.x * per_block);
-  int64_t row = (int64_t)blockIdx.x * per_block + sub;
-  for (int64_t t = 0; t < turns; ++t, row += (int64_t)gridDim.x * per_block) {
-    const bool live = row < a.n;
-    const T* px = reinterpret_cast<const T*>(a.x) + (live ? row : 0) * a.ldx;
-    float x[ITER][VEC];
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int v = i * 32 + lane;
-      if (live && v < nv) {
-        load_vec<T, VEC>(px + v * VEC, x[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x[i][j] = 0.0f;
-      }
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) s += x[i][j];
-    }
-    const float mean = lanes_sum(s, a.lanes) * inv_c;
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-      if (i * 32 + lane < nv) {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) q += (x[i][j] - mean) * (x[i][j] - mean);
-      }
-    const float rstd = rsqrtf(lanes_sum(q, a.lanes) * inv_c + a.eps);
-    if (live && lane == 0) {
-      a.mean[row] = mean;
-      a.rstd[row] = rstd;
-    }
-    if constexpr (CODES) {
-      uint32_t top[ITER];
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        top[i] = 0u;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) top[i] = max(top[i], mag_bits(x[i][j]));
-      }
-      group_tops<VEC, ITER>(top, a.group_shift, a.lanes);
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int v = i * 32 + lane;
-        if (!live || v >= nv) continue;
-        const CodeScale cs = code_scale(top[i]);
-        Pack<int8_t, VEC> u;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) u.v[j] = code_of(x[i][j], cs.inv);
-        *reinterpret_cast<Pack<int8_t, VEC>*>(a.codes_out + row * a.c + v * VEC) = u;
-        if (((v * VEC) & ((1 << a.group_shift) - 1)) == 0)
-          a.steps_out[row * a.groups + ((v * VEC) >> a.group_shift)] = cs.step;
-      }
-    }
-    if (live) {
-      T* py = reinterpret_cast<T*>(a.y) + row * a.ldy;
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int v = i * 32 + lane;
-        if (v >= nv) continue;
-        float y[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) y[j] = (x[i][j] - mean) * rstd * w[i][j] + b[i][j];
-        store_vec<T, VEC>(py + v * VEC, y);
-      }
-    }
-  }
-}
-
-// One vector of x, from the tensor or from its checkpoint.
-template <typename T, int VEC, bool CODES>
-__device__ __forceinline__ void load_x(const RowArgs& a, int64_t row, int v, float (&x)[VEC]) {
-  if constexpr (CODES) {
-    const Pack<int8_t, VEC> u = *reinterpret_cast<const Pack<int8_t, VEC>*>(a.codes + row * a.c + v * VEC);
-    const float step = __ldg(a.steps + row * a.groups + ((v * VEC) >> a.group_shift));
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) x[j] = (float)u.v[j] * step;
-  } else {
-    load_vec<T, VEC>(reinterpret_cast<const T*>(a.x) + row * a.ldx + v * VEC, x);
-  }
-}
-
-// Backward of rows of up to 1024 values.  A lane keeps the same channels for
-// all its rows, so its parts of dw and db stay in registers; the block adds
-// its lanes' parts in a fixed order and writes them once.
-template <typename T, int VEC, int ITER, bool CODES>
-__global__ void __launch_bounds__(kThreads) k_norm_rows_bwd(const __grid_constant__ RowArgs a) {
-  extern __shared__ float sh[];  // [kThreads / lanes][c]
-  const int lane = threadIdx.x & (a.lanes - 1);
-  const int per_block = kThreads / a.lanes;
-  const int sub = threadIdx.x / a.lanes;
-  const int nv = a.c / VEC;
-  const float inv_c = 1.0f / (float)a.c;
-  float w[ITER][VEC], dw[ITER][VEC], db[ITER][VEC];
-#pragma unroll
-  for (int i = 0; i < ITER; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int at = (i * 32 + lane) * VEC + j;
-      w[i][j] = a.w && at < a.c ? __ldg(a.w + at) : 1.0f;
-      dw[i][j] = db[i][j] = 0.0f;
-    }
-  const int64_t turns = (a.n + (int64_t)gridDim.x * per_block - 1) / ((int64_t)gridDim.x * per_block);
-  int64_t row = (int64_t)blockIdx.x * per_block + sub;
-  for (int64_t t = 0; t < turns; ++t, row += (int64_t)gridDim.x * per_block) {
-    const bool live = row < a.n;
-    const int64_t r = live ? row : 0;
-    const float mean = __ldg(a.mean_in + r), rstd = __ldg(a.rstd_in + r);
-    float xh[ITER][VEC], g[ITER][VEC];
-    float sg = 0.0f, sgx = 0.0f;
-#pragma unroll
-    for (int i = 0; i < ITER; ++i) {
-      const int v = i * 32 + lane;
-      if (live && v < nv) {
-        load_x<T, VEC, CODES>(a, r, v, xh[i]);
-        load_vec<T, VEC>(reinterpret_cast<const T*>(a.dy) + r * a.lddy + v * VEC, g[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          xh[i][j] = mean;
-          g[i][j] = 0.0f;
-        }
-      }
-    }
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        if (live && i * 32 + lane < nv) {
-          xh[i][j] = (xh[i][j] - mean) * rstd;
-          dw[i][j] += g[i][j] * xh[i][j];
-          db[i][j] += g[i][j];
-          g[i][j] *= w[i][j];
-          sg += g[i][j];
-          sgx += g[i][j] * xh[i][j];
-        }
-      }
-    sg = lanes_sum(sg, a.lanes) * inv_c;
-    sgx = lanes_sum(sgx, a.lanes) * inv_c;
-    if (live) {
-      T* py = reinterpret_cast<T*>(a.y) + row * a.ldy;
-#pragma unroll
-      for (int i = 0; i < ITER; ++i) {
-        const int v = i * 32 + lane;
-        if (v >= nv) continue;
-        float d[VEC];
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) d[j] = rstd * (g[i][j] - sg - xh[i][j] * sgx);
-        store_vec<T, VEC>(py + v * VEC, d);
-      }
-    }
-  }
-  if (!a.part) return;
-  for (int pass = 0; pass < 2; ++pass) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < ITER; ++i)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int at = (i * 32 + lane) * VEC + j;
-        if (at < a.c) sh[sub * a.c + at] = pass ? db[i][j] : dw[i][j];
-      }
-    __syncthreads();
-    for (int at = threadIdx.x; at < a.c; at += kThreads) {
-      float s = 0.0f;
-      for (int k = 0; k < per_block; ++k) s += sh[k * a.c + at];
-      a.part[((int64_t)blockIdx.x * 2 + pass) * a.c + at] = s;
-    }
-  }
+  rows.direct((int64_t)blockIdx.x * per_block, (int64_t)gridDim.x * per_block, a.n);
+  if constexpr (OpIs<OP>::kBack) rows.write_parts(sh, kThreads);
 }
 
 // dw, db = sums of the blocks' parts: 32 channels per block, 8 rows of threads
@@ -340,8 +37,16 @@ __global__ void __launch_bounds__(kThreads) k_norm_sum_parts(const float* __rest
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int at = blockIdx.x * 32 + tx;  // over 2c values: dw, then db
   float s = 0.0f;
-  if (at < 2 * c)
-    for (int p = ty; p < parts; p += 8) s += __ldg(part + (int64_t)p * 2 * c + at);
+  if (at < 2 * c) {
+    const float* src = part + at;
+    int p = ty;
+    for (; p + 24 < parts; p += 32) {
+      const float x = __ldg(src + (int64_t)p * 2 * c), y = __ldg(src + (int64_t)(p + 8) * 2 * c),
+                  z = __ldg(src + (int64_t)(p + 16) * 2 * c), t = __ldg(src + (int64_t)(p + 24) * 2 * c);
+      s += (x + y) + (z + t);
+    }
+    for (; p < parts; p += 8) s += __ldg(src + (int64_t)p * 2 * c);
+  }
   sh[ty][tx] = s;
   __syncthreads();
   if (ty == 0 && at < 2 * c) {
@@ -354,6 +59,19 @@ __global__ void __launch_bounds__(kThreads) k_norm_sum_parts(const float* __rest
 }
 
 // ---------------------------------------------------------------- rows wider than 1024
+// One vector of x, from the tensor or from its checkpoint.
+template <typename T, int VEC, bool CODES>
+__device__ __forceinline__ void load_x(const RowArgs& a, int64_t row, int v, float (&x)[VEC]) {
+  if constexpr (CODES) {
+    codes_to_float<VEC>(raw_vec<int8_t, VEC>(a.codes + row * a.c + v * VEC), x);
+    const float step = __ldg(a.steps + row * a.groups + ((v * VEC) >> a.group_shift));
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) x[j] *= step;
+  } else {
+    load_vec<T, VEC>(reinterpret_cast<const T*>(a.x) + row * a.ldx + v * VEC, x);
+  }
+}
+
 __device__ __forceinline__ float block_sum(float v, float* sh) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   v = lanes_sum(v, 32);
@@ -468,64 +186,52 @@ __global__ void __launch_bounds__(kThreads) k_norm_wide_dw(const __grid_constant
 }
 
 // ---------------------------------------------------------------- checkpoints
-// Pack: `lanes` lanes per group of a row, SPAN vectors per lane.
+// Pack of rows wider than 1024 values: `lanes` lanes per group of a row, SPAN
+// vectors per lane.
 template <typename T, int VEC, int SPAN>
-__global__ void __launch_bounds__(kThreads) k_ck_pack(const __grid_constant__ RowArgs a) {
+__global__ void __launch_bounds__(kThreads) k_ck_pack_wide(const __grid_constant__ RowArgs a) {
   const int lane = threadIdx.x & (a.lanes - 1);
   const int per_block = kThreads / a.lanes;
-  const int64_t units = a.n * a.groups;
-  const int64_t turns = (units + (int64_t)gridDim.x * per_block - 1) / ((int64_t)gridDim.x * per_block);
-  int64_t u = (int64_t)blockIdx.x * per_block + threadIdx.x / a.lanes;
-  for (int64_t t = 0; t < turns; ++t, u += (int64_t)gridDim.x * per_block) {
-    const bool live = u < units;
-    const int64_t row = live ? (a.groups == 1 ? u : u / a.groups) : 0;
-    const int grp = live ? (int)(u - row * a.groups) : 0;
-    const T* px = reinterpret_cast<const T*>(a.x) + row * a.ldx;
+  const int64_t units = a.n * a.groups, step = (int64_t)gridDim.x * per_block;
+  const int64_t turns = (units + step - 1) / step;
+  int64_t unit = (int64_t)blockIdx.x * per_block + threadIdx.x / a.lanes;
+  for (int64_t t = 0; t < turns; ++t, unit += step) {
+    const bool live = unit < units;
+    const int64_t row = live ? unit / a.groups : 0;
+    const int first = live ? (int)(unit - row * a.groups) << a.group_shift : 0;
+    const int left = live ? min(a.c - first, 1 << a.group_shift) : 0;
+    const T* px = reinterpret_cast<const T*>(a.x) + row * a.ldx + first;
     float x[SPAN][VEC];
     uint32_t top = 0u;
 #pragma unroll
     for (int i = 0; i < SPAN; ++i) {
-      const int at = (grp << a.group_shift) + (i * 32 + lane) * VEC;
-      const bool in = live && (i * 32 + lane) * VEC < (1 << a.group_shift) && at < a.c;
-      if (in) {
-        load_vec<T, VEC>(px + at, x[i]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) x[i][j] = 0.0f;
-      }
+      const int at = (i * 32 + lane) * VEC;
+      widen<T, VEC>(at < left ? raw_vec<T, VEC>(px + at) : no_vec<T, VEC>(), x[i]);
 #pragma unroll
       for (int j = 0; j < VEC; ++j) top = max(top, mag_bits(x[i][j]));
     }
     for (int o = a.lanes >> 1; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (!live) continue;
     const CodeScale cs = code_scale(top);
 #pragma unroll
     for (int i = 0; i < SPAN; ++i) {
-      const int at = (grp << a.group_shift) + (i * 32 + lane) * VEC;
-      if ((i * 32 + lane) * VEC >= (1 << a.group_shift) || at >= a.c) continue;
-      Pack<int8_t, VEC> p;
+      const int at = (i * 32 + lane) * VEC;
+      if (at >= left) continue;
+      float q[VEC];
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) p.v[j] = code_of(x[i][j], cs.inv);
-      *reinterpret_cast<Pack<int8_t, VEC>*>(a.codes_out + row * a.c + at) = p;
+      for (int j = 0; j < VEC; ++j) q[j] = __fadd_rn(__fmul_rn(x[i][j], cs.inv), kMagic);
+      store_codes<VEC>(a.codes_out + row * a.c + first + at, q, cs.inv == 0.0f);
     }
-    if (lane == 0) a.steps_out[u] = cs.step;
+    if (lane == 0 && live) a.steps_out[unit] = cs.step;
   }
 }
 
-// Restore, and (NORM) the layer norm of the restored rows with given statistics.
+// Restore of rows wider than 1024 values, one block per row.
 template <typename T, int VEC, bool NORM>
-__global__ void __launch_bounds__(kThreads) k_ck_restore(const __grid_constant__ RowArgs a) {
-  const int lane = threadIdx.x & (a.lanes - 1);
-  const int per_block = kThreads / a.lanes;
+__global__ void __launch_bounds__(kThreads) k_ck_wide(const __grid_constant__ RowArgs a) {
   const int nv = a.c / VEC;
-  for (int64_t row = (int64_t)blockIdx.x * per_block + threadIdx.x / a.lanes; row < a.n;
-       row += (int64_t)gridDim.x * per_block) {
-    float mean = 0.0f, rstd = 1.0f;
-    if constexpr (NORM) {
-      mean = __ldg(a.mean_in + row);
-      rstd = __ldg(a.rstd_in + row);
-    }
-    for (int v = lane; v < nv; v += a.lanes) {
+  for (int64_t row = blockIdx.x; row < a.n; row += gridDim.x) {
+    const float mean = NORM ? __ldg(a.mean_in + row) : 0.0f, rstd = NORM ? __ldg(a.rstd_in + row) : 1.0f;
+    for (int v = threadIdx.x; v < nv; v += kThreads) {
       float x[VEC];
       load_x<T, VEC, true>(a, row, v, x);
       if constexpr (NORM) {
@@ -561,7 +267,12 @@ int pow2_at_least(int64_t v, int most) {
   while (p < v && p < most) p <<= 1;
   return p;
 }
-int iters_for(int64_t c, int vec) { return (int)((c / vec + 31) / 32); }
+// Lanes of a row and vectors per lane.
+int lanes_for(int64_t c, int vec) { return pow2_at_least(c / vec, 32); }
+int iters_for(int64_t c, int vec) {
+  const int lanes = lanes_for(c, vec);
+  return (int)((c / vec + lanes - 1) / lanes);
+}
 
 // Blocks for `units` units of `per_block`, at most `per_sm` per multiprocessor.
 int grid_for(int64_t units, int per_block, int sms, int per_sm) {
@@ -653,22 +364,80 @@ fvx_status check_group(const char* who, int32_t group, int64_t n, const void* co
   return FVX_OK;
 }
 
-fvx_status pack_launch(fvx_dtype dt, RowArgs a, cudaStream_t s, int sms) {
+fvx_status pack_wide(fvx_dtype dt, RowArgs a, cudaStream_t s, int sms) {
   RowArgs only = a;
   only.y = nullptr;
   only.dy = nullptr;
   const int vec = pick_vec(dt, a.c, only);
-  const int64_t in_group = std::min<int64_t>(a.c, 1 << a.group_shift);
+  const int in_group = 1 << a.group_shift;
   a.lanes = pow2_at_least((in_group + vec - 1) / vec, 32);
-  const int span = (int)((in_group + vec * 32 - 1) / (vec * 32));
-  const int grid = grid_for(a.n * a.groups, kThreads / a.lanes, sms, 8);
+  const int span = (in_group + vec * 32 - 1) / (vec * 32);
+  const int grid = grid_for(a.n * a.groups, kThreads / a.lanes, sms, 32);
   return by_vec(dt, vec, [&]<typename T, int VEC>() {
     if constexpr (VEC * sizeof(T) == 16) {
-      return launch("ck_pack", k_ck_pack<T, VEC, 1>, dim3(grid), 0, s, a);
+      return launch("ck_pack", k_ck_pack_wide<T, VEC, 1>, dim3(grid), 0, s, a);
     } else {
-      return span <= 1 ? launch("ck_pack", k_ck_pack<T, VEC, 1>, dim3(grid), 0, s, a)
-                       : launch("ck_pack", k_ck_pack<T, VEC, 4>, dim3(grid), 0, s, a);
+      return span <= 1 ? launch("ck_pack", k_ck_pack_wide<T, VEC, 1>, dim3(grid), 0, s, a)
+                       : launch("ck_pack", k_ck_pack_wide<T, VEC, 4>, dim3(grid), 0, s, a);
     }
+  });
+}
+
+// Blocks of the row kernels; the backward ones write a part of dw and db each.
+struct RowGrid {
+  int blocks;
+  bool stream;
+  StreamArgs args;
+};
+// Dense rows of 16-byte vectors, enough of them for every block to take several
+// stages, are streamed through shared memory.
+template <int OP>
+RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
+  using Is = OpIs<OP>;
+  const int elem = dt == FVX_F32 ? 4 : 2, per_block = kThreads / a.lanes;
+  RowGrid g = {};
+  g.blocks = grid_for(a.n, per_block, sms, Is::kBack ? 4 : 16);
+  auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  if (vec * elem != 16) return g;
+  if (!Is::kFromCodes && !(a.ldx == a.c && at16(a.x))) return g;
+  if (Is::kFromCodes && !(at16(a.codes) && at16(a.steps))) return g;
+  if (Is::kBack && !(a.lddy == a.c && at16(a.dy))) return g;
+  if (Is::kStats && !(at16(a.mean_in) && at16(a.rstd_in))) return g;
+  const int x_row = a.c * (Is::kFromCodes ? 1 : elem);
+  const int row = x_row + (Is::kBack ? a.c * elem : 0);
+  StreamArgs& s = g.args;
+  s.r = a;
+  // a multiple of the rows of a turn (eight at least: the small arrays' copies
+  // are then multiples of 16 bytes), about 10 KB
+  s.rows = per_block * std::max(1, 10240 / (per_block * row));
+  s.stages = a.n / s.rows;
+  auto up = [](int v) { return (v + 15) & ~15; };
+  s.off_dy = up(s.rows * x_row);
+  s.off_steps = s.off_dy + (Is::kBack ? up(s.rows * a.c * elem) : 0);
+  s.off_mean = s.off_steps + (Is::kFromCodes ? up(s.rows * a.groups * 4) : 0);
+  s.off_rstd = s.off_mean + (Is::kStats ? up(s.rows * 4) : 0);
+  s.stage_bytes = (s.off_rstd + (Is::kStats ? up(s.rows * 4) : 0) + 127) & ~127;
+  const int per_sm = std::min(Is::kBack ? 3 : 4, 227 * 1024 / (kStreamStages * s.stage_bytes + 128 + 1024));
+  if (per_sm < 1 || s.stages < (int64_t)sms * per_sm * 4) return g;
+  s.status = device_status_word();
+  if (!s.status) return g;
+  g.stream = true;
+  g.blocks = sms * per_sm;
+  return g;
+}
+template <int OP>
+fvx_status rows_launch(const char* name, fvx_dtype dt, int vec, const RowArgs& a, const RowGrid& g, cudaStream_t s) {
+  constexpr bool kBack = OpIs<OP>::kBack;
+  const size_t parts = kBack ? (size_t)(kThreads / a.lanes) * a.c * 4 : 0;  // at most 8 * 1024 or 256 * 8 values
+  if (g.stream) {
+    const size_t smem = 128 + std::max((size_t)kStreamStages * g.args.stage_bytes, parts);
+    StreamArgs args = g.args;
+    args.r = a;
+    return (dt == FVX_F32 ? stream_rows_f32 : stream_rows_bf16)(name, (RowOp)OP, iters_for(a.c, vec), args, g.blocks,
+                                                                smem, s);
+  }
+  return by_row_shape(dt, vec, iters_for(a.c, vec), [&]<typename T, int VEC, int ITER>() -> fvx_status {
+    return launch(name, k_rows<T, VEC, ITER, OP>, dim3(g.blocks), parts, s, a);
   });
 }
 
@@ -718,18 +487,15 @@ fvx_status fvx_layer_norm(fvx_dtype dt, const void* x, int64_t ldx, int64_t n, i
   }
   const int vec = pick_vec(dt, c, a);
   if (c <= kRegCols) {
-    a.lanes = pow2_at_least(c / vec, 32);
-    const int grid = grid_for(n, kThreads / a.lanes, sms, 8);
-    return by_row_shape(dt, vec, iters_for(c, vec), [&]<typename T, int VEC, int ITER>() {
-      return group ? launch("norm_rows", k_norm_rows<T, VEC, ITER, true>, dim3(grid), 0, s, a)
-                   : launch("norm_rows", k_norm_rows<T, VEC, ITER, false>, dim3(grid), 0, s, a);
-    });
+    a.lanes = lanes_for(c, vec);
+    return group ? rows_launch<kForwardCodes>("norm_rows", dt, vec, a, row_grid<kForwardCodes>(dt, vec, a, sms), s)
+                 : rows_launch<kForward>("norm_rows", dt, vec, a, row_grid<kForward>(dt, vec, a, sms), s);
   }
   const int grid = grid_for(n, 1, sms, 8);
   FVX_TRY(by_vec(dt, vec, [&]<typename T, int VEC>() {
     return launch("norm_wide", k_norm_wide<T, VEC>, dim3(grid), 0, s, a);
   }));
-  return group ? pack_launch(dt, a, s, sms) : FVX_OK;
+  return group ? pack_wide(dt, a, s, sms) : FVX_OK;
 }
 
 fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, const void* x, int64_t ldx,
@@ -782,14 +548,12 @@ fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, c
   const bool sums = dw || db;
   int parts = 0;
   if (c <= kRegCols) {
-    a.lanes = pow2_at_least(c / vec, 32);
-    parts = grid_for(n, kThreads / a.lanes, sms, 4);
+    a.lanes = lanes_for(c, vec);
+    const RowGrid g = group ? row_grid<kBackwardCodes>(dt, vec, a, sms) : row_grid<kBackward>(dt, vec, a, sms);
+    parts = g.blocks;
     if (sums && !(a.part = scr.get<float>((size_t)parts * 2 * c))) return FVX_ERR_ALLOC;
-    const size_t smem = (size_t)(kThreads / a.lanes) * c * 4;  // at most 8 * 1024 or 256 * 8 values
-    FVX_TRY(by_row_shape(dt, vec, iters_for(c, vec), [&]<typename T, int VEC, int ITER>() {
-      return group ? launch("norm_rows_bwd", k_norm_rows_bwd<T, VEC, ITER, true>, dim3(parts), smem, s, a)
-                   : launch("norm_rows_bwd", k_norm_rows_bwd<T, VEC, ITER, false>, dim3(parts), smem, s, a);
-    }));
+    FVX_TRY(group ? rows_launch<kBackwardCodes>("norm_rows_bwd", dt, vec, a, g, s)
+                  : rows_launch<kBackward>("norm_rows_bwd", dt, vec, a, g, s));
   } else {
     const int grid = grid_for(n, 1, sms, 8);
     const int slabs = (int)((c / vec + kThreads - 1) / kThreads);
@@ -829,7 +593,10 @@ fvx_status fvx_checkpoint_pack(fvx_dtype dt, const void* x, int64_t ldx, int64_t
   a.steps_out = steps;
   a.group_shift = shift;
   a.groups = (int)((c + group - 1) >> shift);
-  return pack_launch(dt, a, (cudaStream_t)stream, sms);
+  if (c > kRegCols) return pack_wide(dt, a, (cudaStream_t)stream, sms);
+  const int vec = pick_vec(dt, c, a);
+  a.lanes = lanes_for(c, vec);
+  return rows_launch<kPack>("ck_pack", dt, vec, a, row_grid<kPack>(dt, vec, a, sms), (cudaStream_t)stream);
 }
 
 fvx_status fvx_checkpoint_restore(fvx_dtype dt, int32_t group, const int8_t* codes, const float* steps, int64_t n,
@@ -865,11 +632,15 @@ fvx_status fvx_checkpoint_restore(fvx_dtype dt, int32_t group, const int8_t* cod
   a.group_shift = shift;
   a.groups = (int)((c + group - 1) >> shift);
   const int vec = pick_vec(dt, c, a);
-  a.lanes = pow2_at_least(c / vec, kThreads);
-  const int grid = grid_for(n, kThreads / a.lanes, sms, 8);
+  if (c <= kRegCols) {
+    a.lanes = lanes_for(c, vec);
+    return mean ? rows_launch<kRestoreNorm>("ck_restore", dt, vec, a, row_grid<kRestoreNorm>(dt, vec, a, sms), s)
+                : rows_launch<kRestore>("ck_restore", dt, vec, a, row_grid<kRestore>(dt, vec, a, sms), s);
+  }
+  const int grid = grid_for(n, 1, sms, 8);
   return by_vec(dt, vec, [&]<typename T, int VEC>() {
-    return mean ? launch("ck_restore", k_ck_restore<T, VEC, true>, dim3(grid), 0, s, a)
-                : launch("ck_restore", k_ck_restore<T, VEC, false>, dim3(grid), 0, s, a);
+    return mean ? launch("ck_restore", k_ck_wide<T, VEC, true>, dim3(grid), 0, s, a)
+                : launch("ck_restore", k_ck_wide<T, VEC, false>, dim3(grid), 0, s, a);
   });
 }
 

@@ -232,6 +232,25 @@ def test_checkpoint_bits(n, c, pad, lead, group, dtype):
     assert np.all(np.abs(held - xr) <= np.repeat(steps, group, 1)[:, :c] * (0.5 + 127 * 2.0 ** -22))
 
 
+def test_checkpoint_quotients():
+    """step = top / 127 and x (127 / top) as the fp32 division rounds them, for
+    two million maxima over the whole range of magnitudes, both ends included."""
+    import torch
+
+    import sparse_convolution_gb300 as fvx
+
+    g = torch.Generator(device="cuda").manual_seed(5)
+    bits = torch.randint(0x0D800000, 0x7F800000, (1 << 21,), generator=g, device="cuda", dtype=torch.int32)
+    bits[:4] = torch.tensor([0x0D800000, 0x0D800001, 0x7F7FFFFF, 0x7E800000], dtype=torch.int32)
+    top = bits.view(torch.float32)
+    x = top[:, None] * torch.rand(1 << 21, 32, generator=g, device="cuda")
+    x[:, 7] = -top
+    ck = fvx.Checkpoint8.pack(x, group=32)
+    most = torch.full_like(top, 127.0)
+    assert torch.equal(ck.steps[:, 0], top / most)
+    assert torch.equal(ck.codes, torch.round(x * (most / top)[:, None]).to(torch.int8))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_checkpoint_special_values(dtype):
     import torch
@@ -269,6 +288,57 @@ def test_backward_from_checkpoint(n, c, group, dtype):
     bound = 8 * U * ((np.abs(held) + np.abs(m)) * r * np.abs(wr) + np.abs(br) + np.abs(want))
     _close(_np(ck.layer_norm(mean, rstd, w, b)), want, bound + (BF16_OUT_REL * np.abs(want) if dtype == "bf16" else 0),
            "again")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c,group", [(300_003, 8, 32), (200_011, 64, 32), (150_001, 256, 64), (300_017, 48, 128),
+                                       (60_007, 504, 64), (50_021, 1024, 128)])
+def test_long_tensors(n, c, group, dtype):
+    """Lengths that take the streaming kernels, with a last stage that is not
+    full: rows from every part against the definitions, dweight and dbias
+    against sums in 64 bits."""
+    import torch
+
+    import sparse_convolution_gb300 as fvx
+
+    x, w, b, dy = _inputs(n, c, dtype, c)
+    y, mean, rstd, ck = fvx.layer_norm(x, w, b, checkpoint_group=group)
+    plain = fvx.layer_norm(x, w, b)
+    assert all(torch.equal(p, q) for p, q in zip(plain, (y, mean, rstd)))
+    packed = fvx.Checkpoint8.pack(x, group=group)
+    assert torch.equal(packed.codes, ck.codes) and torch.equal(packed.steps, ck.steps)
+    restored, again = ck.restore(torch.float32), ck.layer_norm(mean, rstd, w, b)
+    at = torch.cat([torch.arange(0, 70), torch.arange(n // 2, n // 2 + 70), torch.arange(n - 600, n)]).cuda()
+    xs = x[at]
+    _check_forward(y[at], mean[at], rstd[at], xs, _np(w), _np(b), 1e-5, dtype)
+    codes, steps = _codes_ref(xs.float().cpu().numpy(), group)
+    held = _held(codes, steps, group)
+    assert np.array_equal(ck.codes[at].cpu().numpy(), codes) and np.array_equal(ck.steps[at].cpu().numpy(), steps)
+    assert np.array_equal(restored[at].cpu().numpy(), held)
+    m, r, wr, br = _np(mean[at])[:, None], _np(rstd[at])[:, None], _np(w), _np(b)
+    want = (held - m) * r * wr + br
+    bound = 8 * U * ((np.abs(held) + np.abs(m)) * r * np.abs(wr) + np.abs(br) + np.abs(want))
+    _close(_np(again[at]), want, bound + (BF16_OUT_REL * np.abs(want) if dtype == "bf16" else 0), "again")
+    for source, xr in ((x, _np(xs)), (ck, held.astype(np.float64))):
+        got = fvx.layer_norm_backward(dy, source, mean, rstd, w)
+        fvx.device_status()
+        repeat = fvx.layer_norm_backward(dy, source, mean, rstd, w)
+        assert all(torch.equal(p, q) for p, q in zip(got, repeat))
+        dyr = _np(dy[at])
+        dxr = _ref_backward(dyr, xr, m, r, wr)[0]
+        g, xh = np.abs(dyr * wr), np.abs((xr - m) * r)
+        exh = 4 * U * (np.abs(xr) + np.abs(m)) * r
+        scale = r * (g + g.mean(1, keepdims=True) + xh * (g * xh).mean(1, keepdims=True))
+        more = r * (exh * (g * xh).mean(1, keepdims=True) + xh * (g * exh).mean(1, keepdims=True))
+        _close(_np(got[0][at]), dxr, _k(c) * U * scale + more + (BF16_OUT_REL * np.abs(dxr) if dtype == "bf16" else 0), "dx")
+        full = (source.float() if source is x else restored).double()
+        xh = (full - mean.double()[:, None]) * rstd.double()[:, None]
+        ex = 4 * U * (full.abs() + mean.double().abs()[:, None]) * rstd.double()[:, None]
+        d = dy.double()
+        # rows of a lane one after the other, then groups, blocks and parts: at most n / 128 + 800 here
+        bound = (n / 128 + 800) * U
+        _close(_np(got[1]), _np((d * xh).sum(0)), bound * _np((d * xh).abs().sum(0)) + _np((d.abs() * ex).sum(0)), "dweight")
+        _close(_np(got[2]), _np(d.sum(0)), bound * _np(d.abs().sum(0)), "dbias")
 
 
 def test_another_stream():
