@@ -19,7 +19,7 @@ LIB = os.path.join(HERE, "libfvx.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cu", "primitives.cu", "build.cu", "kmap.cu", "conv.cu", "rays.cu", "norm.cu", "norm_stream_f32.cu",
-           "norm_stream_bf16.cu", "attn.cu", "attn_tc.cu"]
+           "norm_stream_bf16.cu", "attn.cu", "attn_tc.cu", "attn_few.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -714,6 +714,7 @@ fvx_status fvx_cross_attention(fvx_dtype dt, const void* q, int64_t q_token, int
     int sms = 0;
     FVX_TRY(device_sm_count(&sms));
     Scratch scr(s);
+    if (attn_few_serves(c)) return attn_few_forward(c, s, scr);
     if (attn_tc_serves(c, false)) return attn_tc_forward(c, s, scr);
     return by_type(dt, d, [&]<typename T, int DP>() { return fma_forward<T, DP>(c, s, scr, sms); });
   } catch (const std::exception& e) {

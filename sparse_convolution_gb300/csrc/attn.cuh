@@ -1,5 +1,6 @@
 // Shared by the cross-attention kernels (attn.cu: fp32 arithmetic on the CUDA
-// cores, reductions and the C entry points; attn_tc.cu: bf16 on the tensor cores).
+// cores, reductions and the C entry points; attn_tc.cu: bf16 on the tensor
+// cores; attn_few.cu: a few rows per key head).
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -73,7 +74,11 @@ bool attn_tc_serves(const AttnCall& c, bool backward);
 fvx_status attn_tc_forward(const AttnCall& c, cudaStream_t s, Scratch& scr);
 fvx_status attn_tc_backward(const AttnCall& c, cudaStream_t s, Scratch& scr);
 
-// attn.cu helpers that both use
+// The kernel for a few rows per key head (attn_few.cu).
+bool attn_few_serves(const AttnCall& c);
+fvx_status attn_few_forward(const AttnCall& c, cudaStream_t s, Scratch& scr);
+
+// attn.cu helpers that the others use
 // more: the arrays after the offsets, `arrays - 2` times items + 1 values
 fvx_status attn_items(const AttnCall& c, const int32_t* more, int arrays, cudaStream_t s, Scratch& scr,
                       AttnItems* out);

@@ -156,6 +156,38 @@ def test_long_keys_few_queries(dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("qlens,klens,heads,kv_heads,d", [
+    ([1], [1], 1, 1, 8), ([1, 0, 1], [37, 5, 0], 8, 1, 64), ([1, 1], [129, 4000], 8, 2, 128), ([2, 3], [600, 31], 2, 2, 40),
+    ([1], [70000], 4, 4, 32), ([1] * 40, [50 + 7 * i for i in range(40)], 6, 2, 96), ([8, 7], [1000, 3], 1, 1, 128),
+    ([1, 1, 1], [255, 256, 257], 7, 1, 72)])
+def test_a_few_rows(qlens, klens, heads, kv_heads, d, dtype):
+    """At most eight rows per key head: lengths around a block's turn, many
+    samples, one sample long enough for several clusters, none kept."""
+    for drop in (0.0, 0.4):
+        t, qo, ko, mask = _case(qlens, klens, heads, kv_heads, d, dtype, sum(klens) + d, drop)
+        got = _check(t, qo, ko, mask, backward=False)
+        again = _run(t, qo, ko, mask, backward=False)
+        assert all((got[n] == again[n]).all() for n in got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [2.5, -0.7, 0.0])
+def test_a_few_rows_that_hold_anything(scale, dtype):
+    """Masked keys of NaN and infinities, a sample of none but those, sharp,
+    negative and no scores."""
+    import torch
+
+    t, qo, ko, _ = _case([1, 2, 1], [300, 40, 200], 4, 2, 64, dtype, 31)
+    mask = torch.ones(ko[-1], dtype=torch.bool, device="cuda")
+    mask[5:290:4] = False
+    mask[ko[1]:ko[2]] = False
+    clean = _check(t, qo, ko, mask, scale=scale, backward=False)
+    t["k"][~mask], t["v"][~mask] = float("nan"), float("inf")
+    got = _run(t, qo, ko, mask, scale=scale, backward=False)
+    assert all(torch.equal(got[n], clean[n]) for n in got)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_many_queries_few_keys(dtype):
     """The rows are split over many units whose key gradients are summed."""
     t, qo, ko, mask = _case([6000, 3001], [5, 70], 4, 4, 64, dtype, 4, 0.2)
