@@ -24,13 +24,13 @@
 #include <vector>
 
 #include "attn.cuh"
+#include "tc.cuh"
 
 namespace fvx {
 namespace {
 
 constexpr int kMaxD = 128;
 constexpr int kTile = 64;    // rows and keys of a tile
-constexpr int kPitch = 68;   // 64 + 4: float4 reads stay aligned, columns spread over the banks
 constexpr int kFmaThreads = 256;
 
 template <typename T>
@@ -46,83 +46,185 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
+// The fp32 kernels: tiles of 64 rows by 64 keys in shared memory, row after row
+// with a pitch of 4 more words than a row has, so that the 16 byte reads of
+// neighbouring rows lie in different banks.  Thread (ty, tx) of 16 x 16 owns the
+// scores of rows ty + 16 i and keys tx + 16 j, and of the results the columns
+// 4 tx .. 4 tx + 3 of every 64 in the same rows.  Products run on pairs: over
+// even and odd dimensions for the scores, over neighbouring columns for the
+// results.  Shared memory's bandwidth and the multiplications bound a long tile
+// about equally (8 reads of 16 bytes for 32 paired products of a thread); what
+// bounds a small call is the latency of a tile's loads, so inner loops are
+// split until there are two blocks per multiprocessor.
 struct FmaArgs {
   AttnItems items;
   HeadsView q, k, v, dout;
   const uint8_t* mask;
   const float* delta;
   const float* lse_in;
-  void* out;         // forward: out (one split); dq
+  void* out;                  // forward: out (one split); backward: dq (one split)
+  void *dk, *dv;              // one split
   float* lse;
   float *part, *top, *total;  // several splits: [split][nq * heads][d], [split][nq * heads]
-  float *dk_part, *dv_part;   // [split][nk * kv_heads][d]
+  float *dk_part, *dv_part;   // several splits: [split][nk * kv_heads][d]
   int64_t nq, nk;
-  int heads, kv_heads, shared, d, splits;
+  int heads, kv_heads, shared, d;
+  int splits, key_splits;     // ranges that a row tile's keys and a key tile's rows are cut into
+  int key_units;              // backward: the first units are key tiles, the others row tiles
+  int vec;                    // rows can be read four values at a time
   float scale;
 };
 
-// rows [r0, r0 + 64) of an item's (token, shared head) rows into dst[d][row], zeros past the end
-template <typename T, int DP>
-__device__ __forceinline__ void load_rows(float* dst, const HeadsView& t, int token0, int r0, int rows, int shared,
-                                          int head0, int d) {
-  for (int e = threadIdx.x; e < kTile * DP; e += kFmaThreads) {
-    const int r = e / DP, c = e - r * DP;
-    float v = 0.0f;
-    if (r0 + r < rows && c < d) {
-      const int tok = (r0 + r) / shared, g = (r0 + r) - tok * shared;
-      v = as_f32<T>(reinterpret_cast<const T*>(t.p)[(int64_t)(token0 + tok) * t.token +
-                                                    (int64_t)(head0 + g) * t.head + c]);
+constexpr int pitch_of(int columns) { return columns + 4; }
+constexpr int kScorePitch = pitch_of(kTile);
+
+// values [c, c + 4) of a row of d, zeros past the end
+template <typename T>
+__device__ __forceinline__ float4 load4(const T* row, int c, int d, bool vec) {
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (vec) {
+    if (c < d) {
+      if constexpr (sizeof(T) == 4) {
+        v = __ldg(reinterpret_cast<const float4*>(row + c));
+      } else {
+        const uint2 u = __ldg(reinterpret_cast<const uint2*>(row + c));
+        v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                        __uint_as_float(u.y & 0xffff0000u));
+      }
     }
-    dst[c * kPitch + r] = v;
+    return v;
+  }
+  if (c < d) v.x = as_f32<T>(row[c]);
+  if (c + 1 < d) v.y = as_f32<T>(row[c + 1]);
+  if (c + 2 < d) v.z = as_f32<T>(row[c + 2]);
+  if (c + 3 < d) v.w = as_f32<T>(row[c + 3]);
+  return v;
+}
+template <typename T>
+__device__ __forceinline__ void store4(void* dst, int64_t row, int c, int d, const float (&v)[4]) {
+  T* const p = reinterpret_cast<T*>(dst) + row * d + c;
+  if (d % 4 == 0) {
+    if (c >= d) return;
+    if constexpr (sizeof(T) == 4) *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *reinterpret_cast<uint2*>(p) = make_uint2(tc::pack_bf16(v[0], v[1]), tc::pack_bf16(v[2], v[3]));
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (c + i < d) p[i] = from_f32<T>(v[i]);
+}
+
+// rows [r0, r0 + 64) of an item's (token, shared head) rows, zeros past the end
+template <typename T, int DP>
+__device__ __forceinline__ void load_rows(const FmaArgs& a, float* dst, const HeadsView& t, int token0, int r0,
+                                          int rows, int head0) {
+  constexpr int kQuads = DP / 4;
+#pragma unroll
+  for (int e = threadIdx.x; e < kTile * kQuads; e += kFmaThreads) {
+    const int r = e / kQuads, c = (e % kQuads) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (r0 + r < rows) {
+      const int tok = (r0 + r) / a.shared, g = (r0 + r) - tok * a.shared;
+      v = load4<T>(reinterpret_cast<const T*>(t.p) + (int64_t)(token0 + tok) * t.token + (int64_t)(head0 + g) * t.head,
+                   c, a.d, a.vec);
+    }
+    *reinterpret_cast<float4*>(dst + r * pitch_of(DP) + c) = v;
   }
 }
-// keys [j0, j0 + 64) of head h; a key that is masked or past the end reads as zeros
+// keys [j0, j0 + 64) of head h; a key that is masked or past the end reads as
+// zeros (a masked one's row is fetched beside its mask, and not used)
 template <typename T, int DP>
-__device__ __forceinline__ void load_keys(float* dst, const HeadsView& t, const uint8_t* mask, int key0, int j0,
-                                          int keys, int h, int d) {
-  for (int e = threadIdx.x; e < kTile * DP; e += kFmaThreads) {
-    const int j = e / DP, c = e - j * DP;
-    float v = 0.0f;
-    if (j0 + j < keys && c < d && (!mask || mask[key0 + j0 + j]))
-      v = as_f32<T>(reinterpret_cast<const T*>(t.p)[(int64_t)(key0 + j0 + j) * t.token + (int64_t)h * t.head + c]);
-    dst[c * kPitch + j] = v;
+__device__ __forceinline__ void load_keys(const FmaArgs& a, float* dst, const HeadsView& t, int key0, int j0, int keys,
+                                          int h) {
+  constexpr int kQuads = DP / 4;
+#pragma unroll
+  for (int e = threadIdx.x; e < kTile * kQuads; e += kFmaThreads) {
+    const int j = e / kQuads, c = (e % kQuads) * 4;
+    float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (j0 + j < keys) {
+      const int64_t key = key0 + j0 + j;
+      const bool keep = !a.mask || __ldg(a.mask + key);
+      v = load4<T>(reinterpret_cast<const T*>(t.p) + key * t.token + (int64_t)h * t.head, c, a.d, a.vec);
+      if (!keep) v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    *reinterpret_cast<float4*>(dst + j * pitch_of(DP) + c) = v;
   }
 }
 
-// acc[i][j] = sum_d a[d][4 ty + i] b[d][4 tx + j]
+// acc[i][j] = sum_d a[ty + 16 i][d] b[tx + 16 j][d]
 template <int DP>
 __device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty, int tx, int d, float (&acc)[4][4]) {
+  uint64_t sum[4][4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-#pragma unroll 4
-  for (int c = 0; c < d; ++c) {
-    const float4 u = *reinterpret_cast<const float4*>(a + c * kPitch + 4 * ty);
-    const float4 w = *reinterpret_cast<const float4*>(b + c * kPitch + 4 * tx);
-    const float x[4] = {u.x, u.y, u.z, u.w}, y[4] = {w.x, w.y, w.z, w.w};
+    for (int j = 0; j < 4; ++j) sum[i][j] = tc::pair(0.0f, 0.0f);
+  a += ty * pitch_of(DP);
+  b += tx * pitch_of(DP);
+#pragma unroll 2
+  for (int c = 0; c < d; c += 4) {
+    ulonglong2 x[4], y[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      x[i] = *reinterpret_cast<const ulonglong2*>(a + 16 * i * pitch_of(DP) + c);
+      y[i] = *reinterpret_cast<const ulonglong2*>(b + 16 * i * pitch_of(DP) + c);
+    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(x[i], y[j], acc[i][j]);
+      for (int j = 0; j < 4; ++j) sum[i][j] = tc::fma2(x[i].y, y[j].y, tc::fma2(x[i].x, y[j].x, sum[i][j]));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float lo, hi;
+      tc::unpair(sum[i][j], lo, hi);
+      acc[i][j] = lo + hi;
+    }
 }
 
-// acc[i][n] += sum_t p[t][4 ty + i] x[tx + 16 n][t]
+// acc[i][2 n], acc[i][2 n + 1]: pairs of the columns 4 tx + 64 n .. of row
+// ty + 16 i; adds sum_t p[ty + 16 i][t] x[t][column] over t < count, where p and
+// x hold zeros up to a multiple of 4
 template <int DP>
-__device__ __forceinline__ void tile_accumulate(const float* p, const float* x, int ty, int tx,
-                                                float (&acc)[4][DP / 16]) {
-#pragma unroll 2
-  for (int t = 0; t < kTile; ++t) {
-    const float4 u = *reinterpret_cast<const float4*>(p + t * kPitch + 4 * ty);
-    const float a[4] = {u.x, u.y, u.z, u.w};
+__device__ __forceinline__ void tile_accumulate(const float* p, const float* x, int ty, int tx, int count,
+                                                uint64_t (&acc)[4][DP / 32]) {
+  p += ty * kScorePitch;
+  x += 4 * tx;
+  for (int t = 0; t < count; t += 4) {
+    float4 u[4];
 #pragma unroll
-    for (int n = 0; n < DP / 16; ++n) {
-      const float w = x[(tx + 16 * n) * kPitch + t];
+    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(p + 16 * i * kScorePitch + t);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[i][n] = fmaf(a[i], w, acc[i][n]);
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+      for (int n = 0; n < DP / 64; ++n) {
+        const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(x + (t + k) * pitch_of(DP) + 64 * n);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float f = k == 0 ? u[i].x : k == 1 ? u[i].y : k == 2 ? u[i].z : u[i].w;
+          const uint64_t ff = tc::pair(f, f);
+          acc[i][2 * n] = tc::fma2(ff, w.x, acc[i][2 * n]);
+          acc[i][2 * n + 1] = tc::fma2(ff, w.y, acc[i][2 * n + 1]);
+        }
+      }
     }
   }
+}
+template <int DP>
+__device__ __forceinline__ void clear(uint64_t (&acc)[4][DP / 32]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int n = 0; n < DP / 32; ++n) acc[i][n] = tc::pair(0.0f, 0.0f);
+}
+// four columns of a row's results, times f
+__device__ __forceinline__ void columns(uint64_t lo, uint64_t hi, float f, float (&v)[4]) {
+  tc::unpair(lo, v[0], v[1]);
+  tc::unpair(hi, v[2], v[3]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] *= f;
 }
 
 // true when key j0 + j of the item takes part
@@ -146,52 +248,57 @@ struct FmaUnit {
   int b, tile, h, split, q0, rows, key0, keys;
 };
 // Units of an item: tile fastest (neighbours read the same keys), then key
-// head, then split.
-__device__ __forceinline__ FmaUnit fma_unit(const FmaArgs& a, int u, bool by_keys) {
+// head, then split.  `array` holds the items' first units.
+__device__ __forceinline__ FmaUnit fma_unit(const FmaArgs& a, int u, int array) {
   FmaUnit w;
-  w.b = a.items.item_of(u);
+  w.b = a.items.find(array, u);
   w.q0 = a.items.q0(w.b);
   w.rows = (a.items.q0(w.b + 1) - w.q0) * a.shared;
   w.key0 = a.items.k0(w.b);
   w.keys = a.items.k0(w.b + 1) - w.key0;
-  const int tiles = ((by_keys ? w.keys : w.rows) + kTile - 1) / kTile;
-  int i = u - a.items.u0(w.b);
+  const int tiles = ((array == kItemTile ? w.keys : w.rows) + kTile - 1) / kTile;
+  int i = u - a.items.at(array, w.b);
   w.tile = i % tiles;
   i /= tiles;
   w.h = i % a.kv_heads;
   w.split = i / a.kv_heads;
   return w;
 }
+__device__ __forceinline__ int64_t row_of(const FmaArgs& a, const FmaUnit& w, int r) {
+  const int tok = r / a.shared, g = r - tok * a.shared;
+  return (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+}
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kFmaThreads) k_attn_fma(const __grid_constant__ FmaArgs a) {
+__global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma(const __grid_constant__ FmaArgs a) {
   extern __shared__ __align__(16) float sm[];
-  float *qs = sm, *ks = qs + DP * kPitch, *vs = ks + DP * kPitch, *ps = vs + DP * kPitch;
+  constexpr int kOperand = kTile * pitch_of(DP);
+  float *qs = sm, *ks = qs + kOperand, *vs = ks + kOperand, *ps = vs + kOperand;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const FmaUnit w = fma_unit(a, blockIdx.x, false);
+  const FmaUnit w = fma_unit(a, blockIdx.x, kItemUnit);
   const int r0 = w.tile * kTile;
-  load_rows<T, DP>(qs, a.q, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
-  float acc[4][DP / 16], top[4], total[4];
+  load_rows<T, DP>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
+  uint64_t acc[4][DP / 32];
+  clear<DP>(acc);
+  float top[4], total[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     top[i] = -INFINITY;
     total[i] = 0.0f;
-#pragma unroll
-    for (int n = 0; n < DP / 16; ++n) acc[i][n] = 0.0f;
   }
   const int kt = (w.keys + kTile - 1) / kTile;
   const int t0 = (int)((int64_t)kt * w.split / a.splits), t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
   for (int t = t0; t < t1; ++t) {
     const int j0 = t * kTile;
     __syncthreads();
-    load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
-    load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
+    load_keys<T, DP>(a, ks, a.k, w.key0, j0, w.keys, w.h);
+    load_keys<T, DP>(a, vs, a.v, w.key0, j0, w.keys, w.h);
+    bool keep[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
     __syncthreads();
     float s[4][4];
     tile_dot<DP>(qs, ks, ty, tx, a.d, s);
-    bool keep[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + 4 * tx + j, w.keys);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       float m = -INFINITY;
@@ -208,28 +315,30 @@ __global__ void __launch_bounds__(kFmaThreads) k_attn_fma(const __grid_constant_
       for (int j = 0; j < 4; ++j) {
         s[i][j] = expf(s[i][j] - base);
         add += s[i][j];
-        ps[(4 * tx + j) * kPitch + 4 * ty + i] = s[i][j];
+        ps[(ty + 16 * i) * kScorePitch + tx + 16 * j] = s[i][j];
       }
       top[i] = m;
       total[i] = total[i] * fade + sum16(add);
 #pragma unroll
-      for (int n = 0; n < DP / 16; ++n) acc[i][n] *= fade;
+      for (int n = 0; n < DP / 32; ++n) acc[i][n] = tc::mul2(acc[i][n], tc::pair(fade, fade));
     }
     __syncthreads();
-    tile_accumulate<DP>(ps, vs, ty, tx, acc);
+    tile_accumulate<DP>(ps, vs, ty, tx, min(kTile, w.keys - j0), acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 4 * ty + i;
+    const int r = r0 + ty + 16 * i;
     if (r >= w.rows) continue;
-    const int tok = r / a.shared, g = r - tok * a.shared;
-    const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+    const int64_t row = row_of(a, w, r);
+    float v[4];
     if (a.splits == 1) {
       const float inv = total[i] > 0.0f ? 1.0f / total[i] : 0.0f;
       if (tx == 0) a.lse[row] = top[i] + logf(total[i]);
 #pragma unroll
-      for (int n = 0; n < DP / 16; ++n)
-        if (tx + 16 * n < a.d) reinterpret_cast<T*>(a.out)[row * a.d + tx + 16 * n] = from_f32<T>(acc[i][n] * inv);
+      for (int n = 0; n < DP / 64; ++n) {
+        columns(acc[i][2 * n], acc[i][2 * n + 1], inv, v);
+        store4<T>(a.out, row, 4 * tx + 64 * n, a.d, v);
+      }
     } else {
       const int64_t at = (int64_t)w.split * a.nq * a.heads + row;
       if (tx == 0) {
@@ -237,8 +346,10 @@ __global__ void __launch_bounds__(kFmaThreads) k_attn_fma(const __grid_constant_
         a.total[at] = total[i];
       }
 #pragma unroll
-      for (int n = 0; n < DP / 16; ++n)
-        if (tx + 16 * n < a.d) a.part[at * a.d + tx + 16 * n] = acc[i][n];
+      for (int n = 0; n < DP / 64; ++n) {
+        columns(acc[i][2 * n], acc[i][2 * n + 1], 1.0f, v);
+        store4<float>(a.part, at, 4 * tx + 64 * n, a.d, v);
+      }
     }
   }
 }
@@ -259,123 +370,140 @@ __device__ __forceinline__ void row_constants(const FmaArgs& a, const FmaUnit& w
   *lse = -INFINITY;
   *delta = 0.0f;
   if (r < w.rows) {
-    const int tok = r / a.shared, g = r - tok * a.shared;
-    const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+    const int64_t row = row_of(a, w, r);
     *lse = __ldg(a.lse_in + row);
     *delta = __ldg(a.delta + row);
   }
 }
 
+// dq of one tile of rows over a range of key tiles
 template <typename T, int DP>
-__global__ void __launch_bounds__(kFmaThreads) k_attn_fma_dq(const __grid_constant__ FmaArgs a) {
-  extern __shared__ __align__(16) float sm[];
-  float *qs = sm, *os = qs + DP * kPitch, *ks = os + DP * kPitch, *vs = ks + DP * kPitch, *ps = vs + DP * kPitch;
+__device__ __forceinline__ void fma_dq(const FmaArgs& a, float* sm, int unit) {
+  constexpr int kOperand = kTile * pitch_of(DP);
+  float *qs = sm, *os = qs + kOperand, *ks = os + kOperand, *vs = ks + kOperand, *ps = vs + kOperand;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const FmaUnit w = fma_unit(a, blockIdx.x, false);
+  const FmaUnit w = fma_unit(a, unit, kItemUnit);
   const int r0 = w.tile * kTile;
-  load_rows<T, DP>(qs, a.q, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
-  load_rows<T, DP>(os, a.dout, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
-  float acc[4][DP / 16], lse[4], delta[4];
+  load_rows<T, DP>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
+  load_rows<T, DP>(a, os, a.dout, w.q0, r0, w.rows, w.h * a.shared);
+  uint64_t acc[4][DP / 32];
+  clear<DP>(acc);
+  float lse[4], delta[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    row_constants(a, w, r0 + 4 * ty + i, &lse[i], &delta[i]);
-#pragma unroll
-    for (int n = 0; n < DP / 16; ++n) acc[i][n] = 0.0f;
-  }
+  for (int i = 0; i < 4; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
   const int kt = (w.keys + kTile - 1) / kTile;
   const int t0 = (int)((int64_t)kt * w.split / a.splits), t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
   for (int t = t0; t < t1; ++t) {
     const int j0 = t * kTile;
     __syncthreads();
-    load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
-    load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
+    load_keys<T, DP>(a, ks, a.k, w.key0, j0, w.keys, w.h);
+    load_keys<T, DP>(a, vs, a.v, w.key0, j0, w.keys, w.h);
+    bool keep[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
     __syncthreads();
     float s[4][4], dp[4][4];
-    bool keep[4];
     tile_dot<DP>(qs, ks, ty, tx, a.d, s);
     tile_dot<DP>(os, vs, ty, tx, a.d, dp);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + 4 * tx + j, w.keys);
     tile_gradient(a, s, dp, keep, lse, delta);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ps[(4 * tx + j) * kPitch + 4 * ty + i] = dp[i][j];
+      for (int j = 0; j < 4; ++j) ps[(ty + 16 * i) * kScorePitch + tx + 16 * j] = dp[i][j];
     __syncthreads();
-    tile_accumulate<DP>(ps, ks, ty, tx, acc);
+    tile_accumulate<DP>(ps, ks, ty, tx, min(kTile, w.keys - j0), acc);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = r0 + 4 * ty + i;
+    const int r = r0 + ty + 16 * i;
     if (r >= w.rows) continue;
-    const int tok = r / a.shared, g = r - tok * a.shared;
-    const int64_t row = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
+    const int64_t row = row_of(a, w, r);
 #pragma unroll
-    for (int n = 0; n < DP / 16; ++n) {
-      if (tx + 16 * n >= a.d) continue;
-      if (a.splits == 1) reinterpret_cast<T*>(a.out)[row * a.d + tx + 16 * n] = from_f32<T>(acc[i][n]);
-      else a.part[((int64_t)w.split * a.nq * a.heads + row) * a.d + tx + 16 * n] = acc[i][n];
+    for (int n = 0; n < DP / 64; ++n) {
+      float v[4];
+      columns(acc[i][2 * n], acc[i][2 * n + 1], 1.0f, v);
+      if (a.splits == 1) store4<T>(a.out, row, 4 * tx + 64 * n, a.d, v);
+      else store4<float>(a.part, (int64_t)w.split * a.nq * a.heads + row, 4 * tx + 64 * n, a.d, v);
     }
   }
 }
 
-// dk and dv of one tile of keys over a range of row tiles.
+// dk and dv of one tile of keys over a range of row tiles; the scores go to
+// shared memory with the keys in rows
 template <typename T, int DP>
-__global__ void __launch_bounds__(kFmaThreads) k_attn_fma_dkv(const __grid_constant__ FmaArgs a) {
-  extern __shared__ __align__(16) float sm[];
-  float *qs = sm, *os = qs + DP * kPitch, *ks = os + DP * kPitch, *vs = ks + DP * kPitch, *ps = vs + DP * kPitch,
-        *ds = ps + kTile * kPitch;
+__device__ __forceinline__ void fma_dkv(const FmaArgs& a, float* sm, int unit) {
+  constexpr int kOperand = kTile * pitch_of(DP);
+  float *qs = sm, *os = qs + kOperand, *ks = os + kOperand, *vs = ks + kOperand, *ps = vs + kOperand,
+        *ds = ps + kTile * kScorePitch;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const FmaUnit w = fma_unit(a, blockIdx.x, true);
+  const FmaUnit w = fma_unit(a, unit, kItemTile);
   const int j0 = w.tile * kTile;
-  load_keys<T, DP>(ks, a.k, a.mask, w.key0, j0, w.keys, w.h, a.d);
-  load_keys<T, DP>(vs, a.v, a.mask, w.key0, j0, w.keys, w.h, a.d);
-  float dk[4][DP / 16], dv[4][DP / 16];
+  load_keys<T, DP>(a, ks, a.k, w.key0, j0, w.keys, w.h);
+  load_keys<T, DP>(a, vs, a.v, w.key0, j0, w.keys, w.h);
+  uint64_t dk[4][DP / 32], dv[4][DP / 32];
+  clear<DP>(dk);
+  clear<DP>(dv);
   bool keep[4], keep_out[4];  // of the scores' columns, of the rows written
-
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    keep[i] = kept(a, w.key0, j0 + 4 * tx + i, w.keys);
-    keep_out[i] = kept(a, w.key0, j0 + 4 * ty + i, w.keys);
-#pragma unroll
-    for (int n = 0; n < DP / 16; ++n) dk[i][n] = dv[i][n] = 0.0f;
+    keep[i] = kept(a, w.key0, j0 + tx + 16 * i, w.keys);
+    keep_out[i] = kept(a, w.key0, j0 + ty + 16 * i, w.keys);
   }
   const int rt = (w.rows + kTile - 1) / kTile;
-  const int t0 = (int)((int64_t)rt * w.split / a.splits), t1 = (int)((int64_t)rt * (w.split + 1) / a.splits);
+  const int t0 = (int)((int64_t)rt * w.split / a.key_splits), t1 = (int)((int64_t)rt * (w.split + 1) / a.key_splits);
   for (int t = t0; t < t1; ++t) {
     const int r0 = t * kTile;
     __syncthreads();
-    load_rows<T, DP>(qs, a.q, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
-    load_rows<T, DP>(os, a.dout, w.q0, r0, w.rows, a.shared, w.h * a.shared, a.d);
+    load_rows<T, DP>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
+    load_rows<T, DP>(a, os, a.dout, w.q0, r0, w.rows, w.h * a.shared);
+    float lse[4], delta[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
     __syncthreads();
-    float s[4][4], dp[4][4], lse[4], delta[4];
+    float s[4][4], dp[4][4];
     tile_dot<DP>(qs, ks, ty, tx, a.d, s);
     tile_dot<DP>(os, vs, ty, tx, a.d, dp);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) row_constants(a, w, r0 + 4 * ty + i, &lse[i], &delta[i]);
     tile_gradient(a, s, dp, keep, lse, delta);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      *reinterpret_cast<float4*>(ps + (4 * ty + i) * kPitch + 4 * tx) = make_float4(s[i][0], s[i][1], s[i][2], s[i][3]);
-      *reinterpret_cast<float4*>(ds + (4 * ty + i) * kPitch + 4 * tx) =
-          make_float4(dp[i][0], dp[i][1], dp[i][2], dp[i][3]);
-    }
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ps[(tx + 16 * j) * kScorePitch + ty + 16 * i] = s[i][j];
+        ds[(tx + 16 * j) * kScorePitch + ty + 16 * i] = dp[i][j];
+      }
     __syncthreads();
-    tile_accumulate<DP>(ps, os, ty, tx, dv);
-    tile_accumulate<DP>(ds, qs, ty, tx, dk);
+    const int count = min(kTile, w.rows - r0);
+    tile_accumulate<DP>(ps, os, ty, tx, count, dv);
+    tile_accumulate<DP>(ds, qs, ty, tx, count, dk);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int j = j0 + 4 * ty + i;
+    const int j = j0 + ty + 16 * i;
     if (j >= w.keys) continue;
-    const int64_t at = ((int64_t)w.split * a.nk + w.key0 + j) * a.kv_heads + w.h;
+    const int64_t row = (int64_t)(w.key0 + j) * a.kv_heads + w.h, at = (int64_t)w.split * a.nk * a.kv_heads + row;
 #pragma unroll
-    for (int n = 0; n < DP / 16; ++n)
-      if (tx + 16 * n < a.d) {
-        a.dk_part[at * a.d + tx + 16 * n] = keep_out[i] ? dk[i][n] : 0.0f;
-        a.dv_part[at * a.d + tx + 16 * n] = keep_out[i] ? dv[i][n] : 0.0f;
+    for (int n = 0; n < DP / 64; ++n) {
+      float v[4], u[4];
+      columns(dk[i][2 * n], dk[i][2 * n + 1], 1.0f, v);
+      columns(dv[i][2 * n], dv[i][2 * n + 1], 1.0f, u);
+      if (!keep_out[i]) v[0] = v[1] = v[2] = v[3] = u[0] = u[1] = u[2] = u[3] = 0.0f;
+      if (a.key_splits == 1) {
+        store4<T>(a.dk, row, 4 * tx + 64 * n, a.d, v);
+        store4<T>(a.dv, row, 4 * tx + 64 * n, a.d, u);
+      } else {
+        store4<float>(a.dk_part, at, 4 * tx + 64 * n, a.d, v);
+        store4<float>(a.dv_part, at, 4 * tx + 64 * n, a.d, u);
       }
+    }
   }
+}
+
+// The blocks of the key tiles, which take longer, come first.
+template <typename T, int DP>
+__global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma_bwd(const __grid_constant__ FmaArgs a) {
+  extern __shared__ __align__(16) float sm[];
+  if ((int)blockIdx.x < a.key_units) fma_dkv<T, DP>(a, sm, blockIdx.x);
+  else fma_dq<T, DP>(a, sm, blockIdx.x - a.key_units);
 }
 
 // ---------------------------------------------------------------- reductions
@@ -411,11 +539,22 @@ __global__ void __launch_bounds__(kFmaThreads) k_attn_join(const float* __restri
     if (lane + 32 * i < d) out[row * d + lane + 32 * i] = from_f32<T>(acc[i] * inv);
 }
 
+// Up to three arrays (blockIdx.y), each the sum of partial results in their order.
+struct SumArgs {
+  const float* part[3];
+  void* dst[3];
+  int64_t n[3];
+  int splits[3];
+};
 template <typename T>
-__global__ void __launch_bounds__(kFmaThreads) k_attn_sum(const float* __restrict__ part, int splits, int64_t n,
-                                                          T* __restrict__ dst) {
+__global__ void __launch_bounds__(kFmaThreads) k_attn_sum(const __grid_constant__ SumArgs a) {
+  const float* const part = a.part[blockIdx.y];
+  const int64_t n = a.n[blockIdx.y];
+  T* const dst = reinterpret_cast<T*>(a.dst[blockIdx.y]);
+  const int splits = a.splits[blockIdx.y];
   for (int64_t i = (int64_t)blockIdx.x * kFmaThreads + threadIdx.x; i < n; i += (int64_t)gridDim.x * kFmaThreads) {
     float s = 0.0f;
+#pragma unroll 8
     for (int k = 0; k < splits; ++k) s += __ldg(part + k * n + i);
     dst[i] = from_f32<T>(s);
   }
@@ -547,6 +686,11 @@ int pick_splits(const AttnCall& c, bool by_keys, int sms) {
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, longest, 32}));
 }
 
+// four values at a time: 16 bytes of fp32, 8 of bf16
+bool loads4(const AttnCall& c, const HeadsView& t) {
+  return reinterpret_cast<uintptr_t>(t.p) % (4 * elem_size(c.dt)) == 0 && t.token % 4 == 0 && t.head % 4 == 0;
+}
+
 FmaArgs fma_args(const AttnCall& c) {
   FmaArgs a = {};
   a.q = c.q;
@@ -560,6 +704,7 @@ FmaArgs fma_args(const AttnCall& c) {
   a.kv_heads = c.kv_heads;
   a.shared = c.shared;
   a.d = c.d;
+  a.vec = c.d % 4 == 0 && loads4(c, c.q) && loads4(c, c.k) && loads4(c, c.v) && loads4(c, c.dout);
   a.scale = c.scale;
   return a;
 }
@@ -571,8 +716,9 @@ fvx_status fma_launch(const char* name, K kernel, int64_t units, size_t smem, cu
   kernel<<<(unsigned)units, kFmaThreads, smem, s>>>(a);
   return check_launch(name);
 }
+// bytes of `operands` tiles of 64 rows and `tiles` of scores
 constexpr size_t fma_smem(int dp, int operands, int tiles) {
-  return (size_t)(dp * operands + kTile * tiles) * kPitch * 4;
+  return (size_t)kTile * (pitch_of(dp) * operands + kScorePitch * tiles) * 4;
 }
 
 template <typename T, int DP>
@@ -600,30 +746,43 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
   FmaArgs a = fma_args(c);
   a.delta = delta;
   a.lse_in = c.lse;
-  int64_t units = 0;
-  {
-    a.splits = pick_splits(c, false, sms);
-    const std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &units);
-    FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
-    a.out = c.dq;
-    const int64_t values = c.nq * c.heads * c.d;
-    if (a.splits > 1 && !(a.part = scr.get<float>((size_t)a.splits * values))) return FVX_ERR_ALLOC;
-    if (units > 0) {
-      FVX_TRY(fma_launch("attn_fma_dq", k_attn_fma_dq<T, DP>, units, fma_smem(DP, 4, 1), s, a));
-      if (a.splits > 1) FVX_TRY(attn_sum(c.dt, a.part, a.splits, values, c.dq, s));
-    }
+  a.out = c.dq;
+  a.dk = c.dk;
+  a.dv = c.dv;
+  a.splits = pick_splits(c, false, sms);
+  a.key_splits = pick_splits(c, true, sms);
+  int64_t row_units = 0, key_units = 0;
+  std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &row_units);
+  const std::vector<int32_t> by_keys = unit_prefix(c, true, a.key_splits, &key_units);
+  prefix.insert(prefix.end(), by_keys.begin(), by_keys.end());
+  FVX_TRY(attn_items(c, prefix.data(), 4, s, scr, &a.items));
+  a.key_units = (int)key_units;
+  const int64_t q_values = c.nq * c.heads * c.d, k_values = c.nk * c.kv_heads * c.d;
+  if (a.splits > 1 && !(a.part = scr.get<float>((size_t)a.splits * q_values))) return FVX_ERR_ALLOC;
+  if (a.key_splits > 1 && k_values > 0) {
+    a.dk_part = scr.get<float>((size_t)a.key_splits * k_values);
+    a.dv_part = scr.get<float>((size_t)a.key_splits * k_values);
+    if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
   }
-  a.splits = pick_splits(c, true, sms);
-  const std::vector<int32_t> prefix = unit_prefix(c, true, a.splits, &units);
-  if (units == 0) return FVX_OK;
-  FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
-  const int64_t values = c.nk * c.kv_heads * c.d;
-  a.dk_part = scr.get<float>((size_t)a.splits * values);
-  a.dv_part = scr.get<float>((size_t)a.splits * values);
-  if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
-  FVX_TRY(fma_launch("attn_fma_dkv", k_attn_fma_dkv<T, DP>, units, fma_smem(DP, 4, 2), s, a));
-  FVX_TRY(attn_sum(c.dt, a.dk_part, a.splits, values, c.dk, s));
-  return attn_sum(c.dt, a.dv_part, a.splits, values, c.dv, s);
+  FVX_TRY(fma_launch("attn_fma_bwd", k_attn_fma_bwd<T, DP>, key_units + row_units, fma_smem(DP, 4, 2), s, a));
+  SumArgs sum = {};
+  int arrays = 0;
+  auto add = [&](const float* part, void* dst, int64_t n, int splits) {
+    if (splits == 1 || n == 0) return;
+    sum.part[arrays] = part;
+    sum.dst[arrays] = dst;
+    sum.n[arrays] = n;
+    sum.splits[arrays++] = splits;
+  };
+  add(a.part, c.dq, q_values, a.splits);
+  add(a.dk_part, c.dk, k_values, a.key_splits);
+  add(a.dv_part, c.dv, k_values, a.key_splits);
+  if (arrays == 0) return FVX_OK;
+  const int64_t longest = std::max(sum.n[0], std::max(sum.n[1], sum.n[2]));
+  const dim3 grid((unsigned)std::min<int64_t>((longest + kFmaThreads - 1) / kFmaThreads, sms * 16), (unsigned)arrays);
+  LaunchScope ls("attn_sum", s);
+  k_attn_sum<T><<<grid, kFmaThreads, 0, s>>>(sum);
+  return check_launch("attn_sum");
 }
 
 template <typename F>
@@ -672,15 +831,6 @@ fvx_status attn_join(const AttnCall& c, const float* part, const float* top, con
     k_attn_join<__nv_bfloat16>
         <<<grid, kFmaThreads, 0, s>>>(part, top, total, splits, rows, c.d, (__nv_bfloat16*)c.out, c.lse);
   return check_launch("attn_join");
-}
-
-fvx_status attn_sum(fvx_dtype dt, const float* part, int splits, int64_t n, void* dst, cudaStream_t s) {
-  if (n == 0) return FVX_OK;
-  const unsigned grid = (unsigned)std::min<int64_t>((n + kFmaThreads - 1) / kFmaThreads, 152 * 16);
-  LaunchScope ls("attn_sum", s);
-  if (dt == FVX_F32) k_attn_sum<float><<<grid, kFmaThreads, 0, s>>>(part, splits, n, (float*)dst);
-  else k_attn_sum<__nv_bfloat16><<<grid, kFmaThreads, 0, s>>>(part, splits, n, (__nv_bfloat16*)dst);
-  return check_launch("attn_sum");
 }
 
 }  // namespace fvx

@@ -85,7 +85,5 @@ fvx_status attn_items(const AttnCall& c, const int32_t* more, int arrays, cudaSt
 // out = softmax-weighted join of `splits` partial results over ranges of keys
 fvx_status attn_join(const AttnCall& c, const float* part, const float* top, const float* total, int splits,
                      cudaStream_t s);
-// dst[i] = sum over splits of part[split][i], n values
-fvx_status attn_sum(fvx_dtype dt, const float* part, int splits, int64_t n, void* dst, cudaStream_t s);
 
 }  // namespace fvx
