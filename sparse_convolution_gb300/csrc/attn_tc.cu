@@ -1315,82 +1315,70 @@ __global__ void __launch_bounds__(256) k_attn_stats(const __grid_constant__ Attn
   }
 }
 
-// dQ out of its workspace: the key ranges' sums added in order, scaled and
-// rounded; one block per row tile and key head.  Items of one key tile were
-// written by the main kernel; items without keys get zeros.
-template <int DP>
-__global__ void __launch_bounds__(256) k_attn_dq_out(const __grid_constant__ BwdArgs a) {
-  const int tile = blockIdx.x / a.kv_heads, kh = blockIdx.x - tile * a.kv_heads;
-  const int b = a.items.find(kItemTile, tile);
-  const int q0 = a.items.q0(b), rows = (a.items.q0(b + 1) - q0) * a.shared;
-  const int keys = a.items.k0(b + 1) - a.items.k0(b);
-  if (keys > 0 && keys <= kM) return;
-  const int ranges = keys > 0 ? a.items.at(kItemKeys, b) : 0;
-  const int64_t slab = (int64_t)a.tiles * a.kv_heads * (kM * DP);
-  const float* src = a.dq_sum + (int64_t)blockIdx.x * (kM * DP);
-  const int row = threadIdx.x & 127;
-  const int r = (tile - a.items.at(kItemTile, b)) * a.tile_rows + row;
-  if (row >= a.tile_rows || r >= rows) return;
-  const int tok = r / a.shared, g = r - tok * a.shared;
-  __nv_bfloat16* out = a.dq + ((int64_t)(q0 + tok) * a.heads + kh * a.shared + g) * a.d;
-  for (int cc = (threadIdx.x >> 7) * 8; cc < a.d; cc += 16) {
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < ranges; ++k) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4) * (kM * 4) + row * 4));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4 + 1) * (kM * 4) + row * 4));
-      s[0] += x.x;
-      s[1] += x.y;
-      s[2] += x.z;
-      s[3] += x.w;
-      s[4] += y.x;
-      s[5] += y.y;
-      s[6] += y.z;
-      s[7] += y.w;
-    }
-    uint4 v;
-    uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x] * a.scale, s[2 * x + 1] * a.scale);
-    *reinterpret_cast<uint4*>(out + cc) = v;
-  }
+// What the main kernel left as partial sums in fp32, added in the order of their
+// ranges, scaled and rounded: the first blocks dQ, one per row tile and key
+// head (items of one key tile were written by the main kernel, items without
+// keys get zeros), the others dK and dV, one per key tile, key head and 8
+// columns (items whose rows were not cut were written; items without rows get
+// zeros).  A thread has the loads of a whole range under way at once.
+__device__ __forceinline__ void add_parts(float (&s)[8], const float* src) {
+  const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src + kM * 4));
+  s[0] += x.x;
+  s[1] += x.y;
+  s[2] += x.z;
+  s[3] += x.w;
+  s[4] += y.x;
+  s[5] += y.y;
+  s[6] += y.z;
+  s[7] += y.w;
 }
-
-// dK and dV of the items whose rows were cut into ranges: the ranges' parts
-// added in order, one block per key tile and key head.  Items without rows get
-// zeros.
+__device__ __forceinline__ void store_rounded(__nv_bfloat16* dst, const float (&s)[8], float scale) {
+  uint4 v;
+  uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+  for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x] * scale, s[2 * x + 1] * scale);
+  *reinterpret_cast<uint4*>(dst) = v;
+}
 template <int DP>
-__global__ void __launch_bounds__(256) k_attn_dkv_out(const __grid_constant__ BwdArgs a) {
-  const int tile = blockIdx.x / a.kv_heads, kh = blockIdx.x - tile * a.kv_heads;
+__global__ void __launch_bounds__(256) k_attn_sums_out(const __grid_constant__ BwdArgs a, int row_blocks) {
+  const int row = threadIdx.x & 127;
+  if ((int)blockIdx.x < row_blocks) {
+    const int tile = blockIdx.x / a.kv_heads, kh = blockIdx.x - tile * a.kv_heads;
+    const int b = a.items.find(kItemTile, tile);
+    const int q0 = a.items.q0(b), rows = (a.items.q0(b + 1) - q0) * a.shared;
+    const int keys = a.items.k0(b + 1) - a.items.k0(b);
+    if (keys > 0 && keys <= kM) return;
+    const int ranges = keys > 0 ? a.items.at(kItemKeys, b) : 0;
+    const int64_t slab = (int64_t)a.tiles * a.kv_heads * (kM * DP);
+    const int r = (tile - a.items.at(kItemTile, b)) * a.tile_rows + row;
+    if (row >= a.tile_rows || r >= rows) return;
+    const int tok = r / a.shared, g = r - tok * a.shared, c0 = (threadIdx.x >> 7) * 8;
+    const float* src = a.dq_sum + (int64_t)blockIdx.x * (kM * DP) + c0 * kM + row * 4;
+    __nv_bfloat16* out = a.dq + ((int64_t)(q0 + tok) * a.heads + kh * a.shared + g) * a.d;
+    float s[DP / 16][8] = {};
+    for (int k = 0; k < ranges; ++k, src += slab)
+#pragma unroll
+      for (int i = 0; i < DP / 16; ++i)
+        if (c0 + 16 * i < a.d) add_parts(s[i], src + i * 16 * kM);
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i)
+      if (c0 + 16 * i < a.d) store_rounded(out + c0 + 16 * i, s[i], a.scale);
+    return;
+  }
+  const int block = blockIdx.x - row_blocks, part = block / (DP / 8), c0 = (block - part * (DP / 8)) * 8;
+  const int tile = part / a.kv_heads, kh = part - tile * a.kv_heads;
   const int b = a.items.find(kItemKeyTile, tile);
   const int ranges = a.items.at(kItemRows, b);
-  if (ranges == 1) return;
   const int key0 = a.items.k0(b), keys = a.items.k0(b + 1) - key0;
-  const int row = threadIdx.x & 127, j = (tile - a.items.at(kItemKeyTile, b)) * kM + row;
-  if (j >= keys) return;
+  const int j = (tile - a.items.at(kItemKeyTile, b)) * kM + row;
+  if (ranges == 1 || j >= keys || c0 >= a.d) return;
   const bool second = threadIdx.x >= 128;
   const int64_t slab = (int64_t)a.key_tiles * a.kv_heads * (kM * DP);
-  const float* src = (second ? a.dv_part : a.dk_part) + (int64_t)blockIdx.x * (kM * DP) + row * 4;
-  __nv_bfloat16* out = (second ? a.dv : a.dk) + ((int64_t)(key0 + j) * a.kv_heads + kh) * a.d;
-  for (int cc = blockIdx.y * 8; cc < a.d; cc += 8 * gridDim.y) {
-    float s[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-    for (int k = 0; k < ranges; ++k) {
-      const float4 x = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4) * (kM * 4)));
-      const float4 y = __ldg(reinterpret_cast<const float4*>(src + k * slab + (cc / 4 + 1) * (kM * 4)));
-      s[0] += x.x;
-      s[1] += x.y;
-      s[2] += x.z;
-      s[3] += x.w;
-      s[4] += y.x;
-      s[5] += y.y;
-      s[6] += y.z;
-      s[7] += y.w;
-    }
-    uint4 v;
-    uint32_t* pv = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-    for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x], s[2 * x + 1]);
-    *reinterpret_cast<uint4*>(out + cc) = v;
-  }
+  const float* src = (second ? a.dv_part : a.dk_part) + (int64_t)part * (kM * DP) + c0 * kM + row * 4;
+  float s[8] = {};
+#pragma unroll 4
+  for (int k = 0; k < ranges; ++k) add_parts(s, src + k * slab);
+  store_rounded((second ? a.dv : a.dk) + ((int64_t)(key0 + j) * a.kv_heads + kh) * a.d + c0, s, 1.0f);
 }
 
 // ---------------------------------------------------------------- host
@@ -1538,33 +1526,47 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
     single += w > 0 ? c.kv_heads : 0;
   }
   auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
+  // Cycles of a tile of 128 rows by 128 keys and of a key tile (its loads and
+  // its gradients' way out, in fp32 where row ranges add up), measured on units
+  // of 1 to 40 tiles; and of one 128-row slab of partial sums, shared by all.
+  const double tile_cost = c.d <= 64 ? 3500.0 : 7000.0, key_cost = c.d <= 64 ? 5000.0 : 9000.0;
   const double sum_cost = 128.0 * 4 * (c.d <= 64 ? 64 : 128) * c.kv_heads / (sms * 25.0);
-  // Units of 1 / sms of the work each, or a little more, so that they fit in
-  // one wave; with more items than that, one unit per item and key head.
-  for (double room : {1.0, 1.06, 1.15, 1.3, 1.6, 2.0}) {
-    const double target = std::max(1.0, room * (double)work / sms);
+  const double share = std::max((double)work * tile_cost / sms, tile_cost + key_cost);
+  // Main kernel and sums, 17,001 rows on 1024 keys and 15,800 on 1500, 8 heads of
+  // 64: rows in 8 and 11 ranges, keys whole, 406 us; rows in 8 and 5, the second's
+  // keys in 2, 366; rows whole, keys in 8 and 11, 547 (partial sums of dQ past
+  // the L2).  9014 rows x 4 on 77 to 1030 keys, 2 key heads: rows in up to 40
+  // ranges, keys whole, 163 us; in up to 6, keys in up to 9, 89.
+  // The least room above an equal share of the work in which the units fit one
+  // wave; every item then takes the fewest units that stay within it, and among
+  // those the ranges with the least partial sums.  With more items than
+  // multiprocessors, one unit per item and key head.
+  for (double room : {1.0, 1.03, 1.06, 1.1, 1.15, 1.2, 1.3, 1.45, 1.7, 2.1, 3.0, 1e30}) {
+    const double most = single >= sms ? 1e300 : share * room;
     int64_t u = 0;
-    for (int b = 0; b < c.items; ++b) {
+    bool fits = true;
+    for (int b = 0; b < c.items && fits; ++b) {
       const int64_t T = row_tiles(b), K = tiles_of_keys(b);
       rr[b] = kr[b] = 0;
       if (T == 0 || K == 0) continue;
-      int64_t want = single >= sms ? 1 : std::max<int64_t>(1, (int64_t)((double)(T * K) / target + 0.999));
-      want = std::min(want, T * K);
       double best = 1e300;
-      for (int64_t r = 1; r <= std::min(T, want); ++r) {
-        if (r > 24 && r < std::min(T, want)) continue;  // a long tail of small differences
-        const int64_t k = std::min(K, ceil_div(want, r));
-        const double cost = (double)(ceil_div(T, r) * ceil_div(K, k)) * 1500.0 + (double)ceil_div(K, k) * (r > 1 ? 5000.0 : 3000.0) +
-                            sum_cost * ((r > 1 ? 4.0 * r * K : 0.0) + (double)(k * T));
+      for (int64_t k = 1; k <= std::min<int64_t>(K, sms); ++k) {
+        const double ck = (double)ceil_div(K, k);
+        const double rows = std::min((double)T, floor((most - ck * key_cost) / (ck * tile_cost)));
+        if (rows < 1.0) continue;
+        const int64_t r = ceil_div(T, (int64_t)rows);
+        if (r * k * c.kv_heads > std::max<int64_t>(sms, c.kv_heads)) continue;
+        const double cost = (double)(r * k) * 1e9 + sum_cost * ((r > 1 ? 4.0 * r * K : 0.0) + (double)(k * T));
         if (cost < best) {
           best = cost;
           rr[b] = (int32_t)r;
           kr[b] = (int32_t)k;
         }
       }
+      fits = rr[b] > 0;
       u += (int64_t)rr[b] * kr[b] * c.kv_heads;
     }
-    if (u <= sms || single >= sms) break;
+    if (fits && (u <= sms || single >= sms)) break;
   }
   int64_t u = 0, t = 0, kt = 0;
   for (int b = 0; b < c.items; ++b) {
@@ -1649,15 +1651,12 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
     k_attn_tc_bwd<DP><<<std::min(a.units, sms), kBwdThreads, C::kSmem, s>>>(a);
     FVX_TRY(check_launch("attn_tc_bwd"));
   }
-  if (p.dq_sums || p.dq_zeros) {
-    LaunchScope ls("attn_dq_out", s);
-    k_attn_dq_out<DP><<<(unsigned)row_blocks, 256, 0, s>>>(a);
-    FVX_TRY(check_launch("attn_dq_out"));
-  }
-  if (p.dkv_parts) {
-    LaunchScope ls("attn_dkv_out", s);
-    k_attn_dkv_out<DP><<<dim3((unsigned)(p.key_tiles * c.kv_heads), DP / 32), 256, 0, s>>>(a);
-    FVX_TRY(check_launch("attn_dkv_out"));
+  const int64_t dq_blocks = p.dq_sums || p.dq_zeros ? (int64_t)row_blocks : 0;
+  const int64_t dkv_blocks = p.dkv_parts ? (int64_t)p.key_tiles * c.kv_heads * (DP / 8) : 0;
+  if (dq_blocks + dkv_blocks > 0) {
+    LaunchScope ls("attn_sums_out", s);
+    k_attn_sums_out<DP><<<(unsigned)(dq_blocks + dkv_blocks), 256, 0, s>>>(a, (int)dq_blocks);
+    FVX_TRY(check_launch("attn_sums_out"));
   }
   return FVX_OK;
 }
