@@ -95,28 +95,20 @@ struct CodeScale {
 __device__ __forceinline__ CodeScale code_scale(uint32_t top_bits) {
   const float top = __uint_as_float(top_bits);
   CodeScale s;
-  if (top_bits >= 0x7f800000u) {
-    s.inv = 0.0f;
-    s.step = __uint_as_float(0x7fc00000u);
-  } else if (top < kTiny) {
-    s.inv = 0.0f;
-    s.step = 0.0f;
-  } else {
-    // Both quotients rounded once, as division does, at a third of its work: a
-    // first quotient by an approximate reciprocal, corrected by its exact
-    // remainder (Markstein 1990; by a constant, Brisebarre, Muller and Raina
-    // 2004).  They equal the division for every fp32 value from 2^-100 to
-    // 2^126 (all compared); beyond, the reciprocal leaves the normal range.
-    if (top < 8.507059173023462e37f) {
-      float y;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(top));
-      const float q = __fmul_rn(127.0f, y);
-      s.inv = __fmaf_rn(__fmaf_rn(-top, q, 127.0f), y, q);
-    } else {
-      s.inv = __fdiv_rn(127.0f, top);
-    }
-    const float q = __fmul_rn(top, 1.0f / 127.0f);
-    s.step = __fmaf_rn(__fmaf_rn(-127.0f, q, top), 1.0f / 127.0f, q);
+  // Both quotients rounded once, as division does, at a third of its work: a
+  // first quotient by an approximate reciprocal, corrected by its exact
+  // remainder (Markstein 1990; by a constant, Brisebarre, Muller and Raina
+  // 2004).  They equal the division for every fp32 value from 2^-100 to
+  // 2^126 (all compared); beyond, the reciprocal leaves the normal range.
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(top));
+  const float p = __fmul_rn(127.0f, y), q = __fmul_rn(top, 1.0f / 127.0f);
+  s.inv = __fmaf_rn(__fmaf_rn(-top, p, 127.0f), y, p);
+  s.step = __fmaf_rn(__fmaf_rn(-127.0f, q, top), 1.0f / 127.0f, q);
+  if (top_bits - __float_as_uint(kTiny) >= 0x7e800000u - __float_as_uint(kTiny)) {  // not in [2^-100, 2^126)
+    if (top < kTiny) s.inv = s.step = 0.0f;
+    else s.inv = top_bits >= 0x7f800000u ? 0.0f : __fdiv_rn(127.0f, top);
+    if (top_bits >= 0x7f800000u) s.step = __uint_as_float(0x7fc00000u);
   }
   return s;
 }
@@ -130,20 +122,21 @@ constexpr float kMagic = 12582912.0f;
 template <int VEC>
 __device__ __forceinline__ void store_codes(int8_t* p, const float (&q)[VEC], bool none) {
   uint32_t bits[VEC];
+  const uint32_t keep = none ? 0u : 0xffffffffu;
 #pragma unroll
-  for (int j = 0; j < VEC; ++j) bits[j] = none ? 0u : __float_as_uint(q[j]);
+  for (int j = 0; j < VEC; ++j) bits[j] = __float_as_uint(q[j]);
   if constexpr (VEC % 4 == 0) {
     uint32_t w[VEC / 4];
 #pragma unroll
     for (int j = 0; j < VEC / 4; ++j)
       w[j] = __byte_perm(__byte_perm(bits[4 * j], bits[4 * j + 1], 0x0040), __byte_perm(bits[4 * j + 2], bits[4 * j + 3], 0x0040),
-                         0x5410);
+                         0x5410) & keep;
     if constexpr (VEC == 8) *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
     else *reinterpret_cast<uint32_t*>(p) = w[0];
   } else {
     Pack<int8_t, VEC> u;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) u.v[j] = (int8_t)(bits[j] & 255u);
+    for (int j = 0; j < VEC; ++j) u.v[j] = (int8_t)(bits[j] & keep & 255u);
     *reinterpret_cast<Pack<int8_t, VEC>*>(p) = u;
   }
 }
@@ -168,24 +161,28 @@ __device__ __forceinline__ void codes_to_float(const Pack<int8_t, VEC>& u, float
 // Group maxima for the codes.  Lane l of a row holds vectors l, l + lanes, ...
 // A group is 2^group_shift values: a run of lanes of one vector index, or (few
 // lanes or narrow vectors) all lanes of 2, 4 or more consecutive indices.
-template <int VEC, int ITER>
-__device__ __forceinline__ void group_tops(uint32_t (&top)[ITER], int group_shift, int lanes) {
-  const int per = (1 << group_shift) / VEC;  // vectors of a group
-  const int width = min(per, lanes);
+template <int PER, int ITER>
+__device__ __forceinline__ void group_tops_of(uint32_t (&top)[ITER], int lanes) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
-    if (o < width) {
+    if (o < PER && o < lanes) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i) top[i] = max(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
     }
 #pragma unroll
   for (int d = 1; d < ITER; d <<= 1) {
-    if (per >= 2 * d * lanes) {
+    if (PER >= 2 * d * lanes) {
 #pragma unroll
       for (int i = 0; i < ITER; ++i)
         if ((i & d) == 0) top[i] = top[i ^ d] = max(top[i], top[i ^ d]);
     }
   }
+}
+template <int VEC, int ITER>
+__device__ __forceinline__ void group_tops(uint32_t (&top)[ITER], int group_shift, int lanes) {
+  if (group_shift == 5) group_tops_of<32 / VEC, ITER>(top, lanes);
+  else if (group_shift == 6) group_tops_of<64 / VEC, ITER>(top, lanes);
+  else group_tops_of<128 / VEC, ITER>(top, lanes);
 }
 
 template <typename T, int VEC>
