@@ -394,9 +394,9 @@ struct RowGrid {
 template <int OP>
 RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
   using Is = OpIs<OP>;
-  const int elem = dt == FVX_F32 ? 4 : 2, per_block = kThreads / a.lanes;
+  const int elem = dt == FVX_F32 ? 4 : 2;
   RowGrid g = {};
-  g.blocks = grid_for(a.n, per_block, sms, Is::kBack ? 4 : 16);
+  g.blocks = grid_for(a.n, kThreads / a.lanes, sms, Is::kBack ? 4 : 16);
   auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   if (vec * elem != 16) return g;
   if (!Is::kFromCodes && !(a.ldx == a.c && at16(a.x))) return g;
@@ -407,6 +407,13 @@ RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
   const int row = x_row + (Is::kBack ? a.c * elem : 0);
   StreamArgs& s = g.args;
   s.r = a;
+  // Two vectors of 16 lanes instead of one of 32 halve the steps of a row's sums
+  // (300,000 x 256 bf16: forward 61 to 55 us, backward 88 to 86; x 200: 64 to
+  // 56; 150,001 x 256 forward with codes 51 both ways, and the same order of the
+  // sums as without codes); from codes the registers of two vectors cost a
+  // block per multiprocessor (150,001 x 256 backward 57 to 74 us).
+  if ((Is::kNorm || OP == kBackward) && dt == FVX_BF16 && a.lanes == 32 && a.c <= 32 * vec) s.r.lanes = 16;
+  const int per_block = kThreads / s.r.lanes;
   // a multiple of the rows of a turn (eight at least: the small arrays' copies
   // are then multiples of 16 bytes), about 10 KB
   s.rows = per_block * std::max(1, 10240 / (per_block * row));
@@ -428,12 +435,14 @@ RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
 template <int OP>
 fvx_status rows_launch(const char* name, fvx_dtype dt, int vec, const RowArgs& a, const RowGrid& g, cudaStream_t s) {
   constexpr bool kBack = OpIs<OP>::kBack;
-  const size_t parts = kBack ? (size_t)(kThreads / a.lanes) * a.c * 4 : 0;  // at most 8 * 1024 or 256 * 8 values
+  const size_t parts = kBack ? (size_t)(kThreads / (g.stream ? g.args.r.lanes : a.lanes)) * a.c * 4 : 0;  // at most 8 * 1024 or 256 * 8 values
   if (g.stream) {
     const size_t smem = 128 + std::max((size_t)kStreamStages * g.args.stage_bytes, parts);
     StreamArgs args = g.args;
+    const int lanes = args.r.lanes;
     args.r = a;
-    return (dt == FVX_F32 ? stream_rows_f32 : stream_rows_bf16)(name, (RowOp)OP, iters_for(a.c, vec), args, g.blocks,
+    args.r.lanes = lanes;
+    return (dt == FVX_F32 ? stream_rows_f32 : stream_rows_bf16)(name, (RowOp)OP, (a.c / vec + lanes - 1) / lanes, args, g.blocks,
                                                                 smem, s);
   }
   return by_row_shape(dt, vec, iters_for(a.c, vec), [&]<typename T, int VEC, int ITER>() -> fvx_status {

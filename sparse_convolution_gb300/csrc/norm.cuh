@@ -289,14 +289,14 @@ struct Rows {
       float f[VEC];
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const int at = (i * 32 + lane) * VEC + j;
+        const int at = (i * lanes + lane) * VEC + j;
         f[j] = a.w && at < a.c ? __ldg(a.w + at) : 1.0f;
       }
       to_pairs<VEC>(f, w[i]);
       if constexpr (!Is::kBack) {
 #pragma unroll
         for (int j = 0; j < VEC; ++j) {
-          const int at = (i * 32 + lane) * VEC + j;
+          const int at = (i * lanes + lane) * VEC + j;
           f[j] = a.b && at < a.c ? __ldg(a.b + at) : 0.0f;
         }
         to_pairs<VEC>(f, b[i]);
@@ -345,7 +345,7 @@ struct Rows {
       group_tops<VEC, ITER>(top, a.group_shift, lanes);
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
-        const int v = i * 32 + lane;
+        const int v = i * lanes + lane;
         if (!live || v >= nv) continue;
         const CodeScale cs = code_scale(top[i]);
         float f[VEC];
@@ -368,7 +368,7 @@ struct Rows {
       const E minus = e_all<E>(-mean);
 #pragma unroll
       for (int i = 0; i < ITER; ++i)
-        if (i * 32 + lane < nv) {
+        if (i * lanes + lane < nv) {
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             const E d = e_add(x[i][j], minus);
@@ -391,7 +391,7 @@ struct Rows {
         float f[VEC];
         widen<T, VEC>(in.dy[i], f);
         to_pairs<VEC>(f, g[i]);
-        if (live && i * 32 + lane < nv) {
+        if (live && i * lanes + lane < nv) {
 #pragma unroll
           for (int j = 0; j < N; ++j) {
             x[i][j] = e_mul(e_add(x[i][j], minus), scale);
@@ -415,7 +415,7 @@ struct Rows {
       T* py = reinterpret_cast<T*>(a.y) + row * a.ldy;
 #pragma unroll
       for (int i = 0; i < ITER; ++i) {
-        const int v = i * 32 + lane;
+        const int v = i * lanes + lane;
         float f[VEC];
         from_pairs<VEC>(x[i], f);
         if (v < nv) store_vec<T, VEC>(py + v * VEC, f);
@@ -434,7 +434,7 @@ struct Rows {
   __device__ __forceinline__ void fetch(In& in, int64_t row, bool live) {
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-      const int v = i * 32 + lane;
+      const int v = i * lanes + lane;
       const bool here = live && v < nv;
       in.step[i] = 0.0f;
       if constexpr (Is::kFromCodes) {
@@ -481,7 +481,7 @@ struct Rows {
           from_pairs<VEC>(pass ? db[i] : dw[i], f);
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int at = (i * 32 + lane) * VEC + j;
+            const int at = (i * lanes + lane) * VEC + j;
             if (at < a.c) sh[sub * a.c + at] = f[j];
           }
         }

@@ -11,12 +11,15 @@ namespace {
 // would hide them (4,000,000 x 64 bf16 backward: 297 us with one row in flight
 // per lane, 307 with two, 461 with the next one fetched early); the copies are
 // under way whatever the warps do.
+// Blocks per multiprocessor: what the registers of a lane's values allow without
+// spills (100,000 x 512 bf16, forward with codes: two 67 us, one 95; backward
+// from codes: two, which spill, 106, one 80).
 constexpr int kStreamThreads = kThreads + 32;
 struct StreamHead {
   uint64_t full[kStreamStages], empty[kStreamStages];
 };
 template <typename T, int VEC, int ITER, int OP, int LANES>
-__global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 8 ? 1 : OpIs<OP>::kBack ? 3 : 4)
+__global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 16 || (VEC * ITER > 8 && OP == kBackwardCodes) ? 1 : VEC * ITER > 8 ? 2 : OpIs<OP>::kBack ? 3 : 4)
     k_rows_stream(const __grid_constant__ StreamArgs s) {
   using Is = OpIs<OP>;
   using X = std::conditional_t<Is::kFromCodes, int8_t, T>;
@@ -82,7 +85,7 @@ __global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 8 ? 1 : OpIs<OP>:
         RowIn<T, VEC, ITER, OP> in;
 #pragma unroll
         for (int k = 0; k < ITER; ++k) {
-          const int v = k * 32 + rows.lane;
+          const int v = k * rows.lanes + rows.lane;
           const bool here = v < rows.nv;
           in.x[k] = here ? raw_vec<X, VEC>(reinterpret_cast<const X*>(from) + r * a.c + v * VEC) : no_vec<X, VEC>();
           in.step[k] = 0.0f;
@@ -125,6 +128,8 @@ fvx_status launch_stream(const char* name, const StreamArgs& a, int blocks, size
 template <typename T, int OP>
 fvx_status by_shape(const char* name, int iters, const StreamArgs& a, int blocks, size_t smem, cudaStream_t s) {
   if (iters > 2) return launch_stream<T, 16 / sizeof(T) == 8 ? 4 : 8, OP, 32>(name, a, blocks, smem, s);
+  if constexpr (sizeof(T) == 2 && (OpIs<OP>::kNorm || OP == kBackward))
+    if (iters == 2 && a.r.lanes == 16) return launch_stream<T, 2, OP, 16>(name, a, blocks, smem, s);
   if (iters == 2) return launch_stream<T, 2, OP, 32>(name, a, blocks, smem, s);
   switch (a.r.lanes) {
     case 1: return launch_stream<T, 1, OP, 1>(name, a, blocks, smem, s);
