@@ -24,6 +24,12 @@
 // is brought to a new maximum only when that exceeds m_ref by more than 2^8
 // (in the exponent's base 2): until then p <= 2^8, far inside bf16's and
 // fp32's range, and the final division by the sum removes the factor exactly.
+//
+// Measured: 65,536 rows x 2048 keys x 8 heads of 128, 399 us, 1380 TFLOP/s (the
+// softmax's warps and the products' issue both take most of that time); 17,001
+// rows x 1024 keys and 15,800 x 1500, 8 heads of 64, 120 us, 700 TFLOP/s: with
+// half the products per score the exponentials bound it (2.7e12 a second, of
+// 4.6e12 that the special function units compute).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -710,6 +716,15 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
 //   warps 16-19     dQ out of tensor memory
 //   warp 20         TMA loads
 //   warp 21         issues the five products
+//
+// Measured: 17,001 rows x 1024 keys and 15,800 x 1500, 8 heads of 64, 321 us, 656
+// TFLOP/s; 2 x 16,384 rows x 2048 keys, 8 heads of 128, 807 us, 850 TFLOP/s.  A
+// step takes 3400 cycles of a multiprocessor (64-wide heads), of which the five
+// products are 1400: each waits for what the step's phases before it made, with
+// some 400 cycles from a product's end to the next one's start.  Without the
+// softmax's arithmetic and the writes of dQ the main kernel still takes 266 of
+// the 64-wide heads' time then of 321 us; the writes of dQ (a value is added to
+// for every key tile) are the next part.
 constexpr int kBwdThreads = 768;  // warps 22, 23 only give their registers away
 constexpr int kBwdLoad = 20, kBwdMma = 21;
 

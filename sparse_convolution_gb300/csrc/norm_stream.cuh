@@ -9,7 +9,7 @@ namespace {
 // of the eight that work on them.  Loads into registers keep at most a few
 // vectors per thread under way, and the registers they need cost the warps that
 // would hide them (4,000,000 x 64 bf16 backward: 297 us with one row in flight
-// per lane, 307 with two, 461 with the next one fetched early); the copies are
+// per lane, not 264, 307 with two, 461 with the next one fetched early); the copies are
 // under way whatever the warps do.
 // Blocks per multiprocessor: what the registers of a lane's values allow without
 // spills (100,000 x 512 bf16, forward with codes: two 67 us, one 95; backward
