@@ -722,9 +722,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
 // step takes 3400 cycles of a multiprocessor (64-wide heads), of which the five
 // products are 1400: each waits for what the step's phases before it made, with
 // some 400 cycles from a product's end to the next one's start.  Without the
-// softmax's arithmetic and the writes of dQ the main kernel still takes 266 of
-// the 64-wide heads' time then of 321 us; the writes of dQ (a value is added to
-// for every key tile) are the next part.
+// softmax's arithmetic and the writes of dQ (a value is added to for every key
+// tile) the first would still take 266 us.
 constexpr int kBwdThreads = 768;  // warps 22, 23 only give their registers away
 constexpr int kBwdLoad = 20, kBwdMma = 21;
 

@@ -33,30 +33,35 @@ __global__ void __launch_bounds__(kThreads) k_rows(const __grid_constant__ RowAr
   if constexpr (OpIs<OP>::kBack) rows.write_parts(sh, kThreads);
 }
 
-// dw, db = sums of the blocks' parts: 32 channels per block, 8 rows of threads
-// over the parts, added in a fixed order.
-__global__ void __launch_bounds__(kThreads) k_norm_sum_parts(const float* __restrict__ part, int parts, int c,
-                                                             float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float sh[8][33];
+// dw, db = sums of the blocks' parts: 32 channels per block, 32 rows of threads
+// over the parts, added in a fixed order.  Latency is all of it: with eight rows
+// of threads, four loads of each at once, 608 parts took 10 us.
+constexpr int kSumRows = 32;
+__global__ void __launch_bounds__(32 * kSumRows) k_norm_sum_parts(const float* __restrict__ part, int parts, int c,
+                                                                  float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float sh[kSumRows][33];
   const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
   const int at = blockIdx.x * 32 + tx;  // over 2c values: dw, then db
   float s = 0.0f;
   if (at < 2 * c) {
-    const float* src = part + at;
-    int p = ty;
-    for (; p + 24 < parts; p += 32) {
-      const float x = __ldg(src + (int64_t)p * 2 * c), y = __ldg(src + (int64_t)(p + 8) * 2 * c),
-                  z = __ldg(src + (int64_t)(p + 16) * 2 * c), t = __ldg(src + (int64_t)(p + 24) * 2 * c);
-      s += (x + y) + (z + t);
+    constexpr int kAtOnce = 10;
+    for (int p = ty; p < parts; p += kAtOnce * kSumRows) {
+      float x[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = p + k * kSumRows;
+        x[k] = i < parts ? __ldg(part + (int64_t)i * 2 * c + at) : 0.0f;
+      }
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) s += x[k];
     }
-    for (; p < parts; p += 8) s += __ldg(src + (int64_t)p * 2 * c);
   }
   sh[ty][tx] = s;
   __syncthreads();
   if (ty == 0 && at < 2 * c) {
     float t = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += sh[k][tx];
+    for (int k = 0; k < kSumRows; ++k) t += sh[k][tx];
     float* out = at < c ? dw : db;
     if (out) out[at < c ? at : at - c] = t;
   }
@@ -582,7 +587,7 @@ fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, c
   }
   if (!sums) return FVX_OK;
   LaunchScope ls("norm_sum_parts", s);
-  k_norm_sum_parts<<<(unsigned)((2 * c + 31) / 32), kThreads, 0, s>>>(a.part, parts, (int)c, dw, db);
+  k_norm_sum_parts<<<(unsigned)((2 * c + 31) / 32), 32 * kSumRows, 0, s>>>(a.part, parts, (int)c, dw, db);
   return check_launch("norm_sum_parts");
 }
 
