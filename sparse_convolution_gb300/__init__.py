@@ -13,6 +13,7 @@ maps, Kernels selected per GPU).
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 
@@ -418,11 +419,18 @@ def _on_device(who, *tensors):
     returns the current stream's handle."""
     import torch
 
-    dev = torch.cuda.current_device()
+    dev = torch._C._cuda_getDevice() if tensors[0].is_cuda else torch.cuda.current_device()
     for t in tensors:
         if t is not None and t.get_device() != dev:
             _refuse(f"{who}: every tensor must be on the current CUDA device {dev}, got {t.device}")
     return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _empty_rows(t):
+    """Room for a result of t's shape and type, dense."""
+    import torch
+
+    return torch.empty_like(t) if t.is_contiguous() else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
 
 def _on_stream(stream, call, *args, **kw):
@@ -566,7 +574,7 @@ def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint_group=None, strea
     n, c = x.shape
     weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
     dev = x.device
-    y = torch.empty((n, c), dtype=x.dtype, device=dev)
+    y = _empty_rows(x)
     mean = torch.empty((n,), dtype=torch.float32, device=dev)
     rstd = torch.empty((n,), dtype=torch.float32, device=dev)
     if not checkpoint_group:
@@ -609,7 +617,7 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, stream=None):
     mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
     weight = _channel_vector(weight, c, who, "weight")
     dev = dy.device
-    dx = torch.empty((n, c), dtype=dy.dtype, device=dev)
+    dx = _empty_rows(dy)
     dw = torch.empty((c,), dtype=torch.float32, device=dev)
     db = torch.empty((c,), dtype=torch.float32, device=dev)
     _check(load().fvx_layer_norm_backward(dt, dy.data_ptr(), lddy, *source, n, c, _at(weight), mean.data_ptr(),
@@ -633,10 +641,7 @@ def _heads(t, who, name):
 
 
 def _host_offsets(o):
-    try:
-        return (ctypes.c_int64 * len(o))(*o)
-    except TypeError:  # a tensor's or an array's elements
-        return (ctypes.c_int64 * len(o))(*map(int, o))
+    return array.array("q", o)  # of ints, or of a tensor's or an array's elements
 
 
 def _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask):
@@ -678,11 +683,11 @@ def cross_attention(q, k, v, q_offsets, kv_offsets, key_mask=None, scale=None, s
     s = _on_device(who, q, k, v, key_mask)
     q, k, v, key_mask, qo, ko, B = _attention_args(who, q, k, v, q_offsets, kv_offsets, key_mask)
     nq, heads, d = q.shape
-    out = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
+    out = _empty_rows(q)
     lse = torch.empty((nq, heads), dtype=torch.float32, device=q.device)
-    _check(load().fvx_cross_attention(dt, *_strided(q), *_strided(k), *_strided(v), qo, ko, B, heads, k.shape[1], d,
-                                      _at(key_mask), d ** -0.5 if scale is None else scale, out.data_ptr(),
-                                      lse.data_ptr(), s))
+    _check(load().fvx_cross_attention(dt, *_strided(q), *_strided(k), *_strided(v), qo.buffer_info()[0],
+                                      ko.buffer_info()[0], B, heads, k.shape[1], d, _at(key_mask),
+                                      d ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(), s))
     return out, lse
 
 
@@ -706,13 +711,11 @@ def cross_attention_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, key
     if lse.dtype != torch.float32 or tuple(lse.shape) != (nq, heads):
         _refuse(f"{who}: lse must be float32 [{nq}, {heads}], got {lse.dtype} {tuple(lse.shape)}")
     dout, out, lse = _heads(dout, who, "dout"), out.contiguous(), lse.contiguous()
-    dq = torch.empty((nq, heads, d), dtype=q.dtype, device=q.device)
-    dk = torch.empty(k.shape, dtype=q.dtype, device=q.device)
-    dv = torch.empty(k.shape, dtype=q.dtype, device=q.device)
+    dq, dk, dv = _empty_rows(q), _empty_rows(k), _empty_rows(k)
     _check(load().fvx_cross_attention_backward(
-        dt, *_strided(dout), *_strided(q), *_strided(k), *_strided(v), out.data_ptr(), lse.data_ptr(), qo, ko, B, heads,
-        k.shape[1], d, _at(key_mask), d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(),
-        dv.data_ptr(), s))
+        dt, *_strided(dout), *_strided(q), *_strided(k), *_strided(v), out.data_ptr(), lse.data_ptr(),
+        qo.buffer_info()[0], ko.buffer_info()[0], B, heads, k.shape[1], d, _at(key_mask),
+        d ** -0.5 if scale is None else scale, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), s))
     return dq, dk, dv
 
 

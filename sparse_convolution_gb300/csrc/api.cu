@@ -170,6 +170,15 @@ fvx_status device_sm_count(int* sms) {
   *sms = counts[dev];
   return FVX_OK;
 }
+fvx_status allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  FVX_CUDA(cudaGetDevice(&dev));
+  const uint64_t bit = (uint64_t)1 << (dev & 63);  // device_sm_count refuses ordinals past 63
+  if (done.load(std::memory_order_relaxed) & bit) return FVX_OK;
+  FVX_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+  done.fetch_or(bit, std::memory_order_relaxed);
+  return FVX_OK;
+}
 
 fvx_status check_launch(const char* name) {
   cudaError_t e = cudaGetLastError();

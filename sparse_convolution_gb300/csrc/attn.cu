@@ -711,9 +711,10 @@ FmaArgs fma_args(const AttnCall& c) {
   return a;
 }
 
-template <typename K>
-fvx_status fma_launch(const char* name, K kernel, int64_t units, size_t smem, cudaStream_t s, const FmaArgs& a) {
-  FVX_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+template <auto kernel>
+fvx_status fma_launch(const char* name, int64_t units, size_t smem, cudaStream_t s, const FmaArgs& a) {
+  static std::atomic<uint64_t> allowed{0};
+  FVX_TRY(allow_smem((const void*)kernel, (int)smem, allowed));
   LaunchScope ls(name, s);
   kernel<<<(unsigned)units, kFmaThreads, smem, s>>>(a);
   return check_launch(name);
@@ -739,7 +740,8 @@ fvx_status fma_forward(const AttnCall& c, cudaStream_t s, Scratch& scr, int sms)
     a.total = scr.get<float>((size_t)a.splits * rows);
     if (!a.part || !a.top || !a.total) return FVX_ERR_ALLOC;
   }
-  FVX_TRY(fma_launch("attn_fma", k_attn_fma<T, DP>, units, fma_smem(DP, 3, 1), s, a));
+  constexpr auto kernel = k_attn_fma<T, DP>;
+  FVX_TRY(fma_launch<kernel>("attn_fma", units, fma_smem(DP, 3, 1), s, a));
   return a.splits > 1 ? attn_join(c, a.part, a.top, a.total, a.splits, s) : FVX_OK;
 }
 
@@ -766,7 +768,8 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
     a.dv_part = scr.get<float>((size_t)a.key_splits * k_values);
     if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
   }
-  FVX_TRY(fma_launch("attn_fma_bwd", k_attn_fma_bwd<T, DP>, key_units + row_units, fma_smem(DP, 4, 2), s, a));
+  constexpr auto kernel = k_attn_fma_bwd<T, DP>;
+  FVX_TRY(fma_launch<kernel>("attn_fma_bwd", key_units + row_units, fma_smem(DP, 4, 2), s, a));
   SumArgs sum = {};
   int arrays = 0;
   auto add = [&](const float* part, void* dst, int64_t n, int splits) {

@@ -569,10 +569,11 @@ __global__ void __launch_bounds__(kFewThreads, DP > 64 ? 2 : 3) k_attn_few_bf16(
   few_join<__nv_bfloat16, DP>(a, p, w_acc, C::kRing / 4, s_top, s_sum, b_acc, b_top, b_sum);
 }
 
-template <typename K>
-fvx_status launch_few(K kernel, int smem, const FewArgs& a, int64_t grid, cudaStream_t s) {
+template <auto kernel>
+fvx_status launch_few(int smem, const FewArgs& a, int64_t grid, cudaStream_t s) {
   LaunchScope ls("attn_few", s);
-  FVX_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  static std::atomic<uint64_t> allowed{0};
+  FVX_TRY(allow_smem((const void*)kernel, smem, allowed));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kFewThreads);
@@ -590,14 +591,14 @@ fvx_status launch_few(K kernel, int smem, const FewArgs& a, int64_t grid, cudaSt
 template <int LK>
 fvx_status few_f32(const FewArgs& a, int rows, int64_t grid, cudaStream_t s) {
   constexpr int kSmem = kFewWarps * kF32Ring;
-  if (rows <= 1) return launch_few(k_attn_few_f32<LK, 1>, kSmem, a, grid, s);
-  if (rows <= 2) return launch_few(k_attn_few_f32<LK, 2>, kSmem, a, grid, s);
-  if (rows <= 4) return launch_few(k_attn_few_f32<LK, 4>, kSmem, a, grid, s);
-  return launch_few(k_attn_few_f32<LK, 8>, kSmem, a, grid, s);
+  if (rows <= 1) return launch_few<k_attn_few_f32<LK, 1>>(kSmem, a, grid, s);
+  if (rows <= 2) return launch_few<k_attn_few_f32<LK, 2>>(kSmem, a, grid, s);
+  if (rows <= 4) return launch_few<k_attn_few_f32<LK, 4>>(kSmem, a, grid, s);
+  return launch_few<k_attn_few_f32<LK, 8>>(kSmem, a, grid, s);
 }
 template <int DP>
 fvx_status few_bf16(const FewArgs& a, int64_t grid, cudaStream_t s) {
-  return launch_few(k_attn_few_bf16<DP>, kFewWarps * FewBf16<DP>::kRing, a, grid, s);
+  return launch_few<k_attn_few_bf16<DP>>(kFewWarps * FewBf16<DP>::kRing, a, grid, s);
 }
 
 int64_t most_rows(const AttnCall& c) {

@@ -1502,7 +1502,8 @@ fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   a.tile_rows = tile_rows(c);
   a.wide_out = c.d % 16 == 0 && reinterpret_cast<uintptr_t>(c.out) % 32 == 0;
   a.c = c.scale * kLog2e;
-  FVX_CUDA(cudaFuncSetAttribute(k_attn_tc_fwd<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+  static std::atomic<uint64_t> allowed{0};
+  FVX_TRY(allow_smem((const void*)k_attn_tc_fwd<DP>, (int)C::kSmem, allowed));
   {
     LaunchScope ls("attn_tc_fwd", s);
     k_attn_tc_fwd<DP><<<std::min(a.units, sms), kFwdThreads, C::kSmem, s>>>(a);
@@ -1660,7 +1661,8 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
                                                         c.kv_heads, c.shared, a.tile_rows, c.d, stats);
       FVX_TRY(check_launch("attn_stats"));
     }
-    FVX_CUDA(cudaFuncSetAttribute(k_attn_tc_bwd<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::kSmem));
+    static std::atomic<uint64_t> allowed{0};
+    FVX_TRY(allow_smem((const void*)k_attn_tc_bwd<DP>, (int)C::kSmem, allowed));
     LaunchScope ls("attn_tc_bwd", s);
     k_attn_tc_bwd<DP><<<std::min(a.units, sms), kBwdThreads, C::kSmem, s>>>(a);
     FVX_TRY(check_launch("attn_tc_bwd"));

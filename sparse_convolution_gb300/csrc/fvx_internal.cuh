@@ -2,6 +2,8 @@
 #pragma once
 
 #include <cuda_runtime.h>
+
+#include <atomic>
 #include <stdint.h>
 
 #include <vector>
@@ -84,6 +86,9 @@ struct LaunchScope {
 fvx_status check_launch(const char* name);
 // Streaming multiprocessors of the current device (queried once per device).
 fvx_status device_sm_count(int* sms);
+// Lets a kernel take `bytes` of dynamic shared memory; `done` (one per kernel)
+// remembers the devices that it holds on, since the call costs a launch's tenth.
+fvx_status allow_smem(const void* kernel, int bytes, std::atomic<uint64_t>& done);
 fvx_status check_staged_status(const char* who, uint32_t staged, cudaStream_t s);
 // Kernel map pair lists are allocated for 27 pairs per output (no count
 // read-back) up to this many bytes (environment FVX_KMAP_CAP_BYTES, default
