@@ -112,8 +112,30 @@ def test_training_lowers_the_loss(dtype):
     assert all(b < a for a, b in zip(losses, losses[1:])), losses
 
 
-def test_training_repeats_bit_for_bit():
-    """No sum depends on the order in which blocks happen to finish."""
-    from examples.voxel_block import train
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_passes_repeat_bit_for_bit(dtype):
+    """No sum depends on the order in which blocks happen to finish, but those
+    of the conv's weight gradient, which adds with atomics."""
+    import sparse_convolution_gb300 as fvx
+    from examples.voxel_block import VoxelBlock
 
-    assert train(voxels=6000, steps=3, dtype=torch.float32) == train(voxels=6000, steps=3, dtype=torch.float32)
+    g = torch.Generator().manual_seed(5)
+    dtype = getattr(torch, dtype)
+    coords = torch.randint(0, 24, (9000, 3), dtype=torch.int32, generator=g).cuda()
+    grid = fvx.Grid.build(coords, [0, 4000, 9000])
+    kmap, kmap_t = fvx.KernelMap(grid, grid, 1), fvx.KernelMap(grid, grid, 1, transposed=True)
+    so = [0, 200, 577]
+    mask = (torch.rand(577, generator=g) < 0.9).cuda()
+    x = torch.randn(grid.n_active, 64, generator=g).cuda().to(dtype)
+    block = VoxelBlock(64, 4, 577, 2, dtype)
+    dreadout = torch.randn(2, 4, 16, generator=g).cuda().to(dtype)
+
+    def once():
+        readout, kept = block.forward(grid, kmap, x, so, mask)
+        grad, dx = block.backward(grid, kmap, kmap_t, so, mask, kept, dreadout)
+        return [readout, dx] + [grad[n] for n in ("k", "v", "query", "norm_w", "norm_b")]
+
+    first = once()
+    for _ in range(3):
+        assert all(torch.equal(a, b) for a, b in zip(first, once()))
+    fvx.device_status()
