@@ -30,7 +30,6 @@ namespace fvx {
 namespace {
 
 constexpr int kMaxD = 128;
-constexpr int kTile = 64;    // rows and keys of a tile
 constexpr int kFmaThreads = 256;
 
 template <typename T>
@@ -46,8 +45,9 @@ __device__ __forceinline__ float from_f32<float>(float v) { return v; }
 template <>
 __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
 
-// The fp32 kernels: tiles of 64 rows by 64 keys in shared memory, row after row
-// with a pitch of 4 more words than a row has, so that the 16 byte reads of
+// The fp32 kernels: tiles of 16 I rows by 16 J keys (64 x 64, and 16 or 32 rows
+// or 16 keys where a sample has no more) in shared memory, row after row with a
+// pitch of 4 more words than a row has, so that the 16 byte reads of
 // neighbouring rows lie in different banks.  Thread (ty, tx) of 16 x 16 owns the
 // scores of rows ty + 16 i and keys tx + 16 j, and of the results the columns
 // 4 tx .. 4 tx + 3 of every 64 in the same rows.  Products run on pairs: over
@@ -78,7 +78,6 @@ struct FmaArgs {
 };
 
 constexpr int pitch_of(int columns) { return columns + 4; }
-constexpr int kScorePitch = pitch_of(kTile);
 
 // values [c, c + 4) of a row of d, zeros past the end
 template <typename T>
@@ -116,13 +115,13 @@ __device__ __forceinline__ void store4(void* dst, int64_t row, int c, int d, con
     if (c + i < d) p[i] = from_f32<T>(v[i]);
 }
 
-// rows [r0, r0 + 64) of an item's (token, shared head) rows, zeros past the end
-template <typename T, int DP>
+// rows [r0, r0 + ROWS) of an item's (token, shared head) rows, zeros past the end
+template <typename T, int DP, int ROWS>
 __device__ __forceinline__ void load_rows(const FmaArgs& a, float* dst, const HeadsView& t, int token0, int r0,
                                           int rows, int head0) {
   constexpr int kQuads = DP / 4;
 #pragma unroll
-  for (int e = threadIdx.x; e < kTile * kQuads; e += kFmaThreads) {
+  for (int e = threadIdx.x; e < ROWS * kQuads; e += kFmaThreads) {
     const int r = e / kQuads, c = (e % kQuads) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (r0 + r < rows) {
@@ -133,14 +132,14 @@ __device__ __forceinline__ void load_rows(const FmaArgs& a, float* dst, const He
     *reinterpret_cast<float4*>(dst + r * pitch_of(DP) + c) = v;
   }
 }
-// keys [j0, j0 + 64) of head h; a key that is masked or past the end reads as
+// keys [j0, j0 + KEYS) of head h; a key that is masked or past the end reads as
 // zeros (a masked one's row is fetched beside its mask, and not used)
-template <typename T, int DP>
+template <typename T, int DP, int KEYS>
 __device__ __forceinline__ void load_keys(const FmaArgs& a, float* dst, const HeadsView& t, int key0, int j0, int keys,
                                           int h) {
   constexpr int kQuads = DP / 4;
 #pragma unroll
-  for (int e = threadIdx.x; e < kTile * kQuads; e += kFmaThreads) {
+  for (int e = threadIdx.x; e < KEYS * kQuads; e += kFmaThreads) {
     const int j = e / kQuads, c = (e % kQuads) * 4;
     float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (j0 + j < keys) {
@@ -154,32 +153,31 @@ __device__ __forceinline__ void load_keys(const FmaArgs& a, float* dst, const He
 }
 
 // acc[i][j] = sum_d a[ty + 16 i][d] b[tx + 16 j][d]
-template <int DP>
-__device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty, int tx, int d, float (&acc)[4][4]) {
-  uint64_t sum[4][4];
+template <int DP, int I, int J>
+__device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty, int tx, int d, float (&acc)[I][J]) {
+  uint64_t sum[I][J];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < I; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) sum[i][j] = tc::pair(0.0f, 0.0f);
+    for (int j = 0; j < J; ++j) sum[i][j] = tc::pair(0.0f, 0.0f);
   a += ty * pitch_of(DP);
   b += tx * pitch_of(DP);
 #pragma unroll 2
   for (int c = 0; c < d; c += 4) {
-    ulonglong2 x[4], y[4];
+    ulonglong2 x[I], y[J];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      x[i] = *reinterpret_cast<const ulonglong2*>(a + 16 * i * pitch_of(DP) + c);
-      y[i] = *reinterpret_cast<const ulonglong2*>(b + 16 * i * pitch_of(DP) + c);
-    }
+    for (int i = 0; i < I; ++i) x[i] = *reinterpret_cast<const ulonglong2*>(a + 16 * i * pitch_of(DP) + c);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < J; ++j) y[j] = *reinterpret_cast<const ulonglong2*>(b + 16 * j * pitch_of(DP) + c);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) sum[i][j] = tc::fma2(x[i].y, y[j].y, tc::fma2(x[i].x, y[j].x, sum[i][j]));
+    for (int i = 0; i < I; ++i)
+#pragma unroll
+      for (int j = 0; j < J; ++j) sum[i][j] = tc::fma2(x[i].y, y[j].y, tc::fma2(x[i].x, y[j].x, sum[i][j]));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < I; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       float lo, hi;
       tc::unpair(sum[i][j], lo, hi);
       acc[i][j] = lo + hi;
@@ -187,24 +185,24 @@ __device__ __forceinline__ void tile_dot(const float* a, const float* b, int ty,
 }
 
 // acc[i][2 n], acc[i][2 n + 1]: pairs of the columns 4 tx + 64 n .. of row
-// ty + 16 i; adds sum_t p[ty + 16 i][t] x[t][column] over t < count, where p and
-// x hold zeros up to a multiple of 4
-template <int DP>
+// ty + 16 i; adds sum_t p[ty + 16 i][t] x[t][column] over t < count, where p (its
+// rows PITCH apart) and x hold zeros up to a multiple of 4
+template <int DP, int PITCH, int I>
 __device__ __forceinline__ void tile_accumulate(const float* p, const float* x, int ty, int tx, int count,
-                                                uint64_t (&acc)[4][DP / 32]) {
-  p += ty * kScorePitch;
+                                                uint64_t (&acc)[I][DP / 32]) {
+  p += ty * PITCH;
   x += 4 * tx;
   for (int t = 0; t < count; t += 4) {
-    float4 u[4];
+    float4 u[I];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = *reinterpret_cast<const float4*>(p + 16 * i * kScorePitch + t);
+    for (int i = 0; i < I; ++i) u[i] = *reinterpret_cast<const float4*>(p + 16 * i * PITCH + t);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
 #pragma unroll
       for (int n = 0; n < DP / 64; ++n) {
         const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(x + (t + k) * pitch_of(DP) + 64 * n);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < I; ++i) {
           const float f = k == 0 ? u[i].x : k == 1 ? u[i].y : k == 2 ? u[i].z : u[i].w;
           const uint64_t ff = tc::pair(f, f);
           acc[i][2 * n] = tc::fma2(ff, w.x, acc[i][2 * n]);
@@ -214,10 +212,10 @@ __device__ __forceinline__ void tile_accumulate(const float* p, const float* x, 
     }
   }
 }
-template <int DP>
-__device__ __forceinline__ void clear(uint64_t (&acc)[4][DP / 32]) {
+template <int DP, int I>
+__device__ __forceinline__ void clear(uint64_t (&acc)[I][DP / 32]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < I; ++i)
 #pragma unroll
     for (int n = 0; n < DP / 32; ++n) acc[i][n] = tc::pair(0.0f, 0.0f);
 }
@@ -251,6 +249,7 @@ struct FmaUnit {
 };
 // Units of an item: tile fastest (neighbours read the same keys), then key
 // head, then split.  `array` holds the items' first units.
+template <int I, int J>
 __device__ __forceinline__ FmaUnit fma_unit(const FmaArgs& a, int u, int array) {
   FmaUnit w;
   w.b = a.items.find(array, u);
@@ -258,7 +257,7 @@ __device__ __forceinline__ FmaUnit fma_unit(const FmaArgs& a, int u, int array) 
   w.rows = (a.items.q0(w.b + 1) - w.q0) * a.shared;
   w.key0 = a.items.k0(w.b);
   w.keys = a.items.k0(w.b + 1) - w.key0;
-  const int tiles = ((array == kItemTile ? w.keys : w.rows) + kTile - 1) / kTile;
+  const int tiles = array == kItemTile ? (w.keys + 16 * J - 1) / (16 * J) : (w.rows + 16 * I - 1) / (16 * I);
   int i = u - a.items.at(array, w.b);
   w.tile = i % tiles;
   i /= tiles;
@@ -271,41 +270,41 @@ __device__ __forceinline__ int64_t row_of(const FmaArgs& a, const FmaUnit& w, in
   return (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
 }
 
-template <typename T, int DP>
-__global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma(const __grid_constant__ FmaArgs a) {
+template <typename T, int DP, int I, int J>
+__global__ void __launch_bounds__(kFmaThreads, DP > 64 && I * J > 4 ? 1 : 2) k_attn_fma(const __grid_constant__ FmaArgs a) {
   extern __shared__ __align__(16) float sm[];
-  constexpr int kOperand = kTile * pitch_of(DP);
-  float *qs = sm, *ks = qs + kOperand, *vs = ks + kOperand, *ps = vs + kOperand;
+  constexpr int kRows = 16 * I * pitch_of(DP), kKeys = 16 * J * pitch_of(DP), kScorePitch = pitch_of(16 * J);
+  float *qs = sm, *ks = qs + kRows, *vs = ks + kKeys, *ps = vs + kKeys;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const FmaUnit w = fma_unit(a, blockIdx.x, kItemUnit);
-  const int r0 = w.tile * kTile;
-  load_rows<T, DP>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
-  uint64_t acc[4][DP / 32];
+  const FmaUnit w = fma_unit<I, J>(a, blockIdx.x, kItemUnit);
+  const int r0 = w.tile * 16 * I;
+  load_rows<T, DP, 16 * I>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
+  uint64_t acc[I][DP / 32];
   clear<DP>(acc);
-  float top[4], total[4];
+  float top[I], total[I];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < I; ++i) {
     top[i] = -INFINITY;
     total[i] = 0.0f;
   }
-  const int kt = (w.keys + kTile - 1) / kTile;
+  const int kt = (w.keys + 16 * J - 1) / (16 * J);
   const int t0 = (int)((int64_t)kt * w.split / a.splits), t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
   for (int t = t0; t < t1; ++t) {
-    const int j0 = t * kTile;
+    const int j0 = t * 16 * J;
     __syncthreads();
-    load_keys<T, DP>(a, ks, a.k, w.key0, j0, w.keys, w.h);
-    load_keys<T, DP>(a, vs, a.v, w.key0, j0, w.keys, w.h);
-    bool keep[4];
+    load_keys<T, DP, 16 * J>(a, ks, a.k, w.key0, j0, w.keys, w.h);
+    load_keys<T, DP, 16 * J>(a, vs, a.v, w.key0, j0, w.keys, w.h);
+    bool keep[J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
+    for (int j = 0; j < J; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
     __syncthreads();
-    float s[4][4];
-    tile_dot<DP>(qs, ks, ty, tx, a.d, s);
+    float s[I][J];
+    tile_dot<DP, I, J>(qs, ks, ty, tx, a.d, s);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < I; ++i) {
       float m = -INFINITY;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         s[i][j] = keep[j] ? s[i][j] * a.scale : -INFINITY;
         m = fmaxf(m, s[i][j]);
       }
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma(const
       const float fade = expf(top[i] - base);
       float add = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         s[i][j] = expf(s[i][j] - base);
         add += s[i][j];
         ps[(ty + 16 * i) * kScorePitch + tx + 16 * j] = s[i][j];
@@ -325,10 +324,10 @@ __global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma(const
       for (int n = 0; n < DP / 32; ++n) acc[i][n] = tc::mul2(acc[i][n], tc::pair(fade, fade));
     }
     __syncthreads();
-    tile_accumulate<DP>(ps, vs, ty, tx, min(kTile, w.keys - j0), acc);
+    tile_accumulate<DP, kScorePitch>(ps, vs, ty, tx, min(16 * J, w.keys - j0), acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < I; ++i) {
     const int r = r0 + ty + 16 * i;
     if (r >= w.rows) continue;
     const int64_t row = row_of(a, w, r);
@@ -357,12 +356,13 @@ __global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma(const
 }
 
 // p and ds of one tile: s and dp in, both overwritten
-__device__ __forceinline__ void tile_gradient(const FmaArgs& a, float (&s)[4][4], float (&dp)[4][4],
-                                              const bool (&keep)[4], const float (&lse)[4], const float (&delta)[4]) {
+template <int I, int J>
+__device__ __forceinline__ void tile_gradient(const FmaArgs& a, float (&s)[I][J], float (&dp)[I][J],
+                                              const bool (&keep)[J], const float (&lse)[I], const float (&delta)[I]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < I; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < J; ++j) {
       const float p = keep[j] && lse[i] != -INFINITY ? expf(s[i][j] * a.scale - lse[i]) : 0.0f;
       s[i][j] = p;
       dp[i][j] = p * (dp[i][j] - delta[i]) * a.scale;
@@ -379,44 +379,44 @@ __device__ __forceinline__ void row_constants(const FmaArgs& a, const FmaUnit& w
 }
 
 // dq of one tile of rows over a range of key tiles
-template <typename T, int DP>
+template <typename T, int DP, int I, int J>
 __device__ __forceinline__ void fma_dq(const FmaArgs& a, float* sm, int unit) {
-  constexpr int kOperand = kTile * pitch_of(DP);
-  float *qs = sm, *os = qs + kOperand, *ks = os + kOperand, *vs = ks + kOperand, *ps = vs + kOperand;
+  constexpr int kRows = 16 * I * pitch_of(DP), kKeys = 16 * J * pitch_of(DP), kScorePitch = pitch_of(16 * J);
+  float *qs = sm, *os = qs + kRows, *ks = os + kRows, *vs = ks + kKeys, *ps = vs + kKeys;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const FmaUnit w = fma_unit(a, unit, kItemUnit);
-  const int r0 = w.tile * kTile;
-  load_rows<T, DP>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
-  load_rows<T, DP>(a, os, a.dout, w.q0, r0, w.rows, w.h * a.shared);
-  uint64_t acc[4][DP / 32];
+  const FmaUnit w = fma_unit<I, J>(a, unit, kItemUnit);
+  const int r0 = w.tile * 16 * I;
+  load_rows<T, DP, 16 * I>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
+  load_rows<T, DP, 16 * I>(a, os, a.dout, w.q0, r0, w.rows, w.h * a.shared);
+  uint64_t acc[I][DP / 32];
   clear<DP>(acc);
-  float lse[4], delta[4];
+  float lse[I], delta[I];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
-  const int kt = (w.keys + kTile - 1) / kTile;
+  for (int i = 0; i < I; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
+  const int kt = (w.keys + 16 * J - 1) / (16 * J);
   const int t0 = (int)((int64_t)kt * w.split / a.splits), t1 = (int)((int64_t)kt * (w.split + 1) / a.splits);
   for (int t = t0; t < t1; ++t) {
-    const int j0 = t * kTile;
+    const int j0 = t * 16 * J;
     __syncthreads();
-    load_keys<T, DP>(a, ks, a.k, w.key0, j0, w.keys, w.h);
-    load_keys<T, DP>(a, vs, a.v, w.key0, j0, w.keys, w.h);
-    bool keep[4];
+    load_keys<T, DP, 16 * J>(a, ks, a.k, w.key0, j0, w.keys, w.h);
+    load_keys<T, DP, 16 * J>(a, vs, a.v, w.key0, j0, w.keys, w.h);
+    bool keep[J];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
+    for (int j = 0; j < J; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
     __syncthreads();
-    float s[4][4], dp[4][4];
-    tile_dot<DP>(qs, ks, ty, tx, a.d, s);
-    tile_dot<DP>(os, vs, ty, tx, a.d, dp);
+    float s[I][J], dp[I][J];
+    tile_dot<DP, I, J>(qs, ks, ty, tx, a.d, s);
+    tile_dot<DP, I, J>(os, vs, ty, tx, a.d, dp);
     tile_gradient(a, s, dp, keep, lse, delta);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < I; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) ps[(ty + 16 * i) * kScorePitch + tx + 16 * j] = dp[i][j];
+      for (int j = 0; j < J; ++j) ps[(ty + 16 * i) * kScorePitch + tx + 16 * j] = dp[i][j];
     __syncthreads();
-    tile_accumulate<DP>(ps, ks, ty, tx, min(kTile, w.keys - j0), acc);
+    tile_accumulate<DP, kScorePitch>(ps, ks, ty, tx, min(16 * J, w.keys - j0), acc);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < I; ++i) {
     const int r = r0 + ty + 16 * i;
     if (r >= w.rows) continue;
     const int64_t row = row_of(a, w, r);
@@ -432,54 +432,54 @@ __device__ __forceinline__ void fma_dq(const FmaArgs& a, float* sm, int unit) {
 
 // dk and dv of one tile of keys over a range of row tiles; the scores go to
 // shared memory with the keys in rows
-template <typename T, int DP>
+template <typename T, int DP, int I, int J>
 __device__ __forceinline__ void fma_dkv(const FmaArgs& a, float* sm, int unit) {
-  constexpr int kOperand = kTile * pitch_of(DP);
-  float *qs = sm, *os = qs + kOperand, *ks = os + kOperand, *vs = ks + kOperand, *ps = vs + kOperand,
-        *ds = ps + kTile * kScorePitch;
+  constexpr int kRows = 16 * I * pitch_of(DP), kKeys = 16 * J * pitch_of(DP), kScorePitch = pitch_of(16 * I);
+  float *qs = sm, *os = qs + kRows, *ks = os + kRows, *vs = ks + kKeys, *ps = vs + kKeys,
+        *ds = ps + 16 * J * kScorePitch;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  const FmaUnit w = fma_unit(a, unit, kItemTile);
-  const int j0 = w.tile * kTile;
-  load_keys<T, DP>(a, ks, a.k, w.key0, j0, w.keys, w.h);
-  load_keys<T, DP>(a, vs, a.v, w.key0, j0, w.keys, w.h);
-  uint64_t dk[4][DP / 32], dv[4][DP / 32];
+  const FmaUnit w = fma_unit<I, J>(a, unit, kItemTile);
+  const int j0 = w.tile * 16 * J;
+  load_keys<T, DP, 16 * J>(a, ks, a.k, w.key0, j0, w.keys, w.h);
+  load_keys<T, DP, 16 * J>(a, vs, a.v, w.key0, j0, w.keys, w.h);
+  uint64_t dk[J][DP / 32], dv[J][DP / 32];
   clear<DP>(dk);
   clear<DP>(dv);
-  bool keep[4], keep_out[4];  // of the scores' columns, of the rows written
+  bool keep[J], keep_out[J];  // of the scores' columns, of the rows written
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < J; ++i) {
     keep[i] = kept(a, w.key0, j0 + tx + 16 * i, w.keys);
     keep_out[i] = kept(a, w.key0, j0 + ty + 16 * i, w.keys);
   }
-  const int rt = (w.rows + kTile - 1) / kTile;
+  const int rt = (w.rows + 16 * I - 1) / (16 * I);
   const int t0 = (int)((int64_t)rt * w.split / a.key_splits), t1 = (int)((int64_t)rt * (w.split + 1) / a.key_splits);
   for (int t = t0; t < t1; ++t) {
-    const int r0 = t * kTile;
+    const int r0 = t * 16 * I;
     __syncthreads();
-    load_rows<T, DP>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
-    load_rows<T, DP>(a, os, a.dout, w.q0, r0, w.rows, w.h * a.shared);
-    float lse[4], delta[4];
+    load_rows<T, DP, 16 * I>(a, qs, a.q, w.q0, r0, w.rows, w.h * a.shared);
+    load_rows<T, DP, 16 * I>(a, os, a.dout, w.q0, r0, w.rows, w.h * a.shared);
+    float lse[I], delta[I];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
+    for (int i = 0; i < I; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
     __syncthreads();
-    float s[4][4], dp[4][4];
-    tile_dot<DP>(qs, ks, ty, tx, a.d, s);
-    tile_dot<DP>(os, vs, ty, tx, a.d, dp);
+    float s[I][J], dp[I][J];
+    tile_dot<DP, I, J>(qs, ks, ty, tx, a.d, s);
+    tile_dot<DP, I, J>(os, vs, ty, tx, a.d, dp);
     tile_gradient(a, s, dp, keep, lse, delta);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < I; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         ps[(tx + 16 * j) * kScorePitch + ty + 16 * i] = s[i][j];
         ds[(tx + 16 * j) * kScorePitch + ty + 16 * i] = dp[i][j];
       }
     __syncthreads();
-    const int count = min(kTile, w.rows - r0);
-    tile_accumulate<DP>(ps, os, ty, tx, count, dv);
-    tile_accumulate<DP>(ds, qs, ty, tx, count, dk);
+    const int count = min(16 * I, w.rows - r0);
+    tile_accumulate<DP, kScorePitch>(ps, os, ty, tx, count, dv);
+    tile_accumulate<DP, kScorePitch>(ds, qs, ty, tx, count, dk);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
+  for (int i = 0; i < J; ++i) {
     const int j = j0 + ty + 16 * i;
     if (j >= w.keys) continue;
     const int64_t row = (int64_t)(w.key0 + j) * a.kv_heads + w.h, at = (int64_t)w.split * a.nk * a.kv_heads + row;
@@ -501,11 +501,11 @@ __device__ __forceinline__ void fma_dkv(const FmaArgs& a, float* sm, int unit) {
 }
 
 // The blocks of the key tiles, which take longer, come first.
-template <typename T, int DP>
-__global__ void __launch_bounds__(kFmaThreads, DP > 64 ? 1 : 2) k_attn_fma_bwd(const __grid_constant__ FmaArgs a) {
+template <typename T, int DP, int I, int J>
+__global__ void __launch_bounds__(kFmaThreads, DP > 64 && I * J > 4 ? 1 : 2) k_attn_fma_bwd(const __grid_constant__ FmaArgs a) {
   extern __shared__ __align__(16) float sm[];
-  if ((int)blockIdx.x < a.key_units) fma_dkv<T, DP>(a, sm, blockIdx.x);
-  else fma_dq<T, DP>(a, sm, blockIdx.x - a.key_units);
+  if ((int)blockIdx.x < a.key_units) fma_dkv<T, DP, I, J>(a, sm, blockIdx.x);
+  else fma_dq<T, DP, I, J>(a, sm, blockIdx.x - a.key_units);
 }
 
 // ---------------------------------------------------------------- reductions
@@ -661,14 +661,19 @@ fvx_status check_call(const char* who, AttnCall& c, int32_t B, int32_t heads, in
   return FVX_OK;
 }
 
+// Rows and keys of a tile.
+struct FmaTile {
+  int rows, keys;
+};
 // Prefix of the items' units; `splits` gives each tile that many.
-std::vector<int32_t> unit_prefix(const AttnCall& c, bool by_keys, int splits, int64_t* units) {
+std::vector<int32_t> unit_prefix(const AttnCall& c, FmaTile t, bool by_keys, int splits, int64_t* units) {
   std::vector<int32_t> p((size_t)c.items + 1);
   int64_t n = 0;
+  const int tile = by_keys ? t.keys : t.rows;
   for (int b = 0; b < c.items; ++b) {
     p[b] = (int32_t)n;
     const int64_t len = by_keys ? c.kv_offsets[b + 1] - c.kv_offsets[b] : (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared;
-    n += (len + kTile - 1) / kTile * c.kv_heads * splits;
+    n += (len + tile - 1) / tile * c.kv_heads * splits;
   }
   p[c.items] = (int32_t)n;
   *units = n;
@@ -677,12 +682,13 @@ std::vector<int32_t> unit_prefix(const AttnCall& c, bool by_keys, int splits, in
 
 // Splits of the inner loop: enough units for two blocks per multiprocessor,
 // no more than the longest inner loop has tiles, and at most 32.
-int pick_splits(const AttnCall& c, bool by_keys, int sms) {
+int pick_splits(const AttnCall& c, FmaTile t, bool by_keys, int sms) {
   int64_t units = 0, longest = 1;
-  unit_prefix(c, by_keys, 1, &units);
+  unit_prefix(c, t, by_keys, 1, &units);
+  const int tile = by_keys ? t.rows : t.keys;
   for (int b = 0; b < c.items; ++b) {
     const int64_t len = by_keys ? (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared : c.kv_offsets[b + 1] - c.kv_offsets[b];
-    longest = std::max(longest, (len + kTile - 1) / kTile);
+    longest = std::max(longest, (len + tile - 1) / tile);
   }
   const int64_t want = units > 0 ? (2 * sms + units - 1) / units : 1;
   return (int)std::max<int64_t>(1, std::min<int64_t>({want, longest, 32}));
@@ -719,17 +725,19 @@ fvx_status fma_launch(const char* name, int64_t units, size_t smem, cudaStream_t
   kernel<<<(unsigned)units, kFmaThreads, smem, s>>>(a);
   return check_launch(name);
 }
-// bytes of `operands` tiles of 64 rows and `tiles` of scores
-constexpr size_t fma_smem(int dp, int operands, int tiles) {
-  return (size_t)kTile * (pitch_of(dp) * operands + kScorePitch * tiles) * 4;
+// bytes of tiles of rows and of keys and of `scores` tiles of scores
+constexpr size_t fma_smem(int dp, FmaTile t, int row_tiles, int key_tiles, int scores) {
+  const int score = std::max(t.rows * pitch_of(t.keys), t.keys * pitch_of(t.rows));
+  return (size_t)((t.rows * row_tiles + t.keys * key_tiles) * pitch_of(dp) + scores * score) * 4;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int I, int J>
 fvx_status fma_forward(const AttnCall& c, cudaStream_t s, Scratch& scr, int sms) {
+  constexpr FmaTile tile{16 * I, 16 * J};
   FmaArgs a = fma_args(c);
-  a.splits = pick_splits(c, false, sms);
+  a.splits = pick_splits(c, tile, false, sms);
   int64_t units = 0;
-  const std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &units);
+  const std::vector<int32_t> prefix = unit_prefix(c, tile, false, a.splits, &units);
   FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
   a.out = c.out;
   a.lse = c.lse;
@@ -740,24 +748,25 @@ fvx_status fma_forward(const AttnCall& c, cudaStream_t s, Scratch& scr, int sms)
     a.total = scr.get<float>((size_t)a.splits * rows);
     if (!a.part || !a.top || !a.total) return FVX_ERR_ALLOC;
   }
-  constexpr auto kernel = k_attn_fma<T, DP>;
-  FVX_TRY(fma_launch<kernel>("attn_fma", units, fma_smem(DP, 3, 1), s, a));
+  constexpr auto kernel = k_attn_fma<T, DP, I, J>;
+  FVX_TRY(fma_launch<kernel>("attn_fma", units, fma_smem(DP, tile, 1, 2, 1), s, a));
   return a.splits > 1 ? attn_join(c, a.part, a.top, a.total, a.splits, s) : FVX_OK;
 }
 
-template <typename T, int DP>
+template <typename T, int DP, int I, int J>
 fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, Scratch& scr, int sms) {
+  constexpr FmaTile tile{16 * I, 16 * J};
   FmaArgs a = fma_args(c);
   a.delta = delta;
   a.lse_in = c.lse;
   a.out = c.dq;
   a.dk = c.dk;
   a.dv = c.dv;
-  a.splits = pick_splits(c, false, sms);
-  a.key_splits = pick_splits(c, true, sms);
+  a.splits = pick_splits(c, tile, false, sms);
+  a.key_splits = pick_splits(c, tile, true, sms);
   int64_t row_units = 0, key_units = 0;
-  std::vector<int32_t> prefix = unit_prefix(c, false, a.splits, &row_units);
-  const std::vector<int32_t> by_keys = unit_prefix(c, true, a.key_splits, &key_units);
+  std::vector<int32_t> prefix = unit_prefix(c, tile, false, a.splits, &row_units);
+  const std::vector<int32_t> by_keys = unit_prefix(c, tile, true, a.key_splits, &key_units);
   prefix.insert(prefix.end(), by_keys.begin(), by_keys.end());
   FVX_TRY(attn_items(c, prefix.data(), 4, s, scr, &a.items));
   a.key_units = (int)key_units;
@@ -768,8 +777,8 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
     a.dv_part = scr.get<float>((size_t)a.key_splits * k_values);
     if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
   }
-  constexpr auto kernel = k_attn_fma_bwd<T, DP>;
-  FVX_TRY(fma_launch<kernel>("attn_fma_bwd", key_units + row_units, fma_smem(DP, 4, 2), s, a));
+  constexpr auto kernel = k_attn_fma_bwd<T, DP, I, J>;
+  FVX_TRY(fma_launch<kernel>("attn_fma_bwd", key_units + row_units, fma_smem(DP, tile, 2, 2, 2), s, a));
   SumArgs sum = {};
   int arrays = 0;
   auto add = [&](const float* part, void* dst, int64_t n, int splits) {
@@ -790,10 +799,24 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
   return check_launch("attn_sum");
 }
 
+// Calls f with the type, the head's size rounded up and the tile: 16 or 32 rows
+// or 16 keys where no sample has more of them.
 template <typename F>
-fvx_status by_type(fvx_dtype dt, int d, F&& f) {
-  if (dt == FVX_F32) return d <= 64 ? f.template operator()<float, 64>() : f.template operator()<float, 128>();
-  return d <= 64 ? f.template operator()<__nv_bfloat16, 64>() : f.template operator()<__nv_bfloat16, 128>();
+fvx_status by_shape(const AttnCall& c, F&& f) {
+  if (c.dt != FVX_F32)
+    return c.d <= 64 ? f.template operator()<__nv_bfloat16, 64, 4, 4>() : f.template operator()<__nv_bfloat16, 128, 4, 4>();
+  int64_t rows = 0, keys = 0;
+  for (int b = 0; b < c.items; ++b) {
+    rows = std::max(rows, (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared);
+    keys = std::max(keys, c.kv_offsets[b + 1] - c.kv_offsets[b]);
+  }
+  auto with = [&]<int DP>() {
+    if (keys <= 16 && rows > 16) return f.template operator()<float, DP, 4, 1>();
+    if (rows <= 16) return f.template operator()<float, DP, 1, 4>();
+    if (rows <= 32) return f.template operator()<float, DP, 2, 4>();
+    return f.template operator()<float, DP, 4, 4>();
+  };
+  return c.d <= 64 ? with.template operator()<64>() : with.template operator()<128>();
 }
 
 }  // namespace
@@ -871,7 +894,7 @@ fvx_status fvx_cross_attention(fvx_dtype dt, const void* q, int64_t q_token, int
     Scratch scr(s);
     if (attn_few_serves(c)) return attn_few_forward(c, s, scr);
     if (attn_tc_serves(c, false)) return attn_tc_forward(c, s, scr);
-    return by_type(dt, d, [&]<typename T, int DP>() { return fma_forward<T, DP>(c, s, scr, sms); });
+    return by_shape(c, [&]<typename T, int DP, int I, int J>() { return fma_forward<T, DP, I, J>(c, s, scr, sms); });
   } catch (const std::exception& e) {
     set_error("%s: %s", who, e.what());
     return FVX_ERR_ALLOC;
@@ -935,7 +958,9 @@ fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t 
             <<<grid, kFmaThreads, 0, s>>>(c.dout, (const __nv_bfloat16*)out, rows, heads, d, delta);
       FVX_TRY(check_launch("attn_delta"));
     }
-    return by_type(dt, d, [&]<typename T, int DP>() { return fma_backward<T, DP>(c, delta, s, scr, sms); });
+    return by_shape(c, [&]<typename T, int DP, int I, int J>() {
+      return fma_backward<T, DP, I, J>(c, delta, s, scr, sms);
+    });
   } catch (const std::exception& e) {
     set_error("%s: %s", who, e.what());
     return FVX_ERR_ALLOC;

@@ -170,6 +170,16 @@ def test_a_few_rows(qlens, klens, heads, kv_heads, d, dtype):
         assert all((got[n] == again[n]).all() for n in got)
 
 
+@pytest.mark.parametrize("drop", [0.0, 0.4])
+@pytest.mark.parametrize("qlens,klens,heads,kv_heads,d", [
+    ([16], [200], 2, 2, 40), ([5, 0, 1], [700, 3, 64], 6, 2, 100), ([4, 8], [65, 130], 4, 2, 128), ([9], [1], 3, 3, 20),
+    ([10, 32, 1], [129, 0, 400], 2, 2, 64), ([8, 7], [513, 64], 12, 3, 128), ([17], [63], 1, 1, 12),
+    ([200, 33, 0], [16, 1, 9], 4, 4, 40), ([300], [7], 6, 2, 128), ([64, 129], [15, 16], 2, 1, 100), ([16], [16], 2, 2, 32)])
+def test_small_tiles(qlens, klens, heads, kv_heads, d, drop):
+    """fp32 tiles of 16 and 32 rows, and of 16 keys."""
+    _check(*_case(qlens, klens, heads, kv_heads, d, "f32", 61, drop=drop))
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("scale", [2.5, -0.7, 0.0])
 def test_a_few_rows_that_hold_anything(scale, dtype):
