@@ -680,23 +680,36 @@ std::vector<int32_t> unit_prefix(const AttnCall& c, FmaTile t, bool by_keys, int
   return p;
 }
 
-// Splits of the inner loops, at most 32: as many as keep the units that have
-// work (a sample's loop has no more ranges than tiles) in one wave of two blocks
-// per multiprocessor.  9 samples of 8 to 26 rows on 1400 to 2600 keys, 5 key
-// heads of 100: 6 splits, 270 units, 107 us; 7, 315 units, 151.
-int pick_splits(const AttnCall& c, FmaTile t, bool by_keys, int sms) {
+// Splits of the inner loops, at most 32, with the least time in tiles: that of
+// the longest unit while the units that have work (a sample's loop has no more
+// ranges than tiles) fit one wave of two blocks per multiprocessor, past that
+// their share and half the longest unit; a unit's start and end and the kernel
+// that adds the ranges up (`join`; backward, one for all three gradients) count as
+// tiles.  9 samples of 8 to 26 rows on 1400 to
+// 2600 keys, 5 key heads of 100: 6 splits, 270 units, 107 us; 7, 315 units, 151.
+int pick_splits(const AttnCall& c, FmaTile t, bool by_keys, int sms, double join) {
+  constexpr double kEnds = 2.0;
   const int outer = by_keys ? t.keys : t.rows, inner = by_keys ? t.rows : t.keys;
   int splits = 1;
-  for (int s = 2; s <= 32; ++s) {
-    int64_t units = 0, longest = 0;
+  double best = 1e300;
+  for (int s = 1; s <= 32; ++s) {
+    int64_t units = 0, longest = 0, tiles = 0;
     for (int b = 0; b < c.items; ++b) {
       const int64_t rows = (c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared, keys = c.kv_offsets[b + 1] - c.kv_offsets[b];
       const int64_t loop = ((by_keys ? rows : keys) + inner - 1) / inner;
-      units += ((by_keys ? keys : rows) + outer - 1) / outer * c.kv_heads * std::min<int64_t>(s, loop);
-      longest = std::max(longest, loop);
+      const int64_t n = ((by_keys ? keys : rows) + outer - 1) / outer * c.kv_heads;
+      units += n * std::min<int64_t>(s, loop);
+      tiles += n * loop;
+      if (n > 0) longest = std::max(longest, (loop + s - 1) / s);
     }
-    if (units > 2 * sms || s > longest) break;
-    splits = s;
+    const double unit = (double)longest + kEnds, wave = 2.0 * sms;
+    const double time = (units <= wave ? unit : ((double)tiles + kEnds * (double)units) / wave + 0.5 * unit) +
+                        (s > 1 ? join : 0.0);
+    if (time < best) {
+      best = time;
+      splits = s;
+    }
+    if (longest <= 1) break;
   }
   return splits;
 }
@@ -742,7 +755,7 @@ template <typename T, int DP, int I, int J>
 fvx_status fma_forward(const AttnCall& c, cudaStream_t s, Scratch& scr, int sms) {
   constexpr FmaTile tile{16 * I, 16 * J};
   FmaArgs a = fma_args(c);
-  a.splits = pick_splits(c, tile, false, sms);
+  a.splits = pick_splits(c, tile, false, sms, 2.0);
   int64_t units = 0;
   const std::vector<int32_t> prefix = unit_prefix(c, tile, false, a.splits, &units);
   FVX_TRY(attn_items(c, prefix.data(), 3, s, scr, &a.items));
@@ -769,8 +782,8 @@ fvx_status fma_backward(const AttnCall& c, const float* delta, cudaStream_t s, S
   a.out = c.dq;
   a.dk = c.dk;
   a.dv = c.dv;
-  a.splits = pick_splits(c, tile, false, sms);
-  a.key_splits = pick_splits(c, tile, true, sms);
+  a.splits = pick_splits(c, tile, false, sms, 0.5);
+  a.key_splits = pick_splits(c, tile, true, sms, 0.5);
   int64_t row_units = 0, key_units = 0;
   std::vector<int32_t> prefix = unit_prefix(c, tile, false, a.splits, &row_units);
   const std::vector<int32_t> by_keys = unit_prefix(c, tile, true, a.key_splits, &key_units);
