@@ -115,11 +115,27 @@ __device__ __forceinline__ void store4(void* dst, int64_t row, int c, int d, con
     if (c + i < d) p[i] = from_f32<T>(v[i]);
 }
 
-// rows [r0, r0 + ROWS) of an item's (token, shared head) rows, zeros past the end
+// rows [r0, r0 + ROWS) of an item's (token, shared head) rows, zeros past the end;
+// copies of fp32 rows are under way until copies_wait
 template <typename T, int DP, int ROWS>
 __device__ __forceinline__ void load_rows(const FmaArgs& a, float* dst, const HeadsView& t, int token0, int r0,
                                           int rows, int head0) {
   constexpr int kQuads = DP / 4;
+  if constexpr (sizeof(T) == 4) {
+    if (a.vec) {
+#pragma unroll
+      for (int e = threadIdx.x; e < ROWS * kQuads; e += kFmaThreads) {
+        const int r = e / kQuads, c = (e % kQuads) * 4;
+        const bool in = r0 + r < rows && c < a.d;
+        const int at = in ? r0 + r : 0, tok = at / a.shared, g = at - tok * a.shared;
+        tc::copy16(tc::smem_u32(dst + r * pitch_of(DP) + c),
+                   reinterpret_cast<const T*>(t.p) + (int64_t)(token0 + tok) * t.token + (int64_t)(head0 + g) * t.head +
+                       (in ? c : 0),
+                   in);
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int e = threadIdx.x; e < ROWS * kQuads; e += kFmaThreads) {
     const int r = e / kQuads, c = (e % kQuads) * 4;
@@ -138,6 +154,35 @@ template <typename T, int DP, int KEYS>
 __device__ __forceinline__ void load_keys(const FmaArgs& a, float* dst, const HeadsView& t, int key0, int j0, int keys,
                                           int h) {
   constexpr int kQuads = DP / 4;
+  if constexpr (sizeof(T) == 4) {
+    if (a.vec) {
+      constexpr int kTurns = KEYS * kQuads / kFmaThreads;
+      static_assert(KEYS * kQuads % kFmaThreads == 0, "every thread copies as much");
+      bool in[kTurns];
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int e = threadIdx.x + i * kFmaThreads;
+        in[i] = j0 + e / kQuads < keys;
+      }
+      if (a.mask) {
+#pragma unroll
+        for (int i = 0; i < kTurns; ++i) {
+          const int j = (threadIdx.x + i * kFmaThreads) / kQuads;
+          in[i] = in[i] && __ldg(a.mask + key0 + min(j0 + j, keys - 1));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int e = threadIdx.x + i * kFmaThreads, j = e / kQuads, c = (e % kQuads) * 4;
+        const bool here = in[i] && c < a.d;
+        tc::copy16(tc::smem_u32(dst + j * pitch_of(DP) + c),
+                   reinterpret_cast<const T*>(t.p) + (int64_t)(key0 + (here ? j0 + j : 0)) * t.token +
+                       (int64_t)h * t.head + (here ? c : 0),
+                   here);
+      }
+      return;
+    }
+  }
 #pragma unroll
   for (int e = threadIdx.x; e < KEYS * kQuads; e += kFmaThreads) {
     const int j = e / kQuads, c = (e % kQuads) * 4;
@@ -297,6 +342,7 @@ __global__ void __launch_bounds__(kFmaThreads, DP > 64 && I * J > 8 ? 1 : 2) k_a
     bool keep[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
+    tc::copies_wait();
     __syncthreads();
     float s[I][J];
     tile_dot<DP, I, J>(qs, ks, ty, tx, a.d, s);
@@ -403,6 +449,7 @@ __device__ __forceinline__ void fma_dq(const FmaArgs& a, float* sm, int unit) {
     bool keep[J];
 #pragma unroll
     for (int j = 0; j < J; ++j) keep[j] = kept(a, w.key0, j0 + tx + 16 * j, w.keys);
+    tc::copies_wait();
     __syncthreads();
     float s[I][J], dp[I][J];
     tile_dot<DP, I, J>(qs, ks, ty, tx, a.d, s);
@@ -461,6 +508,7 @@ __device__ __forceinline__ void fma_dkv(const FmaArgs& a, float* sm, int unit) {
     float lse[I], delta[I];
 #pragma unroll
     for (int i = 0; i < I; ++i) row_constants(a, w, r0 + ty + 16 * i, &lse[i], &delta[i]);
+    tc::copies_wait();
     __syncthreads();
     float s[I][J], dp[I][J];
     tile_dot<DP, I, J>(qs, ks, ty, tx, a.d, s);

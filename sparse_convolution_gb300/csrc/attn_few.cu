@@ -83,11 +83,6 @@ __device__ __forceinline__ FewPiece few_piece(const FewArgs& a) {
   return p;
 }
 
-// 16 bytes into shared memory, zeros where `kept` is false
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool kept) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(kept ? 16 : 0) : "memory");
-}
-
 // The results of the block's warps, each [rows][D] at w * pitch floats, its
 // maxima (in powers of 2) and sums, joined, and then those of the cluster's
 // blocks, each of which writes its share of the columns.  b_acc: shared memory
@@ -220,8 +215,8 @@ __global__ void __launch_bounds__(kFewThreads, R <= 4 ? 4 : 2) k_attn_few_f32(co
       const bool in = j < p.to;
       const int64_t at = p.key0 + (in ? j : 0);
       if (mine) {
-        copy16(tc::smem_u32(dst + i * 32), pk + at * a.k.token, in);
-        copy16(tc::smem_u32(dst + (F + i) * 32), pv + at * a.v.token, in);
+        tc::copy16(tc::smem_u32(dst + i * 32), pk + at * a.k.token, in);
+        tc::copy16(tc::smem_u32(dst + (F + i) * 32), pv + at * a.v.token, in);
       }
       if (in) kept |= (a.mask ? (uint32_t)__ldg(a.mask + at) : 1u) << (8 * i);
     }
@@ -449,8 +444,8 @@ __global__ void __launch_bounds__(kFewThreads, DP > 64 ? 2 : 3) k_attn_few_bf16(
       const bool in = ((kept >> key) & 1u) && mine;  // zeros for what is dropped, whatever lies there
       const int64_t at = p.key0 + (in ? j0 + key : 0);
       const uint32_t to = dst + key * (DP * 2) + ((chunk ^ (key & 7)) * 16);
-      copy16(to, pk + at * a.k.token, in);
-      copy16(to + C::kTile, pv + at * a.v.token, in);
+      tc::copy16(to, pk + at * a.k.token, in);
+      tc::copy16(to + C::kTile, pv + at * a.v.token, in);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
