@@ -372,6 +372,7 @@ __global__ void __launch_bounds__(kFmaThreads, DP > 64 && I * J > 8 ? 1 : 2) k_a
     __syncthreads();
     tile_accumulate<DP, kScorePitch>(ps, vs, ty, tx, min(16 * J, w.keys - j0), acc);
   }
+  tc::copies_wait();  // of a range without tiles
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int r = r0 + ty + 16 * i;
@@ -462,6 +463,7 @@ __device__ __forceinline__ void fma_dq(const FmaArgs& a, float* sm, int unit) {
     __syncthreads();
     tile_accumulate<DP, kScorePitch>(ps, ks, ty, tx, min(16 * J, w.keys - j0), acc);
   }
+  tc::copies_wait();  // of a range without tiles
 #pragma unroll
   for (int i = 0; i < I; ++i) {
     const int r = r0 + ty + 16 * i;
@@ -526,6 +528,7 @@ __device__ __forceinline__ void fma_dkv(const FmaArgs& a, float* sm, int unit) {
     tile_accumulate<DP, kScorePitch>(ps, os, ty, tx, count, dv);
     tile_accumulate<DP, kScorePitch>(ds, qs, ty, tx, count, dk);
   }
+  tc::copies_wait();  // of a range without tiles
 #pragma unroll
   for (int i = 0; i < J; ++i) {
     const int j = j0 + ty + 16 * i;
