@@ -153,15 +153,18 @@ __device__ __forceinline__ Kept kept_keys(const uint8_t* mask, int keys, int t, 
 // shared memory through the async proxy, hence the fence.
 template <int ATOMS>
 __device__ __forceinline__ void zero_dropped(unsigned char* tile, const Kept& k, int words, int lane) {
+  // eight lanes write a row, four rows at once
+  unsigned char* const mine = tile + (lane >> 3) * 128 + (lane & 7) * 16;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    uint32_t drop = i < words ? ~k.w[i] : 0u;
-    while (drop) {
-      const int r = 32 * i + __ffs(drop) - 1;
-      drop &= drop - 1;
+    const uint32_t drop = i < words ? ~k.w[i] >> (lane >> 3) : 0u;
 #pragma unroll
-      for (int at = 0; at < ATOMS; ++at) reinterpret_cast<uint32_t*>(tile + at * kAtom + r * 128)[lane] = 0u;
-    }
+    for (int r = 0; r < 32; r += 4)
+      if ((drop >> r) & 1u) {
+#pragma unroll
+        for (int at = 0; at < ATOMS; ++at)
+          *reinterpret_cast<uint4*>(mine + at * kAtom + (32 * i + r) * 128) = make_uint4(0u, 0u, 0u, 0u);
+      }
   }
   fence_proxy_async();
   __syncwarp();
