@@ -153,18 +153,24 @@ __device__ __forceinline__ Kept kept_keys(const uint8_t* mask, int keys, int t, 
 // shared memory through the async proxy, hence the fence.
 template <int ATOMS>
 __device__ __forceinline__ void zero_dropped(unsigned char* tile, const Kept& k, int words, int lane) {
-  // eight lanes write a row, four rows at once
-  unsigned char* const mine = tile + (lane >> 3) * 128 + (lane & 7) * 16;
+  // Eight lanes write a row, four rows at once.  The loop is unrolled for 64-wide
+  // heads only: the warp that issues the wide heads' products does so slower
+  // with the long code beside them (65,536 rows x 2048 keys 420 us, not 396).
+  auto four_rows = [&](int r) {
+    unsigned char* const at = tile + r * 128 + (lane & 7) * 16;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t drop = i < words ? ~k.w[i] >> (lane >> 3) : 0u;
+    for (int i = 0; i < 4; ++i)
+      if (i < words && !((k.w[i] >> r) & 1u)) {
 #pragma unroll
-    for (int r = 0; r < 32; r += 4)
-      if ((drop >> r) & 1u) {
-#pragma unroll
-        for (int at = 0; at < ATOMS; ++at)
-          *reinterpret_cast<uint4*>(mine + at * kAtom + (32 * i + r) * 128) = make_uint4(0u, 0u, 0u, 0u);
+        for (int x = 0; x < ATOMS; ++x) *reinterpret_cast<uint4*>(at + x * kAtom + i * 4096) = make_uint4(0u, 0u, 0u, 0u);
       }
+  };
+  if constexpr (ATOMS == 1) {
+#pragma unroll
+    for (int r = 0; r < 32; r += 4) four_rows(r + (lane >> 3));
+  } else {
+#pragma unroll 1
+    for (int r = lane >> 3; r < 32; r += 4) four_rows(r);
   }
   fence_proxy_async();
   __syncwarp();
@@ -254,7 +260,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       if (!w.valid) break;
       const int r0 = w.r0 + slot * a.tile_rows;
       if (r0 >= w.rows) continue;  // the pair's second tile has no rows
-      const int n = w.t1 - w.t0;
+      const int n = w.t1 - w.t0, r = r0 + row;
+      const bool live = row < a.tile_rows && r < w.rows;
       float m_ref = -INFINITY, total = 0.0f;
       uint8_t mb[4];
       if (n > 0) mask_bytes(a.mask, w.key0, w.keys, w.t0, lane, mb);
@@ -334,7 +341,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           // found, and taken again in the few tiles where it matters.
           float m8[8] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY, -INFINITY};
           powers(m_ref == -INFINITY ? 0.0f : m_ref, m8);
-          mx = top_of(m8);
+          mx = live ? top_of(m8) : -INFINITY;  // a row that is none holds anything
           done = !__any_sync(0xffffffffu, mx > m_ref + kLazy);
         } else {
           float m8[8];
@@ -344,7 +351,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
           for (int i = 16; i < 128; i += 16)
 #pragma unroll
             for (int k = 0; k < 8; ++k) m8[k] = max3(m8[k], __uint_as_float(r[i + k]), __uint_as_float(r[i + k + 8]));
-          mx = top_of(m8);
+          mx = C::kOwnP && !live ? -INFINITY : top_of(m8);
         }
         if (j == 0) {
           m_ref = mx;
@@ -380,8 +387,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
         if (lane == 0) mbar_arrive(p_ready);
       }
       // ---- the rows' results
-      const int r = r0 + row;
-      const bool live = row < a.tile_rows && r < w.rows;
       const int tok = a.shared == 1 ? r : r / a.shared, g = r - tok * a.shared;
       const int64_t at = (int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g;
       const int64_t pat = (int64_t)w.split * a.all_rows + at;
