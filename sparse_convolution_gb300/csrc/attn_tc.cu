@@ -1542,10 +1542,11 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
     return ((c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared + tile_rows(c) - 1) / tile_rows(c);
   };
   auto tiles_of_keys = [&](int b) { return (c.kv_offsets[b + 1] - c.kv_offsets[b] + kM - 1) / kM; };
-  int64_t work = 0, single = 0;
+  int64_t work = 0, key_work = 0, single = 0;
   for (int b = 0; b < c.items; ++b) {
     const int64_t w = row_tiles(b) * tiles_of_keys(b);
     work += w * c.kv_heads;
+    key_work += w > 0 ? tiles_of_keys(b) * c.kv_heads : 0;
     single += w > 0 ? c.kv_heads : 0;
   }
   auto ceil_div = [](int64_t x, int64_t y) { return (x + y - 1) / y; };
@@ -1554,7 +1555,7 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
   // of 1 to 40 tiles; and of one 128-row slab of partial sums, shared by all.
   const double tile_cost = c.d <= 64 ? 3500.0 : 7000.0, key_cost = c.d <= 64 ? 5000.0 : 9000.0;
   const double sum_cost = 128.0 * 4 * (c.d <= 64 ? 64 : 128) * c.kv_heads / (sms * 25.0);
-  const double share = std::max((double)work * tile_cost / sms, tile_cost + key_cost);
+  const double share = std::max(((double)work * tile_cost + (double)key_work * key_cost) / sms, tile_cost + key_cost);
   // Main kernel and sums, 17,001 rows on 1024 keys and 15,800 on 1500, 8 heads of
   // 64: rows in 8 and 11 ranges, keys whole, 406 us; rows in 8 and 5, the second's
   // keys in 2, 366; rows whole, keys in 8 and 11, 547 (partial sums of dQ past
@@ -1564,7 +1565,7 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
   // wave; every item then takes the fewest units that stay within it, and among
   // those the ranges with the least partial sums.  With more items than
   // multiprocessors, one unit per item and key head.
-  for (double room : {1.0, 1.03, 1.06, 1.1, 1.15, 1.2, 1.3, 1.45, 1.7, 2.1, 3.0, 1e30}) {
+  for (double room : {1.0, 1.03, 1.06, 1.1, 1.15, 1.2, 1.3, 1.45, 1.7, 2.1, 2.6, 3.3, 4.5, 1e30}) {
     const double most = single >= sms ? 1e300 : share * room;
     int64_t u = 0;
     bool fits = true;
