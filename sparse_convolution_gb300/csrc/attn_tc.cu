@@ -1342,7 +1342,8 @@ __global__ void __launch_bounds__(256) k_attn_stats(const __grid_constant__ Attn
 // head (items of one key tile were written by the main kernel, items without
 // keys get zeros), the others dK and dV, one per key tile, key head and 8
 // columns (items whose rows were not cut were written; items without rows get
-// zeros).  A thread has the loads of a whole range under way at once.
+// zeros).  A thread has the loads of a whole range under way at once, or (FINE,
+// few row tiles: 48 with 28 ranges took 49 us) those of 16 columns of four.
 __device__ __forceinline__ void add_parts(float (&s)[8], const float* src) {
   const float4 x = __ldg(reinterpret_cast<const float4*>(src)), y = __ldg(reinterpret_cast<const float4*>(src + kM * 4));
   s[0] += x.x;
@@ -1361,11 +1362,13 @@ __device__ __forceinline__ void store_rounded(__nv_bfloat16* dst, const float (&
   for (int x = 0; x < 4; ++x) pv[x] = pack_bf16(s[2 * x] * scale, s[2 * x + 1] * scale);
   *reinterpret_cast<uint4*>(dst) = v;
 }
-template <int DP>
+template <int DP, bool FINE>
 __global__ void __launch_bounds__(256) k_attn_sums_out(const __grid_constant__ BwdArgs a, int row_blocks) {
   const int row = threadIdx.x & 127;
   if ((int)blockIdx.x < row_blocks) {
-    const int tile = blockIdx.x / a.kv_heads, kh = blockIdx.x - tile * a.kv_heads;
+    constexpr int kPieces = FINE ? DP / 16 : 1, kCols = DP / 16 / kPieces;  // pieces of a tile, 16 columns each or all
+    const int block = blockIdx.x / kPieces, piece = blockIdx.x - block * kPieces;
+    const int tile = block / a.kv_heads, kh = block - tile * a.kv_heads;
     const int b = a.items.find(kItemTile, tile);
     const int q0 = a.items.q0(b), rows = (a.items.q0(b + 1) - q0) * a.shared;
     const int keys = a.items.k0(b + 1) - a.items.k0(b);
@@ -1374,16 +1377,17 @@ __global__ void __launch_bounds__(256) k_attn_sums_out(const __grid_constant__ B
     const int64_t slab = (int64_t)a.tiles * a.kv_heads * (kM * DP);
     const int r = (tile - a.items.at(kItemTile, b)) * a.tile_rows + row;
     if (row >= a.tile_rows || r >= rows) return;
-    const int tok = r / a.shared, g = r - tok * a.shared, c0 = (threadIdx.x >> 7) * 8;
-    const float* src = a.dq_sum + (int64_t)blockIdx.x * (kM * DP) + c0 * kM + row * 4;
+    const int tok = r / a.shared, g = r - tok * a.shared, c0 = (threadIdx.x >> 7) * 8 + piece * 16;
+    const float* src = a.dq_sum + (int64_t)block * (kM * DP) + c0 * kM + row * 4;
     __nv_bfloat16* out = a.dq + ((int64_t)(q0 + tok) * a.heads + kh * a.shared + g) * a.d;
-    float s[DP / 16][8] = {};
-    for (int k = 0; k < ranges; ++k, src += slab)
+    float s[kCols][8] = {};
+#pragma unroll(FINE ? 4 : 1)
+    for (int k = 0; k < ranges; ++k)
 #pragma unroll
-      for (int i = 0; i < DP / 16; ++i)
-        if (c0 + 16 * i < a.d) add_parts(s[i], src + i * 16 * kM);
+      for (int i = 0; i < kCols; ++i)
+        if (c0 + 16 * i < a.d) add_parts(s[i], src + k * slab + i * 16 * kM);
 #pragma unroll
-    for (int i = 0; i < DP / 16; ++i)
+    for (int i = 0; i < kCols; ++i)
       if (c0 + 16 * i < a.d) store_rounded(out + c0 + 16 * i, s[i], a.scale);
     return;
   }
@@ -1676,11 +1680,13 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
     k_attn_tc_bwd<DP><<<std::min(a.units, sms), kBwdThreads, C::kSmem, s>>>(a);
     FVX_TRY(check_launch("attn_tc_bwd"));
   }
-  const int64_t dq_blocks = p.dq_sums || p.dq_zeros ? (int64_t)row_blocks : 0;
+  const bool fine = row_blocks < 4 * (size_t)sms;
+  const int64_t dq_blocks = p.dq_sums || p.dq_zeros ? (int64_t)row_blocks * (fine ? DP / 16 : 1) : 0;
   const int64_t dkv_blocks = p.dkv_parts ? (int64_t)p.key_tiles * c.kv_heads * (DP / 8) : 0;
   if (dq_blocks + dkv_blocks > 0) {
     LaunchScope ls("attn_sums_out", s);
-    k_attn_sums_out<DP><<<(unsigned)(dq_blocks + dkv_blocks), 256, 0, s>>>(a, (int)dq_blocks);
+    if (fine) k_attn_sums_out<DP, true><<<(unsigned)(dq_blocks + dkv_blocks), 256, 0, s>>>(a, (int)dq_blocks);
+    else k_attn_sums_out<DP, false><<<(unsigned)(dq_blocks + dkv_blocks), 256, 0, s>>>(a, (int)dq_blocks);
     FVX_TRY(check_launch("attn_sums_out"));
   }
   return FVX_OK;
