@@ -276,10 +276,15 @@ int pow2_at_least(int64_t v, int most) {
   while (p < v && p < most) p <<= 1;
   return p;
 }
-// Lanes of a row and vectors per lane.
-int lanes_for(int64_t c, int vec) { return pow2_at_least(c / vec, 32); }
-int iters_for(int64_t c, int vec) {
-  const int lanes = lanes_for(c, vec);
+// Lanes of a row and vectors per lane: one each of 16 bytes while that fits a
+// warp, and four of the narrower ones, since a row's shuffles and bookkeeping
+// then cost more instructions than its few values.
+int lanes_for(fvx_dtype dt, int64_t c, int vec) {
+  const int each = vec * (dt == FVX_F32 ? 4 : 2) == 16 ? 1 : 4;
+  return pow2_at_least((c / vec + each - 1) / each, 32);
+}
+int iters_for(fvx_dtype dt, int64_t c, int vec) {
+  const int lanes = lanes_for(dt, c, vec);
   return (int)((c / vec + lanes - 1) / lanes);
 }
 
@@ -444,7 +449,7 @@ fvx_status rows_launch(const char* name, fvx_dtype dt, int vec, const RowArgs& a
     return (dt == FVX_F32 ? stream_rows_f32 : stream_rows_bf16)(name, (RowOp)OP, (a.c / vec + lanes - 1) / lanes, args, g.blocks,
                                                                 smem, s);
   }
-  return by_row_shape(dt, vec, iters_for(a.c, vec), [&]<typename T, int VEC, int ITER>() -> fvx_status {
+  return by_row_shape(dt, vec, iters_for(dt, a.c, vec), [&]<typename T, int VEC, int ITER>() -> fvx_status {
     return launch(name, k_rows<T, VEC, ITER, OP>, dim3(g.blocks), parts, s, a);
   });
 }
@@ -495,7 +500,7 @@ fvx_status fvx_layer_norm(fvx_dtype dt, const void* x, int64_t ldx, int64_t n, i
   }
   const int vec = pick_vec(dt, c, a);
   if (c <= kRegCols) {
-    a.lanes = lanes_for(c, vec);
+    a.lanes = lanes_for(dt, c, vec);
     return group ? rows_launch<kForwardCodes>("norm_rows", dt, vec, a, row_grid<kForwardCodes>(dt, vec, a, sms), s)
                  : rows_launch<kForward>("norm_rows", dt, vec, a, row_grid<kForward>(dt, vec, a, sms), s);
   }
@@ -556,7 +561,7 @@ fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, c
   const bool sums = dw || db;
   int parts = 0;
   if (c <= kRegCols) {
-    a.lanes = lanes_for(c, vec);
+    a.lanes = lanes_for(dt, c, vec);
     const RowGrid g = group ? row_grid<kBackwardCodes>(dt, vec, a, sms) : row_grid<kBackward>(dt, vec, a, sms);
     parts = g.blocks;
     if (sums && !(a.part = scr.get<float>((size_t)parts * 2 * c))) return FVX_ERR_ALLOC;
@@ -603,7 +608,7 @@ fvx_status fvx_checkpoint_pack(fvx_dtype dt, const void* x, int64_t ldx, int64_t
   a.groups = (int)((c + group - 1) >> shift);
   if (c > kRegCols) return pack_wide(dt, a, (cudaStream_t)stream, sms);
   const int vec = pick_vec(dt, c, a);
-  a.lanes = lanes_for(c, vec);
+  a.lanes = lanes_for(dt, c, vec);
   return rows_launch<kPack>("ck_pack", dt, vec, a, row_grid<kPack>(dt, vec, a, sms), (cudaStream_t)stream);
 }
 
@@ -641,7 +646,7 @@ fvx_status fvx_checkpoint_restore(fvx_dtype dt, int32_t group, const int8_t* cod
   a.groups = (int)((c + group - 1) >> shift);
   const int vec = pick_vec(dt, c, a);
   if (c <= kRegCols) {
-    a.lanes = lanes_for(c, vec);
+    a.lanes = lanes_for(dt, c, vec);
     return mean ? rows_launch<kRestoreNorm>("ck_restore", dt, vec, a, row_grid<kRestoreNorm>(dt, vec, a, sms), s)
                 : rows_launch<kRestore>("ck_restore", dt, vec, a, row_grid<kRestore>(dt, vec, a, sms), s);
   }
