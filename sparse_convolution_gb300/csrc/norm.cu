@@ -393,8 +393,8 @@ struct RowGrid {
   bool stream;
   StreamArgs args;
 };
-// Dense rows of 16-byte vectors, enough of them for every block to take several
-// stages, are streamed through shared memory.
+// Rows of 16-byte vectors, dense or nearly so, enough of them for every block to
+// take several stages, are streamed through shared memory.
 template <int OP>
 RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
   using Is = OpIs<OP>;
@@ -403,12 +403,14 @@ RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
   g.blocks = grid_for(a.n, kThreads / a.lanes, sms, Is::kBack ? 4 : 16);
   auto at16 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
   if (vec * elem != 16) return g;
-  if (!Is::kFromCodes && !(a.ldx == a.c && at16(a.x))) return g;
+  // rows a little apart are copied with what lies between them
+  auto close = [&](int64_t ld) { return ld <= a.c + a.c / 4; };
+  if (!Is::kFromCodes && !(close(a.ldx) && at16(a.x))) return g;
   if (Is::kFromCodes && !(at16(a.codes) && at16(a.steps))) return g;
-  if (Is::kBack && !(a.lddy == a.c && at16(a.dy))) return g;
+  if (Is::kBack && !(close(a.lddy) && at16(a.dy))) return g;
   if (Is::kStats && !(at16(a.mean_in) && at16(a.rstd_in))) return g;
-  const int x_row = a.c * (Is::kFromCodes ? 1 : elem);
-  const int row = x_row + (Is::kBack ? a.c * elem : 0);
+  const int x_row = Is::kFromCodes ? a.c : (int)a.ldx * elem, dy_row = Is::kBack ? (int)a.lddy * elem : 0;
+  const int row = x_row + dy_row;
   StreamArgs& s = g.args;
   s.r = a;
   // Two vectors of 16 lanes instead of one of 32 halve the steps of a row's sums
@@ -421,10 +423,12 @@ RowGrid row_grid(fvx_dtype dt, int vec, const RowArgs& a, int sms) {
   // a multiple of the rows of a turn (eight at least: the small arrays' copies
   // are then multiples of 16 bytes), about 10 KB
   s.rows = per_block * std::max(1, 10240 / (per_block * row));
-  s.stages = a.n / s.rows;
+  // the tensor's last row ends with its last channel
+  const bool apart = (!Is::kFromCodes && a.ldx > a.c) || (Is::kBack && a.lddy > a.c);
+  s.stages = (apart ? std::max<int64_t>(a.n - 1, 0) : a.n) / s.rows;
   auto up = [](int v) { return (v + 15) & ~15; };
   s.off_dy = up(s.rows * x_row);
-  s.off_steps = s.off_dy + (Is::kBack ? up(s.rows * a.c * elem) : 0);
+  s.off_steps = s.off_dy + up(s.rows * dy_row);
   s.off_mean = s.off_steps + (Is::kFromCodes ? up(s.rows * a.groups * 4) : 0);
   s.off_rstd = s.off_mean + (Is::kStats ? up(s.rows * 4) : 0);
   s.stage_bytes = (s.off_rstd + (Is::kStats ? up(s.rows * 4) : 0) + 127) & ~127;

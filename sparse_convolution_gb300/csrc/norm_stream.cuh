@@ -5,7 +5,7 @@
 namespace fvx {
 namespace {
 
-// Many dense, aligned rows: a warp copies stages of rows to shared memory ahead
+// Many aligned rows, dense or nearly so: a warp copies stages of rows to shared memory ahead
 // of the eight that work on them.  Loads into registers keep at most a few
 // vectors per thread under way, and the registers they need cost the warps that
 // would hide them (4,000,000 x 64 bf16 backward: 297 us with one row in flight
@@ -36,12 +36,13 @@ __global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 16 || (VEC * ITER
     tc::mbar_init_fence();
   }
   __syncthreads();
+  const int x_pitch = Is::kFromCodes ? a.c : (int)a.ldx, dy_pitch = (int)a.lddy;
   Rows<T, VEC, ITER, OP, LANES> rows(a);
   if (warp == kThreads / 32) {
     if (lane == 0) {
       uint32_t i = 0, phase = 1;
       int64_t k = 0;
-      const uint32_t x_bytes = (uint32_t)(s.rows * a.c * sizeof(X)), dy_bytes = (uint32_t)(s.rows * a.c * sizeof(T)),
+      const uint32_t x_bytes = (uint32_t)(s.rows * x_pitch * sizeof(X)), dy_bytes = (uint32_t)(s.rows * dy_pitch * sizeof(T)),
                      step_bytes = (uint32_t)(s.rows * a.groups * 4), stat_bytes = (uint32_t)(s.rows * 4);
       uint32_t bytes = x_bytes;
       if constexpr (Is::kBack) bytes += dy_bytes;
@@ -56,10 +57,10 @@ __global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 16 || (VEC * ITER
           tc::bulk_load(to, a.codes + row * a.c, x_bytes, bar);
           tc::bulk_load(to + s.off_steps, a.steps + row * a.groups, step_bytes, bar);
         } else {
-          tc::bulk_load(to, reinterpret_cast<const T*>(a.x) + row * a.c, x_bytes, bar);
+          tc::bulk_load(to, reinterpret_cast<const T*>(a.x) + row * x_pitch, x_bytes, bar);
         }
         if constexpr (Is::kBack)
-          tc::bulk_load(to + s.off_dy, reinterpret_cast<const T*>(a.dy) + row * a.c, dy_bytes, bar);
+          tc::bulk_load(to + s.off_dy, reinterpret_cast<const T*>(a.dy) + row * dy_pitch, dy_bytes, bar);
         if constexpr (Is::kStats) {
           tc::bulk_load(to + s.off_mean, a.mean_in + row, stat_bytes, bar);
           tc::bulk_load(to + s.off_rstd, a.rstd_in + row, stat_bytes, bar);
@@ -87,14 +88,14 @@ __global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 16 || (VEC * ITER
         for (int k = 0; k < ITER; ++k) {
           const int v = k * rows.lanes + rows.lane;
           const bool here = v < rows.nv;
-          in.x[k] = here ? raw_vec<X, VEC>(reinterpret_cast<const X*>(from) + r * a.c + v * VEC) : no_vec<X, VEC>();
+          in.x[k] = here ? raw_vec<X, VEC>(reinterpret_cast<const X*>(from) + r * x_pitch + v * VEC) : no_vec<X, VEC>();
           in.step[k] = 0.0f;
           if constexpr (Is::kFromCodes) {
             if (here)
               in.step[k] = reinterpret_cast<const float*>(from + s.off_steps)[r * a.groups + ((v * VEC) >> a.group_shift)];
           }
           if constexpr (Is::kBack)
-            in.dy[k] = here ? raw_vec<T, VEC>(reinterpret_cast<const T*>(from + s.off_dy) + r * a.c + v * VEC)
+            in.dy[k] = here ? raw_vec<T, VEC>(reinterpret_cast<const T*>(from + s.off_dy) + r * dy_pitch + v * VEC)
                             : no_vec<T, VEC>();
         }
         in.mean = in.rstd = 0.0f;

@@ -399,3 +399,36 @@ def test_refusals():
         with pytest.raises(fvx.FvxError) as e:
             call()
         assert e.value.status == "FVX_ERR_INVALID_ARG"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("n,c,pad", [(200_016, 64, 8), (200_000, 64, 16), (60_001, 256, 8), (300_009, 48, 8), (40_000, 1000, 24)])
+def test_long_rows_apart(n, c, pad, dtype):
+    """Rows a little apart, copied with what lies between them: the same bits as
+    from dense ones, whatever lies there, and the last row's end is the tensor's."""
+    import torch
+
+    import sparse_convolution_gb300 as fvx
+
+    x, w, b, dy = _inputs(n, c, dtype, 5 + pad)
+
+    def apart(t):
+        wide = torch.full((n * (c + pad) - pad,), float("nan"), dtype=t.dtype, device="cuda")
+        view = wide.as_strided((n, c), (c + pad, 1))
+        view.copy_(t)
+        return view
+
+    want = fvx.layer_norm(x, w, b, checkpoint_group=64)
+    got = fvx.layer_norm(apart(x), w, b, checkpoint_group=64)
+    assert all(torch.equal(p, q) for p, q in zip(want[:3], got[:3]))
+    assert torch.equal(want[3].codes, got[3].codes) and torch.equal(want[3].steps, got[3].steps)
+    packed = fvx.Checkpoint8.pack(apart(x), group=64)
+    assert torch.equal(packed.codes, want[3].codes)
+    for source, other in ((x, apart(x)), (want[3], want[3])):
+        a = fvx.layer_norm_backward(dy, source, want[1], want[2], w)
+        o = fvx.layer_norm_backward(apart(dy), other, want[1], want[2], w)
+        assert torch.equal(a[0], o[0])
+        # other stages, so the sums over the rows take another order: n terms of fp32
+        for p, q in zip(a[1:], o[1:]):
+            assert (p - q).abs().max() <= 2 * n * U * dy.float().abs().max() * 8
+    fvx.device_status()
