@@ -56,8 +56,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) { retu
 // about equally (8 reads of 16 bytes for 32 paired products of a thread); what
 // bounds a small call is the latency of a tile's loads, so inner loops are
 // split until there are two blocks per multiprocessor.  Measured: 8000 rows x
-// 500 keys and 5000 x 900, 8 heads of 64, forward 645 us, 27 TFLOP/s, backward
-// 1836 us, 24; 1208 rows x 6 heads on 219 keys, 3 key heads of 40, 17 and 43 us.
+// 500 keys and 5000 x 900, 8 heads of 64, forward 525 us, 33 TFLOP/s, backward
+// 1682 us, 26; 1208 rows x 6 heads on 219 keys, 3 key heads of 40, 19 and 35 us.
 struct FmaArgs {
   AttnItems items;
   HeadsView q, k, v, dout;

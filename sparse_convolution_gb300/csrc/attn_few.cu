@@ -21,10 +21,10 @@
 // them, one power to take and one sum to keep.
 //
 // Measured: 8 samples of one token on 777 to 4096 keys, 16 heads on 4 key heads
-// of 128, 20 us (2.4 TB/s; a block has eight turns, so the latencies of the
+// of 128, 18 us (2.6 TB/s; a block has eight turns, so the latencies of the
 // first loads and of the joins are most of it); 32 samples on 8192 keys, 4 key
-// heads of 128, one row each 96 us (5.6 TB/s), eight rows 100; the same in fp32
-// with one row 171 us (6.3 TB/s).
+// heads of 128, one row each 94 us (5.7 TB/s), eight rows 99; the same in fp32
+// with one row 170 us (6.3 TB/s).
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -611,7 +611,7 @@ bool loads16(const HeadsView& t, int elem) {
 
 // At most eight rows per key head of every sample, and rows that 16-byte loads
 // can read.  Against the tensor cores' tiles of 128 rows (bf16): the 8 samples
-// above 20 us and 37 with their join; 4 samples of two rows on 77 to 300 keys 10
+// above 18 us and 37 with their join; 4 samples of two rows on 77 to 300 keys 10
 // and 18; eight rows on 8192 keys, 32 samples, 100 and 100.
 bool attn_few_serves(const AttnCall& c) {
   const int elem = c.dt == FVX_F32 ? 4 : 2;

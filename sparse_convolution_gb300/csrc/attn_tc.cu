@@ -25,10 +25,10 @@
 // (in the exponent's base 2): until then p <= 2^8, far inside bf16's and
 // fp32's range, and the final division by the sum removes the factor exactly.
 //
-// Measured: 65,536 rows x 2048 keys x 8 heads of 128, 399 us, 1380 TFLOP/s (the
+// Measured: 65,536 rows x 2048 keys x 8 heads of 128, 395 us, 1390 TFLOP/s (the
 // softmax's warps and the products' issue both take most of that time); 17,001
-// rows x 1024 keys and 15,800 x 1500, 8 heads of 64, 120 us, 700 TFLOP/s: with
-// half the products per score the exponentials bound it (2.7e12 a second, of
+// rows x 1024 keys and 15,800 x 1500, 8 heads of 64, 124 us, 680 TFLOP/s: with
+// half the products per score the exponentials bound it (2.6e12 a second, of
 // 4.6e12 that the special function units compute).
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -725,13 +725,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
 //   warp 20         TMA loads
 //   warp 21         issues the five products
 //
-// Measured: 17,001 rows x 1024 keys and 15,800 x 1500, 8 heads of 64, 321 us, 656
-// TFLOP/s; 2 x 16,384 rows x 2048 keys, 8 heads of 128, 807 us, 850 TFLOP/s.  A
+// Measured: 17,001 rows x 1024 keys and 15,800 x 1500, 8 heads of 64, 300 us, 702
+// TFLOP/s; 2 x 16,384 rows x 2048 keys, 8 heads of 128, 830 us, 830 TFLOP/s.  A
 // step takes 3400 cycles of a multiprocessor (64-wide heads), of which the five
 // products are 1400: each waits for what the step's phases before it made, with
 // some 400 cycles from a product's end to the next one's start.  Without the
 // softmax's arithmetic and the writes of dQ (a value is added to for every key
-// tile) the first would still take 266 us.
+// tile) the first took 266 us where the whole took 321.
 constexpr int kBwdThreads = 768;  // warps 22, 23 only give their registers away
 constexpr int kBwdLoad = 20, kBwdMma = 21;
 
@@ -1561,10 +1561,10 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
   const double sum_cost = 128.0 * 4 * (c.d <= 64 ? 64 : 128) * c.kv_heads / (sms * 25.0);
   const double share = std::max(((double)work * tile_cost + (double)key_work * key_cost) / sms, tile_cost + key_cost);
   // Main kernel and sums, 17,001 rows on 1024 keys and 15,800 on 1500, 8 heads of
-  // 64: rows in 8 and 11 ranges, keys whole, 406 us; rows in 8 and 5, the second's
-  // keys in 2, 366; rows whole, keys in 8 and 11, 547 (partial sums of dQ past
+  // 64: rows in 8 and 11 ranges, keys whole, 345 us; rows in 8 and 5, the second's
+  // keys in 2, 343; rows whole, keys in 8 and 11, 541 (partial sums of dQ past
   // the L2).  9014 rows x 4 on 77 to 1030 keys, 2 key heads: rows in up to 40
-  // ranges, keys whole, 163 us; in up to 6, keys in up to 9, 89.
+  // ranges, keys whole, 109 us; in up to 6, keys in up to 9, 72.
   // The least room above an equal share of the work in which the units fit one
   // wave; every item then takes the fewest units that stay within it, and among
   // those the ranges with the least partial sums.  With more items than

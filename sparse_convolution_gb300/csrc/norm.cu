@@ -15,8 +15,8 @@
 // memory bounds it.  So each row is read once, stays in registers between its
 // two reductions, and the checkpoint is written by the pass that reads x.
 // Statistics, products and sums are fp32 whatever the storage type.  Measured
-// (bf16, time and bandwidth): 4,000,000 x 64 forward 180 us, 5.7 TB/s, backward
-// 264, 5.8; 10,000,000 x 32 packed in 195 us, 4.9 TB/s, restored in 164, 5.9;
+// (bf16, time and bandwidth): 4,000,000 x 64 forward 182 us, 5.6 TB/s, backward
+// 266, 5.8; 10,000,000 x 32 packed in 195 us, 4.9 TB/s, restored in 164, 5.9;
 // 150,001 x 256 forward with codes 51 us, 3.8 TB/s, backward from codes 57, 3.4
 // (both bound by the instructions of the codes), normed again 23, 5.1.
 #include "norm.cuh"
