@@ -760,7 +760,7 @@ int pick_splits(const AttnCall& c, FmaTile t, bool by_keys, int sms, double join
       best = time;
       splits = s;
     }
-    if (longest <= 1) break;
+    if (longest <= 1 || (double)units > 4.0 * wave) break;  // more ranges than that are never the least
   }
   return splits;
 }

@@ -1570,13 +1570,17 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
   // those the ranges with the least partial sums.  With more items than
   // multiprocessors, one unit per item and key head.
   for (double room : {1.0, 1.03, 1.06, 1.1, 1.15, 1.2, 1.3, 1.45, 1.7, 2.1, 2.6, 3.3, 4.5, 1e30}) {
-    const double most = single >= sms ? 1e300 : share * room;
+    const double most = share * room;
     int64_t u = 0;
     bool fits = true;
     for (int b = 0; b < c.items && fits; ++b) {
       const int64_t T = row_tiles(b), K = tiles_of_keys(b);
       rr[b] = kr[b] = 0;
       if (T == 0 || K == 0) continue;
+      if (single >= sms) {
+        rr[b] = kr[b] = 1;
+        continue;
+      }
       double best = 1e300;
       for (int64_t k = 1; k <= std::min<int64_t>(K, sms); ++k) {
         const double ck = (double)ceil_div(K, k);
