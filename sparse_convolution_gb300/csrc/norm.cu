@@ -257,14 +257,14 @@ __global__ void __launch_bounds__(kThreads) k_ck_wide(const __grid_constant__ Ro
 
 // ---------------------------------------------------------------- host
 // Widest vector (in elements) that the channel count, the pitches and the
-// bases allow: 16 bytes; for bf16 also 4 bytes, so that an even channel count
-// still moves 128 bytes per warp and load.
+// bases allow: 16 bytes, or two values, so that an even channel count still moves
+// 128 bytes or more per warp and load.
 bool aligned(const void* p, int64_t ld, int elem, int vec) {
   return !p || ((reinterpret_cast<uintptr_t>(p) % (size_t)(elem * vec)) == 0 && ld % vec == 0);
 }
 int pick_vec(fvx_dtype dt, int64_t c, const RowArgs& a) {
   const int elem = dt == FVX_F32 ? 4 : 2;
-  for (int vec : {16 / elem, elem == 2 ? 2 : 1, 1}) {
+  for (int vec : {16 / elem, 2, 1}) {
     if (c % vec == 0 && aligned(a.x, a.ldx, elem, vec) && aligned(a.dy, a.lddy, elem, vec) &&
         aligned(a.y, a.ldy, elem, vec) && aligned(a.codes, c, 1, vec) && aligned(a.codes_out, c, 1, vec))
       return vec;
@@ -314,7 +314,10 @@ fvx_status by_iters(int iters, F&& f) {
 }
 template <typename F>
 fvx_status by_row_shape(fvx_dtype dt, int vec, int iters, F&& f) {
-  if (dt == FVX_F32) return vec == 4 ? by_iters<float, 4, 1>(iters, f) : by_iters<float, 1, 1>(iters, f);
+  if (dt == FVX_F32) {
+    if (vec == 4) return by_iters<float, 4, 1>(iters, f);
+    return vec == 2 ? by_iters<float, 2, 1>(iters, f) : by_iters<float, 1, 1>(iters, f);
+  }
   if (vec == 8) return by_iters<__nv_bfloat16, 8, 1>(iters, f);
   return vec == 2 ? by_iters<__nv_bfloat16, 2, 1>(iters, f) : by_iters<__nv_bfloat16, 1, 1>(iters, f);
 }
