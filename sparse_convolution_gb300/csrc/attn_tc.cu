@@ -513,7 +513,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1) k_attn_tc_fwd(const __grid_con
       __syncwarp();
     } else if (warp >= kFwdMma && warp < kFwdMma + 2 / C::kPerWarp) {
       // -------------------------------------------------------------- products
-      constexpr uint32_t kIdS = idesc(kM, kM), kIdO = idesc(kM, DP) | kMnB;
+      constexpr uint32_t kIdO = idesc(kM, DP) | kMnB;
       const uint32_t sq = smem_u32(sm), sr = smem_u32(ring);
       // Everything in this loop is in the way of the tensor cores, so it keeps
       // running indices and phases and touches masks only where keys may drop.
