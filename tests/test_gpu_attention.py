@@ -272,6 +272,26 @@ def test_rising_scores(dtype):
     _check(t, qo, ko, mask)
 
 
+@pytest.mark.parametrize("reach", [1.0, 4.0])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_scores_far_from_zero(dtype, d, reach):
+    """First tiles whose scores all lie far above or below 0, near the limits of
+    what is taken relative to 0, and rows of each kind side by side; a later
+    tile's scores on the other side."""
+    import torch
+
+    t, qo, ko, mask = _case([300], [400], 2, 2, d, dtype, 71)
+    t["q"].mul_(0.05)
+    t["k"].mul_(0.05)
+    t["q"][:, :, 0] = torch.linspace(-12.0, 12.0, 300, device="cuda").to(t["q"].dtype)[:, None]
+    # scores of about +-12 (48) in the first tile, half of that, turned round, in the last
+    t["k"][:128, :, 0] = reach * d ** 0.5
+    t["k"][128:, :, 0] = 0.0
+    t["k"][384:, :, 0] = -0.5 * reach * d ** 0.5
+    _check(t, qo, ko, mask)
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_layouts(dtype):
     """Tensors cut out of wider ones, heads before tokens, heads broadcast."""
