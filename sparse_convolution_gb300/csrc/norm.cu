@@ -321,9 +321,14 @@ fvx_status by_row_shape(fvx_dtype dt, int vec, int iters, F&& f) {
   if (vec == 8) return by_iters<__nv_bfloat16, 8, 1>(iters, f);
   return vec == 2 ? by_iters<__nv_bfloat16, 2, 1>(iters, f) : by_iters<__nv_bfloat16, 1, 1>(iters, f);
 }
+// The same for the kernels of wider rows.  What their launches count in vectors
+// is counted in f by its VEC, never by the width that was asked for.
 template <typename F>
 fvx_status by_vec(fvx_dtype dt, int vec, F&& f) {
-  if (dt == FVX_F32) return vec == 4 ? f.template operator()<float, 4>() : f.template operator()<float, 1>();
+  if (dt == FVX_F32) {
+    if (vec == 4) return f.template operator()<float, 4>();
+    return vec == 2 ? f.template operator()<float, 2>() : f.template operator()<float, 1>();
+  }
   if (vec == 8) return f.template operator()<__nv_bfloat16, 8>();
   return vec == 2 ? f.template operator()<__nv_bfloat16, 2>() : f.template operator()<__nv_bfloat16, 1>();
 }
@@ -376,16 +381,15 @@ fvx_status pack_wide(fvx_dtype dt, RowArgs a, cudaStream_t s, int sms) {
   only.y = nullptr;
   only.dy = nullptr;
   const int vec = pick_vec(dt, a.c, only);
-  const int in_group = 1 << a.group_shift;
-  a.lanes = pow2_at_least((in_group + vec - 1) / vec, 32);
-  const int span = (in_group + vec * 32 - 1) / (vec * 32);
-  const int grid = grid_for(a.n * a.groups, kThreads / a.lanes, sms, 32);
   return by_vec(dt, vec, [&]<typename T, int VEC>() {
+    const int in_group = 1 << a.group_shift;
+    a.lanes = pow2_at_least(in_group / VEC, 32);
+    const int grid = grid_for(a.n * a.groups, kThreads / a.lanes, sms, 32);
     if constexpr (VEC * sizeof(T) == 16) {
       return launch("ck_pack", k_ck_pack_wide<T, VEC, 1>, dim3(grid), 0, s, a);
     } else {
-      return span <= 1 ? launch("ck_pack", k_ck_pack_wide<T, VEC, 1>, dim3(grid), 0, s, a)
-                       : launch("ck_pack", k_ck_pack_wide<T, VEC, 4>, dim3(grid), 0, s, a);
+      return in_group <= 32 * VEC ? launch("ck_pack", k_ck_pack_wide<T, VEC, 1>, dim3(grid), 0, s, a)
+                                  : launch("ck_pack", k_ck_pack_wide<T, VEC, 4>, dim3(grid), 0, s, a);
     }
   });
 }
@@ -576,10 +580,10 @@ fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, c
                   : rows_launch<kBackward>("norm_rows_bwd", dt, vec, a, g, s));
   } else {
     const int grid = grid_for(n, 1, sms, 8);
-    const int slabs = (int)((c / vec + kThreads - 1) / kThreads);
-    parts = (int)std::min<int64_t>(n, std::max(1, 4 * sms / slabs));
-    if (sums && !(a.part = scr.get<float>((size_t)parts * 2 * c))) return FVX_ERR_ALLOC;
     FVX_TRY(by_vec(dt, vec, [&]<typename T, int VEC>() -> fvx_status {
+      const int slabs = (int)((c / VEC + kThreads - 1) / kThreads);
+      parts = (int)std::min<int64_t>(n, std::max(1, 4 * sms / slabs));
+      if (sums && !(a.part = scr.get<float>((size_t)parts * 2 * c))) return FVX_ERR_ALLOC;
       FVX_TRY(group ? launch("norm_wide_dx", k_norm_wide_dx<T, VEC, true>, dim3(grid), 0, s, a)
                     : launch("norm_wide_dx", k_norm_wide_dx<T, VEC, false>, dim3(grid), 0, s, a));
       if (!sums) return FVX_OK;
