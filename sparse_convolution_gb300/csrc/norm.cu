@@ -584,11 +584,12 @@ fvx_status fvx_layer_norm_backward(fvx_dtype dt, const void* dy, int64_t lddy, c
       const int slabs = (int)((c / VEC + kThreads - 1) / kThreads);
       parts = (int)std::min<int64_t>(n, std::max(1, 4 * sms / slabs));
       if (sums && !(a.part = scr.get<float>((size_t)parts * 2 * c))) return FVX_ERR_ALLOC;
-      FVX_TRY(group ? launch("norm_wide_dx", k_norm_wide_dx<T, VEC, true>, dim3(grid), 0, s, a)
-                    : launch("norm_wide_dx", k_norm_wide_dx<T, VEC, false>, dim3(grid), 0, s, a));
-      if (!sums) return FVX_OK;
-      return group ? launch("norm_wide_dw", k_norm_wide_dw<T, VEC, true>, dim3(slabs, parts), 0, s, a)
-                   : launch("norm_wide_dw", k_norm_wide_dw<T, VEC, false>, dim3(slabs, parts), 0, s, a);
+      // dw before dx, which may lie in dy's memory
+      if (sums)
+        FVX_TRY(group ? launch("norm_wide_dw", k_norm_wide_dw<T, VEC, true>, dim3(slabs, parts), 0, s, a)
+                      : launch("norm_wide_dw", k_norm_wide_dw<T, VEC, false>, dim3(slabs, parts), 0, s, a));
+      return group ? launch("norm_wide_dx", k_norm_wide_dx<T, VEC, true>, dim3(grid), 0, s, a)
+                   : launch("norm_wide_dx", k_norm_wide_dx<T, VEC, false>, dim3(grid), 0, s, a);
     }));
   }
   if (!sums) return FVX_OK;
