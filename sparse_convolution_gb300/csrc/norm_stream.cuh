@@ -15,6 +15,7 @@ namespace {
 // spills (100,000 x 512 bf16, forward with codes: two 67 us, one 95; backward
 // from codes: two, which spill, 106, one 80).
 constexpr int kStreamThreads = kThreads + 32;
+constexpr int kMostSmem = 227 * 1024;
 struct StreamHead {
   uint64_t full[kStreamStages], empty[kStreamStages];
 };
@@ -121,7 +122,11 @@ __global__ void __launch_bounds__(kStreamThreads, VEC * ITER > 16 || (VEC * ITER
 template <typename T, int ITER, int OP, int LANES>
 fvx_status launch_stream(const char* name, const StreamArgs& a, int blocks, size_t smem, cudaStream_t s) {
   auto kernel = k_rows_stream<T, 16 / sizeof(T), ITER, OP, LANES>;
-  FVX_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem));
+  // The limit belongs to the kernel, not to the launch, and stages differ in
+  // size: it is set once, to the most that a block may have, so that no thread
+  // lowers it between another's check and launch.
+  static std::atomic<uint64_t> allowed{0};
+  FVX_TRY(allow_smem((const void*)kernel, kMostSmem, allowed));
   LaunchScope ls(name, s);
   kernel<<<blocks, kStreamThreads, smem, s>>>(a);
   return check_launch(name);
