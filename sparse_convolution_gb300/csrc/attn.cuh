@@ -22,7 +22,9 @@ enum AttnArray {
   kItemRows = 4,   // backward: ranges that the item's row tiles are cut into
   kItemKeys = 5,   // backward: ranges that its key tiles are cut into
   kItemKeyTile = 6,  // backward: first key tile
-  kItemArrays = 7
+  kItemRowSlab = 7,  // backward: first slab of dQ's partial sums, one per key range and row tile
+  kItemKeySlab = 8,  // backward: first slab of dK's and dV's, one per row range and key tile
+  kItemArrays = 9
 };
 struct AttnItems {
   const int32_t* ptr;

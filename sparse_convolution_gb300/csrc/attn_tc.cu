@@ -756,16 +756,19 @@ struct alignas(128) BwdArgs {
   AttnItems items;
   const uint8_t* mask;
   const float* stats;  // [row tile][key head][-lse2 of 128 rows, -delta of 128 rows]
-  float* dq_sum;       // [key range][row tile][key head][DP / 4][128][4]
-  float *dk_part, *dv_part;  // [row range][key tile][key head][DP / 4][128][4]
+  // An item's partial sums: its slabs from kItemRowSlab (kItemKeySlab) on, range
+  // after range.  Only items whose sums need them have any.
+  float* dq_sum;             // [key range, row tile][key head][DP / 4][128][4]
+  float *dk_part, *dv_part;  // [row range, key tile][key head][DP / 4][128][4]
   __nv_bfloat16 *dq, *dk, *dv;
   uint32_t* status;
-  int units, tiles, key_tiles, heads, kv_heads, shared, d, tile_rows;
+  int units, heads, kv_heads, shared, d, tile_rows;
   float c, scale;
 };
 
 struct BwdUnit {
-  int q0, rows, key0, keys, h, tile0, key_tile0, i0, i1, t0, t1, r_range, k_range, r_ranges, key_tiles;
+  int q0, rows, key0, keys, h, tile0, i0, i1, t0, t1, r_ranges, key_tiles;
+  int row_slab, key_slab;  // of the range's row tile 0, of its key tile 0
 };
 __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   BwdUnit w;
@@ -776,19 +779,20 @@ __device__ __forceinline__ BwdUnit bwd_unit(const BwdArgs& a, int u) {
   w.keys = a.items.k0(b + 1) - w.key0;
   w.tile0 = a.items.at(kItemTile, b);
   const int tiles = a.items.at(kItemTile, b + 1) - w.tile0;
-  w.key_tile0 = a.items.at(kItemKeyTile, b);
   w.key_tiles = (w.keys + kM - 1) / kM;
   w.r_ranges = a.items.at(kItemRows, b);
   const int k_ranges = a.items.at(kItemKeys, b);
   int i = u - a.items.u0(b);
-  w.r_range = i % w.r_ranges;
+  const int r_range = i % w.r_ranges;
   i /= w.r_ranges;
-  w.k_range = i % k_ranges;
+  const int k_range = i % k_ranges;
   w.h = i / k_ranges;
-  w.i0 = (int)((int64_t)tiles * w.r_range / w.r_ranges);
-  w.i1 = (int)((int64_t)tiles * (w.r_range + 1) / w.r_ranges);
-  w.t0 = (int)((int64_t)w.key_tiles * w.k_range / k_ranges);
-  w.t1 = (int)((int64_t)w.key_tiles * (w.k_range + 1) / k_ranges);
+  w.i0 = (int)((int64_t)tiles * r_range / w.r_ranges);
+  w.i1 = (int)((int64_t)tiles * (r_range + 1) / w.r_ranges);
+  w.t0 = (int)((int64_t)w.key_tiles * k_range / k_ranges);
+  w.t1 = (int)((int64_t)w.key_tiles * (k_range + 1) / k_ranges);
+  w.row_slab = a.items.at(kItemRowSlab, b) + k_range * tiles;
+  w.key_slab = a.items.at(kItemKeySlab, b) + r_range * w.key_tiles;
   return w;
 }
 
@@ -989,8 +993,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
         const bool live = j < w.keys, direct = w.r_ranges == 1;
         __nv_bfloat16* const out = (is_k ? a.dk : a.dv) + row * a.d;
         float* const part = (is_k ? a.dk_part : a.dv_part) +
-                            (((int64_t)w.r_range * a.key_tiles + w.key_tile0 + cur.t) * a.kv_heads + w.h) * (kM * DP) +
-                            key * 4;
+                            ((int64_t)(w.key_slab + cur.t) * a.kv_heads + w.h) * (kM * DP) + key * 4;
         mbar_wait(smem_u32(&h.acc_full), cur.tile & 1u, status);
         __syncwarp();
         fence_after();
@@ -1034,7 +1037,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1) k_attn_tc_bwd(const __grid_con
       const int tok = live ? r / a.shared : 0, g = r - tok * a.shared;
       const bool only = w.key_tiles == 1;  // nothing to collect
       __nv_bfloat16* out = a.dq + ((int64_t)(w.q0 + tok) * a.heads + w.h * a.shared + g) * a.d;
-      float* sum = a.dq_sum + (((int64_t)w.k_range * a.tiles + w.tile0 + cur.i) * a.kv_heads + w.h) * (kM * DP) + row * 4;
+      float* sum = a.dq_sum + ((int64_t)(w.row_slab + cur.i) * a.kv_heads + w.h) * (kM * DP) + row * 4;
       mbar_wait(smem_u32(&h.dq_full), cur.step & 1u, status);
       __syncwarp();
       fence_after();
@@ -1374,18 +1377,20 @@ __global__ void __launch_bounds__(256) k_attn_sums_out(const __grid_constant__ B
     const int keys = a.items.k0(b + 1) - a.items.k0(b);
     if (keys > 0 && keys <= kM) return;
     const int ranges = keys > 0 ? a.items.at(kItemKeys, b) : 0;
-    const int64_t slab = (int64_t)a.tiles * a.kv_heads * (kM * DP);
-    const int r = (tile - a.items.at(kItemTile, b)) * a.tile_rows + row;
+    const int tile0 = a.items.at(kItemTile, b);
+    const int64_t range = (int64_t)(a.items.at(kItemTile, b + 1) - tile0) * a.kv_heads * (kM * DP);
+    const int r = (tile - tile0) * a.tile_rows + row;
     if (row >= a.tile_rows || r >= rows) return;
     const int tok = r / a.shared, g = r - tok * a.shared, c0 = (threadIdx.x >> 7) * 8 + piece * 16;
-    const float* src = a.dq_sum + (int64_t)block * (kM * DP) + c0 * kM + row * 4;
+    const float* src = a.dq_sum + ((int64_t)(a.items.at(kItemRowSlab, b) + tile - tile0) * a.kv_heads + kh) * (kM * DP) +
+                       c0 * kM + row * 4;
     __nv_bfloat16* out = a.dq + ((int64_t)(q0 + tok) * a.heads + kh * a.shared + g) * a.d;
     float s[kCols][8] = {};
 #pragma unroll(FINE ? 4 : 1)
     for (int k = 0; k < ranges; ++k)
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
-        if (c0 + 16 * i < a.d) add_parts(s[i], src + k * slab + i * 16 * kM);
+        if (c0 + 16 * i < a.d) add_parts(s[i], src + k * range + i * 16 * kM);
 #pragma unroll
     for (int i = 0; i < kCols; ++i)
       if (c0 + 16 * i < a.d) store_rounded(out + c0 + 16 * i, s[i], a.scale);
@@ -1396,14 +1401,15 @@ __global__ void __launch_bounds__(256) k_attn_sums_out(const __grid_constant__ B
   const int b = a.items.find(kItemKeyTile, tile);
   const int ranges = a.items.at(kItemRows, b);
   const int key0 = a.items.k0(b), keys = a.items.k0(b + 1) - key0;
-  const int j = (tile - a.items.at(kItemKeyTile, b)) * kM + row;
+  const int tile0 = a.items.at(kItemKeyTile, b), j = (tile - tile0) * kM + row;
   if (ranges == 1 || j >= keys || c0 >= a.d) return;
   const bool second = threadIdx.x >= 128;
-  const int64_t slab = (int64_t)a.key_tiles * a.kv_heads * (kM * DP);
-  const float* src = (second ? a.dv_part : a.dk_part) + (int64_t)part * (kM * DP) + c0 * kM + row * 4;
+  const int64_t range = (int64_t)(a.items.at(kItemKeyTile, b + 1) - tile0) * a.kv_heads * (kM * DP);
+  const float* src = (second ? a.dv_part : a.dk_part) +
+                     ((int64_t)(a.items.at(kItemKeySlab, b) + tile - tile0) * a.kv_heads + kh) * (kM * DP) + c0 * kM + row * 4;
   float s[8] = {};
 #pragma unroll 4
-  for (int k = 0; k < ranges; ++k) add_parts(s, src + k * slab);
+  for (int k = 0; k < ranges; ++k) add_parts(s, src + k * range);
   store_rounded((second ? a.dv : a.dk) + ((int64_t)(key0 + j) * a.kv_heads + kh) * a.d + c0, s, 1.0f);
 }
 
@@ -1533,15 +1539,17 @@ fvx_status forward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
 // in cycles: a step's products and softmax about 1500, a key tile 3000 (with
 // partial sums 5000), 25 bytes a cycle and multiprocessor for the sums.
 struct BwdPlan {
-  std::vector<int32_t> more;  // units, row tiles, row ranges, key ranges, key tiles: items + 1 values each
-  int units = 0, tiles = 0, key_tiles = 0, most_rows = 1, most_keys = 1;
-  bool dq_sums = false, dq_zeros = false, dkv_parts = false;
+  std::vector<int32_t> more;  // the arrays from kItemUnit on: items + 1 values each
+  int units = 0, tiles = 0, key_tiles = 0, row_slabs = 0, key_slabs = 0;
+  bool dq_zeros = false, dkv_zeros = false;
 };
 BwdPlan bwd_plan(const AttnCall& c, int sms) {
   const int n = c.items + 1;
   BwdPlan p;
-  p.more.assign((size_t)5 * n, 0);
-  int32_t *units = p.more.data(), *tiles = units + n, *rr = tiles + n, *kr = rr + n, *key_tiles = kr + n;
+  p.more.assign((size_t)(kItemArrays - kItemUnit) * n, 0);
+  auto array = [&](AttnArray which) { return p.more.data() + (size_t)(which - kItemUnit) * n; };
+  int32_t *units = array(kItemUnit), *tiles = array(kItemTile), *rr = array(kItemRows), *kr = array(kItemKeys),
+          *key_tiles = array(kItemKeyTile), *row_slabs = array(kItemRowSlab), *key_slabs = array(kItemKeySlab);
   auto row_tiles = [&](int b) {
     return ((c.q_offsets[b + 1] - c.q_offsets[b]) * c.shared + tile_rows(c) - 1) / tile_rows(c);
   };
@@ -1600,25 +1608,29 @@ BwdPlan bwd_plan(const AttnCall& c, int sms) {
     }
     if (fits && (u <= sms || single >= sms)) break;
   }
-  int64_t u = 0, t = 0, kt = 0;
+  // Slabs of partial sums: at most one per row tile and key range of the units,
+  // of which there are no more than multiprocessors (or one range each).
+  int64_t u = 0, t = 0, kt = 0, row_slab = 0, key_slab = 0;
   for (int b = 0; b < c.items; ++b) {
     const int64_t T = row_tiles(b), K = tiles_of_keys(b);
     units[b] = (int32_t)u;
     tiles[b] = (int32_t)t;
     key_tiles[b] = (int32_t)kt;
+    row_slabs[b] = (int32_t)row_slab;
+    key_slabs[b] = (int32_t)key_slab;
     t += T;
     kt += K;
     if (T == 0 || K == 0) {
       p.dq_zeros |= T > 0;
-      p.dkv_parts |= K > 0;
+      p.dkv_zeros |= K > 0;
       continue;
     }
     u += (int64_t)rr[b] * kr[b] * c.kv_heads;
-    p.most_rows = std::max(p.most_rows, rr[b]);
-    p.most_keys = std::max(p.most_keys, kr[b]);
-    p.dq_sums |= K > 1;
-    p.dkv_parts |= rr[b] > 1;
+    if (K > 1) row_slab += kr[b] * T;
+    if (rr[b] > 1) key_slab += rr[b] * K;
   }
+  p.row_slabs = (int)row_slab;
+  p.key_slabs = (int)key_slab;
   units[c.items] = p.units = (int)u;
   tiles[c.items] = p.tiles = (int)t;
   key_tiles[c.items] = p.key_tiles = (int)kt;
@@ -1645,8 +1657,6 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
   a.dk = (__nv_bfloat16*)c.dk;
   a.dv = (__nv_bfloat16*)c.dv;
   a.units = p.units;
-  a.tiles = p.tiles;
-  a.key_tiles = p.key_tiles;
   a.heads = c.heads;
   a.kv_heads = c.kv_heads;
   a.shared = c.shared;
@@ -1665,11 +1675,11 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
     float* stats = scr.get<float>(row_blocks * 256);
     if (!stats) return FVX_ERR_ALLOC;
     a.stats = stats;
-    if (p.dq_sums && !(a.dq_sum = scr.get<float>(row_blocks * kM * DP * p.most_keys))) return FVX_ERR_ALLOC;
-    if (p.most_rows > 1) {
-      const size_t values = (size_t)p.key_tiles * c.kv_heads * kM * DP;
-      a.dk_part = scr.get<float>(values * p.most_rows);
-      a.dv_part = scr.get<float>(values * p.most_rows);
+    const size_t slab = (size_t)c.kv_heads * kM * DP;
+    if (p.row_slabs > 0 && !(a.dq_sum = scr.get<float>(p.row_slabs * slab))) return FVX_ERR_ALLOC;
+    if (p.key_slabs > 0) {
+      a.dk_part = scr.get<float>(p.key_slabs * slab);
+      a.dv_part = scr.get<float>(p.key_slabs * slab);
       if (!a.dk_part || !a.dv_part) return FVX_ERR_ALLOC;
     }
     {
@@ -1685,8 +1695,8 @@ fvx_status backward(const AttnCall& c, cudaStream_t s, Scratch& scr) {
     FVX_TRY(check_launch("attn_tc_bwd"));
   }
   const bool fine = row_blocks < 4 * (size_t)sms;
-  const int64_t dq_blocks = p.dq_sums || p.dq_zeros ? (int64_t)row_blocks * (fine ? DP / 16 : 1) : 0;
-  const int64_t dkv_blocks = p.dkv_parts ? (int64_t)p.key_tiles * c.kv_heads * (DP / 8) : 0;
+  const int64_t dq_blocks = p.row_slabs > 0 || p.dq_zeros ? (int64_t)row_blocks * (fine ? DP / 16 : 1) : 0;
+  const int64_t dkv_blocks = p.key_slabs > 0 || p.dkv_zeros ? (int64_t)p.key_tiles * c.kv_heads * (DP / 8) : 0;
   if (dq_blocks + dkv_blocks > 0) {
     LaunchScope ls("attn_sums_out", s);
     if (fine) k_attn_sums_out<DP, true><<<(unsigned)(dq_blocks + dkv_blocks), 256, 0, s>>>(a, (int)dq_blocks);
