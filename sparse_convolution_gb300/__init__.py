@@ -512,6 +512,23 @@ class Checkpoint8:
         _check(load().fvx_checkpoint_pack(dt, x.data_ptr(), ld, n, c, group, ck.codes.data_ptr(), ck.steps.data_ptr(), s))
         return ck
 
+    def _checked(self, who):
+        """(codes, steps) after a look at whether they belong together: the
+        attributes can be set by hand, and the kernels go by the codes' shape."""
+        import torch
+
+        codes, steps, group = self.codes, self.steps, self.group
+        if group not in (32, 64, 128):
+            _refuse(f"{who}: the checkpoint's group must be 32, 64 or 128, got {group}")
+        if codes.dtype != torch.int8 or codes.dim() != 2 or not codes.is_contiguous():
+            _refuse(f"{who}: the checkpoint's codes must be int8 [rows, channels], contiguous, "
+                    f"got {codes.dtype} {tuple(codes.shape)}")
+        want = (codes.shape[0], -(-codes.shape[1] // group))
+        if steps.dtype != torch.float32 or tuple(steps.shape) != want or not steps.is_contiguous():
+            _refuse(f"{who}: the checkpoint's steps must be float32 {list(want)}, contiguous, "
+                    f"got {steps.dtype} {tuple(steps.shape)}")
+        return codes, steps
+
     @property
     def shape(self):
         return self.codes.shape
@@ -520,13 +537,11 @@ class Checkpoint8:
     def nbytes(self):
         return self.codes.numel() + 4 * self.steps.numel()
 
-    def _restore(self, who, mean, rstd, weight, bias, dtype, out):
+    def _restore(self, who, parts, mean, rstd, weight, bias, dtype, out):
         import torch
 
-        codes, steps = self.codes, self.steps
+        codes, steps = parts
         n, c = codes.shape
-        if not codes.is_contiguous() or not steps.is_contiguous():
-            _refuse(f"{who}: codes and steps must be contiguous")
         if out is None:
             out = torch.empty((n, c), dtype=dtype or self.dtype, device=codes.device)
             ld = c
@@ -544,7 +559,8 @@ class Checkpoint8:
         """The values held, in the activations' type or ``dtype``."""
         if stream is not None:
             return _on_stream(stream, self.restore, dtype, out)
-        return self._restore("Checkpoint8.restore", None, None, None, None, dtype, out)
+        who = "Checkpoint8.restore"
+        return self._restore(who, self._checked(who), None, None, None, None, dtype, out)
 
     def layer_norm(self, mean, rstd, weight=None, bias=None, dtype=None, out=None, stream=None):
         """Layer norm of the values held, with the forward pass's statistics:
@@ -552,10 +568,11 @@ class Checkpoint8:
         if stream is not None:
             return _on_stream(stream, self.layer_norm, mean, rstd, weight, bias, dtype, out)
         who = "Checkpoint8.layer_norm"
-        n, c = self.codes.shape
+        parts = self._checked(who)
+        n, c = parts[0].shape
         mean, rstd = _row_vector(mean, n, who, "mean"), _row_vector(rstd, n, who, "rstd")
         weight, bias = _channel_vector(weight, c, who, "weight"), _channel_vector(bias, c, who, "bias")
-        return self._restore(who, mean, rstd, weight, bias, dtype, out)
+        return self._restore(who, parts, mean, rstd, weight, bias, dtype, out)
 
 
 def layer_norm(x, weight=None, bias=None, eps=1e-5, checkpoint_group=None, stream=None):
@@ -606,10 +623,9 @@ def layer_norm_backward(dy, x, mean, rstd, weight=None, stream=None):
     dy, lddy = _rows(dy, who, "dy")
     n, c = dy.shape
     if ck:
-        s = _on_device(who, dy, mean, rstd, weight, ck.codes, ck.steps)
-        if not ck.codes.is_contiguous() or not ck.steps.is_contiguous():
-            _refuse(f"{who}: the checkpoint's codes and steps must be contiguous")
-        source = (None, c, ck.group, ck.codes.data_ptr(), ck.steps.data_ptr())
+        codes, steps = ck._checked(who)
+        s = _on_device(who, dy, mean, rstd, weight, codes, steps)
+        source = (None, c, ck.group, codes.data_ptr(), steps.data_ptr())
     else:
         s = _on_device(who, dy, mean, rstd, weight, x)
         x, ldx = _rows(x, who, "x")
