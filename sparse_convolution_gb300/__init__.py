@@ -727,6 +727,8 @@ def cross_attention_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, key
     if lse.dtype != torch.float32 or tuple(lse.shape) != (nq, heads):
         _refuse(f"{who}: lse must be float32 [{nq}, {heads}], got {lse.dtype} {tuple(lse.shape)}")
     dout, out, lse = _heads(dout, who, "dout"), out.contiguous(), lse.contiguous()
+    if out.data_ptr() & 15:  # a part of something wider that the caller kept
+        out = out.clone()
     dq, dk, dv = _empty_rows(q), _empty_rows(k), _empty_rows(k)
     _check(load().fvx_cross_attention_backward(
         dt, *_strided(dout), *_strided(q), *_strided(k), *_strided(v), out.data_ptr(), lse.data_ptr(),
