@@ -402,7 +402,8 @@ fvx_status fvx_hits_destroy(fvx_hits h);
  * Layer norm, per row r of x [n, c] (c in 1..65536, row pitch ldx >= c):
  *   mean = sum x / c;  rstd = 1 / sqrt(sum (x - mean)^2 / c + eps)
  *   y = (x - mean) * rstd * w + b      (w, b: device [c], NULL = ones / zeros)
- * mean, rstd: device [n], written; the backward pass reads them.
+ * mean, rstd: device [n], written; the backward pass reads them.  y, codes and
+ * steps must not lie in x's memory.
  * group 32, 64 or 128: x's checkpoint is written by the same pass to codes and
  * steps (below); group 0: none, and both are ignored.
  * Errors: FVX_ERR_INVALID_ARG. */
@@ -451,6 +452,10 @@ fvx_status fvx_checkpoint_restore(fvx_dtype dt, int32_t group, const int8_t* cod
  * key takes part in nothing, whatever its row holds.
  * out: device [nq, heads, d], dense, 16-byte aligned.  lse: device fp32 [nq, heads], dense.  A
  * row without kept keys gets out = 0 and lse = -infinity.
+ * bf16 heads of a multiple of 8 values whose rows start at 16 bytes take the
+ * tensor cores: their probabilities (backward also the score gradients) are
+ * rounded to bf16 as operands of the products.  Anything else keeps fp32 up to
+ * the results.
  * Errors: FVX_ERR_INVALID_ARG; FVX_ERR_RANGE past 2^30 rows (tokens * heads). */
 fvx_status fvx_cross_attention(fvx_dtype dt, const void* q, int64_t q_token, int64_t q_head, const void* k,
                                int64_t k_token, int64_t k_head, const void* v, int64_t v_token, int64_t v_head,
@@ -462,7 +467,8 @@ fvx_status fvx_cross_attention(fvx_dtype dt, const void* q, int64_t q_token, int
  * the forward call's out and lse.  dq [nq, heads, d], dk and dv [nk, kv_heads,
  * d]: dense, 16-byte aligned, fully overwritten; gradients of a key head sum over the query
  * heads that read it, those of a masked key are zero.  The order of every sum
- * is fixed: the same call gives the same bits. */
+ * is fixed: the same call gives the same bits.  Scratch: fp32 partial sums, for
+ * each sample those of its own cut. */
 fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t do_token, int64_t do_head,
                                         const void* q, int64_t q_token, int64_t q_head, const void* k,
                                         int64_t k_token, int64_t k_head, const void* v, int64_t v_token,

@@ -9,7 +9,8 @@
 // of its next turns into its own ring in shared memory while it computes, and
 // nothing but its own copies makes it wait.  The running maximum of a row is
 // raised only when a score exceeds it by 2^8, so the accumulators are rarely
-// touched; warps and the cluster's blocks join their results through shared and
+// touched; powers come from the special function unit in fp32 too (relative
+// error about 2^-22; the rounding of a score of 10 makes 2^-21); warps and the cluster's blocks join their results through shared and
 // distributed shared memory, in a fixed order.
 //
 // bf16: the products are m16n8k16 with the keys as the 16 and the rows as the

@@ -1,5 +1,8 @@
-// Thin wrappers of the sm_103a instructions that the attention kernels use:
-// mbarriers with bounded waits, TMA tile loads, tcgen05 MMA and tensor memory.
+// Thin wrappers of the sm_103a instructions that the attention and norm kernels
+// use: mbarriers with bounded waits, TMA tile loads, tcgen05 MMA and tensor
+// memory.  The convolution kernels have forms of their own in conv.cu, whose
+// waits read the clock from the start and tell the caller that they gave up;
+// here a wait that ran out is told by the status word alone.
 #pragma once
 #include <cuda.h>
 #include <cuda_bf16.h>
