@@ -274,7 +274,7 @@ struct Rows {
   static constexpr int N = Lane<VEC>::N;
   const RowArgs& a;
   const int lanes, lane, nv;
-  const float inv_c;
+  const float inv_c;  // means are products with it: half an ulp more than a division, off a row's critical path
   E w[ITER][N], b[ITER][N];    // backward: b unused
   E dw[ITER][N], db[ITER][N];  // backward
 
