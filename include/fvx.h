@@ -477,6 +477,100 @@ fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t 
                                         int32_t d, const uint8_t* key_mask, float scale, void* dq, void* dk, void* dv,
                                         fvx_stream stream);
 
+/* ---------------------------------------------------------------------------
+ * Voxels that attend to voxels: rotary positions of queries and keys, their
+ * norms per head with the rotation in the same pass, and dropout of what a
+ * block adds to its stream.  Types as above (FVX_F32, FVX_BF16; arithmetic and
+ * sums in fp32); asynchronous; nothing is allocated but the scratch named.
+ *
+ * Rotation of a head of d values (1..256).  The first 2P are rotated, in P
+ * pairs: (p, P + p), or, interleaved, (2p, 2p + 1); the others pass as they
+ * are.  The first pairs[0] pairs turn by the first position, the next pairs[1]
+ * by the second, the last pairs[2] by the third (a voxel's coordinates; pairs =
+ * {P, 0, 0} for token positions):  t = position * f_p,
+ *   (u, v) -> magnitude * (u cos t - v sin t, v cos t + u sin t)
+ * turns: HOST array of the P steps f_p / (2 pi), in units of 2^-64 turns, read
+ * during the call.  Angles are taken modulo whole turns in integers: a position
+ * of any int32 value loses nothing. */
+typedef struct {
+  int32_t pairs[3];
+  int32_t interleaved;   /* 0: halves */
+  const uint64_t* turns; /* host [pairs[0] + pairs[1] + pairs[2]] */
+  float magnitude;
+} fvx_rotary_t;
+
+/* Fills turns and magnitude.  Pair i of an axis with n pairs:
+ *   FVX_ROTARY_PLAIN   f = base^(-i / n)
+ *   FVX_ROTARY_LINEAR  f / factor: positions pressed together
+ *   FVX_ROTARY_BASE    f of the base * factor^(n / (n - 1)): the slowest pair
+ *                      as with LINEAR, the fastest as it was
+ *   FVX_ROTARY_PARTS   f * (keep + (1 - keep) / factor), keep = (length f / (2 pi) - 1) / 31
+ *                      cut to 0..1: pairs that make 32 turns within `length`
+ *                      positions stay, those that make less than one are
+ *                      pressed; magnitude 0.1 ln(factor) + 1 (else 1)
+ * base above 1, factor at least 1.  No CUDA work.  Errors: FVX_ERR_INVALID_ARG. */
+typedef enum {
+  FVX_ROTARY_PLAIN = 0,
+  FVX_ROTARY_LINEAR = 1,
+  FVX_ROTARY_BASE = 2,
+  FVX_ROTARY_PARTS = 3
+} fvx_rotary_scaling;
+fvx_status fvx_rotary_turns(const int32_t pairs[3], double base, fvx_rotary_scaling scaling, double factor,
+                            double length, uint64_t* turns, float* magnitude);
+
+/* One tensor [n, heads, d] of a call: the last dimension dense, strides in
+ * elements, not negative, any alignment of whole elements (heads whose bases,
+ * strides and halves are multiples of 16 bytes are faster).  A call takes one or
+ * two (queries and keys) with one launch; each has its own tokens and positions. */
+typedef struct {
+  int64_t n, heads;
+  const void* in;           /* what is rotated; backward: the gradient of the result */
+  int64_t in_token, in_head;
+  void* out;                /* may be in itself (same strides; backward: or x); heads must not lie over each other */
+  int64_t out_token, out_head;
+  const int32_t* positions; /* device [n] or [n, axes]; ignored without a rotation */
+  int64_t pos_token, pos_axis;
+  const float* weight;      /* norm: device [d], NULL = ones */
+  const void* x;            /* norm's backward only: the forward pass's tensor */
+  int64_t x_token, x_head;
+  float* dweight;           /* norm's backward only: device [d], written; NULL = not wanted */
+} fvx_head_tensor_t;
+
+/* out = the rotated tensor; transposed: the transposed matrix, which turns the
+ * gradient of the result into that of the tensor.
+ * Errors: FVX_ERR_INVALID_ARG; FVX_ERR_RANGE past 2^30 rows (n * heads). */
+fvx_status fvx_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* tensors, int32_t count,
+                            const fvx_rotary_t* rotary, int32_t transposed, fvx_stream stream);
+
+/* out = the rotated  x * rstd * weight,  rstd = 1 / sqrt(sum x^2 / d + eps) of
+ * each head; rotary NULL: without the rotation. */
+fvx_status fvx_norm_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* tensors, int32_t count,
+                                 const fvx_rotary_t* rotary, float eps, fvx_stream stream);
+
+/* Its gradients.  With g the gradient turned back:
+ *   dx = rstd * (g w - x rstd^2 sum(g w x) / d);  dweight = sum over tokens and heads of g x rstd
+ * rstd is computed again from x.  The order of every sum is fixed: the same call
+ * gives the same bits.  Scratch: fp32 [blocks, d] partial sums of dweight. */
+fvx_status fvx_norm_rotate_heads_backward(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* tensors, int32_t count,
+                                          const fvx_rotary_t* rotary, float eps, fvx_stream stream);
+
+/* Dropout, its mask drawn and never stored:
+ *   y = residual + (kept ? x / (1 - D / 65536) : 0),  D = p * 65536 rounded half to even
+ * over x [n, c] (pitches in elements), residual like x or NULL.  Value i of the
+ * row-major tensor is kept when its 16 bits are at least D: a probability is met
+ * to 2^-17, and the values' mean exactly.  The bits are those of Philox4x32 with
+ * ten rounds (Salmon, Moraes, Dror and Shaw 2011), counter words (i / 8, offset),
+ * key words seed, low words first; value i takes the i % 8-th sixteen of the
+ * 128, low ones first.  They depend on seed, offset and i alone: the gradient of
+ * x is fvx_dropout of the gradient of y without residual.
+ * state: NULL, or device uint64 [2] read by the kernel: seed is state[0] and
+ * offset counts from state[1] (a captured call draws anew when they change).
+ * A dropped value adds 0, whatever it was.  y may be x's or residual's memory
+ * (same pitch).  p in 0..1.  Errors: FVX_ERR_INVALID_ARG. */
+fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t n,
+                       int64_t c, double p, uint64_t seed, uint64_t offset, const uint64_t* state, void* y,
+                       int64_t ldy, fvx_stream stream);
+
 fvx_status fvx_grid_destroy(fvx_grid g);
 fvx_status fvx_kmap_destroy(fvx_kmap m);
 

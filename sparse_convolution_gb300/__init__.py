@@ -16,6 +16,7 @@ from __future__ import annotations
 import array
 import ctypes
 import os
+import struct
 
 import numpy as np
 
@@ -25,6 +26,7 @@ LIB_PATH = os.path.join(_HERE, "libfvx.so")
 _lib = None
 
 FVX_F32, FVX_BF16, FVX_BF16_OUT_BF16 = 0, 1, 2
+FVX_ROTARY_PLAIN, FVX_ROTARY_LINEAR, FVX_ROTARY_BASE, FVX_ROTARY_PARTS = 0, 1, 2, 3
 FVX_CONV_AUTO, FVX_CONV_GATHER, FVX_CONV_LEAF, FVX_CONV_DIRECT, FVX_CONV_UNION, FVX_CONV_HALO = 0, 1, 2, 3, 4, 5
 
 
@@ -83,6 +85,11 @@ def load():
         "fvx_cross_attention": ([I32] + 3 * [P, I64, I64] + [P, P, I32, I32, I32, I32, P, F32, P, P, P], I32),
         "fvx_cross_attention_backward": ([I32] + 4 * [P, I64, I64] + [P, P, P, P, I32, I32, I32, I32, P, F32, P, P, P,
                                                                      P], I32),
+        "fvx_rotary_turns": ([P, ctypes.c_double, I32, ctypes.c_double, ctypes.c_double, P, P], I32),
+        "fvx_rotate_heads": ([I32, I32, P, I32, P, I32, P], I32),
+        "fvx_norm_rotate_heads": ([I32, I32, P, I32, P, F32, P], I32),
+        "fvx_norm_rotate_heads_backward": ([I32, I32, P, I32, P, F32, P], I32),
+        "fvx_dropout": ([I32, P, I64, P, I64, I64, I64, ctypes.c_double, U64, U64, P, P, I64, P], I32),
         "fvx_grid_destroy": ([P], I32),
         "fvx_kmap_destroy": ([P], I32),
         "fvx_status_string": ([I32], ctypes.c_char_p),
@@ -740,6 +747,258 @@ def cross_attention_backward(dout, q, k, v, out, lse, q_offsets, kv_offsets, key
 def _strided(t):
     st = t.stride()
     return t.data_ptr(), st[0], st[1]
+
+
+# ---------------------------------------------------------------- rotary positions, head norms, dropout
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [("pairs", ctypes.c_int32 * 3), ("interleaved", ctypes.c_int32), ("turns", ctypes.c_void_p),
+                ("magnitude", ctypes.c_float)]
+
+
+class Rotary:
+    """How heads turn with their positions: the first ``size`` channels of a
+    head (an even number) in pairs, pair i of n by position * base^(-i / n).
+
+    axes: 1 for token positions; 2 or 3 for coordinates (``Grid.ijk()``), which
+    share the pairs equally, the first ones taking what is left over.  layout:
+    "half" pairs channels p and p + size / 2, "interleaved" 2p and 2p + 1.
+    scaling, for contexts `factor` times as long as those trained on: "linear"
+    divides the positions, "base" raises the base (the fastest pair stays, the
+    slowest is divided), "parts" divides the pairs that make less than a turn
+    within ``length`` positions, keeps those that make 32, and multiplies the
+    rotated values by 0.1 ln(factor) + 1.
+
+    Lives on the host alone: usable with any device and stream."""
+
+    def __init__(self, size, axes=1, base=10000.0, layout="half", scaling=None, factor=1.0, length=None):
+        who = "Rotary"
+        if size < 2 or size % 2 or size > 256:
+            _refuse(f"{who}: size must be even, in 2..256, got {size}")
+        if axes not in (1, 2, 3):
+            _refuse(f"{who}: axes must be 1, 2 or 3, got {axes}")
+        if layout not in ("half", "interleaved"):
+            _refuse(f'{who}: layout must be "half" or "interleaved", got {layout!r}')
+        codes = {None: FVX_ROTARY_PLAIN, "linear": FVX_ROTARY_LINEAR, "base": FVX_ROTARY_BASE, "parts": FVX_ROTARY_PARTS}
+        if scaling not in codes:
+            _refuse(f'{who}: scaling must be None, "linear", "base" or "parts", got {scaling!r}')
+        if (length is None) != (scaling != "parts"):
+            _refuse(f'{who}: length belongs to the scaling "parts"')
+        pairs = size // 2
+        self.size, self.axes, self.layout = size, axes, layout
+        self.turns = np.zeros(pairs, np.uint64)  # per position step, in 2^-64 turns
+        s = self._struct = _RotaryStruct()
+        for a in range(axes):
+            s.pairs[a] = pairs // axes + (a < pairs % axes)
+        s.interleaved = layout == "interleaved"
+        s.turns = self.turns.ctypes.data
+        _check(load().fvx_rotary_turns(s.pairs, base, codes[scaling], factor, length or 0.0, s.turns,
+                                       ctypes.byref(s, _RotaryStruct.magnitude.offset)))
+        self.magnitude = s.magnitude
+        self._at = ctypes.addressof(s)
+
+
+_HEAD_TENSOR = struct.Struct("2qP2qP2qP2qPP2qP")  # fvx_head_tensor_t
+
+
+def _dense_heads(t, who, name, shape=None, dtype=None):
+    """t [tokens, heads, size] with a dense last dimension (a copy where it is not)."""
+    if t.dim() != 3 or (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype):
+        want = "[tokens, heads, size]" if shape is None else f"{dtype} {tuple(shape)}"
+        _refuse(f"{who}: {name} must be {want}, got {t.dtype} {tuple(t.shape)}")
+    return t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
+
+
+def _head_tensor(who, name, t, positions, rotary, weight, out, x=None, dweight=None):
+    """(packed fvx_head_tensor_t, result, what must outlive the call)"""
+    import torch
+
+    n, heads, d = t.shape
+    if heads < 1 or not 1 <= d <= 256:
+        _refuse(f"{who}: {name} must have at least one head of 1 to 256 values, got {tuple(t.shape)}")
+    pos = (None, 0, 0)
+    if rotary is not None:
+        axes = rotary.axes
+        if rotary.size > d:
+            _refuse(f"{who}: {rotary.size} rotated channels do not fit into heads of {d}")
+        if positions is None:
+            _refuse(f"{who}: positions are missing")
+        ps = positions.shape
+        if positions.dtype != torch.int32 or ps[0] != n or not (len(ps) == 2 and ps[1] == axes or len(ps) == 1 == axes):
+            _refuse(f"{who}: positions of {name} must be int32 [{n}{', %d' % axes if axes > 1 else ''}], "
+                    f"got {positions.dtype} {tuple(ps)}")
+        st = positions.stride()
+        pos = (positions.data_ptr(), st[0], st[1] if len(st) > 1 else 0)
+    weight = _channel_vector(weight, d, who, f"the weight of {name}")
+    if out is None:
+        out = _empty_rows(t)
+    elif out.shape != t.shape or out.dtype != t.dtype or (d > 1 and out.stride(2) != 1):
+        _refuse(f"{who}: out must be {t.dtype} {tuple(t.shape)} with dense heads, got {out.dtype} {tuple(out.shape)}")
+    st, so = t.stride(), out.stride()
+    sx = x.stride() if x is not None else (0, 0)
+    return _HEAD_TENSOR.pack(n, heads, t.data_ptr(), st[0], st[1], out.data_ptr(), so[0], so[1], *pos, _at(weight) or 0,
+                             _at(x) or 0, sx[0], sx[1], _at(dweight) or 0), out, (t, weight, x)
+
+
+def _head_call(who, entry, q, k, positions, k_positions, rotary, weight, k_weight, out, last, grads=None):
+    """One launch over q and (not None) k; grads: (x of q, x of k) for the backward pass."""
+    import torch
+
+    dt = _dtype_code(q, who)
+    if k is None and (k_positions is not None or k_weight is not None):
+        _refuse(f"{who}: k is missing")
+    if out is not None and (k is not None) != isinstance(out, (tuple, list)):
+        _refuse(f"{who}: out must be one tensor, or one for each of q and k")
+    outs = (None, None) if out is None else (out,) if k is None else tuple(out)
+    xs = grads or (None, None)
+    s = _on_device(who, q, k, positions, k_positions, weight, k_weight, *outs, *xs)
+    q = _dense_heads(q, who, "q")
+    if grads:
+        q = _dense_heads(q, who, "dq", xs[0].shape, xs[0].dtype)
+        xq = _dense_heads(xs[0], who, "q")
+    dw = dwk = None
+    if grads:
+        dw = torch.empty((q.shape[2],), dtype=torch.float32, device=q.device)
+    packed, q_out, hold = _head_tensor(who, "q", q, positions, rotary, weight, outs[0], xq if grads else None, dw)
+    count, k_out, k_hold = 1, None, None
+    if k is not None:
+        xk = None
+        if grads:
+            k = _dense_heads(k, who, "dk", xs[1].shape, xs[1].dtype)
+            xk = _dense_heads(xs[1], who, "k")
+            dwk = torch.empty((k.shape[2],), dtype=torch.float32, device=q.device)
+        else:
+            k = _dense_heads(k, who, "k")
+        if k.dtype != q.dtype or k.shape[2] != q.shape[2]:
+            _refuse(f"{who}: q and k must have one type and head size, got {q.dtype} {tuple(q.shape)} and "
+                    f"{k.dtype} {tuple(k.shape)}")
+        more, k_out, k_hold = _head_tensor(who, "k", k, positions if k_positions is None else k_positions, rotary,
+                                           k_weight, outs[1], xk, dwk)
+        packed, count = packed + more, 2
+    _check(entry(dt, q.shape[2], packed, count, rotary._at if rotary is not None else None, last, s))
+    del hold, k_hold
+    return q_out, k_out, dw, dwk
+
+
+def rotate_heads(q, positions, rotary, k=None, k_positions=None, out=None, stream=None):
+    """Turns the heads of q [tokens, heads, size] (float32 or bfloat16, size at
+    most 256) by their tokens' positions, int32 [tokens] or, for a Rotary of
+    several axes, [tokens, axes].  With k, its heads too, in the same launch, by
+    k_positions (default: positions).  out: where to (a tensor, or one for each;
+    q and k themselves will do).  Returns q's result, or (q's, k's)."""
+    if stream is not None:
+        return _on_stream(stream, rotate_heads, q, positions, rotary, k, k_positions, out)
+    q, k, _, _ = _head_call("rotate_heads", load().fvx_rotate_heads, q, k, positions, k_positions, _a_rotary(rotary),
+                            None, None, out, 0)
+    return q if k is None else (q, k)
+
+
+def rotate_heads_backward(dq, positions, rotary, dk=None, k_positions=None, out=None, stream=None):
+    """Gradients of rotate_heads: the gradients dq (and dk) of its results
+    turned back.  Returns dq, or (dq, dk)."""
+    if stream is not None:
+        return _on_stream(stream, rotate_heads_backward, dq, positions, rotary, dk, k_positions, out)
+    q, k, _, _ = _head_call("rotate_heads_backward", load().fvx_rotate_heads, dq, dk, positions, k_positions,
+                            _a_rotary(rotary), None, None, out, 1)
+    return q if k is None else (q, k)
+
+
+def _a_rotary(r):
+    if not isinstance(r, Rotary):
+        _refuse(f"a Rotary is needed, got {type(r).__name__}")
+    return r
+
+
+def norm_rotate_heads(q, positions=None, rotary=None, weight=None, k=None, k_positions=None, k_weight=None, eps=1e-6,
+                      out=None, stream=None):
+    """Each head of q [tokens, heads, size] divided by the root of its mean
+    square (plus eps), times weight (float32 [size] or None), then turned as by
+    rotate_heads (rotary None: not turned), in one pass; with k, its heads too,
+    in the same launch.  The attention's queries and keys may be parts of one
+    product's rows.  Returns q's result, or (q's, k's)."""
+    if stream is not None:
+        return _on_stream(stream, norm_rotate_heads, q, positions, rotary, weight, k, k_positions, k_weight, eps, out)
+    q, k, _, _ = _head_call("norm_rotate_heads", load().fvx_norm_rotate_heads, q, k, positions, k_positions,
+                            None if rotary is None else _a_rotary(rotary), weight, k_weight, out, eps)
+    return q if k is None else (q, k)
+
+
+def norm_rotate_heads_backward(dq, q, positions=None, rotary=None, weight=None, dk=None, k=None, k_positions=None,
+                               k_weight=None, eps=1e-6, out=None, stream=None):
+    """Gradients of norm_rotate_heads from those of its results, dq and dk, and
+    its inputs: (dq, dweight), or with k (dq, dk, dweight, dk_weight); the
+    weights' are float32 [size]."""
+    if stream is not None:
+        return _on_stream(stream, norm_rotate_heads_backward, dq, q, positions, rotary, weight, dk, k, k_positions,
+                          k_weight, eps, out)
+    who = "norm_rotate_heads_backward"
+    if (dk is None) != (k is None):
+        _refuse(f"{who}: dk and k belong together")
+    dq, dk, dw, dwk = _head_call(who, load().fvx_norm_rotate_heads_backward, dq, dk, positions, k_positions,
+                                 None if rotary is None else _a_rotary(rotary), weight, k_weight, out, eps, (q, k))
+    return (dq, dw) if k is None else (dq, dk, dw, dwk)
+
+
+def _pitched(t, who, name, like=None):
+    """t as rows of dense values: (tensor, rows, values per row, pitch).  Tensors of any shape without gaps count as
+    one row."""
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        _refuse(f"{who}: {name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
+    if t.dim() == 2 and not t.is_contiguous() and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
+        return t, t.stride(0)
+    t = t.contiguous()
+    return t, t.shape[-1] if t.dim() else 1
+
+
+def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
+    """residual + x with each value dropped (0) with probability p, the others
+    divided by 1 - p; p is met to 2^-17 and the mean exactly.  x: float32 or
+    bfloat16 of any shape; residual: like x, or None for 0.  No mask is stored:
+    what is kept follows from seed, offset and the value's place in the
+    row-major tensor, whatever its strides and type.
+
+    seed: an int of 64 bits, or an int64 CUDA tensor of two values (seed and
+    offset, `offset` is added) that the kernel reads: a captured call draws anew
+    when a replay finds other values there.  Give every call of a step an offset
+    of its own.  out: where to (x and residual themselves will do)."""
+    if stream is not None:
+        return _on_stream(stream, dropout, x, p, seed, offset, residual, out)
+    return _dropout("dropout", x, p, seed, offset, residual, out)
+
+
+def dropout_backward(dy, p, seed, offset=0, out=None, stream=None):
+    """Gradient of dropout's x from dy, its result's; that of residual is dy itself."""
+    if stream is not None:
+        return _on_stream(stream, dropout_backward, dy, p, seed, offset, out)
+    return _dropout("dropout_backward", dy, p, seed, offset, None, out)
+
+
+def _dropout(who, x, p, seed, offset, residual, out):
+    import torch
+
+    dt = _dtype_code(x, who)
+    state = None
+    if isinstance(seed, torch.Tensor):
+        state, seed = seed, 0
+        if state.dtype != torch.int64 or tuple(state.shape) != (2,) or not state.is_contiguous():
+            _refuse(f"{who}: seed must be an int or an int64 tensor of two values, got {state.dtype} {tuple(state.shape)}")
+    if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
+        _refuse(f"{who}: seed and offset must be in 0..2^64 - 1")
+    s = _on_device(who, x, residual, out, state)
+    x, ldx = _pitched(x, who, "x")
+    ldr = ldx
+    if residual is not None:
+        residual, ldr = _pitched(residual, who, "residual", x)
+    if out is None:
+        y = _empty_rows(x)
+        ldy = x.shape[-1] if x.dim() else 1
+    else:
+        y, ldy = _pitched(out, who, "out", x)
+        if y is not out:
+            _refuse(f"{who}: out must be contiguous, or rows of dense values")
+    c = (x.shape[-1] if x.dim() else 1) or 1
+    _check(load().fvx_dropout(dt, x.data_ptr(), ldx, _at(residual), ldr, x.numel() // c, c, p, seed, offset, _at(state),
+                              y.data_ptr(), ldy, s))
+    return y
 
 
 def device_status(stream=None):

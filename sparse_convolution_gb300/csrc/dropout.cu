@@ -1,0 +1,230 @@
+// Dropout from a counter-based generator: the mask is never stored, the
+// backward pass draws it again.
+//
+//   y = residual + (kept ? x / (1 - drop / 65536) : 0),   kept iff bits(i) >= drop
+// bits(i): 16 bits for value i of the row-major tensor, eight values per
+// counter of Philox4x32 with ten rounds (Salmon, Moraes, Dror and Shaw 2011):
+// counter words (i / 8, offset), key words seed, value i % 8 the i % 8-th
+// sixteen bits, low ones first.  They depend on the place in the tensor alone,
+// whatever its type, pitch or alignment.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <math.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "fvx_internal.cuh"
+#include "norm.cuh"
+
+namespace fvx {
+namespace {
+
+struct DropArgs {
+  const void* x;
+  const void* residual;  // or null
+  void* y;
+  int64_t total, rows, ldx, ldr, ldy;
+  const uint64_t* state;  // seed and offset on the device, or null
+  uint64_t seed, offset;
+  uint32_t c, vecs, magic, drop;  // vecs: vectors of 8 per row
+  float scale;
+};
+
+struct Key {
+  uint32_t k0, k1, c2, c3;
+  __device__ __forceinline__ Key(const DropArgs& a) {
+    uint64_t seed = a.seed, offset = a.offset;
+    if (a.state) {
+      seed = __ldg(reinterpret_cast<const unsigned long long*>(a.state));
+      offset += __ldg(reinterpret_cast<const unsigned long long*>(a.state) + 1);
+    }
+    k0 = (uint32_t)seed;
+    k1 = (uint32_t)(seed >> 32);
+    c2 = (uint32_t)offset;
+    c3 = (uint32_t)(offset >> 32);
+  }
+};
+__device__ __forceinline__ uint4 philox(const Key& key, uint64_t at) {
+  uint32_t c0 = (uint32_t)at, c1 = (uint32_t)(at >> 32), c2 = key.c2, c3 = key.c3, k0 = key.k0, k1 = key.k1;
+#pragma unroll
+  for (int r = 0; r < 10; ++r) {
+    const uint64_t p0 = (uint64_t)c0 * 0xD2511F53u, p1 = (uint64_t)c2 * 0xCD9E8D57u;
+    c0 = (uint32_t)(p1 >> 32) ^ c1 ^ k0;
+    c1 = (uint32_t)p1;
+    c2 = (uint32_t)(p0 >> 32) ^ c3 ^ k1;
+    c3 = (uint32_t)p0;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return make_uint4(c0, c1, c2, c3);
+}
+// Bit k: value k of the counter stays.
+__device__ __forceinline__ uint32_t kept_bits(uint4 r, uint32_t drop) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+  uint32_t m = 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    m |= (w[k] & 0xffffu) >= drop ? 1u << (2 * k) : 0u;
+    m |= (w[k] >> 16) >= drop ? 2u << (2 * k) : 0u;
+  }
+  return m;
+}
+
+// Vectors of eight values; LINE: the tensors are dense, so the place of value i is i.
+template <typename T, bool LINE, bool ADD>
+__global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ DropArgs a) {
+  const Key key(a);
+  const int64_t whole = a.total >> 3, step = (int64_t)gridDim.x * kThreads;
+  const T* x = reinterpret_cast<const T*>(a.x);
+  const T* res = reinterpret_cast<const T*>(a.residual);
+  T* y = reinterpret_cast<T*>(a.y);
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < whole; i += step) {
+    int64_t ax = i * 8, ar = ax, ay = ax;
+    if constexpr (!LINE) {
+      const int64_t row = whole >> 32 ? i / a.vecs : (uint32_t)i / a.vecs;  // 32-bit division where it will do
+      const int64_t col = (i - row * a.vecs) * 8;
+      ax = row * a.ldx + col;
+      ar = row * a.ldr + col;
+      ay = row * a.ldy + col;
+    }
+    float f[8], g[8];
+    load_vec<T, 8>(x + ax, f);
+    if constexpr (ADD) load_vec<T, 8>(res + ar, g);
+    const uint32_t m = kept_bits(philox(key, (uint64_t)i), a.drop);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const float v = f[k] * a.scale;
+      f[k] = (m >> k) & 1u ? v : 0.0f;
+      if constexpr (ADD) f[k] += g[k];
+    }
+    store_vec<T, 8>(y + ay, f);
+  }
+  if (LINE && blockIdx.x == 0 && threadIdx.x < (a.total & 7)) {
+    const int64_t at = whole * 8 + threadIdx.x;
+    const uint32_t m = kept_bits(philox(key, (uint64_t)whole), a.drop);
+    float f = (m >> threadIdx.x) & 1u ? Elem<T>::get(x[at]) * a.scale : 0.0f;
+    if (ADD) f += Elem<T>::get(res[at]);
+    y[at] = Elem<T>::put(f);
+  }
+}
+
+// Any pitch and alignment: a warp takes 256 consecutive values, 32 at a time;
+// lane l draws their l-th counter and hands out its bits.
+template <typename T, bool ADD>
+__global__ void __launch_bounds__(kThreads) k_dropout_any(const __grid_constant__ DropArgs a) {
+  const Key key(a);
+  const int lane = threadIdx.x & 31;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
+  const T* x = reinterpret_cast<const T*>(a.x);
+  const T* res = reinterpret_cast<const T*>(a.residual);
+  T* y = reinterpret_cast<T*>(a.y);
+  const int64_t spans = (a.total + 255) >> 8;
+  for (int64_t span = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); span < spans; span += warps) {
+    const int64_t row0 = (span << 8) / a.c;
+    const uint32_t col0 = (uint32_t)((span << 8) - row0 * a.c);
+    const int64_t left = a.total - (span << 8);
+    float f[8], g[8];
+    int64_t ay[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t at = col0 + 32 * k + lane;
+      // rows further on: fewer than 256 columns past col0 < c
+      const uint32_t down = a.c >= 512u ? (at >= a.c ? 1u : 0u) : a.c == 1u ? at : __umulhi(at, a.magic);
+      const int64_t row = row0 + down;
+      const uint32_t col = at - down * a.c;
+      ay[k] = row * a.ldy + col;
+      const bool mine = 32 * k + lane < left;
+      f[k] = mine ? Elem<T>::get(x[row * a.ldx + col]) : 0.0f;
+      if constexpr (ADD) g[k] = mine ? Elem<T>::get(res[row * a.ldr + col]) : 0.0f;
+    }
+    const uint32_t m = kept_bits(philox(key, (uint64_t)span * 32 + lane), a.drop);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint32_t bits = __shfl_sync(0xffffffffu, m, 4 * k + (lane >> 3));
+      float v = (bits >> (lane & 7)) & 1u ? f[k] * a.scale : 0.0f;
+      if constexpr (ADD) v += g[k];
+      if (32 * k + lane < left) y[ay[k]] = Elem<T>::put(v);
+    }
+  }
+}
+
+fvx_status bad(const char* who, const char* what) {
+  set_error("%s: %s", who, what);
+  return FVX_ERR_INVALID_ARG;
+}
+fvx_status check_rows_of(const char* who, const char* name, const void* p, int64_t ld, int64_t n, int64_t c, int elem) {
+  if (reinterpret_cast<uintptr_t>(p) % elem) {
+    set_error("%s: %s is not aligned to its elements", who, name);
+    return FVX_ERR_INVALID_ARG;
+  }
+  if (n > 1 && ld < c) {
+    set_error("%s: the row pitch of %s is below the channel count", who, name);
+    return FVX_ERR_INVALID_ARG;
+  }
+  return FVX_OK;
+}
+
+template <typename T>
+fvx_status run(const DropArgs& a, bool vectors, bool line, int sms, cudaStream_t s) {
+  const int64_t threads = vectors ? std::max<int64_t>(1, a.total >> 3) : ((a.total + 255) >> 8) * 32;
+  const int blocks = (int)std::min<int64_t>((threads + kThreads - 1) / kThreads, (int64_t)sms * 64);
+  LaunchScope ls("dropout", s);
+  auto go = [&]<bool ADD>() {
+    if (!vectors) k_dropout_any<T, ADD><<<blocks, kThreads, 0, s>>>(a);
+    else if (line) k_dropout<T, true, ADD><<<blocks, kThreads, 0, s>>>(a);
+    else k_dropout<T, false, ADD><<<blocks, kThreads, 0, s>>>(a);
+  };
+  if (a.residual) go.template operator()<true>();
+  else go.template operator()<false>();
+  return check_launch("dropout");
+}
+
+}  // namespace
+}  // namespace fvx
+
+using namespace fvx;
+
+extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, const void* residual, int64_t ldr, int64_t n,
+                                  int64_t c, double p, uint64_t seed, uint64_t offset, const uint64_t* state, void* y,
+                                  int64_t ldy, fvx_stream stream) {
+  const char* who = "fvx_dropout";
+  EntryScope entry(who);
+  if (dt != FVX_F32 && dt != FVX_BF16) return bad(who, "dtype must be FVX_F32 or FVX_BF16");
+  if (n < 0 || c < 1 || c > 0x7fffffff) return bad(who, "rows must not be negative, channels in 1..2^31 - 1");
+  if (n > ((int64_t)1 << 60) / c) return bad(who, "more than 2^60 values");
+  if (!(p >= 0.0 && p <= 1.0)) return bad(who, "p must be in 0..1");
+  const int elem = dt == FVX_F32 ? 4 : 2;
+  if (n > 0 && (!x || !y)) return bad(who, "NULL x or y");
+  FVX_TRY(check_rows_of(who, "x", x, ldx, n, c, elem));
+  FVX_TRY(check_rows_of(who, "y", y, ldy, n, c, elem));
+  if (residual) FVX_TRY(check_rows_of(who, "residual", residual, ldr, n, c, elem));
+  if (reinterpret_cast<uintptr_t>(state) % 8) return bad(who, "state is not aligned to 8 bytes");
+  if (n == 0) return FVX_OK;
+  int sms = 0;
+  FVX_TRY(device_sm_count(&sms));
+  DropArgs a = {};
+  a.x = x;
+  a.residual = residual;
+  a.y = y;
+  a.total = n * c;
+  a.rows = n;
+  a.ldx = n > 1 ? ldx : c;
+  a.ldr = n > 1 ? ldr : c;
+  a.ldy = n > 1 ? ldy : c;
+  a.state = state;
+  a.seed = seed;
+  a.offset = offset;
+  a.c = (uint32_t)c;
+  a.vecs = (uint32_t)(c / 8);
+  a.magic = c > 1 ? (uint32_t)(((uint64_t)1 << 32) / (uint64_t)c + 1) : 0;
+  a.drop = (uint32_t)lrint(p * 65536.0);
+  a.scale = a.drop < 65536 ? (float)(65536.0 / (65536 - (int)a.drop)) : 0.0f;
+  auto wide = [&](const void* q, int64_t ld) {
+    return reinterpret_cast<uintptr_t>(q) % (8 * elem) == 0 && (ld == c || ld % 8 == 0);
+  };
+  const bool line = a.ldx == c && a.ldy == c && (!residual || a.ldr == c);
+  const bool vectors = wide(x, a.ldx) && wide(y, a.ldy) && (!residual || wide(residual, a.ldr)) && (line || c % 8 == 0);
+  return dt == FVX_F32 ? run<float>(a, vectors, line, sms, (cudaStream_t)stream)
+                       : run<__nv_bfloat16>(a, vectors, line, sms, (cudaStream_t)stream);
+}
