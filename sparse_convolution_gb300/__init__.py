@@ -815,7 +815,7 @@ def _head_tensor(who, name, t, positions, rotary, weight, out, x=None, dweight=N
     n, heads, d = t.shape
     if heads < 1 or not 1 <= d <= 256:
         _refuse(f"{who}: {name} must have at least one head of 1 to 256 values, got {tuple(t.shape)}")
-    pos = (None, 0, 0)
+    pos = (0, 0, 0)
     if rotary is not None:
         axes = rotary.axes
         if rotary.size > d:
@@ -823,7 +823,7 @@ def _head_tensor(who, name, t, positions, rotary, weight, out, x=None, dweight=N
         if positions is None:
             _refuse(f"{who}: positions are missing")
         ps = positions.shape
-        if positions.dtype != torch.int32 or ps[0] != n or not (len(ps) == 2 and ps[1] == axes or len(ps) == 1 == axes):
+        if positions.dtype != torch.int32 or tuple(ps) not in (((n,), (n, 1)) if axes == 1 else ((n, axes),)):
             _refuse(f"{who}: positions of {name} must be int32 [{n}{', %d' % axes if axes > 1 else ''}], "
                     f"got {positions.dtype} {tuple(ps)}")
         st = positions.stride()

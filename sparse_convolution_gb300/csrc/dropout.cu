@@ -24,7 +24,7 @@ struct DropArgs {
   const void* x;
   const void* residual;  // or null
   void* y;
-  int64_t total, rows, ldx, ldr, ldy;
+  int64_t total, ldx, ldr, ldy;
   const uint64_t* state;  // seed and offset on the device, or null
   uint64_t seed, offset;
   uint32_t c, vecs, magic, drop;  // vecs: vectors of 8 per row
@@ -191,8 +191,8 @@ extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, cons
   const char* who = "fvx_dropout";
   EntryScope entry(who);
   if (dt != FVX_F32 && dt != FVX_BF16) return bad(who, "dtype must be FVX_F32 or FVX_BF16");
-  if (n < 0 || c < 1 || c > 0x7fffffff) return bad(who, "rows must not be negative, channels in 1..2^31 - 1");
-  if (n > ((int64_t)1 << 60) / c) return bad(who, "more than 2^60 values");
+  if (n < 0 || c < 1) return bad(who, "rows must not be negative, channels at least 1");
+  if (c > (int64_t)1 << 60 || n > ((int64_t)1 << 60) / c) return bad(who, "more than 2^60 values");
   if (!(p >= 0.0 && p <= 1.0)) return bad(who, "p must be in 0..1");
   const int elem = dt == FVX_F32 ? 4 : 2;
   if (n > 0 && (!x || !y)) return bad(who, "NULL x or y");
@@ -201,6 +201,8 @@ extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, cons
   if (residual) FVX_TRY(check_rows_of(who, "residual", residual, ldr, n, c, elem));
   if (reinterpret_cast<uintptr_t>(state) % 8) return bad(who, "state is not aligned to 8 bytes");
   if (n == 0) return FVX_OK;
+  const bool line = n <= 1 || (ldx == c && ldy == c && (!residual || ldr == c));
+  if (!line && c > 0x7fffffff) return bad(who, "rows with gaps must be shorter than 2^31 values");
   int sms = 0;
   FVX_TRY(device_sm_count(&sms));
   DropArgs a = {};
@@ -208,10 +210,11 @@ extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, cons
   a.residual = residual;
   a.y = y;
   a.total = n * c;
-  a.rows = n;
-  a.ldx = n > 1 ? ldx : c;
-  a.ldr = n > 1 ? ldr : c;
-  a.ldy = n > 1 ? ldy : c;
+  // without gaps any cut into rows is as good
+  if (line) c = ldx = ldr = ldy = 1 << 20;
+  a.ldx = ldx;
+  a.ldr = ldr;
+  a.ldy = ldy;
   a.state = state;
   a.seed = seed;
   a.offset = offset;
@@ -221,10 +224,9 @@ extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, cons
   a.drop = (uint32_t)lrint(p * 65536.0);
   a.scale = a.drop < 65536 ? (float)(65536.0 / (65536 - (int)a.drop)) : 0.0f;
   auto wide = [&](const void* q, int64_t ld) {
-    return reinterpret_cast<uintptr_t>(q) % (8 * elem) == 0 && (ld == c || ld % 8 == 0);
+    return reinterpret_cast<uintptr_t>(q) % (8 * elem) == 0 && ld % 8 == 0;
   };
-  const bool line = a.ldx == c && a.ldy == c && (!residual || a.ldr == c);
-  const bool vectors = wide(x, a.ldx) && wide(y, a.ldy) && (!residual || wide(residual, a.ldr)) && (line || c % 8 == 0);
+  const bool vectors = wide(x, ldx) && wide(y, ldy) && (!residual || wide(residual, ldr)) && c % 8 == 0;
   return dt == FVX_F32 ? run<float>(a, vectors, line, sms, (cudaStream_t)stream)
                        : run<__nv_bfloat16>(a, vectors, line, sms, (cudaStream_t)stream);
 }
