@@ -23,23 +23,44 @@ namespace {
 constexpr int kMaxHead = 256;
 constexpr int kMaxPairs = kMaxHead / 2;
 
-// One of the call's tensors.
+// A block's warps: those that work on the heads, and those that fetch the next
+// stages' tensors and compute their angles.
+constexpr int kWorkers = 16, kHelpers = 4, kHeadThreads = 32 * (kWorkers + kHelpers);
+constexpr int kStages = 3;
+constexpr int kMostSmem = 227 * 1024;
+
+// A tensor that is read.  Its part of a stage lies in shared memory as in
+// global, in pieces: all of it (tokens that follow one another), the heads of a
+// token, or one head.
+struct HeadSource {
+  const void* p;
+  int64_t token, head;
+  int s_token, s_head;  // strides in shared memory
+  int at;               // where the part begins, in bytes
+  int bulk_tiles;       // the first tiles go by bulk copies
+  bool whole, by_head;  // the part is one piece; a head is
+};
+// One of the call's tensors, cut into tiles of `tokens` tokens by `head_block` heads.
 struct HeadJob {
-  const void* in;  // forward: x; backward: the gradient of the result
-  const void* x;   // norm backward: the forward pass's input
+  HeadSource in[2];  // forward: x; backward: the gradient of the result, and the forward pass's x
   void* out;
   const float* w;
   const int32_t* pos;
   float* part;  // norm backward: [blocks][d] partial sums of dw
-  int64_t in_token, in_head, x_token, x_head, out_token, out_head, pos_token, pos_axis;
-  int units, heads, chunks;  // a unit is up to HC heads (chunk, chunk + chunks, ...) of a token
-  int block0;                // the job's first block
+  int64_t out_token, out_head, pos_token, pos_axis;
+  int out_token32, out_head32;  // the same within a tile
+  int n, heads, tokens, head_block, head_blocks, tiles;
+  uint32_t block_magic;  // 2^32 / head_block, rounded up
 };
 struct HeadArgs {
   HeadJob job[2];
   uint64_t turns[kMaxPairs];  // turns per position step, in 2^-64
-  int jobs, d, pairs, axis1, axis2;  // pairs from axis1 (axis2) on belong to the second (third) axis
-  int items, items_turned, lanes;    // vectors of pairs, of passing values; lanes that share a head
+  uint32_t* status;
+  int shared;  // a stage holds the same tokens of both tensors; else tiles of the first, then of the second
+  int d, pairs, axes, axis1, axis2;  // pairs from axis1 (axis2) on belong to the second (third) axis
+  int items, items_turned, lanes;    // a head's items: of pairs, of values that pass; lanes that share a head
+  uint32_t pair_magic;               // 2^32 / pairs, rounded up
+  int angles, stage_bytes;           // of a stage: angles, bytes of the tensors
   float magnitude, sign, eps, inv_d;
 };
 
@@ -70,240 +91,460 @@ __device__ __forceinline__ void sincos_turn(uint32_t t, float& s, float& c) {
   if ((q + 1u) & 2u) c = -c;
 }
 
-// What a lane holds of a head: ITEMS items of two vectors of V values each, a
-// pair's partners in the same lane.
-template <typename T, int V, int ITEMS, bool INTERLEAVED>
-struct Place {
-  int a[ITEMS], b[ITEMS], p[ITEMS];  // offsets of the two vectors, first pair (or -1: values that pass)
+enum HeadOp { kRotate, kNormRotate, kNormRotateBack };
+
+__device__ __forceinline__ float e_sub(float a, float b) { return a - b; }
+__device__ __forceinline__ uint64_t e_sub(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ void copy4(uint32_t to, const void* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {  // when this thread's copies have landed
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWorkers) : "memory"); }
+
+// A tile: its first token and head, and how many of each exist.
+struct HeadTile {
+  int token, head, tokens, heads;
+};
+__device__ __forceinline__ HeadTile head_tile(const HeadJob& j, int tile) {
+  const int slab = j.head_blocks == 1 ? tile : tile / j.head_blocks;
+  HeadTile s;
+  s.head = (tile - slab * j.head_blocks) * j.head_block;
+  s.token = slab * j.tokens;
+  s.tokens = min(j.tokens, j.n - s.token);
+  s.heads = min(j.head_block, j.heads - s.head);
+  return s;
+}
+
+// 0 or 1: whether a piece starts in the second half of a 4-byte word (bf16 alone)
+template <typename T>
+__device__ __forceinline__ int odd_start(const HeadSource& src, int token, int head) {
+  if constexpr (sizeof(T) == 2) {
+    if (src.whole) return 0;
+    return (int)(((uint32_t)(reinterpret_cast<uintptr_t>(src.p) >> 1) + (uint32_t)token * (uint32_t)src.token +
+                  (uint32_t)head * (uint32_t)src.head) & 1u);
+  }
+  return 0;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t piece_bytes(const HeadSource& src, const HeadJob& j, const HeadTile& s, int d) {
+  const int values = src.whole ? j.tokens * src.s_token : src.by_head ? d : (s.heads - 1) * src.s_head + d;
+  return ((uint32_t)values * (uint32_t)sizeof(T) + 15u) & ~15u;
+}
+template <typename T>
+__device__ __forceinline__ uint32_t bulk_bytes(const HeadSource& src, const HeadJob& j, int tile, const HeadTile& s, int d) {
+  if (tile >= src.bulk_tiles) return 0u;
+  return piece_bytes<T>(src, j, s, d) * (src.whole ? 1 : s.tokens * (src.by_head ? s.heads : 1));
+}
+// Starts the copies of a tile's part of src to the stage at `to`.
+template <typename T>
+__device__ __forceinline__ void fetch_source(const HeadSource& src, const HeadJob& j, int tile, const HeadTile& s, int d,
+                                             uint32_t to, uint32_t bar, int helper) {
+  const int lane = threadIdx.x & 31;
+  const T* base = reinterpret_cast<const T*>(src.p);
+  const int per_token = src.by_head ? s.heads : 1;
+  to += src.at;
+  if (tile < src.bulk_tiles) {
+    if (helper) return;
+    const int pieces = src.whole ? 1 : s.tokens * per_token;
+    const uint32_t bytes = piece_bytes<T>(src, j, s, d);
+    for (int i = lane; i < pieces; i += 32) {
+      const int t = per_token == 1 ? i : i / per_token, h = i - t * per_token;
+      tc::bulk_load(to + (t * src.s_token + h * src.s_head) * (int)sizeof(T),
+                    base + (s.token + t) * src.token + (s.head + h) * src.head, bytes, bar);
+    }
+    return;
+  }
+  const int values = src.by_head ? d : (s.heads - 1) * src.s_head + d;
+  // whole words: the halves of a piece's first and last word that are not its own are copied with them
+  for (int i = helper; i < s.tokens * per_token; i += kHelpers) {
+    const int t = per_token == 1 ? i : i / per_token, h = i - t * per_token;
+    const uintptr_t from = reinterpret_cast<uintptr_t>(base + (s.token + t) * src.token + (s.head + h) * src.head);
+    const uint32_t dst = to + (t * src.s_token + h * src.s_head + odd_start<T>(src, s.token + t, s.head + h)) * (int)sizeof(T);
+    const int words = (int)((from + values * sizeof(T) + 3) / 4 - from / 4);
+    for (int k = lane; k < words; k += 32) copy4((dst & ~3u) + 4 * k, reinterpret_cast<const void*>((from & ~(uintptr_t)3) + 4 * k));
+  }
+}
+// Cosines and sines of a tile's tokens, each computed once for all its heads.
+__device__ __forceinline__ void angles_of(const HeadArgs& a, const HeadJob& j, const HeadTile& s, const uint64_t* turns,
+                                          float* angles, int helper) {
+#pragma unroll 4
+  for (int i = helper * 32 + (threadIdx.x & 31); i < s.tokens * a.pairs; i += 32 * kHelpers) {
+    const int t = a.pairs == 1 ? i : (int)__umulhi((uint32_t)i, a.pair_magic), p = i - t * a.pairs;
+    const int axis = (p >= a.axis1) + (p >= a.axis2);
+    float sn, cs;
+    sincos_turn(turn_of(turns[p], __ldg(j.pos + (s.token + t) * j.pos_token + axis * j.pos_axis)), sn, cs);
+    angles[i] = cs * a.magnitude;
+    angles[a.angles + i] = sn * a.magnitude * a.sign;
+  }
+}
+
+// A lane holds ITEMS items of a head, each two vectors of V values in memory:
+// for V pairs their first and second partners (u and v), the latter P further on
+// (halves) or interleaved with them; or up to 2V values that pass, split alike.
+// Pairs of fp32 values are computed on two at a time.  FULL: every lane has all
+// its items.
+template <typename T, int V, int ITEMS, bool INTERLEAVED, int OP, bool FULL>
+struct Heads {
+  static constexpr bool kNorm = OP != kRotate, kBack = OP == kNormRotateBack;
+  using E = typename Lane<V>::E;
+  static constexpr int N = Lane<V>::N;
+  const HeadArgs& a;
+  const int lane, group, groups;
+  int at[ITEMS], second[ITEMS];
   bool has_a[ITEMS], has_b[ITEMS];
-  __device__ __forceinline__ Place(const HeadArgs& args, int lane) {
+  E dw[kBack ? ITEMS : 1][2][N];
+
+  __device__ __forceinline__ explicit Heads(const HeadArgs& args)
+      : a(args), lane(threadIdx.x & (args.lanes - 1)), group((threadIdx.x & 31) / args.lanes), groups(32 / args.lanes) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const int item = lane + i * args.lanes;
-      const bool turned = item < args.items_turned;
-      p[i] = turned ? item * V : -1;
-      a[i] = turned ? (INTERLEAVED ? 2 : 1) * item * V : 2 * args.pairs + (item - args.items_turned) * 2 * V;
-      b[i] = turned && !INTERLEAVED ? a[i] + args.pairs : a[i] + V;
-      has_a[i] = item < args.items;
-      has_b[i] = has_a[i] && b[i] < args.d;
-      if (!has_a[i]) p[i] = -1;
+      const int item = lane + i * a.lanes;
+      place(a, item, at[i], second[i]);
+      has_a[i] = FULL || item < a.items;
+      has_b[i] = FULL || (has_a[i] && second[i] < a.d);
+    }
+    clear();
+  }
+  __device__ __forceinline__ void clear() {
+    if constexpr (kBack) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int k = 0; k < N; ++k) dw[i][0][k] = dw[i][1][k] = e_all<E>(0.0f);
     }
   }
-};
-
-template <int V, int ITEMS>
-struct Angles {
-  float c[ITEMS][V], s[ITEMS][V];
-};
-template <int V, int ITEMS, typename P>
-__device__ __forceinline__ void angles_at(const HeadArgs& a, const HeadJob& j, const P& pl, int64_t token,
-                                          const uint64_t (&step)[ITEMS][V], Angles<V, ITEMS>& out) {
-  const int32_t* at = j.pos + token * j.pos_token;
-  int pos[3];
-  pos[0] = __ldg(at);
-  pos[1] = a.axis1 < a.pairs ? __ldg(at + j.pos_axis) : 0;
-  pos[2] = a.axis2 < a.pairs ? __ldg(at + 2 * j.pos_axis) : 0;
+  // where an item's two vectors start in the head
+  static __device__ __forceinline__ void place(const HeadArgs& a, int item, int& first, int& second) {
+    const bool turned = item < a.items_turned;
+    first = turned ? (INTERLEAVED ? 2 : 1) * item * V : 2 * a.pairs + (item - a.items_turned) * 2 * V;
+    second = turned && !INTERLEAVED ? first + a.pairs : first + V;
+  }
+  // the channel of value k of an item's side (0: u, 1: v); d or more: none
+  static __device__ __forceinline__ int channel(const HeadArgs& a, int item, int side, int k) {
+    int first, second;
+    place(a, item, first, second);
+    return INTERLEAVED ? first + 2 * k + side : (side ? second : first) + k;
+  }
+  // sum over the lanes that share a head
+  __device__ __forceinline__ float head_sum(float v) const {
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      const int p = pl.p[i] + k;
-      const int at_axis = p >= a.axis2 ? pos[2] : p >= a.axis1 ? pos[1] : pos[0];
-      float s, c;
-      sincos_turn(turn_of(step[i][k], at_axis), s, c);
-      out.c[i][k] = c * a.magnitude;
-      out.s[i][k] = s * a.magnitude * a.sign;
+    for (int o = 1; o < 32; o <<= 1) {
+      if (o >= a.lanes) break;
+      v += __shfl_xor_sync(0xffffffffu, v, o);
     }
-}
-
-// (u, v) of a lane's pairs, as stored in its two vectors, turned.
-template <int V, bool INTERLEAVED>
-__device__ __forceinline__ void turn(float (&x)[2 * V], const float (&c)[V], const float (&s)[V]) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    const int iu = INTERLEAVED ? 2 * k : k, iv = INTERLEAVED ? 2 * k + 1 : V + k;
-    const float u = x[iu], v = x[iv];
-    x[iu] = fmaf(u, c[k], -(v * s[k]));
-    x[iv] = fmaf(v, c[k], u * s[k]);
+    return v;
   }
-}
 
-template <typename T, int V>
-__device__ __forceinline__ void join(const Pack<T, V>& a, const Pack<T, V>& b, float (&f)[2 * V]) {
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    f[k] = Elem<T>::get(a.v[k]);
-    f[V + k] = Elem<T>::get(b.v[k]);
-  }
-}
-template <typename T, int V>
-__device__ __forceinline__ void split_store(T* p, int a, int b, bool has_a, bool has_b, const float (&f)[2 * V]) {
-  Pack<T, V> u, v;
-#pragma unroll
-  for (int k = 0; k < V; ++k) {
-    u.v[k] = Elem<T>::put(f[k]);
-    v.v[k] = Elem<T>::put(f[V + k]);
-  }
-  if (has_a) *reinterpret_cast<Pack<T, V>*>(p + a) = u;
-  if (has_b) *reinterpret_cast<Pack<T, V>*>(p + b) = v;
-}
-
-template <typename T, int V, int ITEMS, bool INTERLEAVED, bool NORM, int HC>
-__global__ void __launch_bounds__(kThreads) k_heads(const __grid_constant__ HeadArgs args) {
-  const HeadJob& j = args.job[args.jobs > 1 && (int)blockIdx.x >= args.job[1].block0];
-  const int lane = threadIdx.x & (args.lanes - 1);
-  const int unit = (blockIdx.x - j.block0) * (kThreads / args.lanes) + threadIdx.x / args.lanes;
-  const bool live = unit < j.units;
-  const int token = live ? unit / j.chunks : 0, h0 = unit - token * j.chunks;
-  const Place<T, V, ITEMS, INTERLEAVED> pl(args, lane);
-  Pack<T, V> xa[HC][ITEMS], xb[HC][ITEMS];
-  const T* in = reinterpret_cast<const T*>(j.in) + token * j.in_token;
-#pragma unroll
-  for (int h = 0; h < HC; ++h) {
-    const int head = h0 + h * j.chunks;
-    const bool mine = live && head < j.heads;
+  // A group's head within the tile.  Groups without one take the tile's first and store nothing.
+  struct Row {
+    int token, head;
+    bool live;
+  };
+  __device__ __forceinline__ void read(const HeadSource& src, const unsigned char* stage, const HeadTile& s, const Row& r,
+                                       E (&e)[ITEMS][2][N]) const {
+    int off = r.token * src.s_token + r.head * src.s_head;
+    if constexpr (V == 1) off += odd_start<T>(src, s.token + r.token, s.head + (src.by_head ? r.head : 0));
+    const T* p = reinterpret_cast<const T*>(stage + src.at) + off;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      xa[h][i] = mine && pl.has_a[i] ? raw_vec<T, V>(in + head * j.in_head + pl.a[i]) : no_vec<T, V>();
-      xb[h][i] = mine && pl.has_b[i] ? raw_vec<T, V>(in + head * j.in_head + pl.b[i]) : no_vec<T, V>();
+      const Pack<T, V> x = has_a[i] ? raw_vec<T, V>(p + at[i]) : no_vec<T, V>(),
+                       y = has_b[i] ? raw_vec<T, V>(p + second[i]) : no_vec<T, V>();
+      float f[2 * V], u[V], v[V];
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        f[k] = Elem<T>::get(x.v[k]);
+        f[V + k] = Elem<T>::get(y.v[k]);
+      }
+#pragma unroll
+      for (int k = 0; k < V; ++k) {
+        u[k] = INTERLEAVED ? f[2 * k] : f[k];
+        v[k] = INTERLEAVED ? f[2 * k + 1] : f[V + k];
+      }
+      to_pairs<V>(u, e[i][0]);
+      to_pairs<V>(v, e[i][1]);
     }
   }
-  uint64_t step[ITEMS][V];
+  __device__ __forceinline__ void store(const HeadJob& j, T* out, const Row& r, const E (&e)[ITEMS][2][N]) const {
+    out += r.token * j.out_token32 + r.head * j.out_head32;
 #pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
+    for (int i = 0; i < ITEMS; ++i) {
+      float u[V], v[V];
+      from_pairs<V>(e[i][0], u);
+      from_pairs<V>(e[i][1], v);
+      Pack<T, V> x, y;
 #pragma unroll
-    for (int k = 0; k < V; ++k) step[i][k] = pl.p[i] >= 0 ? args.turns[pl.p[i] + k] : 0;
-  Angles<V, ITEMS> an;
-  if (args.pairs) angles_at<V, ITEMS>(args, j, pl, token, step, an);
-  float w[ITEMS][2 * V];
-  if constexpr (NORM) {
+      for (int k = 0; k < 2 * V; ++k) {
+        const float f = INTERLEAVED ? (k & 1 ? v[k / 2] : u[k / 2]) : k < V ? u[k % V] : v[k % V];
+        (k < V ? x : y).v[k % V] = Elem<T>::put(f);
+      }
+      if (r.live && has_a[i]) *reinterpret_cast<Pack<T, V>*>(out + at[i]) = x;
+      if (r.live && has_b[i]) *reinterpret_cast<Pack<T, V>*>(out + second[i]) = y;
+    }
+  }
+  static __device__ __forceinline__ void vector(const float* p, E (&e)[N]) {
+    float f[V];
+    const Pack<float, (V > 4 ? 4 : V)>* q = reinterpret_cast<const Pack<float, (V > 4 ? 4 : V)>*>(p);
+#pragma unroll
+    for (int k = 0; k < V; ++k) f[k] = q[k / 4].v[k % 4];
+    to_pairs<V>(f, e);
+  }
+  __device__ __forceinline__ void rotate(const float* angles, const Row& r, E (&e)[ITEMS][2][N]) const {
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i) {
+      const int item = lane + i * a.lanes;
+      if (item < a.items_turned) {
+        const float* p = angles + r.token * a.pairs + item * V;
+        E c[N], s[N];
+        vector(p, c);
+        vector(p + a.angles, s);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const E u = e[i][0][k], v = e[i][1][k];
+          e[i][0][k] = e_sub(e_mul(u, c[k]), e_mul(v, s[k]));
+          e[i][1][k] = e_fma(v, c[k], e_mul(u, s[k]));
+        }
+      }
+    }
+  }
+
+  __device__ __forceinline__ void forward(const HeadJob& j, const unsigned char* stage, const float* angles, const float* w,
+                                          const HeadTile& s, const Row& r, T* out) const {
+    E e[ITEMS][2][N], sum = e_all<E>(0.0f);
+    read(j.in[0], stage, s, r, e);
+    if constexpr (kNorm) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int k = 0; k < N; ++k) sum = e_fma(e[i][1][k], e[i][1][k], e_fma(e[i][0][k], e[i][0][k], sum));
+      const E rstd = e_all<E>(rsqrtf(fmaf(head_sum(e_sum(sum)), a.inv_d, a.eps)));
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+        for (int side = 0; side < 2; ++side) {
+          E wt[N];
+          vector(w + ((lane + i * a.lanes) * 2 + side) * V, wt);
+#pragma unroll
+          for (int k = 0; k < N; ++k) e[i][side][k] = e_mul(e_mul(e[i][side][k], rstd), wt[k]);
+        }
+    }
+    rotate(angles, r, e);
+    store(j, out, r, e);
+  }
+  __device__ __forceinline__ void backward(const HeadJob& j, const unsigned char* stage, const float* angles, const float* w,
+                                           const HeadTile& s, const Row& r, T* out) {
+    E g[ITEMS][2][N], x[ITEMS][2][N], xx = e_all<E>(0.0f), gx = xx;
+    read(j.in[0], stage, s, r, g);
+    rotate(angles, r, g);
+    read(j.in[1], stage, s, r, x);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        w[i][k] = j.w && pl.has_a[i] ? __ldg(j.w + pl.a[i] + k) : 1.0f;
-        w[i][V + k] = j.w && pl.has_b[i] ? __ldg(j.w + pl.b[i] + k) : 1.0f;
+      for (int side = 0; side < 2; ++side) {
+        E wt[N];
+        vector(w + ((lane + i * a.lanes) * 2 + side) * V, wt);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          xx = e_fma(x[i][side][k], x[i][side][k], xx);
+          gx = e_fma(e_mul(g[i][side][k], wt[k]), x[i][side][k], gx);
+        }
       }
+    const float rstd = rsqrtf(fmaf(head_sum(e_sum(xx)), a.inv_d, a.eps));
+    // a group without a head adds nothing to dw
+    const E rs = e_all<E>(rstd), mine = e_all<E>(r.live ? rstd : 0.0f),
+            back = e_all<E>(-(head_sum(e_sum(gx)) * a.inv_d) * rstd * rstd);
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+#pragma unroll
+      for (int side = 0; side < 2; ++side) {
+        E wt[N];
+        vector(w + ((lane + i * a.lanes) * 2 + side) * V, wt);
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+          const E gk = g[i][side][k], xk = x[i][side][k];
+          if (kBack) dw[i][side][k] = e_fma(gk, e_mul(xk, mine), dw[i][side][k]);
+          g[i][side][k] = e_mul(rs, e_fma(xk, back, e_mul(gk, wt[k])));
+        }
+      }
+    store(j, out, r, g);
   }
+  // The block's part of dw: groups of a warp by shuffles, then its warps, in a fixed order.
+  __device__ __forceinline__ void write_part(float* sh, float* part) {
 #pragma unroll
-  for (int h = 0; h < HC; ++h) {
-    const int head = h0 + h * j.chunks;
-    const bool mine = live && head < j.heads;
-    float x[ITEMS][2 * V], sum = 0.0f;
+    for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      join<T, V>(xa[h][i], xb[h][i], x[i]);
-      if constexpr (NORM) {
+      for (int side = 0; side < 2; ++side) {
+        float f[V];
+        from_pairs<V>(dw[i][side], f);
 #pragma unroll
-        for (int k = 0; k < 2 * V; ++k) sum = fmaf(x[i][k], x[i][k], sum);
+        for (int k = 0; k < V; ++k) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1)
+            if (o >= a.lanes) f[k] += __shfl_xor_sync(0xffffffffu, f[k], o);
+          const int c = channel(a, lane + i * a.lanes, side, k);
+          if (group == 0 && has_a[i] && c < a.d) sh[(threadIdx.x >> 5) * a.d + c] = f[k];
+        }
       }
-    }
-    float rstd = 1.0f;
-    if constexpr (NORM) rstd = rsqrtf(fmaf(lanes_sum(sum, args.lanes), args.inv_d, args.eps));
-    T* out = reinterpret_cast<T*>(j.out) + token * j.out_token + head * j.out_head;
+    workers_sync();
+    if (part)
+      for (int c = threadIdx.x; c < a.d; c += 32 * kWorkers) {
+        float s = 0.0f;
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      if constexpr (NORM) {
-#pragma unroll
-        for (int k = 0; k < 2 * V; ++k) x[i][k] *= rstd * w[i][k];
+        for (int k = 0; k < kWorkers; ++k) s += sh[k * a.d + c];
+        part[c] = s;
       }
-      if (pl.p[i] >= 0) turn<V, INTERLEAVED>(x[i], an.c[i], an.s[i]);
-      split_store<T, V>(out, pl.a[i], pl.b[i], mine && pl.has_a[i], mine && pl.has_b[i], x[i]);
-    }
+    workers_sync();
+    clear();
   }
-}
+};
 
-// The norm's gradients.  Blocks stay and walk their job's units; a lane keeps
-// its channels, so its part of dw stays in registers until the end.
-template <typename T, int V, int ITEMS, bool INTERLEAVED, int HC>
-__global__ void __launch_bounds__(kThreads) k_heads_bwd(const __grid_constant__ HeadArgs args) {
-  extern __shared__ float sh[];  // [kThreads / lanes][d]
-  const int which = args.jobs > 1 && (int)blockIdx.x >= args.job[1].block0;
-  const HeadJob& j = args.job[which];
-  const int block = blockIdx.x - j.block0;
-  const int blocks = (which + 1 < args.jobs ? args.job[1].block0 : (int)gridDim.x) - j.block0;
-  const int lane = threadIdx.x & (args.lanes - 1), group = threadIdx.x / args.lanes, groups = kThreads / args.lanes;
-  const Place<T, V, ITEMS, INTERLEAVED> pl(args, lane);
-  uint64_t step[ITEMS][V];
-  float w[ITEMS][2 * V], dw[ITEMS][2 * V];
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      step[i][k] = pl.p[i] >= 0 ? args.turns[pl.p[i] + k] : 0;
-      w[i][k] = j.w && pl.has_a[i] ? __ldg(j.w + pl.a[i] + k) : 1.0f;
-      w[i][V + k] = j.w && pl.has_b[i] ? __ldg(j.w + pl.b[i] + k) : 1.0f;
-    }
-#pragma unroll
-    for (int k = 0; k < 2 * V; ++k) dw[i][k] = 0.0f;
+// Shared memory: barriers, steps, both tensors' weights, the workers' parts of
+// dw, then the stages' angles and tensors.
+struct HeadLayout {
+  int turns, w, parts, angles, stages, bytes;
+  __host__ __device__ HeadLayout(const HeadArgs& a, int weights, bool back) {
+    turns = 64;
+    w = turns + ((a.pairs + 1) & ~1) * 8;
+    parts = w + 2 * ((weights + 3) & ~3) * 4;
+    angles = parts + (back ? kWorkers * a.d * 4 : 0);
+    stages = (angles + kStages * 2 * a.angles * 4 + 127) & ~127;
+    bytes = stages + kStages * a.stage_bytes;
   }
-  // every group of a warp takes the same number of turns: they sum together
-  for (int64_t first = (int64_t)block * groups; first < j.units; first += (int64_t)blocks * groups) {
-    const int64_t unit = first + group;
-    const bool live = unit < j.units;
-    const int token = live ? (int)unit / j.chunks : 0, h0 = (int)unit - token * j.chunks;
-    Pack<T, V> xa[HC][ITEMS], xb[HC][ITEMS], ga[HC][ITEMS], gb[HC][ITEMS];
-    const T* in = reinterpret_cast<const T*>(j.in) + token * j.in_token;
-    const T* xs = reinterpret_cast<const T*>(j.x) + token * j.x_token;
-#pragma unroll
-    for (int h = 0; h < HC; ++h) {
-      const int head = h0 + h * j.chunks;
-      const bool mine = live && head < j.heads;
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        const bool a = mine && pl.has_a[i], b = mine && pl.has_b[i];
-        xa[h][i] = a ? raw_vec<T, V>(xs + head * j.x_head + pl.a[i]) : no_vec<T, V>();
-        xb[h][i] = b ? raw_vec<T, V>(xs + head * j.x_head + pl.b[i]) : no_vec<T, V>();
-        ga[h][i] = a ? raw_vec<T, V>(in + head * j.in_head + pl.a[i]) : no_vec<T, V>();
-        gb[h][i] = b ? raw_vec<T, V>(in + head * j.in_head + pl.b[i]) : no_vec<T, V>();
-      }
+};
+
+template <typename T, int V, int ITEMS, bool INTERLEAVED, int OP, bool FULL>
+__global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant__ HeadArgs args) {
+  using H = Heads<T, V, ITEMS, INTERLEAVED, OP, FULL>;
+  extern __shared__ __align__(128) unsigned char sm[];
+  const int weights = H::kNorm ? args.lanes * ITEMS * 2 * V : 0;
+  const HeadLayout lay(args, weights, H::kBack);
+  uint64_t* const turns = reinterpret_cast<uint64_t*>(sm + lay.turns);
+  float* const w = reinterpret_cast<float*>(sm + lay.w);
+  float* const angles = reinterpret_cast<float*>(sm + lay.angles);
+  unsigned char* const stages = sm + lay.stages;
+  const uint32_t full = tc::smem_u32(sm), empty = full + 8 * kStages;
+  const int warp = threadIdx.x >> 5;
+  const int tiles = args.shared ? args.job[0].tiles : args.job[0].tiles + args.job[1].tiles;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      // the helpers' threads when their copies have landed, their warps when the angles are there, the bytes of the bulk copies
+      tc::mbar_init(full + 8 * i, 32 * kHelpers + kHelpers + 1);
+      tc::mbar_init(empty + 8 * i, kWorkers);
     }
-    Angles<V, ITEMS> an;
-    if (args.pairs) angles_at<V, ITEMS>(args, j, pl, token, step, an);
-#pragma unroll
-    for (int h = 0; h < HC; ++h) {
-      const int head = h0 + h * j.chunks;
-      const bool mine = live && head < j.heads;
-      float x[ITEMS][2 * V], g[ITEMS][2 * V], xx = 0.0f, gx = 0.0f;
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-        join<T, V>(xa[h][i], xb[h][i], x[i]);
-        join<T, V>(ga[h][i], gb[h][i], g[i]);
-        if (pl.p[i] >= 0) turn<V, INTERLEAVED>(g[i], an.c[i], an.s[i]);
-#pragma unroll
-        for (int k = 0; k < 2 * V; ++k) {
-          xx = fmaf(x[i][k], x[i][k], xx);
-          gx = fmaf(g[i][k] * w[i][k], x[i][k], gx);
-        }
-      }
-      const float rstd = rsqrtf(fmaf(lanes_sum(xx, args.lanes), args.inv_d, args.eps));
-      const float back = lanes_sum(gx, args.lanes) * args.inv_d * rstd * rstd;
-      T* out = reinterpret_cast<T*>(j.out) + token * j.out_token + head * j.out_head;
-#pragma unroll
-      for (int i = 0; i < ITEMS; ++i) {
-#pragma unroll
-        for (int k = 0; k < 2 * V; ++k) {
-          const float xr = x[i][k] * rstd;
-          if (mine) dw[i][k] = fmaf(g[i][k], xr, dw[i][k]);
-          g[i][k] = rstd * fmaf(-x[i][k], back, g[i][k] * w[i][k]);
-        }
-        split_store<T, V>(out, pl.a[i], pl.b[i], mine && pl.has_a[i], mine && pl.has_b[i], g[i]);
-      }
-    }
+    tc::mbar_init_fence();
   }
-  if (!j.part) return;
-#pragma unroll
-  for (int i = 0; i < ITEMS; ++i)
-#pragma unroll
-    for (int k = 0; k < V; ++k) {
-      if (pl.has_a[i]) sh[group * args.d + pl.a[i] + k] = dw[i][k];
-      if (pl.has_b[i]) sh[group * args.d + pl.b[i] + k] = dw[i][V + k];
+  for (int p = threadIdx.x; p < args.pairs; p += kHeadThreads) turns[p] = args.turns[p];
+  if constexpr (H::kNorm)
+    for (int i = threadIdx.x; i < 2 * weights; i += kHeadThreads) {
+      const int seg = i >= weights, k = i - seg * weights;
+      const int c = H::channel(args, k / (2 * V), (k / V) & 1, k % V);
+      const float* from = seg ? args.job[1].w : args.job[0].w;
+      w[seg * ((weights + 3) & ~3) + k] = from && c < args.d ? __ldg(from + c) : 1.0f;
     }
   __syncthreads();
-  for (int c = threadIdx.x; c < args.d; c += kThreads) {
-    float s = 0.0f;
-    for (int k = 0; k < groups; ++k) s += sh[k * args.d + c];
-    j.part[(int64_t)block * args.d + c] = s;
+  uint32_t i = 0, phase = 0, taken = 0;
+  auto next_stage = [&]() {
+    ++taken;
+    if (++i == kStages) {
+      i = 0;
+      phase ^= 1u;
+    }
+  };
+  if (warp >= kWorkers) {
+    // ---------------------------------------------------------------- helpers
+    const int helper = warp - kWorkers, lane = threadIdx.x & 31;
+    auto fetch = [&](const HeadJob& j, int tile, const HeadTile& s, uint32_t to) {
+      fetch_source<T>(j.in[0], j, tile, s, args.d, to, full + 8 * i, helper);
+      if constexpr (H::kBack) fetch_source<T>(j.in[1], j, tile, s, args.d, to, full + 8 * i, helper);
+    };
+    auto bytes = [&](const HeadJob& j, int tile, const HeadTile& s) {
+      uint32_t b = bulk_bytes<T>(j.in[0], j, tile, s, args.d);
+      if constexpr (H::kBack) b += bulk_bytes<T>(j.in[1], j, tile, s, args.d);
+      return b;
+    };
+    for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+      if (taken >= kStages) tc::mbar_wait(empty + 8 * i, phase ^ 1u, args.status);
+      __syncwarp();
+      const uint32_t to = tc::smem_u32(stages) + i * args.stage_bytes;
+      float* const mine = angles + i * 2 * args.angles;
+      const bool second = !args.shared && tile >= args.job[0].tiles;
+      const int t0 = second ? 0 : tile, t1 = args.shared ? tile : tile - args.job[0].tiles;
+      if (helper == 0) {
+        // what was written here by other copies and read is behind; bulk copies come next
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        uint32_t b = 0;
+        if (!second) b += bytes(args.job[0], t0, head_tile(args.job[0], t0));
+        if (second || args.shared) b += bytes(args.job[1], t1, head_tile(args.job[1], t1));
+        if (lane == 0) tc::mbar_expect_tx(full + 8 * i, b);
+        __syncwarp();
+      }
+      if (!second) {
+        const HeadTile s = head_tile(args.job[0], t0);
+        fetch(args.job[0], t0, s, to);
+        if (args.pairs) angles_of(args, args.job[0], s, turns, mine, helper);
+      }
+      if (second || args.shared) {
+        const HeadTile s = head_tile(args.job[1], t1);
+        fetch(args.job[1], t1, s, to);
+        if (second && args.pairs) angles_of(args, args.job[1], s, turns, mine, helper);
+      }
+      copies_arrive(full + 8 * i);
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(full + 8 * i);
+      next_stage();
+    }
+    // after a give-up, let the copies in flight land before the block exits
+    for (uint32_t k = 1; k <= kStages && k <= taken; ++k)
+      tc::mbar_drain(full + 8 * ((taken - k) % kStages), ((taken - k) / kStages) & 1u);
+    return;
+  }
+  // ------------------------------------------------------------------ workers
+  H h(args);
+  bool first_done = false;
+  auto rows = [&](const HeadJob& j, int tile, const float* weight) {
+    const HeadTile s = head_tile(j, tile);
+    const unsigned char* const stage = stages + i * args.stage_bytes;
+    const float* const at = angles + i * 2 * args.angles;
+    T* const out = reinterpret_cast<T*>(j.out) + s.token * j.out_token + s.head * j.out_head;
+    const int count = s.tokens * j.head_block;
+    for (int r0 = warp * h.groups; r0 < count; r0 += kWorkers * h.groups) {
+      typename H::Row r;
+      const int k = r0 + h.group;
+      r.token = j.head_block == 1 ? k : (int)__umulhi((uint32_t)k, j.block_magic);
+      r.head = k - r.token * j.head_block;
+      r.live = r.token < s.tokens && r.head < s.heads;
+      if (!r.live) r.token = r.head = 0;
+      if constexpr (H::kBack) h.backward(j, stage, at, weight, s, r, out);
+      else h.forward(j, stage, at, weight, s, r, out);
+    }
+  };
+  float* const parts = reinterpret_cast<float*>(sm + lay.parts);
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    tc::mbar_wait(full + 8 * i, phase, args.status);
+    __syncwarp();
+    const bool second = !args.shared && tile >= args.job[0].tiles;
+    if (!second) rows(args.job[0], tile, w);
+    if (second || args.shared) {
+      if constexpr (H::kBack) {
+        if (!first_done) {
+          first_done = true;
+          h.write_part(parts, args.job[0].part ? args.job[0].part + (int64_t)blockIdx.x * args.d : nullptr);
+        }
+      }
+      rows(args.job[1], args.shared ? tile : tile - args.job[0].tiles, w + ((weights + 3) & ~3));
+    }
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + 8 * i);
+    next_stage();
+  }
+  if constexpr (H::kBack) {
+    if (!first_done) h.write_part(parts, args.job[0].part ? args.job[0].part + (int64_t)blockIdx.x * args.d : nullptr);
+    h.write_part(parts, args.job[1].part ? args.job[1].part + (int64_t)blockIdx.x * args.d : nullptr);
   }
 }
 
@@ -365,6 +606,11 @@ fvx_status check_view(const char* who, const char* name, const void* p, int64_t 
   return FVX_OK;
 }
 
+uint32_t magic_of(int v) { return (uint32_t)((((uint64_t)1 << 32) + v - 1) / v); }
+
+// Items that make 16 values of bf16 or 8 of fp32 per lane, however narrow its vectors.
+int items_of_lane(fvx_dtype dt, int vec) { return (dt == FVX_F32 ? 4 : 8) / vec; }
+
 // Results must not lie over each other.
 bool apart(int64_t n, int64_t heads, int64_t d, int64_t token, int64_t head) {
   if (n <= 1) return heads <= 1 || head >= d;
@@ -379,7 +625,7 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
   if (count < 1 || count > 2 || !t) return bad(who, "one or two tensors are taken");
   const int elem = dt == FVX_F32 ? 4 : 2;
   HeadArgs& a = c->a;
-  a.jobs = count;
+  a.job[0] = a.job[1] = {};
   a.d = d;
   a.inv_d = 1.0f / (float)d;
   a.sign = 1.0f;
@@ -434,12 +680,15 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
     if (r && (x.pos_token < 0 || (axes > 1 && x.pos_axis < 0))) return bad(who, "positions has a negative stride");
     HeadJob& j = a.job[i];
     j = {};
-    j.in = x.in;
-    j.in_token = x.in_token;
-    j.in_head = x.in_head;
-    j.x = x.x;
-    j.x_token = x.x_token;
-    j.x_head = x.x_head;
+    auto source = [&](const void* p, int64_t token, int64_t head) {
+      HeadSource s = {};
+      s.p = p;
+      s.token = x.n > 1 ? token : 0;
+      s.head = x.heads > 1 ? head : 0;
+      return s;
+    };
+    j.in[0] = source(x.in, x.in_token, x.in_head);
+    if (back) j.in[1] = source(x.x, x.x_token, x.x_head);
     j.out = x.out;
     j.out_token = x.out_token;
     j.out_head = x.out_head;
@@ -448,7 +697,7 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
     j.pos_token = x.pos_token;
     j.pos_axis = x.pos_axis;
     j.heads = (int)x.heads;
-    j.units = (int)x.n;  // times chunks, below
+    j.n = (int)x.n;
     c->head_rows += x.n * x.heads;
     if (x.n == 0) continue;
     view(x, x.in, x.in_token, x.in_head);
@@ -458,67 +707,228 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
   c->vec = vec;
   a.items_turned = a.pairs / vec;
   a.items = a.items_turned + (d - 2 * a.pairs + 2 * vec - 1) / (2 * vec);
+  const int per_lane = items_of_lane(dt, vec);
   a.lanes = 1;
-  while (a.lanes < 32 && a.lanes < a.items) a.lanes *= 2;
+  while (a.lanes * per_lane < a.items) a.lanes *= 2;  // 32 at most: 256 values in eights (fp32) or sixteens
+  a.axes = axes;
+  a.pair_magic = a.pairs > 1 ? magic_of(a.pairs) : 0;
   return FVX_OK;
 }
 
 // f<T, V, ITEMS, INTERLEAVED>() for the call's type, vectors and layout
 template <typename F>
 fvx_status by_shape(fvx_dtype dt, const Call& c, F&& f) {
-  auto layout = [&]<typename T, int V, int ITEMS>() -> fvx_status {
-    return c.interleaved ? f.template operator()<T, V, ITEMS, true>() : f.template operator()<T, V, ITEMS, false>();
+  auto layout = [&]<typename T, int V>() -> fvx_status {
+    constexpr int kItems = (sizeof(T) == 4 ? 4 : 8) / V;
+    return c.interleaved ? f.template operator()<T, V, kItems, true>() : f.template operator()<T, V, kItems, false>();
   };
-  const bool one = c.a.items <= c.a.lanes;
   if (dt == FVX_F32) {
-    if (c.vec == 4) return layout.template operator()<float, 4, 1>();
-    if (c.vec == 2) return one ? layout.template operator()<float, 2, 1>() : layout.template operator()<float, 2, 2>();
-    return one ? layout.template operator()<float, 1, 1>() : layout.template operator()<float, 1, 4>();
+    if (c.vec == 4) return layout.template operator()<float, 4>();
+    return c.vec == 2 ? layout.template operator()<float, 2>() : layout.template operator()<float, 1>();
   }
-  if (c.vec == 8) return layout.template operator()<__nv_bfloat16, 8, 1>();
-  if (c.vec == 4) return layout.template operator()<__nv_bfloat16, 4, 1>();
-  if (c.vec == 2) return one ? layout.template operator()<__nv_bfloat16, 2, 1>() : layout.template operator()<__nv_bfloat16, 2, 2>();
-  return one ? layout.template operator()<__nv_bfloat16, 1, 1>() : layout.template operator()<__nv_bfloat16, 1, 4>();
+  if (c.vec == 8) return layout.template operator()<__nv_bfloat16, 8>();
+  if (c.vec == 4) return layout.template operator()<__nv_bfloat16, 4>();
+  return c.vec == 2 ? layout.template operator()<__nv_bfloat16, 2>() : layout.template operator()<__nv_bfloat16, 1>();
 }
 
-// Cuts the tensors into units of up to hc heads; blocks for all of them, at most `most` if given.
-int cut(HeadArgs& a, int hc, int most) {
-  const int per_block = kThreads / a.lanes;
-  int64_t all = 0;
-  for (int i = 0; i < a.jobs; ++i) {
-    HeadJob& j = a.job[i];
-    j.chunks = (j.heads + hc - 1) / hc;
-    j.units *= j.chunks;
-    all += ((int64_t)j.units + per_block - 1) / per_block;
-  }
-  int at = 0;
-  for (int i = 0; i < a.jobs; ++i) {
-    HeadJob& j = a.job[i];
-    j.block0 = at;
-    int64_t b = ((int64_t)j.units + per_block - 1) / per_block;
-    if (most && all > most && b > 0) b = std::max<int64_t>(1, b * most / all);
-    at += (int)b;
-  }
-  return at;
+int64_t up(int64_t v, int64_t to) { return (v + to - 1) / to * to; }
+
+// Heads of a token that a quarter of their size at most lies between go in one piece.
+bool near(const HeadSource& s, int d) { return s.head <= d + d / 4; }
+// Tokens that follow one another likewise: their tiles are one piece.
+bool in_line(const HeadSource& s, const HeadJob& j, int d) {
+  return near(s, d) && (j.heads > 1 ? s.token == j.heads * s.head : s.token <= d + d / 4) && s.token >= d;
 }
 
-fvx_status run_heads(const char* name, fvx_dtype dt, Call& c, bool norm, cudaStream_t s) {
+// How a tile's part of a tensor is copied and lies in shared memory; its bytes.
+int64_t place_source(HeadSource& s, const HeadJob& j, int d, int elem) {
+  auto at16 = [&](int64_t values) { return values * elem % 16 == 0; };
+  const bool base16 = reinterpret_cast<uintptr_t>(s.p) % 16 == 0;
+  const int64_t slabs = ((int64_t)j.n + j.tokens - 1) / j.tokens;
+  s.whole = s.by_head = false;
+  s.bulk_tiles = 0;
+  if (!near(s, d)) {
+    s.by_head = true;
+    s.s_head = (int)up(d + 1, 16 / elem);
+    s.s_token = s.s_head * j.head_block;
+    if (base16 && at16(s.token) && at16(s.head) && at16(d)) s.bulk_tiles = j.tiles;
+    return (int64_t)j.tokens * s.s_token * elem;
+  }
+  s.s_head = (int)s.head;
+  const int64_t chunk = (j.head_block - 1) * s.head + d;
+  if (j.head_blocks == 1 && in_line(s, j, d) && base16 && at16(j.tokens * s.token)) {
+    s.whole = true;
+    s.s_token = (int)s.token;
+    // a piece must not reach past the last head's end
+    s.bulk_tiles = (int)(((j.n - 1) * s.token + chunk) / (j.tokens * s.token));
+    return (int64_t)j.tokens * s.s_token * elem;
+  }
+  s.s_token = (int)up(chunk + 1, 16 / elem);
+  if (base16 && at16(s.token) && (j.head_blocks == 1 || at16(j.head_block * s.head))) {
+    // Pieces end at multiples of 16 bytes: where the last head of a token does
+    // not, that is in the gap to the next token, and past the last one's end.
+    const int64_t last = ((j.heads - 1) % j.head_block) * s.head + d;
+    const bool gaps = s.token >= (j.heads - 1) * s.head + d;
+    s.bulk_tiles = (int)((at16(last) ? slabs : gaps ? (j.n - 1) / j.tokens : 0) * j.head_blocks);
+  }
+  return (int64_t)j.tokens * s.s_token * elem;
+}
+// Whether offsets of results within a tile fit 32 bits; sets the strides they are computed from.
+bool results_near(HeadJob& j) {
+  const int64_t token = j.tokens > 1 ? j.out_token : 0, head = j.head_block > 1 ? j.out_head : 0;
+  j.out_token32 = (int)token;
+  j.out_head32 = (int)head;
+  constexpr int64_t kMost = (int64_t)1 << 30;
+  return token < kMost && head < kMost && token * j.tokens + head * j.head_block < kMost;
+}
+
+// Cuts a tensor into tiles of whole tokens, or (tokens of more than `room` bytes)
+// of heads of one token.
+void cut(HeadJob& j, int tokens, int heads) {
+  j.tokens = tokens;
+  j.head_block = heads;
+  j.head_blocks = (j.heads + heads - 1) / heads;
+  j.tiles = (int)(((int64_t)j.n + tokens - 1) / tokens * j.head_blocks);
+  j.block_magic = heads > 1 ? magic_of(heads) : 0;
+}
+
+// Tokens of a stage: as many as fit, fewer where not every
+// multiprocessor would get a stage; of those, the number whose heads fill the
+// workers' last turn best.
+int stage_tokens(const HeadArgs& a, const HeadJob* jobs, int count, int64_t fitting, int line, int sms) {
+  const int n = std::max(jobs[0].n, count > 1 ? jobs[1].n : 0), turn = kWorkers * (32 / a.lanes);
+  const int64_t most = std::max<int64_t>(1, std::min<int64_t>({fitting, ((int64_t)n + sms - 1) / sms, 2048}));
+  int best = (int)most;
+  double best_used = 0.0;
+  for (int t = (int)most; t >= 1 && t * 8 >= most * 5; --t) {
+    double used = 0.0;
+    for (int k = 0; k < count; ++k) {
+      const int64_t rows = (int64_t)t * jobs[k].heads;
+      used += (double)rows / (double)up(rows, turn) / count;
+    }
+    used += t % line == 0 ? 1.0 : 0.0;
+    if (used > best_used + 0.02) {
+      best_used = used;
+      best = t;
+    }
+  }
+  return best;
+}
+
+template <typename T, int V, int ITEMS, bool IL, int OP, bool FULL>
+fvx_status launch_heads(const char* name, HeadArgs& a, int jobs, const fvx_head_tensor_t* t, DwArgs* dw, cudaStream_t s,
+                        Scratch* scr) {
+  using H = Heads<T, V, ITEMS, IL, OP, FULL>;
+  constexpr int kElem = (int)sizeof(T), kSources = H::kBack ? 2 : 1;
+  int sms = 0;
+  FVX_TRY(device_sm_count(&sms));
+  a.status = device_status_word();
+  if (!a.status) {
+    set_error("%s: could not set up the device status word", t_entry);
+    return FVX_ERR_CUDA;
+  }
+  const int weights = H::kNorm ? a.lanes * ITEMS * 2 * V : 0;
+  a.angles = a.stage_bytes = 0;
+  const HeadLayout fixed(a, weights, H::kBack);
+  const int64_t room = (kMostSmem - fixed.bytes - 256) / kStages - 512;
+  // bytes of a token (its heads from global memory, or one by one) and of its angles
+  auto token_bytes = [&](const HeadJob& j, int heads) {
+    int64_t b = 0;
+    for (int k = 0; k < kSources; ++k)
+      b += (near(j.in[k], a.d) ? heads * std::max<int64_t>(j.in[k].head, a.d) + (heads == 1 ? a.d / 4 : 0) + 16 / kElem
+                               : (int64_t)heads * (a.d + 16 / kElem)) * kElem;
+    return b;
+  };
+  auto line_of = [&](const HeadJob& j) {
+    int line = 1;
+    for (int k = 0; k < kSources; ++k)
+      if (in_line(j.in[k], j, a.d))
+        while (line * j.in[k].token * kElem % 16) line *= 2;
+    return line;
+  };
+  // Queries and keys of the same tokens share a stage and its angles (the
+  // backward pass keeps one tensor's dw in registers at a time).
+  a.shared = OP != kNormRotateBack && jobs == 2 && a.job[0].n == a.job[1].n && a.job[0].pos == a.job[1].pos &&
+             a.job[0].pos_token == a.job[1].pos_token && a.job[0].pos_axis == a.job[1].pos_axis && a.job[0].n > 0;
+  const int angle_bytes = 8 * a.pairs;
+  if (a.shared) {
+    const int64_t bytes = token_bytes(a.job[0], a.job[0].heads) + token_bytes(a.job[1], a.job[1].heads) + angle_bytes;
+    if (bytes > room) a.shared = 0;
+    else {
+      const int tokens = stage_tokens(a, a.job, 2, room / bytes, std::max(line_of(a.job[0]), line_of(a.job[1])), sms);
+      for (int i = 0; i < 2; ++i) cut(a.job[i], tokens, a.job[i].heads);
+      if (!results_near(a.job[0]) || !results_near(a.job[1])) a.shared = 0;
+    }
+  }
+  // the angles' part of a stage: what the tensor with the smaller tokens needs
+  int64_t angle_room = 0;
+  for (int i = 0; i < jobs && !a.shared; ++i)
+    if (a.job[i].n > 0)
+      angle_room = std::max(angle_room, room * angle_bytes / (token_bytes(a.job[i], a.job[i].heads) + angle_bytes));
+  angle_room = std::max<int64_t>(angle_room, angle_bytes);
+  for (int i = 0; i < jobs && !a.shared; ++i) {
+    HeadJob& j = a.job[i];
+    if (j.n == 0) continue;
+    const int64_t bytes = token_bytes(j, j.heads);
+    if (bytes <= room - angle_room) {
+      const int64_t most = (room - angle_room) / bytes;
+      cut(j, stage_tokens(a, &j, 1, angle_bytes ? std::min(most, angle_room / angle_bytes) : most, line_of(j), sms), j.heads);
+    } else {
+      const int turn = kWorkers * (32 / a.lanes);
+      int64_t heads = (room - angle_room) / token_bytes(j, 1);
+      if (heads > turn) heads -= heads % turn;
+      cut(j, 1, (int)std::max<int64_t>(1, std::min<int64_t>(heads, j.heads)));
+    }
+    if (!results_near(j)) {  // tokens or heads 2^30 values apart: a head at a time
+      cut(j, 1, 1);
+      results_near(j);
+    }
+  }
+  for (int i = 0; i < jobs; ++i) {
+    HeadJob& j = a.job[i];
+    if (j.n == 0) continue;
+    int64_t at = a.shared && i == 1 ? a.stage_bytes : 0;
+    for (int k = 0; k < kSources; ++k) {
+      j.in[k].at = (int)at;
+      at += up(place_source(j.in[k], j, a.d, kElem), 128);
+    }
+    a.stage_bytes = (int)std::max<int64_t>(a.stage_bytes, at);
+    a.angles = std::max(a.angles, (j.tokens * a.pairs + 3) & ~3);
+  }
+  const HeadLayout lay(a, weights, H::kBack);
+  if (lay.bytes > kMostSmem) {
+    set_error("%s: a stage needs %d bytes of shared memory", t_entry, lay.bytes);
+    return FVX_ERR_INVALID_ARG;
+  }
+  const int64_t tiles = a.shared ? a.job[0].tiles : (int64_t)a.job[0].tiles + a.job[1].tiles;
+  const int blocks = (int)std::min<int64_t>(tiles, sms);
+  for (int i = 0; i < jobs && dw; ++i) {
+    if (t[i].n == 0 || !t[i].dweight) continue;
+    dw->parts[i] = blocks;
+    dw->dw[i] = t[i].dweight;
+    if (!(a.job[i].part = scr->get<float>((size_t)blocks * a.d))) return FVX_ERR_ALLOC;
+    dw->part[i] = a.job[i].part;
+  }
+  static std::atomic<uint64_t> allowed{0};
+  FVX_TRY(allow_smem((const void*)k_heads<T, V, ITEMS, IL, OP, FULL>, kMostSmem, allowed));
+  LaunchScope ls(name, s);
+  k_heads<T, V, ITEMS, IL, OP, FULL><<<blocks, kHeadThreads, lay.bytes, s>>>(a);
+  return check_launch(name);
+}
+
+fvx_status run_heads(const char* name, fvx_dtype dt, Call& c, HeadOp op, int jobs, const fvx_head_tensor_t* t, DwArgs* dw,
+                     cudaStream_t s, Scratch* scr) {
   if (c.head_rows == 0) return FVX_OK;
   return by_shape(dt, c, [&]<typename T, int V, int ITEMS, bool IL>() -> fvx_status {
-    int sms = 0;
-    FVX_TRY(device_sm_count(&sms));
-    const bool many = c.head_rows * c.a.lanes >= (int64_t)sms * 2048 * 2;
-    constexpr int kMany = ITEMS == 1 ? 2 : 1;
-    const int blocks = cut(c.a, many ? kMany : 1, 0);
-    LaunchScope ls(name, s);
-    if (norm) {
-      if (many) k_heads<T, V, ITEMS, IL, true, kMany><<<blocks, kThreads, 0, s>>>(c.a);
-      else k_heads<T, V, ITEMS, IL, true, 1><<<blocks, kThreads, 0, s>>>(c.a);
-    } else {
-      if (many) k_heads<T, V, ITEMS, IL, false, kMany><<<blocks, kThreads, 0, s>>>(c.a);
-      else k_heads<T, V, ITEMS, IL, false, 1><<<blocks, kThreads, 0, s>>>(c.a);
-    }
-    return check_launch(name);
+    auto go = [&]<bool FULL>() -> fvx_status {
+      if (op == kRotate) return launch_heads<T, V, ITEMS, IL, kRotate, FULL>(name, c.a, jobs, t, dw, s, scr);
+      if (op == kNormRotate) return launch_heads<T, V, ITEMS, IL, kNormRotate, FULL>(name, c.a, jobs, t, dw, s, scr);
+      return launch_heads<T, V, ITEMS, IL, kNormRotateBack, FULL>(name, c.a, jobs, t, dw, s, scr);
+    };
+    // heads of 16, 32, 64, 128 or 256 values: no lane asks what it has
+    if constexpr (V * sizeof(T) == 16)
+      if (c.a.d == c.a.lanes * ITEMS * 2 * V) return go.template operator()<true>();
+    return go.template operator()<false>();
   });
 }
 
@@ -569,7 +979,7 @@ fvx_status fvx_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* t,
   if (!rotary) return bad(who, "NULL rotary");
   FVX_TRY(prepare(who, dt, d, t, count, rotary, false, &c));
   c.a.sign = transposed ? -1.0f : 1.0f;
-  return run_heads("rotate_heads", dt, c, false, (cudaStream_t)stream);
+  return run_heads("rotate_heads", dt, c, kRotate, count, t, nullptr, (cudaStream_t)stream, nullptr);
 }
 
 fvx_status fvx_norm_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* t, int32_t count,
@@ -580,7 +990,7 @@ fvx_status fvx_norm_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_
   if (!(eps >= 0.0f)) return bad(who, "eps must not be negative");
   FVX_TRY(prepare(who, dt, d, t, count, rotary, false, &c));
   c.a.eps = eps;
-  return run_heads("norm_rotate_heads", dt, c, true, (cudaStream_t)stream);
+  return run_heads("norm_rotate_heads", dt, c, kNormRotate, count, t, nullptr, (cudaStream_t)stream, nullptr);
 }
 
 fvx_status fvx_norm_rotate_heads_backward(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* t, int32_t count,
@@ -602,22 +1012,7 @@ fvx_status fvx_norm_rotate_heads_backward(fvx_dtype dt, int32_t d, const fvx_hea
   Scratch scr(s);
   DwArgs w = {};
   w.d = d;
-  FVX_TRY(by_shape(dt, c, [&]<typename T, int V, int ITEMS, bool IL>() -> fvx_status {
-    int sms = 0;
-    FVX_TRY(device_sm_count(&sms));
-    const int blocks = cut(c.a, 1, 4 * sms);
-    for (int i = 0; i < count; ++i) {
-      if (t[i].n == 0 || !t[i].dweight) continue;
-      w.parts[i] = (i + 1 < count ? c.a.job[1].block0 : blocks) - c.a.job[i].block0;
-      w.dw[i] = t[i].dweight;
-      if (!(c.a.job[i].part = scr.get<float>((size_t)w.parts[i] * d))) return FVX_ERR_ALLOC;
-      w.part[i] = c.a.job[i].part;
-    }
-    const size_t smem = (size_t)(kThreads / c.a.lanes) * d * 4;  // a lane holds 16 values at most: 16 KB (passing ones 32)
-    LaunchScope ls("norm_rotate_heads_bwd", s);
-    k_heads_bwd<T, V, ITEMS, IL, 1><<<blocks, kThreads, smem, s>>>(c.a);
-    return check_launch("norm_rotate_heads_bwd");
-  }));
+  FVX_TRY(run_heads("norm_rotate_heads_bwd", dt, c, kNormRotateBack, count, t, &w, s, &scr));
   if (!sums) return FVX_OK;
   LaunchScope ls("norm_rotate_heads_dw", s);
   k_heads_dw<<<dim3((unsigned)((d + 31) / 32), (unsigned)count), 1024, 0, s>>>(w);
