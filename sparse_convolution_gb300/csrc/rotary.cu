@@ -25,7 +25,7 @@ constexpr int kMaxPairs = kMaxHead / 2;
 
 // A block's warps: those that work on the heads, and those that fetch the next
 // stages' tensors and compute their angles.
-constexpr int kWorkers = 16, kHelpers = 4, kHeadThreads = 32 * (kWorkers + kHelpers);
+constexpr int kWorkers = 16, kHelpers = 8, kHeadThreads = 32 * (kWorkers + kHelpers);
 constexpr int kStages = 3;
 constexpr int kMostSmem = 227 * 1024;
 
@@ -59,7 +59,7 @@ struct HeadArgs {
   int shared;  // a stage holds the same tokens of both tensors; else tiles of the first, then of the second
   int d, pairs, axes, axis1, axis2;  // pairs from axis1 (axis2) on belong to the second (third) axis
   int items, items_turned, lanes;    // a head's items: of pairs, of values that pass; lanes that share a head
-  uint32_t pair_magic;               // 2^32 / pairs, rounded up
+  int pair_lanes;                    // helper threads of a token's angles: pairs, to the next power of two
   int angles, stage_bytes;           // of a stage: angles, bytes of the tensors
   float magnitude, sign, eps, inv_d;
 };
@@ -170,17 +170,27 @@ __device__ __forceinline__ void fetch_source(const HeadSource& src, const HeadJo
     for (int k = lane; k < words; k += 32) copy4((dst & ~3u) + 4 * k, reinterpret_cast<const void*>((from & ~(uintptr_t)3) + 4 * k));
   }
 }
-// Cosines and sines of a tile's tokens, each computed once for all its heads.
+// Cosines and sines of a tile's tokens, each computed once for all its heads.  A
+// thread keeps its pair; four tokens' positions are under way at once.
 __device__ __forceinline__ void angles_of(const HeadArgs& a, const HeadJob& j, const HeadTile& s, const uint64_t* turns,
-                                          float* angles, int helper) {
-#pragma unroll 4
-  for (int i = helper * 32 + (threadIdx.x & 31); i < s.tokens * a.pairs; i += 32 * kHelpers) {
-    const int t = a.pairs == 1 ? i : (int)__umulhi((uint32_t)i, a.pair_magic), p = i - t * a.pairs;
-    const int axis = (p >= a.axis1) + (p >= a.axis2);
-    float sn, cs;
-    sincos_turn(turn_of(turns[p], __ldg(j.pos + (s.token + t) * j.pos_token + axis * j.pos_axis)), sn, cs);
-    angles[i] = cs * a.magnitude;
-    angles[a.angles + i] = sn * a.magnitude * a.sign;
+                                          float* angles, int thread) {
+  const int p = thread & (a.pair_lanes - 1), apart = 32 * kHelpers / a.pair_lanes;
+  if (p >= a.pairs) return;
+  const uint64_t step = turns[p];
+  const int32_t* pos = j.pos + ((p >= a.axis1) + (p >= a.axis2)) * j.pos_axis + (int64_t)s.token * j.pos_token;
+  const float ms = a.magnitude * a.sign;
+  for (int t = thread / a.pair_lanes; t < s.tokens; t += 4 * apart) {
+    int at[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) at[k] = t + k * apart < s.tokens ? __ldg(pos + (t + k * apart) * j.pos_token) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (t + k * apart >= s.tokens) break;
+      float sn, cs;
+      sincos_turn(turn_of(step, at[k]), sn, cs);
+      angles[(t + k * apart) * a.pairs + p] = cs * a.magnitude;
+      angles[a.angles + (t + k * apart) * a.pairs + p] = sn * ms;
+    }
   }
 }
 
@@ -455,8 +465,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
       phase ^= 1u;
     }
   };
+  // Registers: 768 threads at 80 are launched, 61,440: 512 at 96 and 256 at 48.
   if (warp >= kWorkers) {
     // ---------------------------------------------------------------- helpers
+    tc::setmaxnreg_dec<48>();
     const int helper = warp - kWorkers, lane = threadIdx.x & 31;
     auto fetch = [&](const HeadJob& j, int tile, const HeadTile& s, uint32_t to) {
       fetch_source<T>(j.in[0], j, tile, s, args.d, to, full + 8 * i, helper);
@@ -486,12 +498,12 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
       if (!second) {
         const HeadTile s = head_tile(args.job[0], t0);
         fetch(args.job[0], t0, s, to);
-        if (args.pairs) angles_of(args, args.job[0], s, turns, mine, helper);
+        if (args.pairs) angles_of(args, args.job[0], s, turns, mine, threadIdx.x - 32 * kWorkers);
       }
       if (second || args.shared) {
         const HeadTile s = head_tile(args.job[1], t1);
         fetch(args.job[1], t1, s, to);
-        if (second && args.pairs) angles_of(args, args.job[1], s, turns, mine, helper);
+        if (second && args.pairs) angles_of(args, args.job[1], s, turns, mine, threadIdx.x - 32 * kWorkers);
       }
       copies_arrive(full + 8 * i);
       __syncwarp();
@@ -504,6 +516,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
     return;
   }
   // ------------------------------------------------------------------ workers
+  tc::setmaxnreg_inc<96>();
   H h(args);
   bool first_done = false;
   auto rows = [&](const HeadJob& j, int tile, const float* weight) {
@@ -711,7 +724,8 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
   a.lanes = 1;
   while (a.lanes * per_lane < a.items) a.lanes *= 2;  // 32 at most: 256 values in eights (fp32) or sixteens
   a.axes = axes;
-  a.pair_magic = a.pairs > 1 ? magic_of(a.pairs) : 0;
+  a.pair_lanes = 1;
+  while (a.pair_lanes < a.pairs) a.pair_lanes *= 2;
   return FVX_OK;
 }
 
