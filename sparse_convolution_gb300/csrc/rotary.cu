@@ -59,6 +59,7 @@ struct HeadArgs {
   int shared;  // a stage holds the same tokens of both tensors; else tiles of the first, then of the second
   int d, pairs, axes, axis1, axis2;  // pairs from axis1 (axis2) on belong to the second (third) axis
   int items, items_turned, lanes;    // a head's items: of pairs, of values that pass; lanes that share a head
+  int fours;                         // the angles' order: see angles_of
   int pair_lanes;                    // helper threads of a token's angles: pairs, to the next power of two
   int angles, stage_bytes;           // of a stage: angles, bytes of the tensors
   float magnitude, sign, eps, inv_d;
@@ -179,24 +180,37 @@ __device__ __forceinline__ void angles_of(const HeadArgs& a, const HeadJob& j, c
   const uint64_t step = turns[p];
   const int32_t* pos = j.pos + ((p >= a.axis1) + (p >= a.axis2)) * j.pos_axis + (int64_t)s.token * j.pos_token;
   const float ms = a.magnitude * a.sign;
-  for (int t = thread / a.pair_lanes; t < s.tokens; t += 4 * apart) {
-    int at[4];
+  // halves in vectors of eight: the first four pairs of every eight, then the others, as the lanes read them
+  const int place = a.fours ? (p >> 2 & 1) * (a.pairs >> 1) + (p >> 3 << 2) + (p & 3) : p;
+  constexpr int kAtOnce = 4;
+  int t = thread / a.pair_lanes, at[kAtOnce];
+  auto ahead = [&](int from) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) at[k] = t + k * apart < s.tokens ? __ldg(pos + (t + k * apart) * j.pos_token) : 0;
+    for (int k = 0; k < kAtOnce; ++k)
+      at[k] = from + k * apart < s.tokens ? __ldg(pos + (from + k * apart) * j.pos_token) : 0;
+  };
+  ahead(t);
+  while (t < s.tokens) {
+    int now[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (t + k * apart >= s.tokens) break;
+    for (int k = 0; k < kAtOnce; ++k) now[k] = at[k];
+    ahead(t + kAtOnce * apart);
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k, t += apart) {
       float sn, cs;
-      sincos_turn(turn_of(step, at[k]), sn, cs);
-      angles[(t + k * apart) * a.pairs + p] = cs * a.magnitude;
-      angles[a.angles + (t + k * apart) * a.pairs + p] = sn * ms;
+      sincos_turn(turn_of(step, now[k]), sn, cs);
+      if (t < s.tokens) {
+        angles[t * a.pairs + place] = cs * a.magnitude;
+        angles[a.angles + t * a.pairs + place] = sn * ms;
+      }
     }
   }
 }
 
-// A lane holds ITEMS items of a head, each two vectors of V values in memory:
-// for V pairs their first and second partners (u and v), the latter P further on
-// (halves) or interleaved with them; or up to 2V values that pass, split alike.
+// A lane holds ITEMS items of a head, each two vectors of V values in memory, P
+// apart: the first and second partners (u and v) of V pairs (halves), or V / 2
+// interleaved pairs each; or up to 2V values that pass, split alike.  So a
+// group's lanes always read and write side by side.
 // Pairs of fp32 values are computed on two at a time.  FULL: every lane has all
 // its items.
 template <typename T, int V, int ITEMS, bool INTERLEAVED, int OP, bool FULL>
@@ -232,14 +246,20 @@ struct Heads {
   // where an item's two vectors start in the head
   static __device__ __forceinline__ void place(const HeadArgs& a, int item, int& first, int& second) {
     const bool turned = item < a.items_turned;
-    first = turned ? (INTERLEAVED ? 2 : 1) * item * V : 2 * a.pairs + (item - a.items_turned) * 2 * V;
-    second = turned && !INTERLEAVED ? first + a.pairs : first + V;
+    if (INTERLEAVED && V == 1 && turned) {
+      first = 2 * item;
+      second = first + 1;
+      return;
+    }
+    first = turned ? item * V : 2 * a.pairs + (item - a.items_turned) * V;
+    second = first + (turned ? a.pairs : (a.items - a.items_turned) * V);
   }
   // the channel of value k of an item's side (0: u, 1: v); d or more: none
   static __device__ __forceinline__ int channel(const HeadArgs& a, int item, int side, int k) {
     int first, second;
     place(a, item, first, second);
-    return INTERLEAVED ? first + 2 * k + side : (side ? second : first) + k;
+    if (!INTERLEAVED || V == 1) return (side ? second : first) + k;
+    return (k < V / 2 ? first + 2 * k : second + 2 * k - V) + side;
   }
   // sum over the lanes that share a head
   __device__ __forceinline__ float head_sum(float v) const {
@@ -297,22 +317,31 @@ struct Heads {
       if (r.live && has_b[i]) *reinterpret_cast<Pack<T, V>*>(out + second[i]) = y;
     }
   }
-  static __device__ __forceinline__ void vector(const float* p, E (&e)[N]) {
+  // V values in shared memory, in pieces of W that are `apart` apart
+  template <int W>
+  static __device__ __forceinline__ void vector(const float* p, int apart, E (&e)[N]) {
     float f[V];
-    const Pack<float, (V > 4 ? 4 : V)>* q = reinterpret_cast<const Pack<float, (V > 4 ? 4 : V)>*>(p);
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = q[k / 4].v[k % 4];
+    for (int k = 0; k < V; ++k) f[k] = reinterpret_cast<const Pack<float, W>*>(p + k / W * apart)->v[k % W];
     to_pairs<V>(f, e);
+  }
+  static constexpr int kWide = V > 4 ? 4 : V;
+  static __device__ __forceinline__ int weight_place(const HeadArgs& a, int item, int side, int k) {
+    return ((side * (V / kWide) + k / kWide) * a.lanes * ITEMS + item) * kWide + k % kWide;
+  }
+  __device__ __forceinline__ void weights(const float* w, int i, int side, E (&e)[N]) const {
+    vector<kWide>(w + weight_place(a, lane + i * a.lanes, side, 0), a.lanes * ITEMS * kWide, e);
   }
   __device__ __forceinline__ void rotate(const float* angles, const Row& r, E (&e)[ITEMS][2][N]) const {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int item = lane + i * a.lanes;
       if (item < a.items_turned) {
-        const float* p = angles + r.token * a.pairs + item * V;
+        constexpr int W = V == 8 || (INTERLEAVED && V > 1) ? V / 2 : V;
+        const float* p = angles + r.token * a.pairs + item * W;
         E c[N], s[N];
-        vector(p, c);
-        vector(p + a.angles, s);
+        vector<W>(p, a.pairs / 2, c);
+        vector<W>(p + a.angles, a.pairs / 2, s);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const E u = e[i][0][k], v = e[i][1][k];
@@ -338,7 +367,7 @@ struct Heads {
 #pragma unroll
         for (int side = 0; side < 2; ++side) {
           E wt[N];
-          vector(w + ((lane + i * a.lanes) * 2 + side) * V, wt);
+          weights(w, i, side, wt);
 #pragma unroll
           for (int k = 0; k < N; ++k) e[i][side][k] = e_mul(e_mul(e[i][side][k], rstd), wt[k]);
         }
@@ -357,7 +386,7 @@ struct Heads {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         E wt[N];
-        vector(w + ((lane + i * a.lanes) * 2 + side) * V, wt);
+        weights(w, i, side, wt);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           xx = e_fma(x[i][side][k], x[i][side][k], xx);
@@ -373,7 +402,7 @@ struct Heads {
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
         E wt[N];
-        vector(w + ((lane + i * a.lanes) * 2 + side) * V, wt);
+        weights(w, i, side, wt);
 #pragma unroll
         for (int k = 0; k < N; ++k) {
           const E gk = g[i][side][k], xk = x[i][side][k];
@@ -452,9 +481,9 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
   if constexpr (H::kNorm)
     for (int i = threadIdx.x; i < 2 * weights; i += kHeadThreads) {
       const int seg = i >= weights, k = i - seg * weights;
-      const int c = H::channel(args, k / (2 * V), (k / V) & 1, k % V);
+      const int item = k / (2 * V), side = k / V & 1, c = H::channel(args, item, side, k % V);
       const float* from = seg ? args.job[1].w : args.job[0].w;
-      w[seg * ((weights + 3) & ~3) + k] = from && c < args.d ? __ldg(from + c) : 1.0f;
+      w[seg * ((weights + 3) & ~3) + H::weight_place(args, item, side, k % V)] = from && c < args.d ? __ldg(from + c) : 1.0f;
     }
   __syncthreads();
   uint32_t i = 0, phase = 0, taken = 0;
@@ -724,6 +753,7 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
   a.lanes = 1;
   while (a.lanes * per_lane < a.items) a.lanes *= 2;  // 32 at most: 256 values in eights (fp32) or sixteens
   a.axes = axes;
+  a.fours = vec == 8 && !c->interleaved;
   a.pair_lanes = 1;
   while (a.pair_lanes < a.pairs) a.pair_lanes *= 2;
   return FVX_OK;
