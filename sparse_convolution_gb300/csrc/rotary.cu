@@ -106,6 +106,33 @@ __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {  // when this thread's copies have landed
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
+// tc::mbar_wait for the long waits of a kernel that memory bounds: its polls
+// sleep up to a microsecond, or those of the warps that wait take the issue
+// slots of the warps that work (150 of 300 instructions per 512 values).
+__device__ __forceinline__ uint32_t stage_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(1000u)
+      : "memory");
+  return ok;
+}
+__device__ __forceinline__ void stage_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
+  if (stage_try(bar, parity)) return;
+  unsigned long long t0 = 0;
+  for (uint32_t it = 1;; ++it) {
+    __nanosleep(64);
+    if (stage_try(bar, parity)) return;
+    if ((it & 255u) == 0u) {
+      if (t0 == 0) t0 = tc::globaltimer();
+      if (tc::globaltimer() - t0 > tc::kWaitNs || *(volatile uint32_t*)status != 0u) {
+        report_device_error(status, DEV_TIMEOUT);
+        return;
+      }
+    }
+  }
+}
 __device__ __forceinline__ void workers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWorkers) : "memory"); }
 
 // A tile: its first token and head, and how many of each exist.
@@ -151,10 +178,9 @@ __device__ __forceinline__ void fetch_source(const HeadSource& src, const HeadJo
   const int per_token = src.by_head ? s.heads : 1;
   to += src.at;
   if (tile < src.bulk_tiles) {
-    if (helper) return;
     const int pieces = src.whole ? 1 : s.tokens * per_token;
     const uint32_t bytes = piece_bytes<T>(src, j, s, d);
-    for (int i = lane; i < pieces; i += 32) {
+    for (int i = helper + kHelpers * lane; i < pieces; i += 32 * kHelpers) {
       const int t = per_token == 1 ? i : i / per_token, h = i - t * per_token;
       tc::bulk_load(to + (t * src.s_token + h * src.s_head) * (int)sizeof(T),
                     base + (s.token + t) * src.token + (s.head + h) * src.head, bytes, bar);
@@ -212,7 +238,7 @@ __device__ __forceinline__ void angles_of(const HeadArgs& a, const HeadJob& j, c
 // interleaved pairs each; or up to 2V values that pass, split alike.  So a
 // group's lanes always read and write side by side.
 // Pairs of fp32 values are computed on two at a time.  FULL: every lane has all
-// its items.
+// its items, and all turn.
 template <typename T, int V, int ITEMS, bool INTERLEAVED, int OP, bool FULL>
 struct Heads {
   static constexpr bool kNorm = OP != kRotate, kBack = OP == kNormRotateBack;
@@ -261,14 +287,13 @@ struct Heads {
     if (!INTERLEAVED || V == 1) return (side ? second : first) + k;
     return (k < V / 2 ? first + 2 * k : second + 2 * k - V) + side;
   }
-  // sum over the lanes that share a head
-  __device__ __forceinline__ float head_sum(float v) const {
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      if (o >= a.lanes) break;
+  // sums over the lanes that share a head
+  __device__ __forceinline__ void head_sums(float& v, float& w) const {
+#pragma unroll 1
+    for (int o = a.lanes >> 1; o > 0; o >>= 1) {
       v += __shfl_xor_sync(0xffffffffu, v, o);
+      if constexpr (kBack) w += __shfl_xor_sync(0xffffffffu, w, o);
     }
-    return v;
   }
 
   // A group's head within the tile.  Groups without one take the tile's first and store nothing.
@@ -276,20 +301,39 @@ struct Heads {
     int token, head;
     bool live;
   };
+  struct In {
+    Pack<T, V> x[ITEMS], y[ITEMS];
+  };
   __device__ __forceinline__ void read(const HeadSource& src, const unsigned char* stage, const HeadTile& s, const Row& r,
-                                       E (&e)[ITEMS][2][N]) const {
+                                       In& in) const {
     int off = r.token * src.s_token + r.head * src.s_head;
     if constexpr (V == 1) off += odd_start<T>(src, s.token + r.token, s.head + (src.by_head ? r.head : 0));
     const T* p = reinterpret_cast<const T*>(stage + src.at) + off;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      const Pack<T, V> x = has_a[i] ? raw_vec<T, V>(p + at[i]) : no_vec<T, V>(),
-                       y = has_b[i] ? raw_vec<T, V>(p + second[i]) : no_vec<T, V>();
-      float f[2 * V], u[V], v[V];
+      in.x[i] = has_a[i] ? raw_vec<T, V>(p + at[i]) : no_vec<T, V>();
+      in.y[i] = has_b[i] ? raw_vec<T, V>(p + second[i]) : no_vec<T, V>();
+    }
+  }
+  static __device__ __forceinline__ void split(const In& in, E (&e)[ITEMS][2][N]) {
 #pragma unroll
-      for (int k = 0; k < V; ++k) {
-        f[k] = Elem<T>::get(x.v[k]);
-        f[V + k] = Elem<T>::get(y.v[k]);
+    for (int i = 0; i < ITEMS; ++i) {
+      float f[2 * V], u[V], v[V];
+      if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t words[V];  // two values each
+        memcpy(words, &in.x[i], 2 * V);
+        memcpy(words + V / 2, &in.y[i], 2 * V);
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          f[2 * k] = __uint_as_float(words[k] << 16);
+          f[2 * k + 1] = __uint_as_float(words[k] & 0xffff0000u);
+        }
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          f[k] = Elem<T>::get(in.x[i].v[k]);
+          f[V + k] = Elem<T>::get(in.y[i].v[k]);
+        }
       }
 #pragma unroll
       for (int k = 0; k < V; ++k) {
@@ -300,6 +344,21 @@ struct Heads {
       to_pairs<V>(v, e[i][1]);
     }
   }
+  // Keeps the compiler from holding the widened values instead: they are twice the registers.
+  static __device__ __forceinline__ void keep_narrow(In& in) {
+    if constexpr (sizeof(T) == 2 && V > 1) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        uint32_t words[V];
+        memcpy(words, &in.x[i], 2 * V);
+        memcpy(words + V / 2, &in.y[i], 2 * V);
+#pragma unroll
+        for (int k = 0; k < V; ++k) asm volatile("" : "+r"(words[k]));
+        memcpy(&in.x[i], words, 2 * V);
+        memcpy(&in.y[i], words + V / 2, 2 * V);
+      }
+    }
+  }
   __device__ __forceinline__ void store(const HeadJob& j, T* out, const Row& r, const E (&e)[ITEMS][2][N]) const {
     out += r.token * j.out_token32 + r.head * j.out_head32;
 #pragma unroll
@@ -308,10 +367,21 @@ struct Heads {
       from_pairs<V>(e[i][0], u);
       from_pairs<V>(e[i][1], v);
       Pack<T, V> x, y;
+      float f[2 * V];
 #pragma unroll
-      for (int k = 0; k < 2 * V; ++k) {
-        const float f = INTERLEAVED ? (k & 1 ? v[k / 2] : u[k / 2]) : k < V ? u[k % V] : v[k % V];
-        (k < V ? x : y).v[k % V] = Elem<T>::put(f);
+      for (int k = 0; k < 2 * V; ++k) f[k] = INTERLEAVED ? (k & 1 ? v[k / 2] : u[k / 2]) : k < V ? u[k % V] : v[k % V];
+      if constexpr (sizeof(T) == 2 && V > 1) {
+        uint32_t words[V];
+#pragma unroll
+        for (int k = 0; k < V; ++k) words[k] = tc::pack_bf16(f[2 * k], f[2 * k + 1]);
+        memcpy(&x, words, 2 * V);
+        memcpy(&y, words + V / 2, 2 * V);
+      } else {
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+          x.v[k] = Elem<T>::put(f[k]);
+          y.v[k] = Elem<T>::put(f[V + k]);
+        }
       }
       if (r.live && has_a[i]) *reinterpret_cast<Pack<T, V>*>(out + at[i]) = x;
       if (r.live && has_b[i]) *reinterpret_cast<Pack<T, V>*>(out + second[i]) = y;
@@ -322,7 +392,11 @@ struct Heads {
   static __device__ __forceinline__ void vector(const float* p, int apart, E (&e)[N]) {
     float f[V];
 #pragma unroll
-    for (int k = 0; k < V; ++k) f[k] = reinterpret_cast<const Pack<float, W>*>(p + k / W * apart)->v[k % W];
+    for (int k = 0; k < V; k += W) {
+      const Pack<float, W> x = raw_vec<float, W>(p + k / W * apart);
+#pragma unroll
+      for (int n = 0; n < W; ++n) f[k + n] = x.v[n];
+    }
     to_pairs<V>(f, e);
   }
   static constexpr int kWide = V > 4 ? 4 : V;
@@ -336,7 +410,7 @@ struct Heads {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int item = lane + i * a.lanes;
-      if (item < a.items_turned) {
+      if (FULL || item < a.items_turned) {
         constexpr int W = V == 8 || (INTERLEAVED && V > 1) ? V / 2 : V;
         const float* p = angles + r.token * a.pairs + item * W;
         E c[N], s[N];
@@ -355,13 +429,17 @@ struct Heads {
   __device__ __forceinline__ void forward(const HeadJob& j, const unsigned char* stage, const float* angles, const float* w,
                                           const HeadTile& s, const Row& r, T* out) const {
     E e[ITEMS][2][N], sum = e_all<E>(0.0f);
-    read(j.in[0], stage, s, r, e);
+    In in;
+    read(j.in[0], stage, s, r, in);
+    split(in, e);
     if constexpr (kNorm) {
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
         for (int k = 0; k < N; ++k) sum = e_fma(e[i][1][k], e[i][1][k], e_fma(e[i][0][k], e[i][0][k], sum));
-      const E rstd = e_all<E>(rsqrtf(fmaf(head_sum(e_sum(sum)), a.inv_d, a.eps)));
+      float square = e_sum(sum), none = 0.0f;
+      head_sums(square, none);
+      const E rstd = e_all<E>(rsqrtf(fmaf(square, a.inv_d, a.eps)));
 #pragma unroll
       for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
@@ -377,26 +455,36 @@ struct Heads {
   }
   __device__ __forceinline__ void backward(const HeadJob& j, const unsigned char* stage, const float* angles, const float* w,
                                            const HeadTile& s, const Row& r, T* out) {
-    E g[ITEMS][2][N], x[ITEMS][2][N], xx = e_all<E>(0.0f), gx = xx;
-    read(j.in[0], stage, s, r, g);
+    E g[ITEMS][2][N], xx = e_all<E>(0.0f), gx = xx;
+    In in, xs;
+    read(j.in[0], stage, s, r, in);
+    read(j.in[1], stage, s, r, xs);
+    split(in, g);
     rotate(angles, r, g);
-    read(j.in[1], stage, s, r, x);
+    {
+      E x[ITEMS][2][N];
+      split(xs, x);
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i)
+      for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
-      for (int side = 0; side < 2; ++side) {
-        E wt[N];
-        weights(w, i, side, wt);
+        for (int side = 0; side < 2; ++side) {
+          E wt[N];
+          weights(w, i, side, wt);
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          xx = e_fma(x[i][side][k], x[i][side][k], xx);
-          gx = e_fma(e_mul(g[i][side][k], wt[k]), x[i][side][k], gx);
+          for (int k = 0; k < N; ++k) {
+            xx = e_fma(x[i][side][k], x[i][side][k], xx);
+            gx = e_fma(e_mul(g[i][side][k], wt[k]), x[i][side][k], gx);
+          }
         }
-      }
-    const float rstd = rsqrtf(fmaf(head_sum(e_sum(xx)), a.inv_d, a.eps));
+    }
+    float square = e_sum(xx), product = e_sum(gx);
+    head_sums(square, product);
+    const float rstd = rsqrtf(fmaf(square, a.inv_d, a.eps));
     // a group without a head adds nothing to dw
-    const E rs = e_all<E>(rstd), mine = e_all<E>(r.live ? rstd : 0.0f),
-            back = e_all<E>(-(head_sum(e_sum(gx)) * a.inv_d) * rstd * rstd);
+    const E rs = e_all<E>(rstd), mine = e_all<E>(r.live ? rstd : 0.0f), back = e_all<E>(-(product * a.inv_d) * rstd * rstd);
+    keep_narrow(xs);
+    E x[ITEMS][2][N];
+    split(xs, x);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
@@ -509,15 +597,15 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
       return b;
     };
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      if (taken >= kStages) tc::mbar_wait(empty + 8 * i, phase ^ 1u, args.status);
+      if (taken >= kStages) stage_wait(empty + 8 * i, phase ^ 1u, args.status);
       __syncwarp();
       const uint32_t to = tc::smem_u32(stages) + i * args.stage_bytes;
       float* const mine = angles + i * 2 * args.angles;
       const bool second = !args.shared && tile >= args.job[0].tiles;
       const int t0 = second ? 0 : tile, t1 = args.shared ? tile : tile - args.job[0].tiles;
+      // what was written here by other copies and read is behind; bulk copies come next
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       if (helper == 0) {
-        // what was written here by other copies and read is behind; bulk copies come next
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         uint32_t b = 0;
         if (!second) b += bytes(args.job[0], t0, head_tile(args.job[0], t0));
         if (second || args.shared) b += bytes(args.job[1], t1, head_tile(args.job[1], t1));
@@ -567,7 +655,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
   };
   float* const parts = reinterpret_cast<float*>(sm + lay.parts);
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    tc::mbar_wait(full + 8 * i, phase, args.status);
+    stage_wait(full + 8 * i, phase, args.status);
     __syncwarp();
     const bool second = !args.shared && tile >= args.job[0].tiles;
     if (!second) rows(args.job[0], tile, w);
@@ -969,9 +1057,9 @@ fvx_status run_heads(const char* name, fvx_dtype dt, Call& c, HeadOp op, int job
       if (op == kNormRotate) return launch_heads<T, V, ITEMS, IL, kNormRotate, FULL>(name, c.a, jobs, t, dw, s, scr);
       return launch_heads<T, V, ITEMS, IL, kNormRotateBack, FULL>(name, c.a, jobs, t, dw, s, scr);
     };
-    // heads of 16, 32, 64, 128 or 256 values: no lane asks what it has
+    // heads of 16, 32, 64, 128 or 256 values that turn as a whole: no lane asks what it has
     if constexpr (V * sizeof(T) == 16)
-      if (c.a.d == c.a.lanes * ITEMS * 2 * V) return go.template operator()<true>();
+      if (c.a.d == c.a.lanes * ITEMS * 2 * V && 2 * c.a.pairs == c.a.d) return go.template operator()<true>();
     return go.template operator()<false>();
   });
 }
