@@ -65,31 +65,34 @@ struct HeadArgs {
   float magnitude, sign, eps, inv_d;
 };
 
-// A turn's fraction in 2^-32: the product wraps at whole turns by itself, so a
-// position of any size loses nothing that its step does not.
-__device__ __forceinline__ uint32_t turn_of(uint64_t step, int pos) {
-  return (uint32_t)((step * (uint64_t)(int64_t)pos) >> 32);
-}
-// Sine and cosine of a fraction of a turn: the nearest quarter is taken off
-// exactly, and the Taylor series end where they are below 2e-9 on the 1/8 turn left.
-__device__ __forceinline__ void sincos_turn(uint32_t t, float& s, float& c) {
-  const uint32_t q = (t + 0x20000000u) >> 30;
-  const float x = (float)(int32_t)(t - (q << 30)) * 1.46291807926715968e-9f;  // 2 pi / 2^32
-  const float x2 = x * x;
-  float a = fmaf(x2, 2.75573192239858907e-6f, -1.98412698412698413e-4f);
-  a = fmaf(x2, a, 8.33333333333333333e-3f);
-  a = fmaf(x2, a, -1.66666666666666667e-1f);
-  a = fmaf(x * x2, a, x);
-  float b = fmaf(x2, -2.75573192239858907e-7f, 2.48015873015873016e-5f);
-  b = fmaf(x2, b, -1.38888888888888889e-3f);
-  b = fmaf(x2, b, 4.16666666666666667e-2f);
-  b = fmaf(x2, b, -0.5f);
-  b = fmaf(x2, b, 1.0f);
-  const bool swap = q & 1u;
-  s = swap ? b : a;
-  c = swap ? a : b;
-  if (q & 2u) s = -s;
-  if ((q + 1u) & 2u) c = -c;
+// Sines and cosines of two angles.  s: a turn's fraction in 2^-32, plus 1/8: its
+// top two bits are the quarter, the rest minus 1/8 lies within 1/8 turn of
+// zero, where the Taylor series end below 2e-9.
+__device__ __forceinline__ void sincos_two(uint32_t s0, uint32_t s1, float m, float ms, float& sin0, float& cos0, float& sin1,
+                                           float& cos1) {
+  auto both = [](float v) { return tc::pair(v, v); };
+  const uint64_t x = tc::mul2(tc::pair((float)(int32_t)((s0 << 2) ^ 0x80000000u), (float)(int32_t)((s1 << 2) ^ 0x80000000u)),
+                              both(3.65729519816789921e-10f));  // 2 pi / 2^34
+  const uint64_t x2 = tc::mul2(x, x);
+  uint64_t a = tc::fma2(x2, both(2.75573192239858907e-6f), both(-1.98412698412698413e-4f));
+  a = tc::fma2(x2, a, both(8.33333333333333333e-3f));
+  a = tc::fma2(x2, a, both(-1.66666666666666667e-1f));
+  a = tc::fma2(tc::mul2(x, x2), a, x);
+  uint64_t b = tc::fma2(x2, both(-2.75573192239858907e-7f), both(2.48015873015873016e-5f));
+  b = tc::fma2(x2, b, both(-1.38888888888888889e-3f));
+  b = tc::fma2(x2, b, both(4.16666666666666667e-2f));
+  b = tc::fma2(x2, b, both(-0.5f));
+  b = tc::fma2(x2, b, both(1.0f));
+  float a0, a1, b0, b1;
+  tc::unpair(a, a0, a1);
+  tc::unpair(b, b0, b1);
+  auto quarter = [&](uint32_t s, float sine, float cosine, float& sn, float& cs) {
+    const bool swap = s & 0x40000000u;
+    sn = __uint_as_float(__float_as_uint(swap ? cosine : sine) ^ (s & 0x80000000u)) * ms;
+    cs = __uint_as_float(__float_as_uint(swap ? sine : cosine) ^ ((s ^ (s << 1)) & 0x80000000u)) * m;
+  };
+  quarter(s0, a0, b0, sin0, cos0);
+  quarter(s1, a1, b1, sin1, cos1);
 }
 
 enum HeadOp { kRotate, kNormRotate, kNormRotateBack };
@@ -106,9 +109,9 @@ __device__ __forceinline__ void copy4(uint32_t to, const void* from) {
 __device__ __forceinline__ void copies_arrive(uint32_t bar) {  // when this thread's copies have landed
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
 }
-// tc::mbar_wait for the long waits of a kernel that memory bounds: its polls
-// sleep up to a microsecond, or those of the warps that wait take the issue
-// slots of the warps that work (150 of 300 instructions per 512 values).
+// tc::mbar_wait for the long waits of a kernel that memory bounds: its polls are
+// apart, or those of the warps that wait take the issue slots of the warps that
+// work (150 of 300 instructions per 512 values).
 __device__ __forceinline__ uint32_t stage_try(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile(
@@ -118,11 +121,12 @@ __device__ __forceinline__ uint32_t stage_try(uint32_t bar, uint32_t parity) {
       : "memory");
   return ok;
 }
+template <int NAP>
 __device__ __forceinline__ void stage_wait(uint32_t bar, uint32_t parity, uint32_t* status) {
   if (stage_try(bar, parity)) return;
   unsigned long long t0 = 0;
   for (uint32_t it = 1;; ++it) {
-    __nanosleep(64);
+    __nanosleep(NAP);
     if (stage_try(bar, parity)) return;
     if ((it & 255u) == 0u) {
       if (t0 == 0) t0 = tc::globaltimer();
@@ -198,40 +202,74 @@ __device__ __forceinline__ void fetch_source(const HeadSource& src, const HeadJo
   }
 }
 // Cosines and sines of a tile's tokens, each computed once for all its heads.  A
-// thread keeps its pair; four tokens' positions are under way at once.
-__device__ __forceinline__ void angles_of(const HeadArgs& a, const HeadJob& j, const HeadTile& s, const uint64_t* turns,
-                                          float* angles, int thread) {
-  const int p = thread & (a.pair_lanes - 1), apart = 32 * kHelpers / a.pair_lanes;
-  if (p >= a.pairs) return;
-  const uint64_t step = turns[p];
-  const int32_t* pos = j.pos + ((p >= a.axis1) + (p >= a.axis2)) * j.pos_axis + (int64_t)s.token * j.pos_token;
-  const float ms = a.magnitude * a.sign;
-  // halves in vectors of eight: the first four pairs of every eight, then the others, as the lanes read them
-  const int place = a.fours ? (p >> 2 & 1) * (a.pairs >> 1) + (p >> 3 << 2) + (p & 3) : p;
-  constexpr int kAtOnce = 4;
-  int t = thread / a.pair_lanes, at[kAtOnce];
-  auto ahead = [&](int from) {
+// helper thread keeps its pair; the positions of its next four tokens are under
+// way while it computes, those of a tile's first ones since before its stage
+// was free.
+struct AngleThread {
+  static constexpr int kAtOnce = 4;
+  const HeadArgs& a;
+  const int p, first, apart, place;
+  const bool has;
+  uint32_t lo, hi, c;  // the pair's step, and what the position's bias and the 1/8 turn make
+  int at[kAtOnce];
+
+  __device__ __forceinline__ AngleThread(const HeadArgs& args, const uint64_t* turns, int thread)
+      : a(args),
+        p(thread & (args.pair_lanes - 1)),
+        first(thread / args.pair_lanes),
+        apart(32 * kHelpers / args.pair_lanes),
+        // halves in vectors of eight: the first four pairs of every eight, then the others, as the lanes read them
+        place(args.fours ? (p >> 2 & 1) * (args.pairs >> 1) + (p >> 3 << 2) + (p & 3) : p),
+        has(p < args.pairs) {
+    const uint64_t step = has ? turns[p] : 0;
+    lo = (uint32_t)step;
+    hi = (uint32_t)(step >> 32);
+    c = 0x20000000u - (uint32_t)((step << 31) >> 32);
+  }
+  // The upper half of step * position modulo 2^64, plus 1/8 turn: the product
+  // wraps at whole turns by itself, so a position of any size loses nothing that
+  // its step does not.
+  __device__ __forceinline__ uint32_t turn(int pos) const {
+    const uint32_t u = (uint32_t)pos ^ 0x80000000u;  // pos + 2^31
+    return __umulhi(lo, u) + hi * u + c;
+  }
+  __device__ __forceinline__ const int32_t* positions(const HeadJob& j, const HeadTile& s) const {
+    return j.pos + ((p >= a.axis1) + (p >= a.axis2)) * j.pos_axis + (int64_t)(s.token + first) * j.pos_token;
+  }
+  __device__ __forceinline__ void ahead(const HeadJob& j, const int32_t* pos, int left) {
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k)
-      at[k] = from + k * apart < s.tokens ? __ldg(pos + (from + k * apart) * j.pos_token) : 0;
-  };
-  ahead(t);
-  while (t < s.tokens) {
-    int now[kAtOnce];
+    for (int k = 0; k < kAtOnce; ++k) at[k] = has && k * apart < left ? __ldg(pos + (int64_t)(k * apart) * j.pos_token) : 0;
+  }
+  __device__ __forceinline__ void start(const HeadJob& j, const HeadTile& s) { ahead(j, positions(j, s), s.tokens - first); }
+  __device__ __forceinline__ void compute(const HeadJob& j, const HeadTile& s, float* angles) {
+    if (!has) return;
+    const float ms = a.magnitude * a.sign;
+    const int32_t* pos = positions(j, s);
+    float* to = angles + first * a.pairs + place;
+    for (int left = s.tokens - first; left > 0; left -= kAtOnce * apart) {
+      uint32_t turns[kAtOnce];
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k) now[k] = at[k];
-    ahead(t + kAtOnce * apart);
+      for (int k = 0; k < kAtOnce; ++k) turns[k] = turn(at[k]);
+      pos += (int64_t)(kAtOnce * apart) * j.pos_token;
+      ahead(j, pos, left - kAtOnce * apart);
 #pragma unroll
-    for (int k = 0; k < kAtOnce; ++k, t += apart) {
-      float sn, cs;
-      sincos_turn(turn_of(step, now[k]), sn, cs);
-      if (t < s.tokens) {
-        angles[t * a.pairs + place] = cs * a.magnitude;
-        angles[a.angles + t * a.pairs + place] = sn * ms;
+      for (int k = 0; k < kAtOnce; k += 2) {
+        float s0, c0, s1, c1;
+        sincos_two(turns[k], turns[k + 1], a.magnitude, ms, s0, c0, s1, c1);
+        if (k * apart < left) {
+          to[0] = c0;
+          to[a.angles] = s0;
+        }
+        to += apart * a.pairs;
+        if ((k + 1) * apart < left) {
+          to[0] = c1;
+          to[a.angles] = s1;
+        }
+        to += apart * a.pairs;
       }
     }
   }
-}
+};
 
 // A lane holds ITEMS items of a head, each two vectors of V values in memory, P
 // apart: the first and second partners (u and v) of V pairs (halves), or V / 2
@@ -400,11 +438,13 @@ struct Heads {
     to_pairs<V>(f, e);
   }
   static constexpr int kWide = V > 4 ? 4 : V;
-  static __device__ __forceinline__ int weight_place(const HeadArgs& a, int item, int side, int k) {
-    return ((side * (V / kWide) + k / kWide) * a.lanes * ITEMS + item) * kWide + k % kWide;
+  // Weights: a row of a group's lanes for each item, side and four values, 32 (bf16: 16) lanes apart.
+  static constexpr int kLanes = sizeof(T) == 4 ? 32 : 16, kWeights = kLanes * ITEMS * 2 * V;
+  static __device__ __forceinline__ int weight_place(int lane, int i, int side, int k) {
+    return (((i * 2 + side) * (V / kWide) + k / kWide) * kLanes + lane) * kWide + k % kWide;
   }
   __device__ __forceinline__ void weights(const float* w, int i, int side, E (&e)[N]) const {
-    vector<kWide>(w + weight_place(a, lane + i * a.lanes, side, 0), a.lanes * ITEMS * kWide, e);
+    vector<kWide>(w + weight_place(0, i, side, 0), kLanes * kWide, e);
   }
   __device__ __forceinline__ void rotate(const float* angles, const Row& r, E (&e)[ITEMS][2][N]) const {
 #pragma unroll
@@ -537,7 +577,7 @@ struct HeadLayout {
   __host__ __device__ HeadLayout(const HeadArgs& a, int weights, bool back) {
     turns = 64;
     w = turns + ((a.pairs + 1) & ~1) * 8;
-    parts = w + 2 * ((weights + 3) & ~3) * 4;
+    parts = w + 2 * weights * 4;
     angles = parts + (back ? kWorkers * a.d * 4 : 0);
     stages = (angles + kStages * 2 * a.angles * 4 + 127) & ~127;
     bytes = stages + kStages * a.stage_bytes;
@@ -548,7 +588,7 @@ template <typename T, int V, int ITEMS, bool INTERLEAVED, int OP, bool FULL>
 __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant__ HeadArgs args) {
   using H = Heads<T, V, ITEMS, INTERLEAVED, OP, FULL>;
   extern __shared__ __align__(128) unsigned char sm[];
-  const int weights = H::kNorm ? args.lanes * ITEMS * 2 * V : 0;
+  constexpr int weights = H::kNorm ? H::kWeights : 0;
   const HeadLayout lay(args, weights, H::kBack);
   uint64_t* const turns = reinterpret_cast<uint64_t*>(sm + lay.turns);
   float* const w = reinterpret_cast<float*>(sm + lay.w);
@@ -567,11 +607,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
   }
   for (int p = threadIdx.x; p < args.pairs; p += kHeadThreads) turns[p] = args.turns[p];
   if constexpr (H::kNorm)
-    for (int i = threadIdx.x; i < 2 * weights; i += kHeadThreads) {
-      const int seg = i >= weights, k = i - seg * weights;
-      const int item = k / (2 * V), side = k / V & 1, c = H::channel(args, item, side, k % V);
+    for (int n = threadIdx.x; n < 2 * args.lanes * ITEMS * 2 * V; n += kHeadThreads) {
+      const int k = n % V, side = n / V & 1, item = (n / (2 * V)) % (args.lanes * ITEMS), seg = n / (2 * V) / (args.lanes * ITEMS);
+      const int c = H::channel(args, item, side, k);
       const float* from = seg ? args.job[1].w : args.job[0].w;
-      w[seg * ((weights + 3) & ~3) + H::weight_place(args, item, side, k % V)] = from && c < args.d ? __ldg(from + c) : 1.0f;
+      w[seg * weights + H::weight_place(item % args.lanes, item / args.lanes, side, k)] = from && c < args.d ? __ldg(from + c) : 1.0f;
     }
   __syncthreads();
   uint32_t i = 0, phase = 0, taken = 0;
@@ -582,10 +622,10 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
       phase ^= 1u;
     }
   };
-  // Registers: 768 threads at 80 are launched, 61,440: 512 at 96 and 256 at 48.
+  // Registers: 768 threads at 80 are launched, 61,440: 512 at 88 and 256 at 64 for the backward pass.
   if (warp >= kWorkers) {
     // ---------------------------------------------------------------- helpers
-    tc::setmaxnreg_dec<48>();
+    if constexpr (H::kBack) tc::setmaxnreg_dec<64>();
     const int helper = warp - kWorkers, lane = threadIdx.x & 31;
     auto fetch = [&](const HeadJob& j, int tile, const HeadTile& s, uint32_t to) {
       fetch_source<T>(j.in[0], j, tile, s, args.d, to, full + 8 * i, helper);
@@ -596,31 +636,35 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
       if constexpr (H::kBack) b += bulk_bytes<T>(j.in[1], j, tile, s, args.d);
       return b;
     };
+    AngleThread angle(args, turns, threadIdx.x - 32 * kWorkers);
     for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-      if (taken >= kStages) stage_wait(empty + 8 * i, phase ^ 1u, args.status);
-      __syncwarp();
       const uint32_t to = tc::smem_u32(stages) + i * args.stage_bytes;
       float* const mine = angles + i * 2 * args.angles;
       const bool second = !args.shared && tile >= args.job[0].tiles;
       const int t0 = second ? 0 : tile, t1 = args.shared ? tile : tile - args.job[0].tiles;
+      HeadTile s0 = {}, s1 = {};
+      if (!second) s0 = head_tile(args.job[0], t0);
+      if (second || args.shared) s1 = head_tile(args.job[1], t1);
+      if (args.pairs) {
+        if (second) angle.start(args.job[1], s1);
+        else angle.start(args.job[0], s0);
+      }
+      if (taken >= kStages) stage_wait<300>(empty + 8 * i, phase ^ 1u, args.status);
+      __syncwarp();
       // what was written here by other copies and read is behind; bulk copies come next
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       if (helper == 0) {
         uint32_t b = 0;
-        if (!second) b += bytes(args.job[0], t0, head_tile(args.job[0], t0));
-        if (second || args.shared) b += bytes(args.job[1], t1, head_tile(args.job[1], t1));
+        if (!second) b += bytes(args.job[0], t0, s0);
+        if (second || args.shared) b += bytes(args.job[1], t1, s1);
         if (lane == 0) tc::mbar_expect_tx(full + 8 * i, b);
         __syncwarp();
       }
-      if (!second) {
-        const HeadTile s = head_tile(args.job[0], t0);
-        fetch(args.job[0], t0, s, to);
-        if (args.pairs) angles_of(args, args.job[0], s, turns, mine, threadIdx.x - 32 * kWorkers);
-      }
-      if (second || args.shared) {
-        const HeadTile s = head_tile(args.job[1], t1);
-        fetch(args.job[1], t1, s, to);
-        if (second && args.pairs) angles_of(args, args.job[1], s, turns, mine, threadIdx.x - 32 * kWorkers);
+      if (!second) fetch(args.job[0], t0, s0, to);
+      if (second || args.shared) fetch(args.job[1], t1, s1, to);
+      if (args.pairs) {
+        if (second) angle.compute(args.job[1], s1, mine);
+        else angle.compute(args.job[0], s0, mine);
       }
       copies_arrive(full + 8 * i);
       __syncwarp();
@@ -633,10 +677,11 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
     return;
   }
   // ------------------------------------------------------------------ workers
-  tc::setmaxnreg_inc<96>();
+  if constexpr (H::kBack) tc::setmaxnreg_inc<88>();
   H h(args);
   bool first_done = false;
-  auto rows = [&](const HeadJob& j, int tile, const float* weight) {
+  auto rows = [&](const HeadJob& j, int tile, const float* seg_weights) {
+    const float* const weight = seg_weights + h.lane * H::kWide;
     const HeadTile s = head_tile(j, tile);
     const unsigned char* const stage = stages + i * args.stage_bytes;
     const float* const at = angles + i * 2 * args.angles;
@@ -655,7 +700,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
   };
   float* const parts = reinterpret_cast<float*>(sm + lay.parts);
   for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    stage_wait(full + 8 * i, phase, args.status);
+    stage_wait<40>(full + 8 * i, phase, args.status);
     __syncwarp();
     const bool second = !args.shared && tile >= args.job[0].tiles;
     if (!second) rows(args.job[0], tile, w);
@@ -666,7 +711,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
           h.write_part(parts, args.job[0].part ? args.job[0].part + (int64_t)blockIdx.x * args.d : nullptr);
         }
       }
-      rows(args.job[1], args.shared ? tile : tile - args.job[0].tiles, w + ((weights + 3) & ~3));
+      rows(args.job[1], args.shared ? tile : tile - args.job[0].tiles, w + weights);
     }
     __syncwarp();
     if ((threadIdx.x & 31) == 0) tc::mbar_arrive(empty + 8 * i);
@@ -924,26 +969,31 @@ void cut(HeadJob& j, int tokens, int heads) {
   j.block_magic = heads > 1 ? magic_of(heads) : 0;
 }
 
-// Tokens of a stage: as many as fit, fewer where not every
-// multiprocessor would get a stage; of those, the number whose heads fill the
-// workers' last turn best.
-int stage_tokens(const HeadArgs& a, const HeadJob* jobs, int count, int64_t fitting, int line, int sms) {
-  const int n = std::max(jobs[0].n, count > 1 ? jobs[1].n : 0), turn = kWorkers * (32 / a.lanes);
-  const int64_t most = std::max<int64_t>(1, std::min<int64_t>({fitting, ((int64_t)n + sms - 1) / sms, 2048}));
-  int best = (int)most;
-  double best_used = 0.0;
-  for (int t = (int)most; t >= 1 && t * 8 >= most * 5; --t) {
-    double used = 0.0;
-    for (int k = 0; k < count; ++k) {
-      const int64_t rows = (int64_t)t * jobs[k].heads;
-      used += (double)rows / (double)up(rows, turn) / count;
-    }
-    used += t % line == 0 ? 1.0 : 0.0;
-    if (used > best_used + 0.02) {
-      best_used = used;
-      best = t;
-    }
+// Tokens of a stage of `count` tensors: up to `most` and no more than give every
+// multiprocessor a stage; of the numbers that fill the workers' last turn the one
+// that costs least.  A stage costs its workers' turns and about half of one to
+// hand over.  Returns the turns per token.
+double stage_tokens(const HeadArgs& a, const HeadJob* jobs, int count, int64_t most, int line, int sms, int* tokens) {
+  const int turn = kWorkers * (32 / a.lanes);
+  int n = 0, heads = 0;
+  for (int k = 0; k < count; ++k) {
+    n = std::max(n, jobs[k].n);
+    heads = std::max(heads, jobs[k].heads);
   }
+  most = std::max<int64_t>(1, std::min<int64_t>({most, ((int64_t)n + sms - 1) / sms, 4096}));
+  double best = 1e300;
+  auto consider = [&](int64_t t) {
+    if (t >= line) t -= t % line;
+    if (t < 1) return;
+    double turns = 0.6;
+    for (int k = 0; k < count; ++k) turns += (double)((t * jobs[k].heads + turn - 1) / turn);
+    if (turns / t < best * 0.99) {
+      best = turns / t;
+      *tokens = (int)t;
+    }
+  };
+  consider(most);
+  for (int64_t k = most * heads / turn; k >= 1 && 2 * k * turn >= most * heads; --k) consider(k * turn / heads);
   return best;
 }
 
@@ -959,7 +1009,7 @@ fvx_status launch_heads(const char* name, HeadArgs& a, int jobs, const fvx_head_
     set_error("%s: could not set up the device status word", t_entry);
     return FVX_ERR_CUDA;
   }
-  const int weights = H::kNorm ? a.lanes * ITEMS * 2 * V : 0;
+  constexpr int weights = H::kNorm ? H::kWeights : 0;
   a.angles = a.stage_bytes = 0;
   const HeadLayout fixed(a, weights, H::kBack);
   const int64_t room = (kMostSmem - fixed.bytes - 256) / kStages - 512;
@@ -987,24 +1037,46 @@ fvx_status launch_heads(const char* name, HeadArgs& a, int jobs, const fvx_head_
     const int64_t bytes = token_bytes(a.job[0], a.job[0].heads) + token_bytes(a.job[1], a.job[1].heads) + angle_bytes;
     if (bytes > room) a.shared = 0;
     else {
-      const int tokens = stage_tokens(a, a.job, 2, room / bytes, std::max(line_of(a.job[0]), line_of(a.job[1])), sms);
+      int tokens = 1;
+      stage_tokens(a, a.job, 2, room / bytes, std::max(line_of(a.job[0]), line_of(a.job[1])), sms, &tokens);
       for (int i = 0; i < 2; ++i) cut(a.job[i], tokens, a.job[i].heads);
       if (!results_near(a.job[0]) || !results_near(a.job[1])) a.shared = 0;
     }
   }
-  // the angles' part of a stage: what the tensor with the smaller tokens needs
+  // Tensors of their own stages: the angles' part of a stage is what the one or
+  // the other needs, or between; the cheapest.
   int64_t angle_room = 0;
-  for (int i = 0; i < jobs && !a.shared; ++i)
-    if (a.job[i].n > 0)
-      angle_room = std::max(angle_room, room * angle_bytes / (token_bytes(a.job[i], a.job[i].heads) + angle_bytes));
-  angle_room = std::max<int64_t>(angle_room, angle_bytes);
+  if (!a.shared) {
+    double best = 1e300;
+    auto needs = [&](const HeadJob& j) {
+      return std::max<int64_t>(room * angle_bytes / (token_bytes(j, j.heads) + angle_bytes), angle_bytes);
+    };
+    const int64_t lo = std::min(needs(a.job[0]), needs(a.job[jobs - 1])), hi = std::max(needs(a.job[0]), needs(a.job[jobs - 1]));
+    for (int k = 0; k < (lo == hi ? 1 : 4); ++k) {
+      const int64_t angles = lo + (hi - lo) * k / 3;
+      double turns = 0.0;
+      for (int i = 0; i < jobs; ++i) {
+        const HeadJob& j = a.job[i];
+        int tokens = 1;
+        const int64_t fit = (room - angles) / token_bytes(j, j.heads);
+        if (j.n > 0 && fit > 0)
+          turns += j.n * stage_tokens(a, &j, 1, angle_bytes ? std::min(fit, angles / angle_bytes) : fit, line_of(j), sms, &tokens);
+      }
+      if (turns < best) {
+        best = turns;
+        angle_room = angles;
+      }
+    }
+  }
   for (int i = 0; i < jobs && !a.shared; ++i) {
     HeadJob& j = a.job[i];
     if (j.n == 0) continue;
     const int64_t bytes = token_bytes(j, j.heads);
     if (bytes <= room - angle_room) {
       const int64_t most = (room - angle_room) / bytes;
-      cut(j, stage_tokens(a, &j, 1, angle_bytes ? std::min(most, angle_room / angle_bytes) : most, line_of(j), sms), j.heads);
+      int tokens = 1;
+      stage_tokens(a, &j, 1, angle_bytes ? std::min(most, angle_room / angle_bytes) : most, line_of(j), sms, &tokens);
+      cut(j, tokens, j.heads);
     } else {
       const int turn = kWorkers * (32 / a.lanes);
       int64_t heads = (room - angle_room) / token_bytes(j, 1);
