@@ -26,7 +26,7 @@ constexpr int kMaxPairs = kMaxHead / 2;
 // A block's warps: those that work on the heads, and those that fetch the next
 // stages' tensors and compute their angles.
 constexpr int kWorkers = 16, kHelpers = 8, kHeadThreads = 32 * (kWorkers + kHelpers);
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr int kMostSmem = 227 * 1024;
 
 // A tensor that is read.  Its part of a stage lies in shared memory as in
@@ -1012,7 +1012,13 @@ fvx_status launch_heads(const char* name, HeadArgs& a, int jobs, const fvx_head_
   constexpr int weights = H::kNorm ? H::kWeights : 0;
   a.angles = a.stage_bytes = 0;
   const HeadLayout fixed(a, weights, H::kBack);
-  const int64_t room = (kMostSmem - fixed.bytes - 256) / kStages - 512;
+  // Long stages, since a stage costs its hand-over: two of 110 KB for the backward
+  // pass, two of 90 KB forward, where reads too far ahead of the writes cost the
+  // memory more than the hand-over (1,000,000 x 8 + 8 x 64 bf16 normed in 612 us
+  // with two of 90 KB, 642 of 110, 657 with three of 72; backward 1051, 967,
+  // 1010; 300,000 x 4 + 4 x 256 normed 379, 379, 481; 300,000 x 16 + 16 x 64 fp32
+  // normed 717, 779, 809).
+  const int64_t room = (int64_t)(kMostSmem - fixed.bytes - 256) * 2 / (H::kBack ? 4 : 5) - 512;
   // bytes of a token (its heads from global memory, or one by one) and of its angles
   auto token_bytes = [&](const HeadJob& j, int heads) {
     int64_t b = 0;
