@@ -2,6 +2,7 @@
 // backward pass draws it again.
 //
 //   y = residual + (kept ? x / (1 - drop / 65536) : 0),   kept iff bits(i) >= drop
+// in one fused multiply-add, whichever kernel runs.
 // bits(i): 16 bits for value i of the row-major tensor, eight values per
 // counter of Philox4x32 with ten rounds (Salmon, Moraes, Dror and Shaw 2011):
 // counter words (i / 8, offset), key words seed, value i % 8 the i % 8-th
@@ -71,14 +72,23 @@ __device__ __forceinline__ uint32_t kept_bits(uint4 r, uint32_t drop) {
   return m;
 }
 
+// The value kept or dropped: one rounding, the same in every kernel.
+template <bool ADD>
+__device__ __forceinline__ float dropped(bool keep, float x, float scale, float add) {
+  if constexpr (ADD) return keep ? fmaf(x, scale, add) : add;
+  return keep ? x * scale : 0.0f;
+}
+
 // Vectors of eight values; LINE: the tensors are dense, so the place of value i is i.
 template <typename T, bool LINE, bool ADD>
-__global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ DropArgs a) {
+__global__ void __launch_bounds__(kThreads, 6) k_dropout(const __grid_constant__ DropArgs a) {
   const Key key(a);
   const int64_t whole = a.total >> 3, step = (int64_t)gridDim.x * kThreads;
   const T* x = reinterpret_cast<const T*>(a.x);
   const T* res = reinterpret_cast<const T*>(a.residual);
   T* y = reinterpret_cast<T*>(a.y);
+  const uint32_t first_kept = a.drop << 16;  // 65536, all dropped, passes the end
+  const bool some = a.drop < 65536u;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < whole; i += step) {
     int64_t ax = i * 8, ar = ax, ay = ax;
     if constexpr (!LINE) {
@@ -91,60 +101,107 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const __grid_constant__ Dr
     float f[8], g[8];
     load_vec<T, 8>(x + ax, f);
     if constexpr (ADD) load_vec<T, 8>(res + ar, g);
-    const uint32_t m = kept_bits(philox(key, (uint64_t)i), a.drop);
+    const uint4 r = philox(key, (uint64_t)i);
+    const uint32_t words[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const float v = f[k] * a.scale;
-      f[k] = (m >> k) & 1u ? v : 0.0f;
-      if constexpr (ADD) f[k] += g[k];
+      // either half is compared in the upper one's place
+      const bool keep = (k & 1 ? words[k / 2] : words[k / 2] << 16) >= first_kept;
+      f[k] = dropped<ADD>(keep && some, f[k], a.scale, ADD ? g[k] : 0.0f);
     }
     store_vec<T, 8>(y + ay, f);
   }
   if (LINE && blockIdx.x == 0 && threadIdx.x < (a.total & 7)) {
     const int64_t at = whole * 8 + threadIdx.x;
     const uint32_t m = kept_bits(philox(key, (uint64_t)whole), a.drop);
-    float f = (m >> threadIdx.x) & 1u ? Elem<T>::get(x[at]) * a.scale : 0.0f;
-    if (ADD) f += Elem<T>::get(res[at]);
-    y[at] = Elem<T>::put(f);
+    const float add = ADD ? Elem<T>::get(res[at]) : 0.0f;
+    y[at] = Elem<T>::put(dropped<ADD>((m >> threadIdx.x) & 1u, Elem<T>::get(x[at]), a.scale, add));
+  }
+}
+
+// x or residual of any pitch and alignment, rows of at least eight values, into
+// a dense y: a thread reads its counter's eight values one by one, from one row
+// or the end of one and the start of the next, and writes them at once.  Lanes
+// sixteen bytes apart use every byte of the lines that they touch.
+template <typename T, bool ADD>
+__global__ void __launch_bounds__(kThreads, 5) k_dropout_rows(const __grid_constant__ DropArgs a) {
+  const Key key(a);
+  const int64_t counters = (a.total + 7) >> 3, step = (int64_t)gridDim.x * kThreads;
+  const bool small = a.total >> 32 == 0;  // 32-bit division will do
+  const uint32_t first_kept = a.drop << 16;
+  const bool some = a.drop < 65536u;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < counters; i += step) {
+    const int64_t row = small ? (uint32_t)(i * 8) / a.c : i * 8 / a.c;
+    const uint32_t col = (uint32_t)(i * 8 - row * a.c);
+    const int left = (int)min((int64_t)8, a.total - i * 8);
+    auto read = [&](const void* from, int64_t ld, T (&v)[8]) {
+      const T* p = reinterpret_cast<const T*>(from) + row * ld + col;
+      const T* q = p + (ld - (int64_t)a.c);  // the next row's values, as far on
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left) v[k] = (col + k < a.c ? p : q)[k];
+    };
+    T x[8], g[8];
+    read(a.x, a.ldx, x);
+    if constexpr (ADD) read(a.residual, a.ldr, g);
+    const uint4 r = philox(key, (uint64_t)i);
+    const uint32_t words[4] = {r.x, r.y, r.z, r.w};
+    float f[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const bool keep = (k & 1 ? words[k / 2] : words[k / 2] << 16) >= first_kept;
+      f[k] = k < left ? Elem<T>::get(x[k]) : 0.0f;
+      const float add = ADD && k < left ? Elem<T>::get(g[k]) : 0.0f;
+      f[k] = dropped<ADD>(keep && some, f[k], a.scale, add);
+    }
+    T* y = reinterpret_cast<T*>(a.y) + i * 8;
+    if (left == 8) {
+      store_vec<T, 8>(y, f);
+    } else {
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < left) y[k] = Elem<T>::put(f[k]);
+    }
   }
 }
 
 // Any pitch and alignment: a warp takes 256 consecutive values, 32 at a time;
-// lane l draws their l-th counter and hands out its bits.
-template <typename T, bool ADD>
+// lane l draws their l-th counter and hands out its bits.  NEAR: the rows of 256
+// values lie within 2^30 values of their first, and offsets from it take 32 bits.
+template <typename T, bool ADD, bool NEAR>
 __global__ void __launch_bounds__(kThreads) k_dropout_any(const __grid_constant__ DropArgs a) {
+  using Off = std::conditional_t<NEAR, uint32_t, int64_t>;
   const Key key(a);
   const int lane = threadIdx.x & 31;
-  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32);
-  const T* x = reinterpret_cast<const T*>(a.x);
-  const T* res = reinterpret_cast<const T*>(a.residual);
-  T* y = reinterpret_cast<T*>(a.y);
-  const int64_t spans = (a.total + 255) >> 8;
+  const int64_t warps = (int64_t)gridDim.x * (kThreads / 32), spans = (a.total + 255) >> 8;
+  const bool small = a.total >> 32 == 0;  // 32-bit division will do
   for (int64_t span = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); span < spans; span += warps) {
-    const int64_t row0 = (span << 8) / a.c;
-    const uint32_t col0 = (uint32_t)((span << 8) - row0 * a.c);
-    const int64_t left = a.total - (span << 8);
-    float f[8], g[8];
-    int64_t ay[8];
+    const int64_t row0 = small ? (uint32_t)(span << 8) / a.c : (span << 8) / a.c;
+    const uint32_t col0 = (uint32_t)((span << 8) - row0 * a.c) + lane;
+    const int left = (int)min((int64_t)256, a.total - (span << 8)) - lane;
+    const T* x = reinterpret_cast<const T*>(a.x) + row0 * a.ldx;
+    const T* res = reinterpret_cast<const T*>(a.residual) + (ADD ? row0 * a.ldr : 0);
+    T* y = reinterpret_cast<T*>(a.y) + row0 * a.ldy;
+    // rows below: fewer than 256 columns past a start below c
+    auto down_of = [&](uint32_t at) { return a.c >= 512u ? (at >= a.c ? 1u : 0u) : a.c == 1u ? at : __umulhi(at, a.magic); };
+    T f[8], g[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
-      const uint32_t at = col0 + 32 * k + lane;
-      // rows further on: fewer than 256 columns past col0 < c
-      const uint32_t down = a.c >= 512u ? (at >= a.c ? 1u : 0u) : a.c == 1u ? at : __umulhi(at, a.magic);
-      const int64_t row = row0 + down;
-      const uint32_t col = at - down * a.c;
-      ay[k] = row * a.ldy + col;
-      const bool mine = 32 * k + lane < left;
-      f[k] = mine ? Elem<T>::get(x[row * a.ldx + col]) : 0.0f;
-      if constexpr (ADD) g[k] = mine ? Elem<T>::get(res[row * a.ldr + col]) : 0.0f;
+      const uint32_t at = col0 + 32 * k, down = down_of(at), col = at - down * a.c;
+      if (32 * k < left) {
+        f[k] = x[(Off)down * (Off)a.ldx + col];
+        if constexpr (ADD) g[k] = res[(Off)down * (Off)a.ldr + col];
+      }
     }
     const uint32_t m = kept_bits(philox(key, (uint64_t)span * 32 + lane), a.drop);
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const uint32_t bits = __shfl_sync(0xffffffffu, m, 4 * k + (lane >> 3));
-      float v = (bits >> (lane & 7)) & 1u ? f[k] * a.scale : 0.0f;
-      if constexpr (ADD) v += g[k];
-      if (32 * k + lane < left) y[ay[k]] = Elem<T>::put(v);
+      if (32 * k < left) {
+        const uint32_t at = col0 + 32 * k, down = down_of(at);
+        const float v = dropped<ADD>((bits >> (lane & 7)) & 1u, Elem<T>::get(f[k]), a.scale, ADD ? Elem<T>::get(g[k]) : 0.0f);
+        y[(Off)down * (Off)a.ldy + (at - down * a.c)] = Elem<T>::put(v);
+      }
     }
   }
 }
@@ -166,12 +223,17 @@ fvx_status check_rows_of(const char* who, const char* name, const void* p, int64
 }
 
 template <typename T>
-fvx_status run(const DropArgs& a, bool vectors, bool line, int sms, cudaStream_t s) {
-  const int64_t threads = vectors ? std::max<int64_t>(1, a.total >> 3) : ((a.total + 255) >> 8) * 32;
+fvx_status run(const DropArgs& a, bool vectors, bool line, bool to_line, int sms, cudaStream_t s) {
+  const int64_t threads = vectors || to_line ? (a.total + 7) >> 3 : ((a.total + 255) >> 8) * 32;
   const int blocks = (int)std::min<int64_t>((threads + kThreads - 1) / kThreads, (int64_t)sms * 64);
+  // rows that a span of 256 values reaches below its first
+  const int64_t rows = 256 / (int64_t)a.c + 2, most = ((int64_t)1 << 30) / rows;
+  const bool near = a.ldx < most && a.ldy < most && (!a.residual || a.ldr < most);
   LaunchScope ls("dropout", s);
   auto go = [&]<bool ADD>() {
-    if (!vectors) k_dropout_any<T, ADD><<<blocks, kThreads, 0, s>>>(a);
+    if (!vectors && to_line) k_dropout_rows<T, ADD><<<blocks, kThreads, 0, s>>>(a);
+    else if (!vectors && near) k_dropout_any<T, ADD, true><<<blocks, kThreads, 0, s>>>(a);
+    else if (!vectors) k_dropout_any<T, ADD, false><<<blocks, kThreads, 0, s>>>(a);
     else if (line) k_dropout<T, true, ADD><<<blocks, kThreads, 0, s>>>(a);
     else k_dropout<T, false, ADD><<<blocks, kThreads, 0, s>>>(a);
   };
@@ -212,6 +274,7 @@ extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, cons
   a.total = n * c;
   // without gaps any cut into rows is as good
   if (line) c = ldx = ldr = ldy = 1 << 20;
+  const bool to_line = ldy == c && c >= 8 && reinterpret_cast<uintptr_t>(y) % (8 * elem) == 0;
   a.ldx = ldx;
   a.ldr = ldr;
   a.ldy = ldy;
@@ -227,6 +290,6 @@ extern "C" fvx_status fvx_dropout(fvx_dtype dt, const void* x, int64_t ldx, cons
     return reinterpret_cast<uintptr_t>(q) % (8 * elem) == 0 && ld % 8 == 0;
   };
   const bool vectors = wide(x, ldx) && wide(y, ldy) && (!residual || wide(residual, ldr)) && c % 8 == 0;
-  return dt == FVX_F32 ? run<float>(a, vectors, line, sms, (cudaStream_t)stream)
-                       : run<__nv_bfloat16>(a, vectors, line, sms, (cudaStream_t)stream);
+  return dt == FVX_F32 ? run<float>(a, vectors, line, to_line, sms, (cudaStream_t)stream)
+                       : run<__nv_bfloat16>(a, vectors, line, to_line, sms, (cudaStream_t)stream);
 }

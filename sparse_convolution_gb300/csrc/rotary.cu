@@ -296,6 +296,9 @@ struct Heads {
       place(a, item, at[i], second[i]);
       has_a[i] = FULL || item < a.items;
       has_b[i] = FULL || (has_a[i] && second[i] < a.d);
+      // what a lane does not have it reads elsewhere and clears
+      if (!has_a[i]) at[i] = 0;
+      if (!has_b[i]) second[i] = at[i];
     }
     clear();
   }
@@ -349,8 +352,10 @@ struct Heads {
     const T* p = reinterpret_cast<const T*>(stage + src.at) + off;
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
-      in.x[i] = has_a[i] ? raw_vec<T, V>(p + at[i]) : no_vec<T, V>();
-      in.y[i] = has_b[i] ? raw_vec<T, V>(p + second[i]) : no_vec<T, V>();
+      in.x[i] = raw_vec<T, V>(p + at[i]);
+      in.y[i] = raw_vec<T, V>(p + second[i]);
+      if (!FULL && !has_a[i]) in.x[i] = no_vec<T, V>();
+      if (!FULL && !has_b[i]) in.y[i] = no_vec<T, V>();
     }
   }
   static __device__ __forceinline__ void split(const In& in, E (&e)[ITEMS][2][N]) {
@@ -438,31 +443,36 @@ struct Heads {
     to_pairs<V>(f, e);
   }
   static constexpr int kWide = V > 4 ? 4 : V;
-  // Weights: a row of a group's lanes for each item, side and four values, 32 (bf16: 16) lanes apart.
-  static constexpr int kLanes = sizeof(T) == 4 ? 32 : 16, kWeights = kLanes * ITEMS * 2 * V;
+  // Weights: a row of a group's lanes for each item, side and four values, 32 lanes apart.
+  static constexpr int kLanes = 32, kWeights = kLanes * ITEMS * 2 * V;
   static __device__ __forceinline__ int weight_place(int lane, int i, int side, int k) {
     return (((i * 2 + side) * (V / kWide) + k / kWide) * kLanes + lane) * kWide + k % kWide;
   }
   __device__ __forceinline__ void weights(const float* w, int i, int side, E (&e)[N]) const {
     vector<kWide>(w + weight_place(0, i, side, 0), kLanes * kWide, e);
   }
+  __device__ __forceinline__ void rotate_item(const float* angles, int item, E (&e)[2][N]) const {
+    constexpr int W = V == 8 || (INTERLEAVED && V > 1) ? V / 2 : V;
+    const float* p = angles + item * W;
+    E c[N], s[N];
+    vector<W>(p, a.pairs / 2, c);
+    vector<W>(p + a.angles, a.pairs / 2, s);
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const E u = e[0][k], v = e[1][k];
+      e[0][k] = e_sub(e_mul(u, c[k]), e_mul(v, s[k]));
+      e[1][k] = e_fma(v, c[k], e_mul(u, s[k]));
+    }
+  }
   __device__ __forceinline__ void rotate(const float* angles, const Row& r, E (&e)[ITEMS][2][N]) const {
+    const float* p = angles + r.token * a.pairs;
+    if (FULL || a.items_turned == a.items) {  // the same for all lanes; those without an item turn their zeros
 #pragma unroll
-    for (int i = 0; i < ITEMS; ++i) {
-      const int item = lane + i * a.lanes;
-      if (FULL || item < a.items_turned) {
-        constexpr int W = V == 8 || (INTERLEAVED && V > 1) ? V / 2 : V;
-        const float* p = angles + r.token * a.pairs + item * W;
-        E c[N], s[N];
-        vector<W>(p, a.pairs / 2, c);
-        vector<W>(p + a.angles, a.pairs / 2, s);
+      for (int i = 0; i < ITEMS; ++i) rotate_item(p, has_a[i] ? lane + i * a.lanes : 0, e[i]);
+    } else {
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-          const E u = e[i][0][k], v = e[i][1][k];
-          e[i][0][k] = e_sub(e_mul(u, c[k]), e_mul(v, s[k]));
-          e[i][1][k] = e_fma(v, c[k], e_mul(u, s[k]));
-        }
-      }
+      for (int i = 0; i < ITEMS; ++i)
+        if (lane + i * a.lanes < a.items_turned) rotate_item(p, lane + i * a.lanes, e[i]);
     }
   }
 
@@ -783,8 +793,12 @@ fvx_status check_view(const char* who, const char* name, const void* p, int64_t 
 
 uint32_t magic_of(int v) { return (uint32_t)((((uint64_t)1 << 32) + v - 1) / v); }
 
-// Items that make 16 values of bf16 or 8 of fp32 per lane, however narrow its vectors.
-int items_of_lane(fvx_dtype dt, int vec) { return (dt == FVX_F32 ? 4 : 8) / vec; }
+// Items of a lane.  16 values of bf16 in vectors of eight or two, 8 of fp32 and
+// of bf16 in others (300,000 x 8 + 8 x 100 normed: 16 values 544 us, 8 639; the
+// backward pass of x 64 out of odd rows, values one at a time: 16 values, whose
+// registers spill, 1202 us, 8 667; 500,000 x 8 + 8 x 40 rotated: 16 values, of
+// which lanes have 10 or none, 361 us, 8 261).
+constexpr int items_of_lane(bool f32, int vec) { return f32 ? 4 / vec : vec == 1 ? 4 : vec == 2 ? 4 : 1; }
 
 // Results must not lie over each other.
 bool apart(int64_t n, int64_t heads, int64_t d, int64_t token, int64_t head) {
@@ -882,7 +896,7 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
   c->vec = vec;
   a.items_turned = a.pairs / vec;
   a.items = a.items_turned + (d - 2 * a.pairs + 2 * vec - 1) / (2 * vec);
-  const int per_lane = items_of_lane(dt, vec);
+  const int per_lane = items_of_lane(dt == FVX_F32, vec);
   a.lanes = 1;
   while (a.lanes * per_lane < a.items) a.lanes *= 2;  // 32 at most: 256 values in eights (fp32) or sixteens
   a.axes = axes;
@@ -896,7 +910,7 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
 template <typename F>
 fvx_status by_shape(fvx_dtype dt, const Call& c, F&& f) {
   auto layout = [&]<typename T, int V>() -> fvx_status {
-    constexpr int kItems = (sizeof(T) == 4 ? 4 : 8) / V;
+    constexpr int kItems = items_of_lane(sizeof(T) == 4, V);
     return c.interleaved ? f.template operator()<T, V, kItems, true>() : f.template operator()<T, V, kItems, false>();
   };
   if (dt == FVX_F32) {
