@@ -828,15 +828,19 @@ def _head_tensor(who, name, t, positions, rotary, weight, out, x=None, dweight=N
                     f"got {positions.dtype} {tuple(ps)}")
         st = positions.stride()
         pos = (positions.data_ptr(), st[0], st[1] if len(st) > 1 else 0)
-    weight = _channel_vector(weight, d, who, f"the weight of {name}")
+    if weight is not None:
+        weight = _channel_vector(weight, d, who, f"the weight of {name}")
     if out is None:
         out = _empty_rows(t)
     elif out.shape != t.shape or out.dtype != t.dtype or (d > 1 and out.stride(2) != 1):
         _refuse(f"{who}: out must be {t.dtype} {tuple(t.shape)} with dense heads, got {out.dtype} {tuple(out.shape)}")
     st, so = t.stride(), out.stride()
-    sx = x.stride() if x is not None else (0, 0)
-    return _HEAD_TENSOR.pack(n, heads, t.data_ptr(), st[0], st[1], out.data_ptr(), so[0], so[1], *pos, _at(weight) or 0,
-                             _at(x) or 0, sx[0], sx[1], _at(dweight) or 0), out, (t, weight, x)
+    back = (0, 0, 0, 0)
+    if x is not None:
+        sx = x.stride()
+        back = (x.data_ptr(), sx[0], sx[1], dweight.data_ptr())
+    return _HEAD_TENSOR.pack(n, heads, t.data_ptr(), st[0], st[1], out.data_ptr(), so[0], so[1], *pos,
+                             0 if weight is None else weight.data_ptr(), *back), out, (t, weight, x)
 
 
 def _head_call(who, entry, q, k, positions, k_positions, rotary, weight, k_weight, out, last, grads=None):
@@ -846,9 +850,11 @@ def _head_call(who, entry, q, k, positions, k_positions, rotary, weight, k_weigh
     dt = _dtype_code(q, who)
     if k is None and (k_positions is not None or k_weight is not None):
         _refuse(f"{who}: k is missing")
-    if out is not None and (k is not None) != isinstance(out, (tuple, list)):
+    if out is not None and (k is None) != isinstance(out, torch.Tensor):
         _refuse(f"{who}: out must be one tensor, or one for each of q and k")
     outs = (None, None) if out is None else (out,) if k is None else tuple(out)
+    if k is not None and len(outs) != 2:
+        _refuse(f"{who}: out must be one tensor for each of q and k, got {len(outs)}")
     xs = grads or (None, None)
     s = _on_device(who, q, k, positions, k_positions, weight, k_weight, *outs, *xs)
     q = _dense_heads(q, who, "q")
