@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import array
 import ctypes
+import operator
 import os
 import struct
 
@@ -785,16 +786,30 @@ class Rotary:
             _refuse(f'{who}: length belongs to the scaling "parts"')
         pairs = size // 2
         self.size, self.axes, self.layout = size, axes, layout
-        self.turns = np.zeros(pairs, np.uint64)  # per position step, in 2^-64 turns
+        self._made_with = (size, axes, base, layout, scaling, factor, length)
+        self._turns = np.zeros(pairs, np.uint64)
         s = self._struct = _RotaryStruct()
         for a in range(axes):
             s.pairs[a] = pairs // axes + (a < pairs % axes)
         s.interleaved = layout == "interleaved"
-        s.turns = self.turns.ctypes.data
+        s.turns = self._turns.ctypes.data
         _check(load().fvx_rotary_turns(s.pairs, base, codes[scaling], factor, length or 0.0, s.turns,
                                        ctypes.byref(s, _RotaryStruct.magnitude.offset)))
-        self.magnitude = s.magnitude
+        self._turns.setflags(write=False)
         self._at = ctypes.addressof(s)
+
+    @property
+    def turns(self):
+        """The pairs' steps per position, in 2^-64 turns (uint64, read-only)."""
+        return self._turns
+
+    @property
+    def magnitude(self):
+        """What the rotated values are multiplied by."""
+        return self._struct.magnitude
+
+    def __reduce__(self):  # a copy points at steps of its own
+        return Rotary, self._made_with
 
 
 _HEAD_TENSOR = struct.Struct("2qP2qP2qP2qPP2qP")  # fvx_head_tensor_t
@@ -987,6 +1002,7 @@ def _dropout(who, x, p, seed, offset, residual, out):
         state, seed = seed, 0
         if state.dtype != torch.int64 or tuple(state.shape) != (2,) or not state.is_contiguous():
             _refuse(f"{who}: seed must be an int or an int64 tensor of two values, got {state.dtype} {tuple(state.shape)}")
+    seed, offset = operator.index(seed), operator.index(offset)
     if not (0 <= seed < 1 << 64 and 0 <= offset < 1 << 64):
         _refuse(f"{who}: seed and offset must be in 0..2^64 - 1")
     s = _on_device(who, x, residual, out, state)

@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libfvx.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 SOURCES = ["api.cu", "primitives.cu", "build.cu", "kmap.cu", "conv.cu", "rays.cu", "norm.cu", "norm_stream_f32.cu",
-           "norm_stream_bf16.cu", "attn.cu", "attn_tc.cu", "attn_few.cu", "rotary.cu", "dropout.cu"]
+           "norm_stream_bf16.cu", "attn.cu", "attn_tc.cu", "attn_few.cu", "rotary.cu", "rotary_f32.cu", "rotary_bf16.cu",
+           "dropout.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -204,6 +204,14 @@ def test_no_tokens(nq, nk):
     _check_norm_backward(gk, dwk, k, k, one, rotary, _angles(rotary, ak), 1e-6, "f32")
 
 
+def test_no_tokens_of_repeated_heads():
+    """An empty result has whatever strides its tensor had: nothing lies over anything."""
+    import sparse_convolution_gb300 as fvx
+
+    q = torch.empty(0, 1, 16, device="cuda").expand(0, 5, 16)
+    assert fvx.norm_rotate_heads(q).shape == (0, 5, 16)
+
+
 @pytest.mark.parametrize("scaling", ["linear", "base", "parts"])
 def test_stretched_contexts(scaling):
     """The steps themselves are tested on the host; here the magnitude and far positions, exactly in turns."""

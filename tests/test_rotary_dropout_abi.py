@@ -68,6 +68,26 @@ def test_rotary_refuses(lib, bad):
     assert e.value.status == "FVX_ERR_INVALID_ARG"
 
 
+def test_copies_own_their_steps(lib):
+    """A copied or unpickled Rotary does not point into the original's memory."""
+    import copy
+    import gc
+    import pickle
+
+    import sparse_convolution_gb300 as fvx
+
+    r = fvx.Rotary(64, axes=2, layout="interleaved", scaling="parts", factor=4.0, length=1000)
+    want, copies = r.turns.copy(), [copy.copy(r), copy.deepcopy(r), pickle.loads(pickle.dumps(r))]
+    assert not r.turns.flags.writeable
+    del r
+    gc.collect()
+    for c in copies:
+        held = np.ctypeslib.as_array(ctypes.cast(c._struct.turns, ctypes.POINTER(ctypes.c_uint64)), (32,))
+        assert np.array_equal(held, want) and c._struct.turns == c.turns.ctypes.data
+        assert c._at == ctypes.addressof(c._struct) and (c.axes, c.layout, c.size) == (2, "interleaved", 64)
+        assert c.magnitude == pytest.approx(0.1 * math.log(4) + 1, rel=2.0 ** -23)
+
+
 def test_turns_refuses(lib):
     f = lib.fvx_rotary_turns
     turns, m = (ctypes.c_uint64 * 128)(), ctypes.c_float()
