@@ -491,7 +491,8 @@ fvx_status fvx_cross_attention_backward(fvx_dtype dt, const void* dout, int64_t 
  *   (u, v) -> magnitude * (u cos t - v sin t, v cos t + u sin t)
  * turns: HOST array of the P steps f_p / (2 pi), in units of 2^-64 turns, read
  * during the call.  Angles are taken modulo whole turns in integers: a position
- * of any int32 value loses nothing. */
+ * of any int32 value loses nothing.  A tensor's rotated values are within 12
+ * units of 2^-24 of magnitude * (|u| + |v|), plus the result's rounding. */
 typedef struct {
   int32_t pairs[3];
   int32_t interleaved;   /* 0: halves */
@@ -526,7 +527,8 @@ typedef struct {
   int64_t n, heads;
   const void* in;           /* what is rotated; backward: the gradient of the result */
   int64_t in_token, in_head;
-  void* out;                /* may be in itself (same strides; backward: or x); heads must not lie over each other */
+  void* out;                /* may be in itself (same strides; backward: or x); otherwise no result may lie over
+                             * another's memory or a tensor's that is read */
   int64_t out_token, out_head;
   const int32_t* positions; /* device [n] or [n, axes]; ignored without a rotation */
   int64_t pos_token, pos_axis;
@@ -543,7 +545,8 @@ fvx_status fvx_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* te
                             const fvx_rotary_t* rotary, int32_t transposed, fvx_stream stream);
 
 /* out = the rotated  x * rstd * weight,  rstd = 1 / sqrt(sum x^2 / d + eps) of
- * each head; rotary NULL: without the rotation. */
+ * each head; rotary NULL: without the rotation.  Squares are summed in fp32:
+ * values up to about 10^18. */
 fvx_status fvx_norm_rotate_heads(fvx_dtype dt, int32_t d, const fvx_head_tensor_t* tensors, int32_t count,
                                  const fvx_rotary_t* rotary, float eps, fvx_stream stream);
 

@@ -1,6 +1,31 @@
-// Heads normed and turned: what a call is (rotary.cu reads it from the C entry
-// points) and the kernels that do it, compiled for one storage type per file
-// (rotary_f32.cu, rotary_bf16.cu).
+// Heads normed and turned (formulas: rotary.cu): what a call is and the kernels
+// that do it, compiled for one storage type per file (rotary_f32.cu,
+// rotary_bf16.cu).
+//
+// A few bytes and a few operations per value: memory bounds it, if the
+// instructions allow.  A kernel that computed a token's angles in every group of
+// lanes and kept loads in registers spent 20 instructions per value of bf16 where
+// the memory's rate leaves 22 (1,000,000 x 8 + 8 x 64 normed and turned in 1113 us,
+// backward 1801).  So a persistent block per multiprocessor divides the work:
+//   warps 0-15   workers: a head per group of lanes, 16 values of bf16 (8 of
+//                fp32) a lane, out of shared memory, two values at a time; the
+//                results go straight to global memory
+//   warps 16-23  helpers: copy the next stage's tokens to shared memory, by bulk
+//                copies where bases and strides are multiples of 16 bytes, by
+//                words else, and compute their angles, once per token for all
+//                heads of queries and keys
+// 13 instructions per value (17 with the norm; counted over all warps, waits
+// included), and copies under way whatever the workers do.
+//
+// Measured (bf16 unless said, of the copy rate of 6.76 TB/s): 1,000,000 x 8 + 8 x 64
+// turned by three coordinates in 630 us (96%), normed and turned 609 (99%),
+// backward 972 (94%); 300,000 x 4 + 4 x 256 397 (91%), 378 (96%), 681 (80%);
+// 150,001 x 8 + 2 x 128 out of rows of 12 heads 130 (88%), 125 (91%), 235 (73%);
+// 300,000 x 16 + 16 x 64 fp32, 32 turned, 754 (97%), 718 (101%), 1066 (102%).
+// What bounds the rest: two heads of 128 per token need an angle for every four
+// values (2,400,000 x 2 x 128 normed 616 us, 59%); heads of 80 or 96 leave lanes
+// idle (500,000 x 8 + 8 x 96 normed 681 us, 67%); rows that only 2-byte accesses
+// read (300,000 x 8 + 8 x 64 out of rows of odd length 487 us, 37%).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -54,7 +79,7 @@ struct HeadArgs {
   int shared;  // a stage holds the same tokens of both tensors; else tiles of the first, then of the second
   int d, pairs, axes, axis1, axis2;  // pairs from axis1 (axis2) on belong to the second (third) axis
   int items, items_turned, lanes;    // a head's items: of pairs, of values that pass; lanes that share a head
-  int fours;                         // the angles' order: see angles_of
+  int fours;                         // the angles' order: see AngleThread
   int pair_lanes;                    // helper threads of a token's angles: pairs, to the next power of two
   int angles, stage_bytes;           // of a stage: angles, bytes of the tensors
   float magnitude, sign, eps, inv_d;
