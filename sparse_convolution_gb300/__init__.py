@@ -815,88 +815,97 @@ class Rotary:
 _HEAD_TENSOR = struct.Struct("2qP2qP2qP2qPP2qP")  # fvx_head_tensor_t
 
 
-def _dense_heads(t, who, name, shape=None, dtype=None):
-    """t [tokens, heads, size] with a dense last dimension (a copy where it is not)."""
-    if t.dim() != 3 or (shape is not None and t.shape != shape) or (dtype is not None and t.dtype != dtype):
-        want = "[tokens, heads, size]" if shape is None else f"{dtype} {tuple(shape)}"
+def _head_views(t, who, name, like=None):
+    """(t [tokens, heads, size] with a dense last dimension, its shape, its
+    strides); a copy where it has gaps.  like: the tensor whose shape and type it
+    must have."""
+    if t.dim() != 3 or (like is not None and (t.shape != like.shape or t.dtype != like.dtype)):
+        want = "[tokens, heads, size]" if like is None else f"{like.dtype} {tuple(like.shape)}"
         _refuse(f"{who}: {name} must be {want}, got {t.dtype} {tuple(t.shape)}")
-    return t if t.stride(2) == 1 or t.shape[2] == 1 else t.contiguous()
+    shape, st = t.shape, t.stride()
+    if st[2] != 1 and shape[2] != 1:
+        t = t.contiguous()
+        st = t.stride()
+    return t, shape, st
 
 
-def _head_tensor(who, name, t, positions, rotary, weight, out, x=None, dweight=None):
-    """(packed fvx_head_tensor_t, result, what must outlive the call)"""
-    import torch
+def _head_positions(who, name, positions, n, rotary, int32):
+    """(address, token stride, axis stride)"""
+    if positions is None:
+        _refuse(f"{who}: positions are missing")
+    axes, ps = rotary.axes, positions.shape
+    if positions.dtype is not int32 or not (ps == (n, axes) or (axes == 1 and ps == (n,))):
+        _refuse(f"{who}: positions of {name} must be int32 [{n}{', %d' % axes if axes > 1 else ''}], "
+                f"got {positions.dtype} {tuple(ps)}")
+    st = positions.stride()
+    return positions.data_ptr(), st[0], st[1] if len(st) > 1 else 0
 
-    n, heads, d = t.shape
+
+def _head_tensor(who, name, views, positions, rotary, weight, out, x, dweight, torch):
+    """(packed fvx_head_tensor_t, result, what must outlive the call); x: the views of the norm's input."""
+    t, (n, heads, d), st = views
     if heads < 1 or not 1 <= d <= 256:
         _refuse(f"{who}: {name} must have at least one head of 1 to 256 values, got {tuple(t.shape)}")
     pos = (0, 0, 0)
     if rotary is not None:
-        axes = rotary.axes
         if rotary.size > d:
             _refuse(f"{who}: {rotary.size} rotated channels do not fit into heads of {d}")
-        if positions is None:
-            _refuse(f"{who}: positions are missing")
-        ps = positions.shape
-        if positions.dtype != torch.int32 or tuple(ps) not in (((n,), (n, 1)) if axes == 1 else ((n, axes),)):
-            _refuse(f"{who}: positions of {name} must be int32 [{n}{', %d' % axes if axes > 1 else ''}], "
-                    f"got {positions.dtype} {tuple(ps)}")
-        st = positions.stride()
-        pos = (positions.data_ptr(), st[0], st[1] if len(st) > 1 else 0)
+        pos = _head_positions(who, name, positions, n, rotary, torch.int32)
     if weight is not None:
         weight = _channel_vector(weight, d, who, f"the weight of {name}")
     if out is None:
-        out = _empty_rows(t)
+        out = torch.empty_like(t) if t.is_contiguous() else torch.empty((n, heads, d), dtype=t.dtype, device=t.device)
     elif out.shape != t.shape or out.dtype != t.dtype or (d > 1 and out.stride(2) != 1):
         _refuse(f"{who}: out must be {t.dtype} {tuple(t.shape)} with dense heads, got {out.dtype} {tuple(out.shape)}")
-    st, so = t.stride(), out.stride()
-    back = (0, 0, 0, 0)
-    if x is not None:
-        sx = x.stride()
-        back = (x.data_ptr(), sx[0], sx[1], dweight.data_ptr())
+    so = out.stride()
+    back = (0, 0, 0, 0) if x is None else (x[0].data_ptr(), x[2][0], x[2][1], dweight.data_ptr())
     return _HEAD_TENSOR.pack(n, heads, t.data_ptr(), st[0], st[1], out.data_ptr(), so[0], so[1], *pos,
-                             0 if weight is None else weight.data_ptr(), *back), out, (t, weight, x)
+                             0 if weight is None else weight.data_ptr(), *back), out, weight
 
 
 def _head_call(who, entry, q, k, positions, k_positions, rotary, weight, k_weight, out, last, grads=None):
     """One launch over q and (not None) k; grads: (x of q, x of k) for the backward pass."""
     import torch
 
-    dt = _dtype_code(q, who)
+    dtype = q.dtype
+    dt = FVX_BF16 if dtype is torch.bfloat16 else _dtype_code(q, who)
+    if rotary is not None and not isinstance(rotary, Rotary):
+        _refuse(f"{who}: a Rotary is needed, got {type(rotary).__name__}")
     if k is None and (k_positions is not None or k_weight is not None):
         _refuse(f"{who}: k is missing")
-    if out is not None and (k is None) != isinstance(out, torch.Tensor):
-        _refuse(f"{who}: out must be one tensor, or one for each of q and k")
-    outs = (None, None) if out is None else (out,) if k is None else tuple(out)
-    if k is not None and len(outs) != 2:
-        _refuse(f"{who}: out must be one tensor for each of q and k, got {len(outs)}")
-    xs = grads or (None, None)
-    s = _on_device(who, q, k, positions, k_positions, weight, k_weight, *outs, *xs)
-    q = _dense_heads(q, who, "q")
-    if grads:
-        q = _dense_heads(q, who, "dq", xs[0].shape, xs[0].dtype)
-        xq = _dense_heads(xs[0], who, "q")
-    dw = dwk = None
-    if grads:
-        dw = torch.empty((q.shape[2],), dtype=torch.float32, device=q.device)
-    packed, q_out, hold = _head_tensor(who, "q", q, positions, rotary, weight, outs[0], xq if grads else None, dw)
-    count, k_out, k_hold = 1, None, None
-    if k is not None:
-        xk = None
-        if grads:
-            k = _dense_heads(k, who, "dk", xs[1].shape, xs[1].dtype)
-            xk = _dense_heads(xs[1], who, "k")
-            dwk = torch.empty((k.shape[2],), dtype=torch.float32, device=q.device)
+    q_out = k_out = None
+    if out is not None:
+        if (k is None) != isinstance(out, torch.Tensor):
+            _refuse(f"{who}: out must be one tensor, or one for each of q and k")
+        if k is None:
+            q_out = out
+        elif len(out) != 2:
+            _refuse(f"{who}: out must be one tensor for each of q and k, got {len(out)}")
         else:
-            k = _dense_heads(k, who, "k")
-        if k.dtype != q.dtype or k.shape[2] != q.shape[2]:
-            _refuse(f"{who}: q and k must have one type and head size, got {q.dtype} {tuple(q.shape)} and "
+            q_out, k_out = out
+    xq, xk = grads or (None, None)
+    s = _on_device(who, q, k, positions, k_positions, weight, k_weight, q_out, k_out, xq, xk)
+    dw = dwk = None
+    if grads is None:
+        q = _head_views(q, who, "q")
+    else:
+        q, xq = _head_views(q, who, "dq", xq), _head_views(xq, who, "q")
+        dw = torch.empty((2, q[1][2]), dtype=torch.float32, device=xq[0].device)
+        dw, dwk = dw[0], dw[1]
+    packed, q_out, hold = _head_tensor(who, "q", q, positions, rotary, weight, q_out, xq, dw, torch)
+    count = 1
+    if k is not None:
+        if k.dtype is not dtype or (k.dim() == 3 and k.shape[2] != q[1][2]):
+            _refuse(f"{who}: q and k must have one type and head size, got {dtype} {tuple(q[1])} and "
                     f"{k.dtype} {tuple(k.shape)}")
+        if grads is None:
+            k = _head_views(k, who, "k")
+        else:
+            k, xk = _head_views(k, who, "dk", xk), _head_views(xk, who, "k")
         more, k_out, k_hold = _head_tensor(who, "k", k, positions if k_positions is None else k_positions, rotary,
-                                           k_weight, outs[1], xk, dwk)
+                                           k_weight, k_out, xk, dwk, torch)
         packed, count = packed + more, 2
-    _check(entry(dt, q.shape[2], packed, count, rotary._at if rotary is not None else None, last, s))
-    del hold, k_hold
+    _check(entry(dt, q[1][2], packed, count, None if rotary is None else rotary._at, last, s))
     return q_out, k_out, dw, dwk
 
 
@@ -908,8 +917,9 @@ def rotate_heads(q, positions, rotary, k=None, k_positions=None, out=None, strea
     q and k themselves will do).  Returns q's result, or (q's, k's)."""
     if stream is not None:
         return _on_stream(stream, rotate_heads, q, positions, rotary, k, k_positions, out)
-    q, k, _, _ = _head_call("rotate_heads", load().fvx_rotate_heads, q, k, positions, k_positions, _a_rotary(rotary),
-                            None, None, out, 0)
+    if rotary is None:
+        _refuse("rotate_heads: a Rotary is needed, got None")
+    q, k, _, _ = _head_call("rotate_heads", load().fvx_rotate_heads, q, k, positions, k_positions, rotary, None, None, out, 0)
     return q if k is None else (q, k)
 
 
@@ -918,15 +928,11 @@ def rotate_heads_backward(dq, positions, rotary, dk=None, k_positions=None, out=
     turned back.  Returns dq, or (dq, dk)."""
     if stream is not None:
         return _on_stream(stream, rotate_heads_backward, dq, positions, rotary, dk, k_positions, out)
+    if rotary is None:
+        _refuse("rotate_heads_backward: a Rotary is needed, got None")
     q, k, _, _ = _head_call("rotate_heads_backward", load().fvx_rotate_heads, dq, dk, positions, k_positions,
-                            _a_rotary(rotary), None, None, out, 1)
+                            rotary, None, None, out, 1)
     return q if k is None else (q, k)
-
-
-def _a_rotary(r):
-    if not isinstance(r, Rotary):
-        _refuse(f"a Rotary is needed, got {type(r).__name__}")
-    return r
 
 
 def norm_rotate_heads(q, positions=None, rotary=None, weight=None, k=None, k_positions=None, k_weight=None, eps=1e-6,
@@ -939,7 +945,7 @@ def norm_rotate_heads(q, positions=None, rotary=None, weight=None, k=None, k_pos
     if stream is not None:
         return _on_stream(stream, norm_rotate_heads, q, positions, rotary, weight, k, k_positions, k_weight, eps, out)
     q, k, _, _ = _head_call("norm_rotate_heads", load().fvx_norm_rotate_heads, q, k, positions, k_positions,
-                            None if rotary is None else _a_rotary(rotary), weight, k_weight, out, eps)
+                            rotary, weight, k_weight, out, eps)
     return q if k is None else (q, k)
 
 
@@ -955,19 +961,20 @@ def norm_rotate_heads_backward(dq, q, positions=None, rotary=None, weight=None, 
     if (dk is None) != (k is None):
         _refuse(f"{who}: dk and k belong together")
     dq, dk, dw, dwk = _head_call(who, load().fvx_norm_rotate_heads_backward, dq, dk, positions, k_positions,
-                                 None if rotary is None else _a_rotary(rotary), weight, k_weight, out, eps, (q, k))
+                                 rotary, weight, k_weight, out, eps, (q, k))
     return (dq, dw) if k is None else (dq, dk, dw, dwk)
 
 
 def _pitched(t, who, name, like=None):
-    """t as rows of dense values: (tensor, rows, values per row, pitch).  Tensors of any shape without gaps count as
-    one row."""
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        _refuse(f"{who}: {name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(t.shape)}")
-    if t.dim() == 2 and not t.is_contiguous() and t.stride(1) == 1 and t.stride(0) >= t.shape[1]:
-        return t, t.stride(0)
-    t = t.contiguous()
-    return t, t.shape[-1] if t.dim() else 1
+    """(t as rows of dense values, their pitch); tensors of any shape without gaps count as such rows."""
+    shape = t.shape
+    if like is not None and (shape != like.shape or t.dtype != like.dtype):
+        _refuse(f"{who}: {name} must be {like.dtype} {tuple(like.shape)}, got {t.dtype} {tuple(shape)}")
+    if not t.is_contiguous():
+        if len(shape) == 2 and t.stride(1) == 1 and t.stride(0) >= shape[1]:
+            return t, t.stride(0)
+        t = t.contiguous()
+    return t, shape[-1] if shape else 1
 
 
 def dropout(x, p, seed, offset=0, residual=None, out=None, stream=None):
