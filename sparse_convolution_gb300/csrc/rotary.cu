@@ -158,9 +158,7 @@ fvx_status prepare(const char* who, fvx_dtype dt, int32_t d, const fvx_head_tens
   c->vec = vec;
   a.items_turned = a.pairs / vec;
   a.items = a.items_turned + (d - 2 * a.pairs + 2 * vec - 1) / (2 * vec);
-  const int per_lane = items_of_lane(dt == FVX_F32, vec);
-  a.lanes = 1;
-  while (a.lanes * per_lane < a.items) a.lanes *= 2;  // 32 at most: 256 values in eights (fp32) or sixteens
+  a.lanes = lanes_of_head(a.items, items_of_lane(dt == FVX_F32, vec));  // 32 at most: 256 values in eights or sixteens
   a.axes = axes;
   a.fours = vec == 8 && !c->interleaved;
   a.pair_lanes = 1;

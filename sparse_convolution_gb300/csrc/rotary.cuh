@@ -78,7 +78,7 @@ struct HeadArgs {
   uint32_t* status;
   int shared;  // a stage holds the same tokens of both tensors; else tiles of the first, then of the second
   int d, pairs, axes, axis1, axis2;  // pairs from axis1 (axis2) on belong to the second (third) axis
-  int items, items_turned, lanes;    // a head's items: of pairs, of values that pass; lanes that share a head
+  int items, items_turned, lanes;    // a head's items: of pairs, of values that pass; lanes that share a head (32 / lanes heads at a time)
   int fours;                         // the angles' order: see AngleThread
   int pair_lanes;                    // helper threads of a token's angles: pairs, to the next power of two
   int angles, stage_bytes;           // of a stage: angles, bytes of the tensors
@@ -107,12 +107,21 @@ fvx_status run_heads_f32(const char* name, HeadCall& c, HeadOp op, int jobs, con
 fvx_status run_heads_bf16(const char* name, HeadCall& c, HeadOp op, int jobs, const fvx_head_tensor_t* t, HeadDw* dw,
                           cudaStream_t s, Scratch* scr);
 
-// Items of a lane.  16 values of bf16 in vectors of eight or two, 8 of fp32 and
-// of bf16 in others (300,000 x 8 + 8 x 100 normed: 16 values 544 us, 8 639; the
-// backward pass of x 64 out of odd rows, values one at a time: 16 values, whose
-// registers spill, 1202 us, 8 667; 500,000 x 8 + 8 x 40 rotated: 16 values, of
-// which lanes have 10 or none, 361 us, 8 261).
-constexpr int items_of_lane(bool f32, int vec) { return f32 ? 4 / vec : vec == 1 ? 4 : vec == 2 ? 4 : 1; }
+// Items of a lane: 16 values of bf16, 8 of fp32 and of bf16 one at a time
+// (300,000 x 8 + 8 x 100, accesses of two values, normed: 16 values 544 us, 8 639;
+// x 40, of four, 311 and 382; the backward pass of x 64 out of odd rows, one at a
+// time: 16 values, whose registers spill, 1202 us, 8 667).
+constexpr int items_of_lane(bool f32, int vec) { return (f32 || vec == 1 ? 4 : 8) / vec; }
+// Lanes of a head of `items` items: a power of two, over which sums are quick,
+// unless fewer lanes let a warp take more heads at once (500,000 x 8 + 8 x 80 bf16
+// in five lanes, not eight: turned 450 to 380 us, normed 673 to 484, backward 1147
+// to 760; in seven for x 100, which gain no head, normed 476 to 571).
+constexpr int lanes_of_head(int items, int per_lane) {
+  const int least = (items + per_lane - 1) / per_lane;
+  int two = 1;
+  while (two < least) two *= 2;
+  return 32 / least > 32 / two ? least : two;
+}
 
 namespace {
 
@@ -338,7 +347,7 @@ struct Heads {
   E dw[kBack ? ITEMS : 1][2][N];
 
   __device__ __forceinline__ explicit Heads(const HeadArgs& args)
-      : a(args), lane(threadIdx.x & (args.lanes - 1)), group((threadIdx.x & 31) / args.lanes), groups(32 / args.lanes) {
+      : a(args), lane((threadIdx.x & 31) % args.lanes), group((threadIdx.x & 31) / args.lanes), groups(32 / args.lanes) {
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int item = lane + i * a.lanes;
@@ -377,13 +386,40 @@ struct Heads {
     if (!INTERLEAVED || V == 1) return (side ? second : first) + k;
     return (k < V / 2 ? first + 2 * k : second + 2 * k - V) + side;
   }
-  // sums over the lanes that share a head
+  // Sums over the lanes that share a head.  Where they are no power of two, each
+  // lane adds runs of 1, 2, 4, ... lanes from its own on, around the group: one
+  // run for each bit of their number.
   __device__ __forceinline__ void head_sums(float& v, float& w) const {
+    if ((a.lanes & (a.lanes - 1)) == 0) {
 #pragma unroll 1
-    for (int o = a.lanes >> 1; o > 0; o >>= 1) {
-      v += __shfl_xor_sync(0xffffffffu, v, o);
-      if constexpr (kBack) w += __shfl_xor_sync(0xffffffffu, w, o);
+      for (int o = a.lanes >> 1; o > 0; o >>= 1) {
+        v += __shfl_xor_sync(0xffffffffu, v, o);
+        if constexpr (kBack) w += __shfl_xor_sync(0xffffffffu, w, o);
+      }
+      return;
     }
+    float all_v = 0.0f, all_w = 0.0f;
+    const int first = group * a.lanes;
+    auto from = [&](int ahead) {
+      const int l = lane + ahead;
+      return first + (l >= a.lanes ? l - a.lanes : l);
+    };
+    int done = 0;
+#pragma unroll 1
+    for (int run = 1;; run <<= 1) {
+      if (a.lanes & run) {
+        const int at = from(done);
+        all_v += __shfl_sync(0xffffffffu, v, at);
+        if constexpr (kBack) all_w += __shfl_sync(0xffffffffu, w, at);
+        done += run;
+        if (done == a.lanes) break;
+      }
+      const int at = from(run);
+      v += __shfl_sync(0xffffffffu, v, at);
+      if constexpr (kBack) w += __shfl_sync(0xffffffffu, w, at);
+    }
+    v = all_v;
+    w = all_w;
   }
 
   // A group's head within the tile.  Groups without one take the tile's first and store nothing.
@@ -605,15 +641,25 @@ struct Heads {
     for (int i = 0; i < ITEMS; ++i)
 #pragma unroll
       for (int side = 0; side < 2; ++side) {
-        float f[V];
+        float f[V], sum[V];
         from_pairs<V>(dw[i][side], f);
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
+        for (int k = 0; k < V; ++k) sum[k] = f[k];
+        if ((a.lanes & (a.lanes - 1)) == 0) {
+#pragma unroll 1
+          for (int o = a.lanes; o < 32; o <<= 1)
 #pragma unroll
-          for (int o = 16; o > 0; o >>= 1)
-            if (o >= a.lanes) f[k] += __shfl_xor_sync(0xffffffffu, f[k], o);
+            for (int k = 0; k < V; ++k) sum[k] += __shfl_xor_sync(0xffffffffu, sum[k], o);
+        } else {
+#pragma unroll 1
+          for (int g = 1; g < groups; ++g)
+#pragma unroll
+            for (int k = 0; k < V; ++k) sum[k] += __shfl_down_sync(0xffffffffu, f[k], g * a.lanes);
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
           const int c = channel(a, lane + i * a.lanes, side, k);
-          if (group == 0 && has_a[i] && c < a.d) sh[(threadIdx.x >> 5) * a.d + c] = f[k];
+          if (group == 0 && has_a[i] && c < a.d) sh[(threadIdx.x >> 5) * a.d + c] = sum[k];
         }
       }
     workers_sync();
@@ -751,7 +797,7 @@ __global__ void __launch_bounds__(kHeadThreads, 1) k_heads(const __grid_constant
       const int k = r0 + h.group;
       r.token = j.head_block == 1 ? k : (int)__umulhi((uint32_t)k, j.block_magic);
       r.head = k - r.token * j.head_block;
-      r.live = r.token < s.tokens && r.head < s.heads;
+      r.live = r.token < s.tokens && r.head < s.heads && h.group < h.groups;  // lanes left over have none
       if (!r.live) r.token = r.head = 0;
       if constexpr (H::kBack) h.backward(j, stage, at, weight, s, r, out);
       else h.forward(j, stage, at, weight, s, r, out);
@@ -1023,7 +1069,7 @@ fvx_status run_heads(const char* name, HeadCall& c, HeadOp op, int jobs, const f
       if (op == kNormRotate) return launch_heads<T, V, ITEMS, IL, kNormRotate, FULL>(name, c.a, jobs, t, dw, s, scr);
       return launch_heads<T, V, ITEMS, IL, kNormRotateBack, FULL>(name, c.a, jobs, t, dw, s, scr);
     };
-    // heads of 16, 32, 64, 128 or 256 values that turn as a whole: no lane asks what it has
+    // heads of a multiple of 16 (fp32: 8) values that turn as a whole: no lane asks what it has
     if constexpr (V * sizeof(T) == 16)
       if (c.a.d == c.a.lanes * ITEMS * 2 * V && 2 * c.a.pairs == c.a.d) return go.template operator()<true>();
     return go.template operator()<false>();
