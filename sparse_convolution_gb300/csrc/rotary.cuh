@@ -18,14 +18,15 @@
 // included), and copies under way whatever the workers do.
 //
 // Measured (bf16 unless said, of the copy rate of 6.76 TB/s): 1,000,000 x 8 + 8 x 64
-// turned by three coordinates in 630 us (96%), normed and turned 609 (99%),
-// backward 972 (94%); 300,000 x 4 + 4 x 256 397 (91%), 378 (96%), 681 (80%);
-// 150,001 x 8 + 2 x 128 out of rows of 12 heads 130 (88%), 125 (91%), 235 (73%);
-// 300,000 x 16 + 16 x 64 fp32, 32 turned, 754 (97%), 718 (101%), 1066 (102%).
+// turned by three coordinates in 626 us (97%), normed and turned 615 (99%),
+// backward 975 (93%); 300,000 x 4 + 4 x 256 395 (92%), 386 (94%), 669 (82%);
+// 500,000 x 8 + 8 x 80 381 (100%), 484 (78%), 757 (75%); 150,001 x 8 + 2 x 128 out of
+// rows of 12 heads 131 (87%), 129 (89%), 234 (73%); 300,000 x 16 + 16 x 64 fp32, 32
+// turned, 755 (96%), 722 (101%), 1065 (103%).
 // What bounds the rest: two heads of 128 per token need an angle for every four
-// values (2,400,000 x 2 x 128 normed 616 us, 59%); heads of 80 or 96 leave lanes
-// idle (500,000 x 8 + 8 x 96 normed 681 us, 67%); rows that only 2-byte accesses
-// read (300,000 x 8 + 8 x 64 out of rows of odd length 487 us, 37%).
+// values (2,400,000 x 2 x 128 normed 635 us, 57%); halves that only narrow accesses
+// read (300,000 x 8 + 8 x 100, of two values, normed 493 us, 58%), and rows that
+// only single ones do (x 64 out of rows of odd length 495 us, 37%).
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
