@@ -1054,6 +1054,20 @@ fvx_status launch_heads(const char* name, HeadArgs& a, int jobs, const fvx_head_
     if (!(a.job[i].part = scr->get<float>((size_t)blocks * a.d))) return FVX_ERR_ALLOC;
     dw->part[i] = a.job[i].part;
   }
+  if constexpr (H::kBack) {
+    // The warps' shares of registers must not exceed those that the block is
+    // launched with, or they wait for the rest: looked up once.
+    static std::atomic<int> registers{0};
+    if (registers == 0) {
+      cudaFuncAttributes f;
+      FVX_CUDA(cudaFuncGetAttributes(&f, (const void*)k_heads<T, V, ITEMS, IL, OP, FULL>));
+      registers = f.numRegs;
+    }
+    if (registers * kHeadThreads < 32 * (kWorkers * 88 + kHelpers * 64)) {
+      set_error("%s: the kernel was compiled for %d registers", t_entry, registers.load());
+      return FVX_ERR_CUDA;
+    }
+  }
   static std::atomic<uint64_t> allowed{0};
   FVX_TRY(allow_smem((const void*)k_heads<T, V, ITEMS, IL, OP, FULL>, kMostSmem, allowed));
   LaunchScope ls(name, s);
