@@ -399,3 +399,42 @@ def test_refusals():
         with pytest.raises(fvx.FvxError) as e:
             call()
         assert e.value.status == "FVX_ERR_INVALID_ARG"
+
+
+def test_calls_at_once():
+    """Host threads on streams of their own, whose calls take different kernels and amounts of shared memory."""
+    import threading
+
+    import sparse_convolution_gb300 as fvx
+
+    rng = np.random.default_rng(13)
+    calls = []
+    for n, h, d, dtype in ((20000, 8, 64, "bf16"), (7000, 6, 80, "bf16"), (9000, 4, 40, "f32"), (3, 2, 128, "bf16")):
+        q, dq = _heads(n, h, d, dtype, rng), _heads(n, h, d, dtype, rng)
+        at, rotary, w = _positions(n, 3, rng), fvx.Rotary(d // 4 * 2, axes=3), torch.ones(d, device="cuda")
+
+        def call(q=q, dq=dq, at=at, rotary=rotary, w=w):
+            return [fvx.norm_rotate_heads(q, at, rotary, w), *fvx.norm_rotate_heads_backward(dq, q, at, rotary, w),
+                    fvx.dropout(q, 0.3, 5, 6, residual=dq)]
+
+        calls.append((call, call()))
+    torch.cuda.synchronize()
+    failed, start = [], threading.Barrier(len(calls))
+
+    def work(call, want):
+        side = torch.cuda.Stream()
+        start.wait()
+        with torch.cuda.stream(side):
+            for _ in range(30):
+                got = call()
+            side.synchronize()
+            if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                failed.append(want[0].shape)
+
+    threads = [threading.Thread(target=work, args=c) for c in calls]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    fvx.device_status()
+    assert not failed, failed
